@@ -32,6 +32,18 @@ from ._lib import (  # noqa: F401
     lib,
 )
 
+from ._block import (  # noqa: E402,F401
+    BLOCK_LIB_FILE,
+    block_lib,
+    dyt_attn_backward,
+    dyt_attn_bucket_borders,
+    dyt_attn_forward,
+    dyt_ln_backward,
+    dyt_ln_backward_residual,
+    dyt_ln_backward_workspace_size,
+    dyt_ln_forward,
+    dyt_ln_forward_residual,
+)
 from .module import DyT, DyTFunction, DyTResidual, DyTResidualFunction, dyt, dyt_residual  # noqa: E402,F401
 
 __all__ = [
@@ -42,4 +54,7 @@ __all__ = [
     "dyt_backward_residual_partials",
     "dyt_status_string", "dyt_abi_version", "dyt_get_plan", "dyt_get_forward_plan",
     "dyt_get_forward_residual_plan", "dyt_xcd_hint", "dyt_set_xcd_flip_override",
+    "BLOCK_LIB_FILE", "block_lib", "dyt_ln_forward", "dyt_ln_forward_residual", "dyt_ln_backward",
+    "dyt_ln_backward_residual", "dyt_ln_backward_workspace_size", "dyt_attn_forward", "dyt_attn_backward",
+    "dyt_attn_bucket_borders",
 ]

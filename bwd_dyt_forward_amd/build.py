@@ -27,6 +27,16 @@ SOURCES = [os.path.join(CSRC, "dyt_api.hip")] + [
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in (
     "dyt_kernels.hpp", "dyt_math.hpp", "dyt_launch.hpp", "dyt_launch_impl.hpp",
     "dyt_tune_table.inc")] + [os.path.join(INCLUDE, "dyt.h")]
+# The transformer-block operators (layer norm, attention): a library of their
+# own, so that a change here leaves the DyT library and its build id alone.
+BLOCK_LIB_PATH = os.path.join(PKG_DIR, "libdyt_block.so")
+BLOCK_SOURCES = [os.path.join(CSRC, "block_api.hip"), os.path.join(CSRC, "attn_api.hip")] + [
+    os.path.join(CSRC, f"{k}_{t}.hip") for k in ("attn_fwd", "attn_dq", "attn_dkv", "ln_launch")
+    for t in ("f32", "bf16", "f16")]
+BLOCK_DEPENDS = BLOCK_SOURCES + [os.path.join(CSRC, f) for f in (
+    "block_common.hpp", "block_host.hpp", "ln_kernels.hpp", "ln_launch.hpp", "ln_launch_impl.hpp",
+    "attn_tile.hpp", "attn_fwd.hpp", "attn_bwd.hpp", "attn_launch.hpp", "dyt_math.hpp")] + [
+    os.path.join(INCLUDE, "dyt.h"), os.path.join(INCLUDE, "dyt_block.h")]
 # Reference streaming kernels for bench.py's measured ceilings (not part of
 # the DyT ABI; nothing in the package loads them).
 STREAM_REF_SOURCE = os.path.join(CSRC, "stream_ref.hip")
@@ -51,13 +61,13 @@ JOBS = max(1, min(16, len(os.sched_getaffinity(0)) if hasattr(os, "sched_getaffi
 BUILD_ID_MARK = b"DYT_BUILD_ID="
 
 
-def source_hash(extra_flags=()) -> str:
-    """Hash of every source the library is built from (kernels, launch and
+def source_hash(extra_flags=(), depends=None) -> str:
+    """Hash of every source the library (or, with `depends`, another one) is built from (kernels, launch and
     host code, the tile table, the header) with comments and blank space
     removed, and of the compiler flags (plus the extra flags of a variant
     build): two trees with the same hash build the same code."""
     h = hashlib.sha256()
-    for p in DEPENDS:
+    for p in DEPENDS if depends is None else depends:
         with open(p) as f:
             src = f.read()
         src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
@@ -97,8 +107,9 @@ OBJ_CACHE = os.path.join(PKG_DIR, "_build")
 
 def build(out: str = LIB_PATH, extra_flags: list[str] | None = None, verbose: bool = False,
           with_stream_ref: bool = True, cache: bool = False) -> str:
-    """Compile the library (and, by default, the reference streaming kernels
-    next to the default library path); returns the library's path. Always
+    """Compile the library (and, by default, the block operators' library and
+    the reference streaming kernels next to the default library path);
+    returns the library's path. Always
     recompiles every source, unless cache=True, which reuses the object of
     a translation unit whose source, headers and flags are unchanged. Only
     the host translation unit carries the build id."""
@@ -107,7 +118,22 @@ def build(out: str = LIB_PATH, extra_flags: list[str] | None = None, verbose: bo
     _compile(out, SOURCES, extra, verbose, per_source, OBJ_CACHE if cache else None)
     if with_stream_ref and out == LIB_PATH:
         _compile(STREAM_REF_PATH, [STREAM_REF_SOURCE], None, verbose)
+        build_block(verbose=verbose, cache=cache)
     return out
+
+
+def build_block(out: str = BLOCK_LIB_PATH, extra_flags: list[str] | None = None, verbose: bool = False,
+                cache: bool = False) -> str:
+    """Compile the block operators' library; returns its path."""
+    extra = list(extra_flags or [])
+    per_source = {BLOCK_SOURCES[0]: [f'-DDYT_BUILD_ID="{source_hash(extra, BLOCK_DEPENDS)}"']}
+    _compile(out, BLOCK_SOURCES, extra, verbose, per_source, OBJ_CACHE if cache else None, BLOCK_DEPENDS)
+    return out
+
+
+def block_is_stale(path: str = BLOCK_LIB_PATH) -> bool:
+    """True if the block operators' library is missing or from other sources."""
+    return built_id(path) != source_hash((), BLOCK_DEPENDS)
 
 
 def _run(cmd: list[str], verbose: bool) -> None:
@@ -122,9 +148,9 @@ def _run(cmd: list[str], verbose: bool) -> None:
         print(msgs, flush=True)
 
 
-def _object_key(src: str, flags: list[str]) -> str:
+def _object_key(src: str, flags: list[str], depends: list[str]) -> str:
     h = hashlib.sha256()
-    for p in [src] + [d for d in DEPENDS if not d.endswith(".hip")]:
+    for p in [src] + [d for d in depends if not d.endswith(".hip")]:
         with open(p, "rb") as f:
             h.update(os.path.basename(p).encode() + b"\0" + f.read() + b"\0")
     h.update(" ".join(flags).encode())
@@ -132,7 +158,8 @@ def _object_key(src: str, flags: list[str]) -> str:
 
 
 def _compile(out: str, sources: list[str], extra_flags: list[str] | None, verbose: bool,
-             per_source: dict | None = None, cache_dir: str | None = None) -> None:
+             per_source: dict | None = None, cache_dir: str | None = None,
+             depends: list[str] | None = None) -> None:
     """Each source to an object (in parallel), then one shared library."""
     flags = [*HIPCC_FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", *(extra_flags or [])]
     per_source = per_source or {}
@@ -144,7 +171,7 @@ def _compile(out: str, sources: list[str], extra_flags: list[str] | None, verbos
             name = os.path.basename(src)
             if cache_dir:
                 os.makedirs(cache_dir, exist_ok=True)
-                obj = os.path.join(cache_dir, f"{name}-{_object_key(src, f)}.o")
+                obj = os.path.join(cache_dir, f"{name}-{_object_key(src, f, depends or DEPENDS)}.o")
                 if not os.path.exists(obj):
                     jobs.append((f, src, obj))
             else:

@@ -1,0 +1,360 @@
+// attn_api.hip - C ABI of attention (include/dyt_block.h): argument checks,
+// the split of the work, and the bias gradient's last sum.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "attn_launch.hpp"
+#include "block_host.hpp"
+#include "dyt_block.h"
+
+namespace dytb {
+
+// dtable[t, head]: the workgroups' values of bucket t, batch entry by batch
+// entry. A wave per (head, bucket).
+__global__ __launch_bounds__(64) void attn_dtable_kernel(const float* part, int B, int Hq, int per_unit, int buckets,
+                                                         void* dtable, int dt) {
+    const int head = (int)blockIdx.x / buckets, t = (int)blockIdx.x - head * buckets;
+    float s = 0.0f;
+    for (int x = (int)threadIdx.x; x < B * per_unit; x += 64) {
+        const int b = x / per_unit, k = x - b * per_unit;
+        s += part[(((int64_t)b * Hq + head) * per_unit + k) * buckets + t];
+    }
+    s = lanes_sum<64>(s);
+    if (threadIdx.x == 0) store_param(dtable, (int64_t)t * Hq + head, dt, s);
+}
+
+namespace {
+
+constexpr int64_t kMaxRows = (int64_t)1 << 28;   // Sq * G, Sk: 32-bit row arithmetic in the kernels
+
+int fill_borders(int num_buckets, int max_distance, int bidirectional, Borders& o) {
+    if (num_buckets < 2 || num_buckets > DYT_ATTN_MAX_BUCKETS || max_distance < 1 ||
+        max_distance > DYT_ATTN_MAX_DISTANCE || (bidirectional && num_buckets % 2))
+        return DYT_ERR_INVALID_ARG;
+    o.bidirectional = bidirectional;
+    o.n = bidirectional ? num_buckets / 2 : num_buckets;
+    o.e = o.n / 2;
+    if (o.n < 2 || max_distance <= o.e) return DYT_ERR_INVALID_ARG;
+    const int t_all = o.n - o.e;
+    const long double step = logl((long double)max_distance / o.e) / t_all;
+    for (int d = 0; d < o.e; ++d) o.at[d] = d;
+    for (int t = 0; t < t_all; ++t) {
+        // smallest d with (n - e) log(d / e) >= t log(distance / e); where both
+        // sides are equal whole powers the logarithms agree to 1e-15
+        int d = std::max((int)floorl(o.e * expl(step * t)) - 1, o.e);
+        while (logl((long double)d / o.e) < step * t - 1e-13L) ++d;
+        o.at[o.e + t] = std::max(d, o.at[o.e + t - 1]);
+    }
+    o.reach = o.at[o.n - 1];
+    return DYT_OK;
+}
+
+struct Tensor {
+    int64_t S, H;
+    const dyt_attn_strides* st;
+};
+
+// Byte strides for the kernels (0 along dimensions of one element or none)
+// and the span of the tensor in bytes; false where they overflow.
+bool view(const dyt_attn_desc& d, const Tensor& t, bool out, Strides& s, int64_t& span) {
+    const int64_t es = dtype_size(d.dtype);
+    const int64_t size[3] = {d.B, t.S, t.H}, stride[3] = {t.st->b, t.st->s, t.st->h};
+    int64_t bytes[3];
+    span = d.D * es;
+    for (int i = 0; i < 3; ++i) {
+        bytes[i] = 0;
+        if (size[i] <= 1) continue;
+        if (stride[i] < 0 || stride[i] > (((int64_t)1 << 60) / es) / size[i]) return false;
+        bytes[i] = stride[i] * es;
+        span += bytes[i] * (size[i] - 1);
+        if (span > ((int64_t)1 << 61)) return false;
+    }
+    if (out) {
+        // no two elements of an output share memory: every dimension steps
+        // over all of the faster ones
+        int order[3] = {0, 1, 2};
+        std::sort(order, order + 3, [&](int x, int y) { return bytes[x] < bytes[y]; });
+        int64_t covered = d.D * es;
+        for (int i : order) {
+            if (size[i] <= 1) continue;
+            if (bytes[i] < covered) return false;
+            covered = bytes[i] * (size[i] - 1) + covered;
+        }
+    }
+    s = Strides{bytes[0], bytes[1], bytes[2]};
+    return true;
+}
+
+// Whether a tensor takes 16-byte accesses: aligned base, strides and rows,
+// and (streamed tensors) a tile's rows within a 32-bit offset.
+bool vec_ok(const void* p, const Strides& s, int64_t row_bytes, int64_t pack) {
+    if ((uintptr_t)p % 16 || s.b % 16 || s.s % 16 || s.h % 16 || row_bytes % 16) return false;
+    return s.s < ((int64_t)1 << 24) && s.h <= ((int64_t)1 << 30) / pack;
+}
+
+struct Plan {
+    int status;
+    int64_t rows;
+    AttnPick fwd, dq, dkv;
+    int pack, units;
+    int fwd_blocks, fwd_split, fwd_per;
+    int dq_blocks, dq_split, dq_per;
+    int dkv_blocks, dkv_split, dkv_per, dkv_parts;
+    int per_unit;   // dq workgroups of a head
+    size_t fwd_bytes, bwd_bytes;
+    size_t off_tpart, off_part;   // backward workspace: rows, tpart, part
+    bool nothing_out, nothing_keys;
+    Borders borders;
+};
+
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// Waves per workgroup and splits of the long axis. Workgroups of four waves
+// share each tile of the long axis; where they would be fewer than the 256
+// CUs, single waves spread the rows wider. Where still fewer than `want`
+// workgroups result, the long axis is split into runs of at least `least`.
+void choose(int64_t units, int64_t rows, int64_t len, int tile4, int64_t want, int64_t least, int& nw, int& blocks,
+            int& split, int& per) {
+    nw = units * ((rows + 127) / 128) >= 256 ? 4 : 1;
+    const int tile = nw == 4 ? tile4 : 32;
+    blocks = ceil_div(rows, 32 * nw);
+    const int64_t have = std::max<int64_t>(units * blocks * nw, 1);
+    int64_t parts = std::max<int64_t>(1, std::min((want + have - 1) / have, len / least));
+    per = (int)std::max<int64_t>(tile, (ceil_div(len, parts) + tile - 1) / tile * tile);
+    split = std::max(1, ceil_div(len, per));
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+Plan make_plan(const dyt_attn_desc& d) {
+    Plan p{};
+    p.status = DYT_ERR_INVALID_ARG;
+    if (d.B < 0 || d.Sq < 0 || d.Sk < 0 || d.Hq < 0 || d.Hkv < 1 || d.D < 1 || d.D > DYT_ATTN_MAX_D) return p;
+    if (d.Hq % d.Hkv || (d.causal & ~1) || (d.bidirectional & ~1) || d.reserved) return p;
+    if (!(d.scale > 0.0f) || std::isinf(d.scale)) return p;
+    const int64_t G = d.Hq / d.Hkv;
+    if (d.Sk > kMaxRows || d.Sq > kMaxRows || G > kMaxRows || d.Sq * std::max<int64_t>(G, 1) > kMaxRows) return p;
+    if (d.Hq > (1 << 20) || d.B > (1 << 24) || d.B * d.Hq > (1 << 24) || d.B * d.Hkv > (1 << 24)) return p;
+    if (!dtype_ok(d.dtype) || (d.table && !dtype_ok(d.table_dtype))) {
+        p.status = DYT_ERR_UNSUPPORTED_DTYPE;
+        return p;
+    }
+    if (d.table && fill_borders(d.num_buckets, d.max_distance, d.bidirectional, p.borders)) return p;
+    p.nothing_out = d.B == 0 || d.Sq == 0 || d.Hq == 0;
+    p.nothing_keys = d.B == 0 || d.Sk == 0;
+    // the rows of a unit: all heads of a group, unless each needs its own
+    // column of the table, or the group is too large for the row division
+    p.pack = d.table || G > 256 || G < 1 ? 1 : (int)G;
+    p.units = (int)(d.B * (d.Hq / p.pack));
+    p.rows = d.Sq * p.pack;
+    const int dp = attn_dp(d.D), tile = d.dtype == DYT_F32 ? 32 : 64;
+    p.fwd = p.dq = p.dkv = {dp, 1, d.table != nullptr};
+    if (!p.nothing_out) {
+        choose(p.units, p.rows, d.Sk, tile, 2048, 128, p.fwd.nw, p.fwd_blocks, p.fwd_split, p.fwd_per);
+        choose(p.units, p.rows, d.Sk, tile, 1024, 256, p.dq.nw, p.dq_blocks, p.dq_split, p.dq_per);
+    }
+    if (!p.nothing_keys && d.Hq > 0)
+        choose(p.units, d.Sk, p.rows, tile, 1024, 256, p.dkv.nw, p.dkv_blocks, p.dkv_split, p.dkv_per);
+    const int64_t part_rows = p.units * p.rows * (int64_t)dp * 4;
+    if (p.fwd_split > 1) p.fwd_bytes = round256((size_t)p.fwd_split * part_rows) + (size_t)p.fwd_split * p.units * p.rows * 8;
+    p.per_unit = p.dq_blocks * p.dq_split;
+    p.off_tpart = round256((size_t)2 * d.B * d.Hq * d.Sq * 4);
+    p.off_part = p.off_tpart + (d.table ? round256((size_t)p.units * p.per_unit * d.num_buckets * 4) : 0);
+    p.dkv_parts = p.dkv_split * (int)(d.Hq > 0 ? G / p.pack : 1);
+    size_t part = p.dq_split > 1 ? (size_t)p.dq_split * part_rows : 0;
+    if (p.dkv_parts > 1) part = std::max(part, (size_t)p.dkv_parts * 2 * d.B * d.Hkv * d.Sk * dp * 4);
+    p.bwd_bytes = p.off_part + part;
+    p.status = DYT_OK;
+    return p;
+}
+
+template <typename F>
+int with_type(int dt, F&& f) {
+    if (dt == DYT_F32) return f((float*)nullptr);
+    if (dt == DYT_BF16) return f((bf16_t*)nullptr);
+    return f((f16_t*)nullptr);
+}
+
+void fill_args(const dyt_attn_desc& d, const Plan& p, AttnArgs& a) {
+    a.lens = d.seqlens_k;
+    a.starts = d.q_start;
+    a.table = d.table;
+    a.B = (int)d.B; a.Sq = (int)d.Sq; a.Sk = (int)d.Sk; a.Hq = (int)d.Hq; a.Hkv = (int)d.Hkv; a.D = (int)d.D;
+    a.G = (int)std::max<int64_t>(d.Hq / d.Hkv, 1);
+    a.pack = p.pack;
+    a.magic = ((1 << 20) + p.pack - 1) / p.pack;
+    a.units = p.units;
+    a.causal = d.causal;
+    a.table_dt = d.table_dtype;
+    a.buckets = d.num_buckets;
+    a.scale = d.scale;
+    a.borders = p.borders;
+}
+
+struct Spans {
+    int64_t q, k, v, o, dout, dq, dk, dv;
+};
+
+bool lists_aligned(const dyt_attn_desc& d) {
+    return aligned({d.seqlens_k, d.q_start}, 4) && (!d.table || aligned({d.table}, dtype_size(d.table_dtype)));
+}
+
+}  // namespace
+}  // namespace dytb
+
+using namespace dytb;
+
+extern "C" {
+
+int dyt_attn_bucket_borders(int num_buckets, int max_distance, int bidirectional, int32_t* borders) {
+    Borders o;
+    if (!borders || (bidirectional & ~1) || fill_borders(num_buckets, max_distance, bidirectional, o)) return 0;
+    for (int i = 0; i < o.n; ++i) borders[i] = o.at[i];
+    return o.n;
+}
+
+size_t dyt_attn_forward_workspace_size(const dyt_attn_desc* desc) {
+    if (!desc) return 0;
+    const Plan p = make_plan(*desc);
+    return p.status || p.nothing_out ? 0 : p.fwd_bytes;
+}
+
+size_t dyt_attn_backward_workspace_size(const dyt_attn_desc* desc) {
+    if (!desc) return 0;
+    const Plan p = make_plan(*desc);
+    return p.status ? 0 : p.bwd_bytes;
+}
+
+int dyt_attn_forward(const dyt_attn_desc* desc, const void* q, const void* k, const void* v, void* o, float* stats,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    if (!desc) return DYT_ERR_INVALID_ARG;
+    const dyt_attn_desc& d = *desc;
+    const Plan p = make_plan(d);
+    if (p.status) return p.status;
+    AttnArgs a{};
+    Spans n{};
+    if (!view(d, {d.Sq, d.Hq, &d.q}, false, a.qs, n.q) || !view(d, {d.Sk, d.Hkv, &d.k}, false, a.ks, n.k) ||
+        !view(d, {d.Sk, d.Hkv, &d.v}, false, a.vs, n.v) || !view(d, {d.Sq, d.Hq, &d.o}, true, a.os, n.o))
+        return DYT_ERR_INVALID_ARG;
+    if (p.nothing_out) return DYT_OK;
+    if (!q || !o || !stats || (d.Sk > 0 && (!k || !v))) return DYT_ERR_INVALID_ARG;
+    const int64_t es = dtype_size(d.dtype), row = d.D * es;
+    if (d.Sk == 0) n.k = n.v = 0;
+    if (!aligned({q, k, v, o}, es) || !aligned({stats}, 4) || !lists_aligned(d)) return DYT_ERR_MISALIGNED;
+    if (p.fwd_bytes && (!workspace || workspace_bytes < p.fwd_bytes)) return DYT_ERR_WORKSPACE_TOO_SMALL;
+    if (p.fwd_bytes && !aligned({workspace}, 16)) return DYT_ERR_MISALIGNED;
+    const Range in[] = {{q, n.q}, {k, n.k}, {v, n.v}, {d.seqlens_k, d.B * 4}, {d.q_start, d.B * 4},
+                        {d.table, d.table ? d.num_buckets * d.Hq * dtype_size(d.table_dtype) : 0}};
+    const Range out[] = {{o, n.o}, {stats, d.B * d.Hq * d.Sq * 4}, {workspace, (int64_t)p.fwd_bytes}};
+    if (!disjoint(in, 6, out, 3)) return DYT_ERR_INVALID_ARG;
+    fill_args(d, p, a);
+    a.q = (const char*)q; a.k = (const char*)k; a.v = (const char*)v; a.out = (char*)o; a.stats = stats;
+    a.vec_q = vec_ok(q, a.qs, row, p.pack); a.vec_k = vec_ok(k, a.ks, row, 1); a.vec_v = vec_ok(v, a.vs, row, 1);
+    a.vec_out = vec_ok(o, a.os, row, 1);
+    a.blocks = p.fwd_blocks; a.nsplit = p.fwd_split; a.per_split = p.fwd_per;
+    a.part = (float*)workspace;
+    a.part_ml = (float*)((char*)workspace + round256((size_t)p.fwd_split * p.units * p.rows * p.fwd.dp * 4));
+    return with_type(d.dtype, [&](auto* t) {
+        return attn_launch_fwd<std::remove_pointer_t<decltype(t)>>(p.fwd, a, (hipStream_t)stream);
+    });
+}
+
+int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, const void* v, const void* o,
+                      const void* dout, const float* stats, void* dq, void* dk, void* dv, void* dtable,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+    if (!desc) return DYT_ERR_INVALID_ARG;
+    const dyt_attn_desc& d = *desc;
+    const Plan p = make_plan(d);
+    if (p.status) return p.status;
+    AttnArgs a{};
+    Spans n{};
+    if (!view(d, {d.Sq, d.Hq, &d.q}, false, a.qs, n.q) || !view(d, {d.Sk, d.Hkv, &d.k}, false, a.ks, n.k) ||
+        !view(d, {d.Sk, d.Hkv, &d.v}, false, a.vs, n.v) || !view(d, {d.Sq, d.Hq, &d.o}, false, a.os, n.o) ||
+        !view(d, {d.Sq, d.Hq, &d.dout}, false, a.dos, n.dout) || !view(d, {d.Sq, d.Hq, &d.dq}, true, a.dqs, n.dq) ||
+        !view(d, {d.Sk, d.Hkv, &d.dk}, true, a.dks, n.dk) || !view(d, {d.Sk, d.Hkv, &d.dv}, true, a.dvs, n.dv))
+        return DYT_ERR_INVALID_ARG;
+    if (p.nothing_out) n.q = n.o = n.dout = n.dq = 0;
+    if (p.nothing_keys) n.k = n.v = n.dk = n.dv = 0;
+    if (!p.nothing_out && (!q || !o || !dout || !stats || !dq)) return DYT_ERR_INVALID_ARG;
+    if (!p.nothing_keys && (!k || !v || !dk || !dv)) return DYT_ERR_INVALID_ARG;
+    if (d.table && !dtable) return DYT_ERR_INVALID_ARG;
+    const int64_t es = dtype_size(d.dtype), row = d.D * es, ts = d.table ? dtype_size(d.table_dtype) : 1;
+    if (!aligned({q, k, v, o, dout, dq, dk, dv}, es) || !aligned({stats}, 4) || !lists_aligned(d) ||
+        (d.table && !aligned({dtable}, ts)))
+        return DYT_ERR_MISALIGNED;
+    if (p.bwd_bytes && (!workspace || workspace_bytes < p.bwd_bytes)) return DYT_ERR_WORKSPACE_TOO_SMALL;
+    if (p.bwd_bytes && !aligned({workspace}, 16)) return DYT_ERR_MISALIGNED;
+    const int64_t tb = d.table ? d.num_buckets * d.Hq * ts : 0;
+    const Range in[] = {{q, n.q}, {k, n.k}, {v, n.v}, {o, n.o}, {dout, n.dout},
+                        {stats, p.nothing_out ? 0 : d.B * d.Hq * d.Sq * 4},
+                        {d.seqlens_k, d.B * 4}, {d.q_start, d.B * 4}, {d.table, tb}};
+    // dq, dk and dv may be interleaved slices of one tensor: each is held
+    // against the inputs, the workspace and dtable, not against each other
+    const Range outs[] = {{dq, n.dq}, {dk, n.dk}, {dv, n.dv}};
+    const Range rest[] = {{dtable, tb}, {workspace, (int64_t)p.bwd_bytes}};
+    for (int i = 0; i < 3; ++i) {
+        if (!disjoint(in, 9, outs + i, 1) || !disjoint(rest, 2, outs + i, 1)) return DYT_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (outs[i].bytes && outs[j].bytes && outs[i].p == outs[j].p) return DYT_ERR_INVALID_ARG;
+    }
+    if (!disjoint(in, 9, rest, 2)) return DYT_ERR_INVALID_ARG;
+
+    const hipStream_t s = (hipStream_t)stream;
+    fill_args(d, p, a);
+    a.q = (const char*)q; a.k = (const char*)k; a.v = (const char*)v; a.o = (const char*)o;
+    a.dout = (const char*)dout; a.dq = (char*)dq; a.dk = (char*)dk; a.dv = (char*)dv;
+    a.stats = const_cast<float*>(stats);
+    a.dtable = dtable;
+    a.vec_q = vec_ok(q, a.qs, row, p.pack); a.vec_k = vec_ok(k, a.ks, row, 1); a.vec_v = vec_ok(v, a.vs, row, 1);
+    a.vec_o = vec_ok(o, a.os, row, 1); a.vec_do = vec_ok(dout, a.dos, row, p.pack);
+    a.rows = (float*)workspace;
+    a.tpart = (float*)((char*)workspace + p.off_tpart);
+    a.part = (float*)((char*)workspace + p.off_part);
+    return with_type(d.dtype, [&](auto* t) {
+        typedef std::remove_pointer_t<decltype(t)> T;
+        const int dp = p.dq.dp;
+        if (!p.nothing_out) {
+            a.vec_out = vec_ok(dq, a.dqs, row, 1);
+            a.blocks = p.dq_blocks; a.nsplit = p.dq_split; a.per_split = p.dq_per;
+            if (int st = attn_launch_dq<T>(p.dq, a, s)) return st;
+            if (p.dq_split > 1) {
+                const int64_t total = (int64_t)p.units * p.rows;
+                attn_launch_sum<T>(dp, {a.part, total * dp, p.dq_split, (char*)dq, a.dqs, total, (int)p.rows, p.pack,
+                                        (int)(d.Hq / p.pack), (int)d.D}, s);
+            }
+        }
+        if (d.table && d.Hq > 0)
+            attn_dtable_kernel<<<(unsigned)(d.Hq * d.num_buckets), 64, 0, s>>>(
+                a.tpart, p.nothing_out ? 0 : (int)d.B, (int)d.Hq, p.nothing_out ? 1 : p.per_unit, d.num_buckets, dtable,
+                d.table_dtype);
+        if (!p.nothing_keys) {
+            const int64_t total = d.B * d.Hkv * d.Sk, stride = 2 * total * dp;
+            const SumArgs sk = {a.part, stride, p.dkv_parts, (char*)dk, a.dks, total, (int)d.Sk, 1, (int)d.Hkv, (int)d.D};
+            SumArgs sv = sk;
+            sv.part = a.part + total * dp;
+            sv.out = (char*)dv;
+            sv.os = a.dvs;
+            if (d.Hq == 0) {   // no head reads these keys: zeros
+                SumArgs zk = sk, zv = sv;
+                zk.parts = zv.parts = 0;
+                attn_launch_sum<T>(dp, zk, s);
+                attn_launch_sum<T>(dp, zv, s);
+                return hip_status();
+            }
+            a.vec_out = vec_ok(dk, a.dks, row, 1) && vec_ok(dv, a.dvs, row, 1);
+            a.blocks = p.dkv_blocks; a.nsplit = p.dkv_split; a.per_split = p.dkv_per;
+            if (int st = attn_launch_dkv<T>(p.dkv, a, s)) return st;
+            if (p.dkv_parts > 1) {
+                attn_launch_sum<T>(dp, sk, s);
+                attn_launch_sum<T>(dp, sv, s);
+            }
+        }
+        return hip_status();
+    });
+}
+
+}  // extern "C"

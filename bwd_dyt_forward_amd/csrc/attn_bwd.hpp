@@ -1,0 +1,418 @@
+// attn_bwd.hpp - attention backward (gfx950).
+//
+// The probabilities are recomputed from q, k and the forward's log sums.
+// Two kernels, so that no sum is shared between workgroups and none needs
+// atomics:
+//   dq   a wave owns 32 query rows and walks the keys: S^T = K Q^T,
+//        dP^T = V dO^T, dS = P (dP - delta), dQ^T += K^T dS^T. Before, it
+//        takes delta = do . o of its rows and leaves delta and the log sums
+//        (in log2 units) in the workspace for
+//   dkv  a wave owns 32 keys and walks the query rows that see them, of all
+//        heads of the group: S = Q K^T, dP = dO V^T, dV^T += dO^T P,
+//        dK^T += Q^T dS.
+// That is seven products where one kernel would do five, but the sixth and
+// seventh cost less than a float32 dq summed through memory: they read
+// nothing that is not in LDS already.
+//
+// Both take a split of their long axis where there are few blocks; the
+// splits' float32 parts are summed in split order by attn_sum_kernel.
+//
+// Bias gradient (dq kernel): tiles beyond the reach of the last bucket add
+// to one sum per lane. In the others the pairs of one relative position form
+// a diagonal: each lane writes its 16 values of dS into a wave's scratch at
+// [key - query + 31][query] (the positions are the same for every tile, the
+// rest of the scratch stays zero), then lane t adds up diagonal t - 31 and
+// adds the sum to the wave's array of sums by relative position. At the end
+// the waves' arrays are joined in wave order and each bucket's range of
+// positions is summed: one float32 value per workgroup and bucket.
+#pragma once
+
+#include "attn_tile.hpp"
+
+namespace dytb {
+
+constexpr int kDiagPitch = 33;
+constexpr int kDiagFloats = 64 * kDiagPitch;
+
+template <typename T, int NW> struct BwdTile { static constexpr int rows = sizeof(T) == 2 && NW > 1 ? 64 : 32; };
+
+template <typename T, int DP, int NW>
+constexpr int bwd_lds_bytes() { return 2 * 2 * BwdTile<T, NW>::rows * DP * (int)sizeof(T); }
+
+// LDS floats of the dq kernel's bias gradient.
+inline __host__ __device__ int dbias_floats(int entries, int nw) { return nw * (kDiagFloats + entries); }
+
+template <typename T, int DP, int NW, bool BIAS>
+__global__ __launch_bounds__(NW * 64, 1) void attn_dq_kernel(AttnArgs a) {
+    typedef Tile<T, DP> TL;
+    constexpr int KT = BwdTile<T, NW>::rows;
+    constexpr int NS = KT / 32, KB = KT * TL::row_bytes;
+    Work w;
+    if (!find_work(a, w, a.causal != 0)) return;
+    const int lane = (int)threadIdx.x & 63, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int rows = a.Sq * a.pack;
+    const int row0 = (w.block * NW + wave) * 32;
+    const int row = row0 + (lane & 31);
+    const bool there = row < rows;
+    const int rr = min(row, rows - 1);
+    const int pos_i = rr / a.pack, g = rr - pos_i * a.pack;
+    const int pos = w.start + pos_i;
+    const int imin = min(row0, rows - 1) / a.pack;
+    const int imax = min(row0 + 31, rows - 1) / a.pack;
+    int end = min(w.len, (w.split + 1) * a.per_split);
+    if (a.causal) end = min(end, w.start + (min((w.block + 1) * NW * 32, rows) - 1) / a.pack + 1);
+    const int begin = w.split * a.per_split;
+
+    const Rows kr = {a.k + w.b * a.ks.b + w.kv * a.ks.h, a.ks.s, 0, 1, 0, a.vec_k};
+    const Rows vr = {a.v + w.b * a.vs.b + w.kv * a.vs.h, a.vs.s, 0, 1, 0, a.vec_v};
+    const float c = a.scale * kLog2e;
+
+    if (begin < end) {
+        stage<T, DP, KT, NW>(0, kr, begin, begin, 0, end, a.D);
+        stage<T, DP, KT, NW>(2 * KB, vr, begin, begin, 0, end, a.D);
+    }
+    const int entries = BIAS ? bias_entries(a.borders) : 0;
+    float* bias = (float*)(smem + 4 * KB);
+    float* diag = bias + entries + wave * kDiagFloats;
+    float* sums = bias + entries + NW * kDiagFloats;   // [NW][entries]
+    float far_before = 0.0f, far_behind = 0.0f;
+    if constexpr (BIAS) {
+        fill_bias(bias, a, w.head);
+        for (int x = lane; x < kDiagFloats; x += 64) diag[x] = 0.0f;
+        for (int x = lane; x < entries; x += 64) sums[wave * entries + x] = 0.0f;
+    }
+
+    Frag<T> q[DP / 16], dout[DP / 16];
+    float delta = 0.0f;
+    {
+        const int64_t hd = w.head + g;
+        const char* pq = a.q + w.b * a.qs.b + (int64_t)pos_i * a.qs.s + hd * a.qs.h;
+        const char* po = a.o + w.b * a.os.b + (int64_t)pos_i * a.os.s + hd * a.os.h;
+        const char* pd = a.dout + w.b * a.dos.b + (int64_t)pos_i * a.dos.s + hd * a.dos.h;
+#pragma unroll
+        for (int ds = 0; ds < DP / 16; ++ds) {
+            q[ds] = global_frag<T>(pq, ds * 16 + 8 * h, a.D, a.vec_q, there);
+            dout[ds] = global_frag<T>(pd, ds * 16 + 8 * h, a.D, a.vec_do, there);
+            delta += frag_dot<T>(dout[ds], global_frag<T>(po, ds * 16 + 8 * h, a.D, a.vec_o, there));
+        }
+    }
+    delta = swap32_other_sum(delta);
+    float lse = INFINITY;   // a row that sees no key: every p is 2^-inf
+    if (there) {
+        const int64_t at = ((int64_t)w.b * a.Hq + w.head + g) * a.Sq + pos_i;
+        const float s = a.stats[at];
+        if (s != -INFINITY) lse = s * kLog2e;
+        if (h == 0 && w.split == 0) {
+            a.rows[at] = lse;
+            a.rows[(int64_t)a.B * a.Hq * a.Sq + at] = delta;
+        }
+    }
+    f32x16 dq[DP / 32];
+#pragma unroll
+    for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dq[dt][i] = 0.0f;
+
+    int buf = 0;
+    for (int j0 = begin; j0 < end; j0 += KT, buf ^= 1) {
+        loads_landed();
+        __syncthreads();
+        if (j0 + KT < end) {
+            stage<T, DP, KT, NW>((buf ^ 1) * KB, kr, j0 + KT, j0 + KT, 0, end, a.D);
+            stage<T, DP, KT, NW>(2 * KB + (buf ^ 1) * KB, vr, j0 + KT, j0 + KT, 0, end, a.D);
+        }
+        const int kt = buf * KB, vt = 2 * KB + buf * KB;
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+            const int js = j0 + n * 32;
+            if (row0 >= rows || js >= end || (a.causal && js > w.start + imax)) continue;
+            f32x16 s, dp;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
+#pragma unroll
+            for (int ds = 0; ds < DP / 16; ++ds) {
+                s = mma<T>(TL::row_frag(kt, n * 32 + (lane & 31), ds, h), q[ds], s);
+                dp = mma<T>(TL::row_frag(vt, n * 32 + (lane & 31), ds, h), dout[ds], dp);
+            }
+            const int reach = a.borders.reach, after = a.borders.bidirectional ? reach : 0;
+            const bool far_after = js - (w.start + imax) >= after;
+            const bool near = js + 31 - (w.start + imin) > -reach && !far_after;
+            float p[16];
+            if constexpr (BIAS) {
+                if (near) {
+                    const float* at = bias + (js - pos + reach + kPad + 4 * h);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, at[8 * (i / 4) + (i % 4)]) - lse);
+                } else {
+                    const float one = bias[far_after ? entries - 1 : 0];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, one) - lse);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse));
+            }
+            if (js + 32 > end || (a.causal && js + 31 > w.start + imin)) {
+                const int last = a.causal ? min(end - 1, pos) : end - 1;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) p[i] = js + acc_row(i, h) <= last ? p[i] : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p[i] *= dp[i] - delta;
+            if constexpr (BIAS) {
+                if (near) {
+                    float* at = diag + (31 + 4 * h - (lane & 31)) * kDiagPitch + (lane & 31);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) at[(8 * (i / 4) + (i % 4)) * kDiagPitch] = there ? p[i] : 0.0f;
+                    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                    __builtin_amdgcn_wave_barrier();
+                    float d = 0.0f;
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) d += diag[lane * kDiagPitch + x];
+                    // lane 63 has no diagonal: its row of the scratch is never written
+                    float* to = sums + wave * entries + (js - (w.start + row0) + reach + kPad - 31 + lane);
+                    if (lane < 63) *to += d;
+                    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                    __builtin_amdgcn_wave_barrier();
+                } else {
+                    float d = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) d += p[i];
+                    d = there ? d : 0.0f;
+                    if (far_after) far_behind += d;
+                    else far_before += d;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const Frag<T> pf = pack_frag<T>(p + 8 * k);
+#pragma unroll
+                for (int dt = 0; dt < DP / 32; ++dt)
+                    dq[dt] = mma<T>(TL::col_frag(kt, n * 32 + k * 16, dt, lane), pf, dq[dt]);
+            }
+        }
+    }
+    if (row0 < rows) {
+        if (a.nsplit == 1) {
+            char* out = a.dq + w.b * a.dqs.b + (int64_t)pos_i * a.dqs.s + (int64_t)(w.head + g) * a.dqs.h;
+            store_acc<T, DP>(out, dq, a.scale, a.D, a.vec_out, there, h);
+        } else {
+            const int64_t at = ((int64_t)w.split * a.units + w.u) * rows + row;
+            store_part<DP>(a.part + at * DP, dq, a.scale, there, h);
+        }
+    }
+    if constexpr (BIAS) {
+        far_before = lanes_sum<64>(far_before);
+        far_behind = lanes_sum<64>(far_behind);
+        if (lane == 0) {
+            sums[wave * entries] += far_before;             // farther than the reach: the outermost entries
+            sums[wave * entries + entries - 1] += far_behind;
+        }
+        __syncthreads();
+        for (int x = (int)threadIdx.x; x < entries; x += NW * 64) {
+            float s = sums[x];
+            for (int k = 1; k < NW; ++k) s += sums[k * entries + x];
+            sums[x] = s;
+        }
+        __syncthreads();
+        // a bucket is a run of entries: one lane group of 64 per bucket
+        const Borders& o = a.borders;
+        const int mid = o.reach + kPad;   // entry of position 0
+        for (int t = wave; t < a.buckets; t += NW) {
+            int lo, hi;   // entries [lo, hi)
+            if (t < o.n) {
+                lo = t + 1 < o.n ? mid - o.at[t + 1] + 1 : 0;
+                hi = mid - o.at[t] + 1;
+                if (t == 0 && !o.bidirectional) hi = entries;   // every later key
+            } else {
+                // later keys: distance 0 is the other direction's
+                const int d = max(o.at[t - o.n], 1);
+                lo = mid + d;
+                hi = t - o.n + 1 < o.n ? mid + o.at[t - o.n + 1] : entries;
+            }
+            float s = 0.0f;
+            for (int x = lo + lane; x < hi; x += 64) s += sums[x];
+            s = lanes_sum<64>(s);
+            if (lane == 0) a.tpart[w.flat * a.buckets + t] = s;
+        }
+    }
+}
+
+template <typename T, int DP, int NW, bool BIAS>
+__global__ __launch_bounds__(NW * 64, 1) void attn_dkv_kernel(AttnArgs a) {
+    typedef Tile<T, DP> TL;
+    constexpr int RT = BwdTile<T, NW>::rows;
+    constexpr int NS = RT / 32, RB = RT * TL::row_bytes;
+    Work w;
+    if (!find_work(a, w, false)) return;
+    const int lane = (int)threadIdx.x & 63, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int rows = a.Sq * a.pack;
+    const int key0 = (w.block * NW + wave) * 32;
+    const int key = key0 + (lane & 31);
+    const bool there = key < w.len;
+    const float c = a.scale * kLog2e;
+
+    // rows that see a key of this workgroup
+    int begin = w.split * a.per_split, end = min(rows, (w.split + 1) * a.per_split);
+    if (a.causal) {
+        const int first = max(w.block * NW * 32 - w.start, 0);   // position
+        if (first >= a.Sq) begin = end;
+        else begin = max(begin, first * a.pack / RT * RT);
+    }
+    if (w.block * NW * 32 >= w.len) begin = end;
+
+    const Rows qr = {a.q + w.b * a.qs.b + w.head * a.qs.h, a.qs.s, a.qs.h, a.pack, a.magic, a.vec_q};
+    const Rows dr = {a.dout + w.b * a.dos.b + w.head * a.dos.h, a.dos.s, a.dos.h, a.pack, a.magic, a.vec_do};
+    const int64_t row_at = ((int64_t)w.b * a.Hq + w.head) * a.Sq;
+    const int64_t rows_all = (int64_t)a.B * a.Hq * a.Sq;
+    constexpr int kStat = 4 * RB;   // [2 buffers][lse, delta][64]
+    float* bias = (float*)(smem + kStat + 1024);
+    if constexpr (BIAS) fill_bias(bias, a, w.head);
+
+    const auto bring = [&](int r0, int to) {
+        const int i0 = r0 / a.pack, rem = r0 - i0 * a.pack;
+        stage<T, DP, RT, NW>(to * RB, qr, r0, i0, rem, end, a.D);
+        stage<T, DP, RT, NW>(2 * RB + to * RB, dr, r0, i0, rem, end, a.D);
+        // rows that are not there get log sum and delta 0: their dO and q are
+        // zeros, so they add nothing
+        if (wave < 2) {
+            for (int k = wave; k < 2; k += NW < 2 ? 1 : 2) {
+                const int di = div_pack(rem + lane, qr);
+                const int g = rem + lane - di * a.pack;
+                const uint32_t off = lane < RT && r0 + lane < end ? (uint32_t)(g * a.Sq + di) * 4u : kOutside;
+                load_to_lds4(a.rows + k * rows_all + row_at + i0, kStat + to * 512 + k * 256, off);
+            }
+        }
+    };
+    if (begin < end) bring(begin, 0);
+
+    Frag<T> kf[DP / 16], vf[DP / 16];
+    {
+        const int kk = min(key, a.Sk - 1);
+        const char* pk = a.k + w.b * a.ks.b + (int64_t)kk * a.ks.s + w.kv * a.ks.h;
+        const char* pv = a.v + w.b * a.vs.b + (int64_t)kk * a.vs.s + w.kv * a.vs.h;
+#pragma unroll
+        for (int ds = 0; ds < DP / 16; ++ds) {
+            kf[ds] = global_frag<T>(pk, ds * 16 + 8 * h, a.D, a.vec_k, there);
+            vf[ds] = global_frag<T>(pv, ds * 16 + 8 * h, a.D, a.vec_v, there);
+        }
+    }
+    f32x16 dk[DP / 32], dv[DP / 32];
+#pragma unroll
+    for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dk[dt][i] = dv[dt][i] = 0.0f;
+
+    int buf = 0;
+    for (int r0 = begin; r0 < end; r0 += RT, buf ^= 1) {
+        loads_landed();
+        __syncthreads();
+        if (r0 + RT < end) bring(r0 + RT, buf ^ 1);
+        const int qt = buf * RB, dt0 = 2 * RB + buf * RB;
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+            const int rs = r0 + n * 32;
+            if (rs >= end || key0 >= w.len) continue;
+            const int imin = w.start + rs / a.pack, imax = w.start + min(rs + 31, end - 1) / a.pack;   // positions
+            if (a.causal && key0 > imax) continue;
+            f32x16 s, dp;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
+#pragma unroll
+            for (int ds = 0; ds < DP / 16; ++ds) {
+                s = mma<T>(TL::row_frag(qt, n * 32 + (lane & 31), ds, h), kf[ds], s);
+                dp = mma<T>(TL::row_frag(dt0, n * 32 + (lane & 31), ds, h), vf[ds], dp);
+            }
+            const float* st = (const float*)(smem + kStat + buf * 512) + n * 32 + 4 * h;
+            float p[16];
+            if constexpr (BIAS) {
+                const int reach = a.borders.reach, after = a.borders.bidirectional ? reach : 0;
+                const bool far_after = key0 - imax >= after;
+                if (key0 + 31 - imin > -reach && !far_after) {
+                    // pack = 1: the row of register i is acc_row(i, h) positions on
+                    const float* at = bias + (key - w.start - rs + reach + kPad - 4 * h);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int k = 8 * (i / 4) + (i % 4);
+                        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, at[-k]) - st[k]);
+                    }
+                } else {
+                    const float one = bias[far_after ? 2 * (reach + kPad) - 1 : 0];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, one) - st[8 * (i / 4) + (i % 4)]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -st[8 * (i / 4) + (i % 4)]));
+            }
+            if (key0 + 32 > w.len || (a.causal && key0 + 31 > imin)) {
+                // first row that sees the key
+                const int first = there ? (a.causal ? min(max(key - w.start, 0), a.Sq) * a.pack : 0) : 0x7fffffff;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) p[i] = rs + acc_row(i, h) >= first ? p[i] : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const Frag<T> pf = pack_frag<T>(p + 8 * k);
+#pragma unroll
+                for (int dt = 0; dt < DP / 32; ++dt)
+                    dv[dt] = mma<T>(TL::col_frag(dt0, n * 32 + k * 16, dt, lane), pf, dv[dt]);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p[i] *= dp[i] - st[64 + 8 * (i / 4) + (i % 4)];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const Frag<T> pf = pack_frag<T>(p + 8 * k);
+#pragma unroll
+                for (int dt = 0; dt < DP / 32; ++dt)
+                    dk[dt] = mma<T>(TL::col_frag(qt, n * 32 + k * 16, dt, lane), pf, dk[dt]);
+            }
+        }
+    }
+    if (key0 >= a.Sk) return;
+    const bool in = key < a.Sk;
+    const int parts = a.nsplit * (a.G / a.pack);   // float32 parts of each key head
+    if (parts == 1) {
+        const int64_t kk = min(key, a.Sk - 1);
+        store_acc<T, DP>(a.dk + w.b * a.dks.b + kk * a.dks.s + w.kv * a.dks.h, dk, a.scale, a.D, a.vec_out, in, h);
+        store_acc<T, DP>(a.dv + w.b * a.dvs.b + kk * a.dvs.s + w.kv * a.dvs.h, dv, 1.0f, a.D, a.vec_out, in, h);
+    } else {
+        // [part][dk, dv][B, Hkv, Sk, DP]
+        const int64_t heads = (int64_t)a.B * a.Hkv, part = (w.head % a.G) / a.pack + (int64_t)(a.G / a.pack) * w.split;
+        const int64_t at = ((part * 2 * heads + (int64_t)w.b * a.Hkv + w.kv) * a.Sk + min(key, a.Sk - 1)) * DP;
+        store_part<DP>(a.part + at, dk, a.scale, in, h);
+        store_part<DP>(a.part + at + heads * a.Sk * DP, dv, 1.0f, in, h);
+    }
+}
+
+// Sums float32 parts in order and rounds once: out[b, s, h] = sum_p part[p]
+// [(b, hu)][row][DP] with row = s * pack + g and h = hu * pack + g. One part
+// lies `stride` floats after the other. DP / 4 threads per row.
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void attn_sum_kernel(const float* part, int64_t stride, int parts, char* out,
+                                                       Strides os, int64_t total, int rows, int pack, int hu, int D) {
+    constexpr int TPR = DP / 4, PER = 256 / TPR;
+    const int64_t at = (int64_t)blockIdx.x * PER + (int)threadIdx.x / TPR;
+    const int d = ((int)threadIdx.x % TPR) * 4;
+    if ((int)threadIdx.x >= PER * TPR || at >= total) return;
+    float o[4] = {0, 0, 0, 0};
+    for (int p = 0; p < parts; ++p) {
+        const f32x4 v = *(const f32x4*)(part + p * stride + at * DP + d);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] += v[k];
+    }
+    const int u = (int)(at / rows), r = (int)(at - (int64_t)u * rows);
+    const int b = u / hu, i = r / pack, head = (u - b * hu) * pack + (r - i * pack);
+    T* to = (T*)(out + b * os.b + (int64_t)i * os.s + (int64_t)head * os.h);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (d + k < D) to[d + k] = dyt::from_f32<T>(o[k]);
+}
+
+}  // namespace dytb

@@ -1,0 +1,216 @@
+// attn_fwd.hpp - attention forward (gfx950).
+//
+// One pass over the keys with the running maximum and sum of the softmax.
+// A wave owns 32 query rows, a workgroup of NW waves 32 NW; the keys and
+// values pass through LDS in double-buffered tiles. S^T = K Q^T puts a query
+// in each lane (column), so the softmax's maximum and sum over keys are
+// in-lane operations plus one exchange between the lane halves, and the
+// probabilities are already the B fragments of O^T = V^T P^T.
+//
+// Rows are (position, head of the group) pairs: the G query heads that share
+// a key head are rows of one unit, so its keys and values are read once for
+// all of them (single tokens most of all). With the bias, whose table has a
+// column per head, each query head is a unit of its own (pack = 1).
+//
+// The reference maximum only moves when a row's maximum has grown by more
+// than 2^8 over it (then the accumulators are rescaled): probabilities stay
+// below 2^8, well inside every type, and the sums are float32.
+//
+// Few rows over many keys are split along the keys: each split leaves its
+// unnormalised float32 output and (maximum, sum) in the workspace and
+// attn_join_kernel joins them in split order.
+#pragma once
+
+#include "attn_tile.hpp"
+
+namespace dytb {
+
+// Keys per LDS tile.
+template <typename T, int NW> struct FwdTile { static constexpr int keys = sizeof(T) == 2 && NW > 1 ? 64 : 32; };
+
+template <typename T, int DP, int NW>
+constexpr int fwd_lds_bytes() { return 2 * 2 * FwdTile<T, NW>::keys * DP * (int)sizeof(T); }
+
+template <typename T, int DP, int NW, bool BIAS>
+__global__ __launch_bounds__(NW * 64, NW > 1 && sizeof(T) == 2 ? 2 : 1) void attn_fwd_kernel(AttnArgs a) {
+    typedef Tile<T, DP> TL;
+    constexpr int KT = FwdTile<T, NW>::keys;
+    constexpr int NS = KT / 32, KB = KT * TL::row_bytes;
+    Work w;
+    if (!find_work(a, w, a.causal != 0)) return;
+    const int lane = (int)threadIdx.x & 63, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int rows = a.Sq * a.pack;
+    const int row0 = (w.block * NW + wave) * 32;
+    const int row = row0 + (lane & 31);
+    const bool there = row < rows;
+    const int rr = min(row, rows - 1);
+    const int pos_i = rr / a.pack, g = rr - pos_i * a.pack;
+    const int pos = w.start + pos_i;
+    const int imin = min(row0, rows - 1) / a.pack;
+    const int imax = min(row0 + 31, rows - 1) / a.pack;
+    int end = min(w.len, (w.split + 1) * a.per_split);
+    if (a.causal) end = min(end, w.start + (min((w.block + 1) * NW * 32, rows) - 1) / a.pack + 1);
+    const int begin = w.split * a.per_split;
+
+    const Rows kr = {a.k + w.b * a.ks.b + w.kv * a.ks.h, a.ks.s, 0, 1, 0, a.vec_k};
+    const Rows vr = {a.v + w.b * a.vs.b + w.kv * a.vs.h, a.vs.s, 0, 1, 0, a.vec_v};
+    const float c = a.scale * kLog2e;
+
+    if (begin < end) {
+        stage<T, DP, KT, NW>(0, kr, begin, begin, 0, end, a.D);
+        stage<T, DP, KT, NW>(2 * KB, vr, begin, begin, 0, end, a.D);
+    }
+    float* bias = (float*)(smem + 4 * KB);
+    if constexpr (BIAS) fill_bias(bias, a, w.head);
+
+    Frag<T> q[DP / 16];
+    {
+        const char* p = a.q + w.b * a.qs.b + (int64_t)pos_i * a.qs.s + (int64_t)(w.head + g) * a.qs.h;
+#pragma unroll
+        for (int ds = 0; ds < DP / 16; ++ds) q[ds] = global_frag<T>(p, ds * 16 + 8 * h, a.D, a.vec_q, there);
+    }
+    f32x16 o[DP / 32];
+#pragma unroll
+    for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[dt][i] = 0.0f;
+    // m: reference maximum; units of the raw product without bias, of log2
+    // with it. l: this lane's part of the sum.
+    float m = -INFINITY, l = 0.0f;
+    const float mc = BIAS ? 1.0f : c;
+    const float grow = 8.0f / mc;
+
+    int buf = 0;
+    for (int j0 = begin; j0 < end; j0 += KT, buf ^= 1) {
+        loads_landed();
+        __syncthreads();
+        if (j0 + KT < end) {
+            stage<T, DP, KT, NW>((buf ^ 1) * KB, kr, j0 + KT, j0 + KT, 0, end, a.D);
+            stage<T, DP, KT, NW>(2 * KB + (buf ^ 1) * KB, vr, j0 + KT, j0 + KT, 0, end, a.D);
+        }
+        if (row0 >= rows || (a.causal && j0 > w.start + imax)) continue;
+        const int kt = buf * KB, vt = 2 * KB + buf * KB;
+        f32x16 s[NS];
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[n][i] = 0.0f;
+#pragma unroll
+            for (int ds = 0; ds < DP / 16; ++ds)
+                s[n] = mma<T>(TL::row_frag(kt, n * 32 + (lane & 31), ds, h), q[ds], s[n]);
+        }
+        if constexpr (BIAS) {
+#pragma unroll
+            for (int n = 0; n < NS; ++n) {
+                const int js = j0 + n * 32;
+                const int reach = a.borders.reach, after = a.borders.bidirectional ? reach : 0;
+                const bool far_after = js - (w.start + imax) >= after;
+                if (js + 31 - (w.start + imin) > -reach && !far_after) {
+                    const float* at = bias + (js - pos + reach + kPad + 4 * h);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[n][i] = __builtin_fmaf(s[n][i], c, at[8 * (i / 4) + (i % 4)]);
+                } else {
+                    const float one = bias[far_after ? 2 * (reach + kPad) - 1 : 0];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[n][i] = __builtin_fmaf(s[n][i], c, one);
+                }
+            }
+        }
+        if (j0 + KT > end || (a.causal && j0 + KT - 1 > w.start + imin)) {
+            const int last = a.causal ? min(end - 1, pos) : end - 1;
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    s[n][i] = j0 + n * 32 + acc_row(i, h) <= last ? s[n][i] : -INFINITY;
+        }
+        float mt = s[0][0];
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mt = fmaxf(mt, s[n][i]);
+        mt = swap32_max(mt);
+        if (__any(mt > m + grow)) {
+            const float mn = fmaxf(m, mt);
+            const float f = __builtin_amdgcn_exp2f((m - (mn == -INFINITY ? 0.0f : mn)) * mc);
+            l *= f;
+#pragma unroll
+            for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[dt][i] *= f;
+            m = mn;
+        }
+        const float mm = (m == -INFINITY ? 0.0f : m) * mc;
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+            float p[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                p[i] = __builtin_amdgcn_exp2f(BIAS ? s[n][i] - mm : __builtin_fmaf(s[n][i], c, -mm));
+                l += p[i];
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const Frag<T> pf = pack_frag<T>(p + 8 * k);
+#pragma unroll
+                for (int dt = 0; dt < DP / 32; ++dt)
+                    o[dt] = mma<T>(TL::col_frag(vt, n * 32 + k * 16, dt, lane), pf, o[dt]);
+            }
+        }
+    }
+    if (row0 >= rows) return;
+    l = swap32_other_sum(l);
+    const float ml = (m == -INFINITY ? 0.0f : m) * mc;   // log2 units
+    if (a.nsplit == 1) {
+        char* out = a.out + w.b * a.os.b + (int64_t)pos_i * a.os.s + (int64_t)(w.head + g) * a.os.h;
+        store_acc<T, DP>(out, o, l > 0.0f ? 1.0f / l : 0.0f, a.D, a.vec_out, there, h);
+        if (there && h == 0)
+            a.stats[((int64_t)w.b * a.Hq + w.head + g) * a.Sq + pos_i] =
+                l > 0.0f ? (ml + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    } else {
+        const int64_t at = ((int64_t)w.split * a.units + w.u) * rows + row;
+        store_part<DP>(a.part + at * DP, o, 1.0f, there, h);
+        if (there && h == 0) {
+            a.part_ml[2 * at] = l > 0.0f ? ml : -INFINITY;
+            a.part_ml[2 * at + 1] = l;
+        }
+    }
+}
+
+// Joins the splits of a row: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s
+// with M the largest m_s, in split order. DP / 4 threads per row.
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+    constexpr int TPR = DP / 4, PER = 256 / TPR;
+    const int rows = a.Sq * a.pack;
+    const int64_t total = (int64_t)a.units * rows;
+    const int64_t at = (int64_t)blockIdx.x * PER + (int)threadIdx.x / TPR;
+    const int d = ((int)threadIdx.x % TPR) * 4;
+    if ((int)threadIdx.x >= PER * TPR || at >= total) return;
+    float M = -INFINITY;
+    for (int s = 0; s < a.nsplit; ++s) M = fmaxf(M, a.part_ml[2 * (s * total + at)]);
+    const float mm = M == -INFINITY ? 0.0f : M;
+    float l = 0.0f, o[4] = {0, 0, 0, 0};
+    for (int s = 0; s < a.nsplit; ++s) {
+        const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * (s * total + at)] - mm);
+        if (f == 0.0f) continue;
+        l += f * a.part_ml[2 * (s * total + at) + 1];
+        const f32x4 v = *(const f32x4*)(a.part + (s * total + at) * DP + d);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] += f * v[k];
+    }
+    const int u = (int)(at / rows), r = (int)(at - (int64_t)u * rows);
+    const int hu = a.Hq / a.pack;
+    const int b = u / hu, i = r / a.pack, head = (u - b * hu) * a.pack + (r - i * a.pack);
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    T* out = (T*)(a.out + b * a.os.b + (int64_t)i * a.os.s + (int64_t)head * a.os.h);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (d + k < a.D) out[d + k] = dyt::from_f32<T>(o[k] * inv);
+    if (d == 0)
+        a.stats[((int64_t)b * a.Hq + head) * a.Sq + i] =
+            l > 0.0f ? (mm + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+}
+
+}  // namespace dytb

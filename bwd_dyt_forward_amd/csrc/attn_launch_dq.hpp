@@ -1,0 +1,25 @@
+// attn_launch_dq.hpp - launch of the attention backward's dq kernel.
+#pragma once
+
+#include "attn_bwd.hpp"
+#include "attn_launch.hpp"
+
+namespace dytb {
+
+template <typename T>
+int attn_launch_dq(const AttnPick& p, const AttnArgs& a, hipStream_t s) {
+    int st = DYT_OK;
+    with_pick(p, [&](auto dp, auto nw, auto bias) {
+        constexpr int DP = decltype(dp)::value, NW = decltype(nw)::value;
+        constexpr bool BIAS = decltype(bias)::value != 0;
+        size_t lds = bwd_lds_bytes<T, DP, NW>();
+        if (BIAS) {
+            const int entries = 2 * (a.borders.reach + kPad);
+            lds += sizeof(float) * (entries + dbias_floats(entries, NW));
+        }
+        st = launch_lds((const void*)attn_dq_kernel<T, DP, NW, BIAS>, attn_grid(a), NW * 64, lds, a, s);
+    });
+    return st;
+}
+
+}  // namespace dytb

@@ -1,0 +1,488 @@
+// ln_kernels.hpp - layer norm, forward and backward (gfx950).
+//
+// Both directions are bound by HBM traffic: the forward reads x (and the
+// residual) once and writes y (and h), the backward reads x and dy (and
+// dres) once and writes dx. A row therefore stays in registers between its
+// statistics and its use: TPR threads hold a row as V vectors of 16 bytes
+// each. TPR is the smallest power of two that covers the row up to a wave
+// (several rows per wave, sums by lane exchange, no barrier); wider rows
+// take a workgroup each and one barrier per reduction.
+//
+// The variance is the mean of squared distances from the mean, never
+// E[x^2] - mean^2: within a wave a second pass over the registers, across
+// the waves of a row by merging (count, mean, M2) triples,
+//   mean = sum n_w mean_w / N,  M2 = sum M2_w + sum n_w (mean_w - mean)^2.
+//
+// The backward's parameter gradients are sums over rows: each thread adds up
+// its own columns over the rows its workgroup walks, the workgroup's row
+// groups are joined through LDS in group order, and one float32 row
+// [dgamma | dbeta] per workgroup goes to the workspace; a second kernel sums
+// those rows in a fixed order. No atomics.
+#pragma once
+
+#include "block_common.hpp"
+
+namespace dytb {
+
+struct LnArgs {
+    const void* x;        // forward: x; backward: x or h
+    const void* r;        // forward: residual or null
+    void* h;              // forward: x + r, or null
+    void* y;              // forward: y; backward: dx
+    const void* dy;       // backward
+    const void* dres;     // backward: residual gradient or null
+    const void* gamma;
+    const void* beta;
+    float* mean;
+    float* rstd;
+    float* part;          // backward: partial rows
+    int64_t ldx, ldy, lddy;
+    int64_t M;
+    int32_t N;
+    int32_t pdt;
+    float eps;
+    int64_t pitch;        // backward: floats between partial rows
+};
+
+// Elements [c, c + VEC) of the row that starts at element `row`; zeros past
+// N. `limit` is one past the tensor's last element: a whole vector is loaded
+// wherever its 16 bytes lie inside the tensor, and what belongs to the next
+// row (or the pitch's gap) is cleared afterwards.
+template <typename T>
+__device__ __forceinline__ void load_vec(const T* p, int64_t row, int c, int N, int64_t limit,
+                                         float* out) {
+    constexpr int VEC = VecOf<T>::n;
+    if (c + VEC <= N) {
+        unpack16<T>(*(const u32x4_m*)(p + row + c), out);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) out[i] = 0.0f;
+    if (c >= N) return;
+    if (row + c + VEC <= limit) {
+        unpack16<T>(*(const u32x4_m*)(p + row + c), out);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) out[i] = (c + i < N) ? out[i] : 0.0f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (c + i < N) out[i] = to_f32(p[row + c + i]);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_vec(T* p, int64_t row, int c, int N, const float* v) {
+    constexpr int VEC = VecOf<T>::n;
+    if (c + VEC <= N) {
+        *(u32x4_m*)(p + row + c) = pack16<T>(v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (c + i < N) p[row + c + i] = dyt::from_f32<T>(v[i]);
+    }
+}
+
+__device__ __forceinline__ float inv_sqrt(float v) {
+    // one Newton step on the hardware estimate
+    const float y = __builtin_amdgcn_rsqf(v);
+    const float e = __builtin_fmaf(-v * y, y, 1.0f);
+    const float z = __builtin_fmaf(0.5f * y, e, y);
+    return (v > 0.0f && v < INFINITY) ? z : y;   // 0 and inf keep the estimate's inf and 0
+}
+
+template <int TPR> struct LnShape {
+    static constexpr int threads = TPR < 256 ? 256 : TPR;
+    static constexpr int groups = threads / TPR;                 // rows side by side
+    static constexpr int waves = TPR > 64 ? TPR / 64 : 1;        // waves of a row
+    static constexpr int L = TPR > 64 ? 64 : TPR;
+};
+
+template <typename T, int TPR, int V, int U, bool RES>
+__global__ __launch_bounds__(LnShape<TPR>::threads) void ln_fwd_kernel(LnArgs a) {
+    using S = LnShape<TPR>;
+    constexpr int VEC = VecOf<T>::n;
+    constexpr int E = V * VEC;
+    const int t = (int)threadIdx.x % TPR;
+    const int g = (int)threadIdx.x / TPR;
+    const int N = a.N;
+    float gm[E], bt[E];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int c = (t + v * TPR) * VEC + i;
+            gm[v * VEC + i] = c < N ? load_param(a.gamma, c, a.pdt) : 0.0f;
+            bt[v * VEC + i] = c < N ? load_param(a.beta, c, a.pdt) : 0.0f;
+        }
+    const float inv_n = 1.0f / (float)N;
+    const int64_t limit = (a.M - 1) * a.ldx + N;
+    const int64_t step = (int64_t)gridDim.x * S::groups * U;
+    const T* xp = (const T*)a.x;
+    // rows of one iteration lie U apart by the row groups: neighbours in memory
+    for (int64_t base = (int64_t)blockIdx.x * S::groups * U; base < a.M; base += step) {
+        float x[U][E];
+        float mean[U], m2[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t m = base + u * S::groups + g;
+            if (m < a.M) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    load_vec<T>(xp, m * a.ldx, (t + v * TPR) * VEC, N, limit, &x[u][v * VEC]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[u][e] = 0.0f;
+            }
+        }
+        if constexpr (RES) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t m = base + u * S::groups + g;
+                if (m < a.M) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        float r[VEC];
+                        const int c = (t + v * TPR) * VEC;
+                        load_vec<T>((const T*)a.r, m * a.ldx, c, N, limit, r);
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) r[i] += x[u][v * VEC + i];
+                        store_vec<T>((T*)a.h, m * a.ldx, c, N, r);
+                        // the layer's input is h as stored
+                        const u32x4 w = pack16<T>(r);
+                        unpack16<T>(w, &x[u][v * VEC]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) s += x[u][e];
+            s = lanes_sum<S::L>(s);
+            if constexpr (S::waves == 1) {
+                mean[u] = s * inv_n;
+            } else {
+                // columns of this wave
+                int cnt = 0;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const int lo = ((t & ~63) + v * TPR) * VEC;
+                    cnt += min(max(N - lo, 0), 64 * VEC);
+                }
+                mean[u] = cnt ? s / (float)cnt : 0.0f;
+            }
+            float q = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float d = x[u][v * VEC + i] - mean[u];
+                    q += ((t + v * TPR) * VEC + i < N) ? d * d : 0.0f;
+                }
+            m2[u] = lanes_sum<S::L>(q);
+        }
+        if constexpr (S::waves > 1) {
+            static_assert(S::groups == 1, "a row of several waves has the workgroup to itself");
+            __shared__ float red[2][U][S::waves][2];
+            const int w = t >> 6;
+            const int buf = (int)((base / step) & 1);   // the next rows' triples go to the other half
+            if ((t & 63) == 0) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    red[buf][u][w][0] = mean[u];
+                    red[buf][u][w][1] = m2[u];
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float cw[S::waves], mt = 0.0f, q = 0.0f;
+#pragma unroll
+                for (int k = 0; k < S::waves; ++k) {
+                    int cnt = 0;
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        cnt += min(max(N - (k * 64 + v * TPR) * VEC, 0), 64 * VEC);
+                    cw[k] = (float)cnt;
+                    mt += cw[k] * red[buf][u][k][0];
+                }
+                mt *= inv_n;
+#pragma unroll
+                for (int k = 0; k < S::waves; ++k) {
+                    const float d = red[buf][u][k][0] - mt;
+                    q += red[buf][u][k][1] + cw[k] * d * d;
+                }
+                mean[u] = mt;
+                m2[u] = q;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t m = base + u * S::groups + g;
+            if (m >= a.M) continue;
+            const float rs = inv_sqrt(m2[u] * inv_n + a.eps);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float y[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const int e = v * VEC + i;
+                    y[i] = __builtin_fmaf((x[u][e] - mean[u]) * rs, gm[e], bt[e]);
+                }
+                store_vec<T>((T*)a.y, m * a.ldy, (t + v * TPR) * VEC, N, y);
+            }
+            if (t == 0) {
+                a.mean[m] = mean[u];
+                a.rstd[m] = rs;
+            }
+        }
+    }
+}
+
+// Rows longer than 1,024 threads hold in registers: a workgroup per row and
+// three walks over it, the second and third of which find the row in the
+// last-level caches.
+constexpr int kLongThreads = 1024;
+
+__device__ __forceinline__ float block_sum(float v, float* red) {
+    v = lanes_sum<64>(v);
+    __syncthreads();   // the previous sum has been read
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kLongThreads / 64; ++k) s += red[k];
+    return s;
+}
+
+template <typename T, bool RES>
+__global__ __launch_bounds__(kLongThreads) void ln_fwd_long_kernel(LnArgs a) {
+    constexpr int VEC = VecOf<T>::n;
+    __shared__ float red[kLongThreads / 64];
+    const int N = a.N;
+    const int64_t limit = (a.M - 1) * a.ldx + N;
+    const float inv_n = 1.0f / (float)N;
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+        const T* src = (const T*)a.x;
+        float s = 0.0f;
+        for (int c = (int)threadIdx.x * VEC; c < N; c += kLongThreads * VEC) {
+            float x[VEC];
+            load_vec<T>(src, m * a.ldx, c, N, limit, x);
+            if constexpr (RES) {
+                float r[VEC];
+                load_vec<T>((const T*)a.r, m * a.ldx, c, N, limit, r);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) r[i] += x[i];
+                store_vec<T>((T*)a.h, m * a.ldx, c, N, r);
+                unpack16<T>(pack16<T>(r), x);
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) s += x[i];
+        }
+        if constexpr (RES) src = (const T*)a.h;   // each thread reads back its own stores
+        const float mean = block_sum(s, red) * inv_n;
+        float q = 0.0f;
+        for (int c = (int)threadIdx.x * VEC; c < N; c += kLongThreads * VEC) {
+            float x[VEC];
+            load_vec<T>(src, m * a.ldx, c, N, limit, x);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const float d = x[i] - mean;
+                q += (c + i < N) ? d * d : 0.0f;
+            }
+        }
+        const float rs = inv_sqrt(block_sum(q, red) * inv_n + a.eps);
+        for (int c = (int)threadIdx.x * VEC; c < N; c += kLongThreads * VEC) {
+            float x[VEC];
+            load_vec<T>(src, m * a.ldx, c, N, limit, x);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const int k = min(c + i, N - 1);
+                x[i] = __builtin_fmaf((x[i] - mean) * rs, load_param(a.gamma, k, a.pdt),
+                                      load_param(a.beta, k, a.pdt));
+            }
+            store_vec<T>((T*)a.y, m * a.ldy, c, N, x);
+        }
+        if (threadIdx.x == 0) {
+            a.mean[m] = mean;
+            a.rstd[m] = rs;
+        }
+    }
+}
+
+template <typename T, int TPR, int V, bool RES>
+__global__ __launch_bounds__(LnShape<TPR>::threads) void ln_bwd_kernel(LnArgs a) {
+    using S = LnShape<TPR>;
+    constexpr int VEC = VecOf<T>::n;
+    constexpr int E = V * VEC;
+    const int t = (int)threadIdx.x % TPR;
+    const int g = (int)threadIdx.x / TPR;
+    const int N = a.N;
+    float gm[E], ag[E], ab[E];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int c = (t + v * TPR) * VEC + i;
+            gm[v * VEC + i] = c < N ? load_param(a.gamma, c, a.pdt) : 0.0f;
+            ag[v * VEC + i] = 0.0f;
+            ab[v * VEC + i] = 0.0f;
+        }
+    const float inv_n = 1.0f / (float)N;
+    const int64_t limit = (a.M - 1) * a.ldx + N;
+    const int64_t limit_dy = (a.M - 1) * a.lddy + N;
+    const int64_t step = (int64_t)gridDim.x * S::groups;
+    for (int64_t base = (int64_t)blockIdx.x * S::groups; base < a.M; base += step) {
+        const int64_t m = base + g;
+        const bool on = m < a.M;
+        float x[E], dy[E], res[RES ? E : 1];
+        float mean = 0.0f, rs = 0.0f;
+        if (on) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                load_vec<T>((const T*)a.x, m * a.ldx, (t + v * TPR) * VEC, N, limit, &x[v * VEC]);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                load_vec<T>((const T*)a.dy, m * a.lddy, (t + v * TPR) * VEC, N, limit_dy, &dy[v * VEC]);
+            if constexpr (RES) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    load_vec<T>((const T*)a.dres, m * a.ldx, (t + v * TPR) * VEC, N, limit, &res[v * VEC]);
+            }
+            mean = a.mean[m];
+            rs = a.rstd[m];
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = dy[e] = 0.0f;
+        }
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            // past the row's end x is 0, not the mean: dy = gamma = 0 there
+            // keeps the sums clean and the columns are never stored
+            const float n = (x[e] - mean) * rs;
+            const float d = dy[e] * gm[e];
+            ag[e] += dy[e] * n;
+            ab[e] += dy[e];
+            s1 += d;
+            s2 += d * n;
+            x[e] = n;
+        }
+        s1 = lanes_sum<S::L>(s1);
+        s2 = lanes_sum<S::L>(s2);
+        if constexpr (S::waves > 1) {
+            __shared__ float red[2][S::groups][S::waves][2];
+            const int buf = (int)((base / step) & 1);
+            if ((t & 63) == 0) {
+                red[buf][g][t >> 6][0] = s1;
+                red[buf][g][t >> 6][1] = s2;
+            }
+            __syncthreads();
+            s1 = s2 = 0.0f;
+#pragma unroll
+            for (int k = 0; k < S::waves; ++k) {
+                s1 += red[buf][g][k][0];
+                s2 += red[buf][g][k][1];
+            }
+        }
+        if (on) {
+            const float c1 = s1 * inv_n, c2 = s2 * inv_n;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float o[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const int e = v * VEC + i;
+                    const float d = dy[e] * gm[e];
+                    o[i] = rs * (d - c1 - x[e] * c2);
+                    if constexpr (RES) o[i] += res[e];
+                }
+                store_vec<T>((T*)a.y, m * a.ldy, (t + v * TPR) * VEC, N, o);
+            }
+        }
+    }
+    float* row = a.part + (int64_t)blockIdx.x * a.pitch;
+    if constexpr (S::groups == 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const int c = (t + v * TPR) * VEC + i;
+                if (c < N) {
+                    row[c] = ag[v * VEC + i];
+                    row[N + c] = ab[v * VEC + i];
+                }
+            }
+    } else {
+        // join the row groups: columns [0, TPR * E) of every group, one
+        // gradient after the other through the same LDS
+        __shared__ float join[S::groups][TPR * E];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            __syncthreads();
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    join[g][(t + v * TPR) * VEC + i] = k ? ab[v * VEC + i] : ag[v * VEC + i];
+            __syncthreads();
+            for (int c = (int)threadIdx.x; c < N; c += S::threads) {
+                float s = 0.0f;
+                for (int q = 0; q < S::groups; ++q) s += join[q][c];
+                row[k * N + c] = s;
+            }
+        }
+    }
+}
+
+// Long rows: the row sums first, then dx and the parameter gradients. Each
+// workgroup's partial row lives in the workspace and is added to in place
+// (its own columns, thread by thread), the first row's pass writing it.
+template <typename T, bool RES>
+__global__ __launch_bounds__(kLongThreads) void ln_bwd_long_kernel(LnArgs a) {
+    constexpr int VEC = VecOf<T>::n;
+    __shared__ float red[kLongThreads / 64];
+    const int N = a.N;
+    const int64_t limit = (a.M - 1) * a.ldx + N;
+    const int64_t limit_dy = (a.M - 1) * a.lddy + N;
+    const float inv_n = 1.0f / (float)N;
+    float* row = a.part + (int64_t)blockIdx.x * a.pitch;
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+        const bool first = m == blockIdx.x;
+        const float mean = a.mean[m], rs = a.rstd[m];
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int c = (int)threadIdx.x * VEC; c < N; c += kLongThreads * VEC) {
+            float x[VEC], dy[VEC];
+            load_vec<T>((const T*)a.x, m * a.ldx, c, N, limit, x);
+            load_vec<T>((const T*)a.dy, m * a.lddy, c, N, limit_dy, dy);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const int k = min(c + i, N - 1);
+                const float d = dy[i] * load_param(a.gamma, k, a.pdt);   // dy = 0 past the end
+                s1 += d;
+                s2 += d * ((x[i] - mean) * rs);
+            }
+        }
+        const float c1 = block_sum(s1, red) * inv_n;
+        const float c2 = block_sum(s2, red) * inv_n;
+        for (int c = (int)threadIdx.x * VEC; c < N; c += kLongThreads * VEC) {
+            float x[VEC], dy[VEC], res[VEC], o[VEC];
+            load_vec<T>((const T*)a.x, m * a.ldx, c, N, limit, x);
+            load_vec<T>((const T*)a.dy, m * a.lddy, c, N, limit_dy, dy);
+            if constexpr (RES) load_vec<T>((const T*)a.dres, m * a.ldx, c, N, limit, res);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                if (c + i >= N) continue;
+                const float n = (x[i] - mean) * rs;
+                o[i] = rs * (dy[i] * load_param(a.gamma, c + i, a.pdt) - c1 - n * c2);
+                if constexpr (RES) o[i] += res[i];
+                row[c + i] = (first ? 0.0f : row[c + i]) + dy[i] * n;
+                row[N + c + i] = (first ? 0.0f : row[N + c + i]) + dy[i];
+            }
+            store_vec<T>((T*)a.y, m * a.ldy, c, N, o);
+        }
+    }
+}
+
+}  // namespace dytb

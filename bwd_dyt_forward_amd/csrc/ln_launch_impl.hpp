@@ -1,0 +1,87 @@
+// ln_launch_impl.hpp - instances of the layer norm kernels for one type.
+#pragma once
+
+#include <algorithm>
+
+#include "ln_launch.hpp"
+
+namespace dytb {
+
+// Workgroups of a forward launch: enough to fill 256 CUs several times over
+// and no more, since each loads gamma and beta once for all its rows.
+constexpr int kFwdGridThreads = 256 * 2048;
+
+template <typename T, int TPR, int V, int U>
+void ln_fwd_one(const LnArgs& a, hipStream_t s) {
+    using S = LnShape<TPR>;
+    const int64_t per = (int64_t)S::groups * U;
+    const int64_t need = (a.M + per - 1) / per;
+    const int grid = (int)std::min<int64_t>(need, kFwdGridThreads / S::threads);
+    if (a.r) ln_fwd_kernel<T, TPR, V, U, true><<<grid, S::threads, 0, s>>>(a);
+    else ln_fwd_kernel<T, TPR, V, U, false><<<grid, S::threads, 0, s>>>(a);
+}
+
+// U rows per thread at a time keep enough loads in flight where a row is few
+// vectors; with few rows (under one round of the grid) one row per thread
+// spreads them over more CUs.
+template <typename T, int TPR, int V, int U>
+void ln_fwd_pick(const LnArgs& a, hipStream_t s) {
+    if constexpr (U > 1) {
+        if (a.M > (int64_t)LnShape<TPR>::groups * U * 512) return ln_fwd_one<T, TPR, V, U>(a, s);
+    }
+    ln_fwd_one<T, TPR, V, 1>(a, s);
+}
+
+template <typename T>
+void ln_launch_forward(const LnConfig& c, const LnArgs& a, hipStream_t s) {
+    switch (c.threads * 8 + c.vecs) {
+        case 1 * 8 + 1: return ln_fwd_pick<T, 1, 1, 4>(a, s);
+        case 2 * 8 + 1: return ln_fwd_pick<T, 2, 1, 4>(a, s);
+        case 4 * 8 + 1: return ln_fwd_pick<T, 4, 1, 4>(a, s);
+        case 8 * 8 + 1: return ln_fwd_pick<T, 8, 1, 4>(a, s);
+        case 16 * 8 + 1: return ln_fwd_pick<T, 16, 1, 4>(a, s);
+        case 32 * 8 + 1: return ln_fwd_pick<T, 32, 1, 4>(a, s);
+        case 64 * 8 + 1: return ln_fwd_pick<T, 64, 1, 4>(a, s);
+        case 64 * 8 + 2: return ln_fwd_pick<T, 64, 2, 2>(a, s);
+        case 64 * 8 + 4: return ln_fwd_pick<T, 64, 4, 1>(a, s);
+        case 256 * 8 + 2: return ln_fwd_pick<T, 256, 2, 1>(a, s);
+        case 256 * 8 + 4: return ln_fwd_pick<T, 256, 4, 1>(a, s);
+        case 512 * 8 + 4: return ln_fwd_pick<T, 512, 4, 1>(a, s);
+        case 1024 * 8 + 4: return ln_fwd_pick<T, 1024, 4, 1>(a, s);
+        default: break;
+    }
+    const int grid = (int)std::min<int64_t>(a.M, 512);
+    if (a.r) ln_fwd_long_kernel<T, true><<<grid, kLongThreads, 0, s>>>(a);
+    else ln_fwd_long_kernel<T, false><<<grid, kLongThreads, 0, s>>>(a);
+}
+
+template <typename T, int TPR, int V>
+void ln_bwd_one(int grid, const LnArgs& a, hipStream_t s) {
+    using S = LnShape<TPR>;
+    if (a.dres) ln_bwd_kernel<T, TPR, V, true><<<grid, S::threads, 0, s>>>(a);
+    else ln_bwd_kernel<T, TPR, V, false><<<grid, S::threads, 0, s>>>(a);
+}
+
+template <typename T>
+void ln_launch_backward(const LnConfig& c, int grid, const LnArgs& a, hipStream_t s) {
+    switch (c.threads * 8 + c.vecs) {
+        case 1 * 8 + 1: return ln_bwd_one<T, 1, 1>(grid, a, s);
+        case 2 * 8 + 1: return ln_bwd_one<T, 2, 1>(grid, a, s);
+        case 4 * 8 + 1: return ln_bwd_one<T, 4, 1>(grid, a, s);
+        case 8 * 8 + 1: return ln_bwd_one<T, 8, 1>(grid, a, s);
+        case 16 * 8 + 1: return ln_bwd_one<T, 16, 1>(grid, a, s);
+        case 32 * 8 + 1: return ln_bwd_one<T, 32, 1>(grid, a, s);
+        case 64 * 8 + 1: return ln_bwd_one<T, 64, 1>(grid, a, s);
+        case 64 * 8 + 2: return ln_bwd_one<T, 64, 2>(grid, a, s);
+        case 128 * 8 + 2: return ln_bwd_one<T, 128, 2>(grid, a, s);
+        case 256 * 8 + 2: return ln_bwd_one<T, 256, 2>(grid, a, s);
+        case 512 * 8 + 2: return ln_bwd_one<T, 512, 2>(grid, a, s);
+        case 1024 * 8 + 2: return ln_bwd_one<T, 1024, 2>(grid, a, s);
+        case 1024 * 8 + 4: return ln_bwd_one<T, 1024, 4>(grid, a, s);
+        default: break;
+    }
+    if (a.dres) ln_bwd_long_kernel<T, true><<<grid, kLongThreads, 0, s>>>(a);
+    else ln_bwd_long_kernel<T, false><<<grid, kLongThreads, 0, s>>>(a);
+}
+
+}  // namespace dytb
