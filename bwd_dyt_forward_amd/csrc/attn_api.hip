@@ -104,9 +104,9 @@ struct Plan {
     int fwd_blocks, fwd_split, fwd_per;
     int dq_blocks, dq_split, dq_per;
     int dkv_blocks, dkv_split, dkv_per, dkv_parts;
-    int per_unit;   // dq workgroups of a head
+    int per_unit;   // dkv workgroups of a head
     size_t fwd_bytes, bwd_bytes;
-    size_t off_tpart, off_part;   // backward workspace: rows, tpart, part
+    size_t off_rest, off_tpart, off_part;   // backward workspace: rows, rest, tpart, part
     bool nothing_out, nothing_keys;
     Borders borders;
 };
@@ -114,17 +114,31 @@ struct Plan {
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // Waves per workgroup and splits of the long axis. Workgroups of four waves
-// share each tile of the long axis; where they would be fewer than the 256
-// CUs, single waves spread the rows wider. Where still fewer than `want`
-// workgroups result, the long axis is split into runs of at least `least`.
-void choose(int64_t units, int64_t rows, int64_t len, int tile4, int64_t want, int64_t least, int& nw, int& blocks,
-            int& split, int& per) {
-    nw = units * ((rows + 127) / 128) >= 256 ? 4 : 1;
+// share each tile of the long axis; single waves each bring their own, which
+// the L2 only keeps up with while they are few. So four waves wherever their
+// workgroups, with the long axis cut into runs of 1,024, would fill the 256
+// CUs, and single waves below (and for up to 32 rows, one wave's). The
+// number of splits is then the power of two that minimises
+//   tiles per split * waves per SIMD (at least 1) * 0.6 us
+//   + 6 us for the join's launch and 0.1 us for each part it reads.
+void choose(int64_t units, int64_t rows, int64_t len, int tile4, int& nw, int& blocks, int& split, int& per) {
+    const int64_t b4 = units * ((rows + 127) / 128);
+    nw = rows > 32 && b4 * std::max<int64_t>(1, len / 1024) >= 256 ? 4 : 1;
     const int tile = nw == 4 ? tile4 : 32;
     blocks = ceil_div(rows, 32 * nw);
-    const int64_t have = std::max<int64_t>(units * blocks * nw, 1);
-    int64_t parts = std::max<int64_t>(1, std::min((want + have - 1) / have, len / least));
-    per = (int)std::max<int64_t>(tile, (ceil_div(len, parts) + tile - 1) / tile * tile);
+    const double waves = (double)units * blocks * nw;
+    const int64_t tiles = std::max<int64_t>(1, ceil_div(len, tile));
+    double best = 0.0;
+    int64_t parts = 1;
+    for (int64_t n = 1; n == 1 || (n <= 64 && n * 4 <= tiles); n *= 2) {
+        const double t = ceil_div(tiles, n) * (tile / 32) * std::max(1.0, waves * n / 1024.0) * 0.6 +
+                         (n > 1 ? 6.0 + 0.1 * n : 0.0);
+        if (n == 1 || t < best) {
+            best = t;
+            parts = n;
+        }
+    }
+    per = ceil_div(tiles, parts) * tile;
     split = std::max(1, ceil_div(len, per));
 }
 
@@ -154,15 +168,16 @@ Plan make_plan(const dyt_attn_desc& d) {
     const int dp = attn_dp(d.D), tile = d.dtype == DYT_F32 ? 32 : 64;
     p.fwd = p.dq = p.dkv = {dp, 1, d.table != nullptr};
     if (!p.nothing_out) {
-        choose(p.units, p.rows, d.Sk, tile, 2048, 128, p.fwd.nw, p.fwd_blocks, p.fwd_split, p.fwd_per);
-        choose(p.units, p.rows, d.Sk, tile, 1024, 256, p.dq.nw, p.dq_blocks, p.dq_split, p.dq_per);
+        choose(p.units, p.rows, d.Sk, tile, p.fwd.nw, p.fwd_blocks, p.fwd_split, p.fwd_per);
+        choose(p.units, p.rows, d.Sk, tile, p.dq.nw, p.dq_blocks, p.dq_split, p.dq_per);
     }
     if (!p.nothing_keys && d.Hq > 0)
-        choose(p.units, d.Sk, p.rows, tile, 1024, 256, p.dkv.nw, p.dkv_blocks, p.dkv_split, p.dkv_per);
+        choose(p.units, d.Sk, p.rows, tile, p.dkv.nw, p.dkv_blocks, p.dkv_split, p.dkv_per);
     const int64_t part_rows = p.units * p.rows * (int64_t)dp * 4;
     if (p.fwd_split > 1) p.fwd_bytes = round256((size_t)p.fwd_split * part_rows) + (size_t)p.fwd_split * p.units * p.rows * 8;
-    p.per_unit = p.dq_blocks * p.dq_split;
-    p.off_tpart = round256((size_t)2 * d.B * d.Hq * d.Sq * 4);
+    p.per_unit = p.dkv_blocks * p.dkv_split;
+    p.off_rest = round256((size_t)2 * d.B * d.Hq * d.Sq * 4);
+    p.off_tpart = p.off_rest + (p.dq_split > 1 ? round256((size_t)p.dq_split * d.B * d.Hq * d.Sq * 4) : 0);
     p.off_part = p.off_tpart + (d.table ? round256((size_t)p.units * p.per_unit * d.num_buckets * 4) : 0);
     p.dkv_parts = p.dkv_split * (int)(d.Hq > 0 ? G / p.pack : 1);
     size_t part = p.dq_split > 1 ? (size_t)p.dq_split * part_rows : 0;
@@ -312,6 +327,7 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
     a.vec_q = vec_ok(q, a.qs, row, p.pack); a.vec_k = vec_ok(k, a.ks, row, 1); a.vec_v = vec_ok(v, a.vs, row, 1);
     a.vec_o = vec_ok(o, a.os, row, 1); a.vec_do = vec_ok(dout, a.dos, row, p.pack);
     a.rows = (float*)workspace;
+    a.rest = (float*)((char*)workspace + p.off_rest);
     a.tpart = (float*)((char*)workspace + p.off_tpart);
     a.part = (float*)((char*)workspace + p.off_part);
     return with_type(d.dtype, [&](auto* t) {
@@ -324,16 +340,12 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
             if (p.dq_split > 1) {
                 const int64_t total = (int64_t)p.units * p.rows;
                 attn_launch_sum<T>(dp, {a.part, total * dp, p.dq_split, (char*)dq, a.dqs, total, (int)p.rows, p.pack,
-                                        (int)(d.Hq / p.pack), (int)d.D}, s);
+                                        (int)(d.Hq / p.pack), (int)d.D, a.rows + (int64_t)d.B * d.Hq * d.Sq, a.rest}, s);
             }
         }
-        if (d.table && d.Hq > 0)
-            attn_dtable_kernel<<<(unsigned)(d.Hq * d.num_buckets), 64, 0, s>>>(
-                a.tpart, p.nothing_out ? 0 : (int)d.B, (int)d.Hq, p.nothing_out ? 1 : p.per_unit, d.num_buckets, dtable,
-                d.table_dtype);
         if (!p.nothing_keys) {
             const int64_t total = d.B * d.Hkv * d.Sk, stride = 2 * total * dp;
-            const SumArgs sk = {a.part, stride, p.dkv_parts, (char*)dk, a.dks, total, (int)d.Sk, 1, (int)d.Hkv, (int)d.D};
+            const SumArgs sk = {a.part, stride, p.dkv_parts, (char*)dk, a.dks, total, (int)d.Sk, 1, (int)d.Hkv, (int)d.D, nullptr, nullptr};
             SumArgs sv = sk;
             sv.part = a.part + total * dp;
             sv.out = (char*)dv;
@@ -353,6 +365,10 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
                 attn_launch_sum<T>(dp, sv, s);
             }
         }
+        if (d.table && d.Hq > 0)
+            attn_dtable_kernel<<<(unsigned)(d.Hq * d.num_buckets), 64, 0, s>>>(
+                a.tpart, p.nothing_keys ? 0 : (int)d.B, (int)d.Hq, p.nothing_keys ? 1 : p.per_unit, d.num_buckets, dtable,
+                d.table_dtype);
         return hip_status();
     });
 }

@@ -4,8 +4,8 @@
 // Two kernels, so that no sum is shared between workgroups and none needs
 // atomics:
 //   dq   a wave owns 32 query rows and walks the keys: S^T = K Q^T,
-//        dP^T = V dO^T, dS = P (dP - delta), dQ^T += K^T dS^T. Before, it
-//        takes delta = do . o of its rows and leaves delta and the log sums
+//        dP^T = V dO^T, dS = P (dP - delta), dQ^T += K^T dS^T. It takes
+//        delta = do . o of its rows first and leaves delta and the log sums
 //        (in log2 units) in the workspace for
 //   dkv  a wave owns 32 keys and walks the query rows that see them, of all
 //        heads of the group: S = Q K^T, dP = dO V^T, dV^T += dO^T P,
@@ -14,13 +14,17 @@
 // seventh cost less than a float32 dq summed through memory: they read
 // nothing that is not in LDS already.
 //
+// o is rounded to its type, so delta is off by a little in every pair of the
+// row, which a sum over many pairs (dtable) shows: but the row's dS have to
+// add up to zero, so the dq kernel adds their sum to the delta it leaves.
+//
 // Both take a split of their long axis where there are few blocks; the
 // splits' float32 parts are summed in split order by attn_sum_kernel.
 //
-// Bias gradient (dq kernel): tiles beyond the reach of the last bucket add
+// Bias gradient (dkv kernel): tiles beyond the reach of the last bucket add
 // to one sum per lane. In the others the pairs of one relative position form
 // a diagonal: each lane writes its 16 values of dS into a wave's scratch at
-// [key - query + 31][query] (the positions are the same for every tile, the
+// [key - query + 31][key] (the positions are the same for every tile, the
 // rest of the scratch stays zero), then lane t adds up diagonal t - 31 and
 // adds the sum to the wave's array of sums by relative position. At the end
 // the waves' arrays are joined in wave order and each bucket's range of
@@ -39,7 +43,7 @@ template <typename T, int NW> struct BwdTile { static constexpr int rows = sizeo
 template <typename T, int DP, int NW>
 constexpr int bwd_lds_bytes() { return 2 * 2 * BwdTile<T, NW>::rows * DP * (int)sizeof(T); }
 
-// LDS floats of the dq kernel's bias gradient.
+// LDS floats of the bias gradient.
 inline __host__ __device__ int dbias_floats(int entries, int nw) { return nw * (kDiagFloats + entries); }
 
 template <typename T, int DP, int NW, bool BIAS>
@@ -72,16 +76,8 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dq_kernel(AttnArgs a) {
         stage<T, DP, KT, NW>(0, kr, begin, begin, 0, end, a.D);
         stage<T, DP, KT, NW>(2 * KB, vr, begin, begin, 0, end, a.D);
     }
-    const int entries = BIAS ? bias_entries(a.borders) : 0;
-    float* bias = (float*)(smem + 4 * KB);
-    float* diag = bias + entries + wave * kDiagFloats;
-    float* sums = bias + entries + NW * kDiagFloats;   // [NW][entries]
-    float far_before = 0.0f, far_behind = 0.0f;
-    if constexpr (BIAS) {
-        fill_bias(bias, a, w.head);
-        for (int x = lane; x < kDiagFloats; x += 64) diag[x] = 0.0f;
-        for (int x = lane; x < entries; x += 64) sums[wave * entries + x] = 0.0f;
-    }
+    float* bias = (float*)(smem + 4 * KB + kColBytes);
+    if constexpr (BIAS) fill_bias(bias, (float*)(smem + 4 * KB), a, w.head);
 
     Frag<T> q[DP / 16], dout[DP / 16];
     float delta = 0.0f;
@@ -103,11 +99,8 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dq_kernel(AttnArgs a) {
         const int64_t at = ((int64_t)w.b * a.Hq + w.head + g) * a.Sq + pos_i;
         const float s = a.stats[at];
         if (s != -INFINITY) lse = s * kLog2e;
-        if (h == 0 && w.split == 0) {
-            a.rows[at] = lse;
-            a.rows[(int64_t)a.B * a.Hq * a.Sq + at] = delta;
-        }
     }
+    float rest = 0.0f;   // this lane's part of the sum of dS over its row
     f32x16 dq[DP / 32];
 #pragma unroll
     for (int dt = 0; dt < DP / 32; ++dt)
@@ -146,7 +139,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dq_kernel(AttnArgs a) {
                     for (int i = 0; i < 16; ++i)
                         p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, at[8 * (i / 4) + (i % 4)]) - lse);
                 } else {
-                    const float one = bias[far_after ? entries - 1 : 0];
+                    const float one = bias[far_after ? 2 * (reach + kPad) - 1 : 0];
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, one) - lse);
@@ -161,30 +154,9 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dq_kernel(AttnArgs a) {
                 for (int i = 0; i < 16; ++i) p[i] = js + acc_row(i, h) <= last ? p[i] : 0.0f;
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) p[i] *= dp[i] - delta;
-            if constexpr (BIAS) {
-                if (near) {
-                    float* at = diag + (31 + 4 * h - (lane & 31)) * kDiagPitch + (lane & 31);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) at[(8 * (i / 4) + (i % 4)) * kDiagPitch] = there ? p[i] : 0.0f;
-                    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-                    __builtin_amdgcn_wave_barrier();
-                    float d = 0.0f;
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) d += diag[lane * kDiagPitch + x];
-                    // lane 63 has no diagonal: its row of the scratch is never written
-                    float* to = sums + wave * entries + (js - (w.start + row0) + reach + kPad - 31 + lane);
-                    if (lane < 63) *to += d;
-                    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-                    __builtin_amdgcn_wave_barrier();
-                } else {
-                    float d = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) d += p[i];
-                    d = there ? d : 0.0f;
-                    if (far_after) far_behind += d;
-                    else far_before += d;
-                }
+            for (int i = 0; i < 16; ++i) {
+                p[i] *= dp[i] - delta;
+                rest += p[i];
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -204,40 +176,15 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dq_kernel(AttnArgs a) {
             store_part<DP>(a.part + at * DP, dq, a.scale, there, h);
         }
     }
-    if constexpr (BIAS) {
-        far_before = lanes_sum<64>(far_before);
-        far_behind = lanes_sum<64>(far_behind);
-        if (lane == 0) {
-            sums[wave * entries] += far_before;             // farther than the reach: the outermost entries
-            sums[wave * entries + entries - 1] += far_behind;
+    // rest is what delta is too small by (rounded o): the dkv kernel takes the sum
+    rest = swap32_other_sum(rest);
+    if (there && h == 0) {
+        const int64_t at = ((int64_t)w.b * a.Hq + w.head + g) * a.Sq + pos_i, all = (int64_t)a.B * a.Hq * a.Sq;
+        if (w.split == 0) {
+            a.rows[at] = lse;
+            a.rows[all + at] = a.nsplit == 1 ? delta + rest : delta;
         }
-        __syncthreads();
-        for (int x = (int)threadIdx.x; x < entries; x += NW * 64) {
-            float s = sums[x];
-            for (int k = 1; k < NW; ++k) s += sums[k * entries + x];
-            sums[x] = s;
-        }
-        __syncthreads();
-        // a bucket is a run of entries: one lane group of 64 per bucket
-        const Borders& o = a.borders;
-        const int mid = o.reach + kPad;   // entry of position 0
-        for (int t = wave; t < a.buckets; t += NW) {
-            int lo, hi;   // entries [lo, hi)
-            if (t < o.n) {
-                lo = t + 1 < o.n ? mid - o.at[t + 1] + 1 : 0;
-                hi = mid - o.at[t] + 1;
-                if (t == 0 && !o.bidirectional) hi = entries;   // every later key
-            } else {
-                // later keys: distance 0 is the other direction's
-                const int d = max(o.at[t - o.n], 1);
-                lo = mid + d;
-                hi = t - o.n + 1 < o.n ? mid + o.at[t - o.n + 1] : entries;
-            }
-            float s = 0.0f;
-            for (int x = lo + lane; x < hi; x += 64) s += sums[x];
-            s = lanes_sum<64>(s);
-            if (lane == 0) a.tpart[w.flat * a.buckets + t] = s;
-        }
+        if (a.nsplit > 1) a.rest[w.split * all + at] = rest;
     }
 }
 
@@ -270,8 +217,16 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dkv_kernel(AttnArgs a) {
     const int64_t row_at = ((int64_t)w.b * a.Hq + w.head) * a.Sq;
     const int64_t rows_all = (int64_t)a.B * a.Hq * a.Sq;
     constexpr int kStat = 4 * RB;   // [2 buffers][lse, delta][64]
-    float* bias = (float*)(smem + kStat + 1024);
-    if constexpr (BIAS) fill_bias(bias, a, w.head);
+    const int entries = BIAS ? bias_entries(a.borders) : 0;
+    float* bias = (float*)(smem + kStat + 1024 + kColBytes);
+    float* diag = bias + entries + wave * kDiagFloats;
+    float* sums = bias + entries + NW * kDiagFloats;   // [NW][entries]
+    float far_before = 0.0f, far_behind = 0.0f;
+    if constexpr (BIAS) {
+        fill_bias(bias, (float*)(smem + kStat + 1024), a, w.head);
+        for (int x = lane; x < kDiagFloats; x += 64) diag[x] = 0.0f;
+        for (int x = lane; x < entries; x += 64) sums[wave * entries + x] = 0.0f;
+    }
 
     const auto bring = [&](int r0, int to) {
         const int i0 = r0 / a.pack, rem = r0 - i0 * a.pack;
@@ -329,10 +284,11 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dkv_kernel(AttnArgs a) {
             }
             const float* st = (const float*)(smem + kStat + buf * 512) + n * 32 + 4 * h;
             float p[16];
+            const int reach = a.borders.reach, after = a.borders.bidirectional ? reach : 0;
+            const bool far_after = key0 - imax >= after;
+            const bool near = key0 + 31 - imin > -reach && !far_after;
             if constexpr (BIAS) {
-                const int reach = a.borders.reach, after = a.borders.bidirectional ? reach : 0;
-                const bool far_after = key0 - imax >= after;
-                if (key0 + 31 - imin > -reach && !far_after) {
+                if (near) {
                     // pack = 1: the row of register i is acc_row(i, h) positions on
                     const float* at = bias + (key - w.start - rs + reach + kPad - 4 * h);
 #pragma unroll
@@ -341,7 +297,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dkv_kernel(AttnArgs a) {
                         p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, at[-k]) - st[k]);
                     }
                 } else {
-                    const float one = bias[far_after ? 2 * (reach + kPad) - 1 : 0];
+                    const float one = bias[far_after ? entries - 1 : 0];
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, one) - st[8 * (i / 4) + (i % 4)]);
@@ -366,6 +322,30 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dkv_kernel(AttnArgs a) {
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) p[i] *= dp[i] - st[64 + 8 * (i / 4) + (i % 4)];
+            if constexpr (BIAS) {
+                // rows past the end have q = dO = 0 and delta = 0: dS = 0
+                if (near) {
+                    float* at = diag + (31 - 4 * h + (lane & 31)) * kDiagPitch + (lane & 31);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) at[-(8 * (i / 4) + (i % 4)) * kDiagPitch] = p[i];
+                    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                    __builtin_amdgcn_wave_barrier();
+                    float d = 0.0f;
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) d += diag[lane * kDiagPitch + x];
+                    // lane 63 has no diagonal: its row of the scratch is never written
+                    float* to = sums + wave * entries + (key0 - (w.start + rs) + reach + kPad - 31 + lane);
+                    if (lane < 63) *to += d;
+                    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                    __builtin_amdgcn_wave_barrier();
+                } else {
+                    float d = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) d += p[i];
+                    if (far_after) far_behind += d;
+                    else far_before += d;
+                }
+            }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const Frag<T> pf = pack_frag<T>(p + 8 * k);
@@ -373,6 +353,41 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dkv_kernel(AttnArgs a) {
                 for (int dt = 0; dt < DP / 32; ++dt)
                     dk[dt] = mma<T>(TL::col_frag(qt, n * 32 + k * 16, dt, lane), pf, dk[dt]);
             }
+        }
+    }
+    if constexpr (BIAS) {
+        far_before = lanes_sum<64>(far_before);
+        far_behind = lanes_sum<64>(far_behind);
+        if (lane == 0) {
+            sums[wave * entries] += far_before;             // farther than the reach: the outermost entries
+            sums[wave * entries + entries - 1] += far_behind;
+        }
+        __syncthreads();
+        for (int x = (int)threadIdx.x; x < entries; x += NW * 64) {
+            float s = sums[x];
+            for (int k = 1; k < NW; ++k) s += sums[k * entries + x];
+            sums[x] = s;
+        }
+        __syncthreads();
+        // a bucket is a run of entries: one lane group of 64 per bucket
+        const Borders& o = a.borders;
+        const int mid = o.reach + kPad;   // entry of position 0
+        for (int t = wave; t < a.buckets; t += NW) {
+            int lo, hi;   // entries [lo, hi)
+            if (t < o.n) {
+                lo = t + 1 < o.n ? mid - o.at[t + 1] + 1 : 0;
+                hi = mid - o.at[t] + 1;
+                if (t == 0 && !o.bidirectional) hi = entries;   // every later key
+            } else {
+                // later keys: distance 0 is the other direction's
+                const int d = max(o.at[t - o.n], 1);
+                lo = mid + d;
+                hi = t - o.n + 1 < o.n ? mid + o.at[t - o.n + 1] : entries;
+            }
+            float s = 0.0f;
+            for (int x = lo + lane; x < hi; x += 64) s += sums[x];
+            s = lanes_sum<64>(s);
+            if (lane == 0) a.tpart[w.flat * a.buckets + t] = s;
         }
     }
     if (key0 >= a.Sk) return;
@@ -393,26 +408,33 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dkv_kernel(AttnArgs a) {
 
 // Sums float32 parts in order and rounds once: out[b, s, h] = sum_p part[p]
 // [(b, hu)][row][DP] with row = s * pack + g and h = hu * pack + g. One part
-// lies `stride` floats after the other. DP / 4 threads per row.
+// lies `stride` floats after the other. DP / 4 threads per row. With `delta`
+// (dq's sum) the parts of `rest` [part][b, head, i] are added to it.
 template <typename T, int DP>
-__global__ __launch_bounds__(256) void attn_sum_kernel(const float* part, int64_t stride, int parts, char* out,
-                                                       Strides os, int64_t total, int rows, int pack, int hu, int D) {
+__global__ __launch_bounds__(256) void attn_sum_kernel(SumArgs x) {
     constexpr int TPR = DP / 4, PER = 256 / TPR;
     const int64_t at = (int64_t)blockIdx.x * PER + (int)threadIdx.x / TPR;
     const int d = ((int)threadIdx.x % TPR) * 4;
-    if ((int)threadIdx.x >= PER * TPR || at >= total) return;
+    if ((int)threadIdx.x >= PER * TPR || at >= x.total) return;
     float o[4] = {0, 0, 0, 0};
-    for (int p = 0; p < parts; ++p) {
-        const f32x4 v = *(const f32x4*)(part + p * stride + at * DP + d);
+#pragma unroll 4
+    for (int p = 0; p < x.parts; ++p) {
+        const f32x4 v = *(const f32x4*)(x.part + p * x.stride + at * DP + d);
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[k] += v[k];
     }
-    const int u = (int)(at / rows), r = (int)(at - (int64_t)u * rows);
-    const int b = u / hu, i = r / pack, head = (u - b * hu) * pack + (r - i * pack);
-    T* to = (T*)(out + b * os.b + (int64_t)i * os.s + (int64_t)head * os.h);
+    const int u = (int)(at / x.rows), r = (int)(at - (int64_t)u * x.rows);
+    const int b = u / x.hu, i = r / x.pack, head = (u - b * x.hu) * x.pack + (r - i * x.pack);
+    T* to = (T*)(x.out + b * x.os.b + (int64_t)i * x.os.s + (int64_t)head * x.os.h);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-        if (d + k < D) to[d + k] = dyt::from_f32<T>(o[k]);
+        if (d + k < x.D) to[d + k] = dyt::from_f32<T>(o[k]);
+    if (x.delta && d == 0) {
+        const int64_t n = ((int64_t)b * x.hu * x.pack + head) * (x.rows / x.pack) + i;
+        float s = 0.0f;
+        for (int p = 0; p < x.parts; ++p) s += x.rest[p * x.total + n];
+        x.delta[n] += s;
+    }
 }
 
 }  // namespace dytb

@@ -61,8 +61,8 @@ __global__ __launch_bounds__(NW * 64, NW > 1 && sizeof(T) == 2 ? 2 : 1) void att
         stage<T, DP, KT, NW>(0, kr, begin, begin, 0, end, a.D);
         stage<T, DP, KT, NW>(2 * KB, vr, begin, begin, 0, end, a.D);
     }
-    float* bias = (float*)(smem + 4 * KB);
-    if constexpr (BIAS) fill_bias(bias, a, w.head);
+    float* bias = (float*)(smem + 4 * KB + kColBytes);
+    if constexpr (BIAS) fill_bias(bias, (float*)(smem + 4 * KB), a, w.head);
 
     Frag<T> q[DP / 16];
     {
@@ -189,12 +189,14 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     const int d = ((int)threadIdx.x % TPR) * 4;
     if ((int)threadIdx.x >= PER * TPR || at >= total) return;
     float M = -INFINITY;
+#pragma unroll 8
     for (int s = 0; s < a.nsplit; ++s) M = fmaxf(M, a.part_ml[2 * (s * total + at)]);
     const float mm = M == -INFINITY ? 0.0f : M;
     float l = 0.0f, o[4] = {0, 0, 0, 0};
+#pragma unroll 8
     for (int s = 0; s < a.nsplit; ++s) {
+        // an empty split has weight 2^-inf = 0 and a part of zeros
         const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * (s * total + at)] - mm);
-        if (f == 0.0f) continue;
         l += f * a.part_ml[2 * (s * total + at) + 1];
         const f32x4 v = *(const f32x4*)(a.part + (s * total + at) * DP + d);
 #pragma unroll

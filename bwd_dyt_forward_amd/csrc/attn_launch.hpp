@@ -23,15 +23,6 @@ template <typename T> int attn_launch_fwd(const AttnPick&, const AttnArgs&, hipS
 template <typename T> int attn_launch_dq(const AttnPick&, const AttnArgs&, hipStream_t);
 template <typename T> int attn_launch_dkv(const AttnPick&, const AttnArgs&, hipStream_t);
 
-struct SumArgs {
-    const float* part;
-    int64_t stride;
-    int32_t parts;
-    char* out;
-    Strides os;
-    int64_t total;
-    int32_t rows, pack, hu, D;
-};
 template <typename T> void attn_launch_sum(int dp, const SumArgs&, hipStream_t);
 
 // Calls f with the compile-time (DP, NW, BIAS) of the pick.
@@ -77,6 +68,6 @@ inline int launch_lds(const void* kernel, unsigned grid, unsigned threads, size_
     return hipLaunchKernel(kernel, dim3(grid), dim3(threads), args, lds, s) == hipSuccess ? DYT_OK : DYT_ERR_HIP;
 }
 
-inline size_t bias_lds_bytes(const AttnArgs& a) { return (size_t)2 * (a.borders.reach + kPad) * sizeof(float); }
+inline size_t bias_lds_bytes(const AttnArgs& a) { return kColBytes + (size_t)2 * (a.borders.reach + kPad) * sizeof(float); }
 
 }  // namespace dytb

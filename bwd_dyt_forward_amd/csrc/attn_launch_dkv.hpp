@@ -13,7 +13,8 @@ int attn_launch_dkv(const AttnPick& p, const AttnArgs& a, hipStream_t s) {
     with_pick(p, [&](auto dp, auto nw, auto bias) {
         constexpr int DP = decltype(dp)::value, NW = decltype(nw)::value;
         constexpr bool BIAS = decltype(bias)::value != 0;
-        const size_t lds = bwd_lds_bytes<T, DP, NW>() + 1024 + (BIAS ? bias_lds_bytes(a) : 0);
+        size_t lds = bwd_lds_bytes<T, DP, NW>() + 1024;
+        if (BIAS) lds += bias_lds_bytes(a) + sizeof(float) * dbias_floats(2 * (a.borders.reach + kPad), NW);
         st = launch_lds((const void*)attn_dkv_kernel<T, DP, NW, BIAS>, attn_grid(a), NW * 64, lds, a, s);
     });
     return st;
@@ -23,8 +24,7 @@ template <typename T>
 void attn_launch_sum(int dp, const SumArgs& x, hipStream_t s) {
     with_dp(dp, [&](auto d) {
         constexpr int DP = decltype(d)::value, PER = 256 / (DP / 4);
-        attn_sum_kernel<T, DP><<<(unsigned)((x.total + PER - 1) / PER), 256, 0, s>>>(
-            x.part, x.stride, x.parts, x.out, x.os, x.total, x.rows, x.pack, x.hu, x.D);
+        attn_sum_kernel<T, DP><<<(unsigned)((x.total + PER - 1) / PER), 256, 0, s>>>(x);
     });
 }
 

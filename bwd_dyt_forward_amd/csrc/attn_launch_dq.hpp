@@ -12,11 +12,7 @@ int attn_launch_dq(const AttnPick& p, const AttnArgs& a, hipStream_t s) {
     with_pick(p, [&](auto dp, auto nw, auto bias) {
         constexpr int DP = decltype(dp)::value, NW = decltype(nw)::value;
         constexpr bool BIAS = decltype(bias)::value != 0;
-        size_t lds = bwd_lds_bytes<T, DP, NW>();
-        if (BIAS) {
-            const int entries = 2 * (a.borders.reach + kPad);
-            lds += sizeof(float) * (entries + dbias_floats(entries, NW));
-        }
+        const size_t lds = bwd_lds_bytes<T, DP, NW>() + (BIAS ? bias_lds_bytes(a) : 0);
         st = launch_lds((const void*)attn_dq_kernel<T, DP, NW, BIAS>, attn_grid(a), NW * 64, lds, a, s);
     });
     return st;

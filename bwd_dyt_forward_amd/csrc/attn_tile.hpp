@@ -360,7 +360,8 @@ struct AttnArgs {
     float* part;           // partial results, see the kernels
     float* part_ml;
     float* rows;           // backward: [2][B, Hq, Sq]: log2 of the sums, delta
-    float* tpart;          // backward: [units * nrb * nsplit][buckets]
+    float* rest;           // backward, dq split: [nsplit][B, Hq, Sq], what delta is off by
+    float* tpart;          // backward: [units * blocks * nsplit][buckets]
     int32_t B, Sq, Sk, Hq, Hkv, D, G;
     int32_t pack, magic, units;   // units = B * Hq / pack
     int32_t blocks, nsplit, per_split;   // row (or key) blocks per unit, splits of the other axis
@@ -368,6 +369,19 @@ struct AttnArgs {
     int32_t vec_q, vec_k, vec_v, vec_o, vec_do, vec_out;   // vec_out: every output
     float scale;
     Borders borders;
+};
+
+// The sum of float32 parts, see attn_sum_kernel.
+struct SumArgs {
+    const float* part;
+    int64_t stride;
+    int32_t parts;
+    char* out;
+    Strides os;
+    int64_t total;
+    int32_t rows, pack, hu, D;
+    float* delta;
+    const float* rest;
 };
 
 struct Work {
@@ -418,14 +432,21 @@ __device__ __forceinline__ int bucket_of(const Borders& o, int rel) {
 // rel + reach + kPad for rel within reach + kPad of 0. A 32 x 32 tile that
 // touches (-reach, reach) stays inside; all others have one bias.
 constexpr int kPad = 64;
+constexpr int kColBytes = DYT_ATTN_MAX_BUCKETS * 4;   // LDS for the table's column, before the entries
 
 __device__ __forceinline__ int bias_entries(const Borders& o) { return 2 * (o.reach + kPad); }
 
-__device__ __forceinline__ void fill_bias(float* lds, const AttnArgs& a, int head) {
+// `col` has room for the table's column: one load per bucket, then the
+// positions gather from LDS (a dependent global load per position took 6 us
+// of a small problem's kernel). Ends in a barrier's need: the caller's next
+// barrier makes the entries visible.
+__device__ __forceinline__ void fill_bias(float* lds, float* col, const AttnArgs& a, int head) {
     const int n = bias_entries(a.borders);
+    for (int x = (int)threadIdx.x; x < a.buckets; x += (int)blockDim.x)
+        col[x] = load_param(a.table, (int64_t)x * a.Hq + head, a.table_dt) * kLog2e;
+    __syncthreads();
     for (int x = (int)threadIdx.x; x < n; x += (int)blockDim.x)
-        lds[x] = load_param(a.table, (int64_t)bucket_of(a.borders, x - a.borders.reach - kPad) * a.Hq + head,
-                            a.table_dt) * kLog2e;
+        lds[x] = col[bucket_of(a.borders, x - a.borders.reach - kPad)];
 }
 
 __device__ __forceinline__ int acc_row(int i, int h) { return 8 * (i / 4) + 4 * h + (i % 4); }

@@ -44,11 +44,14 @@ __global__ __launch_bounds__(64 * kFinSlices) void ln_finish_kernel(const float*
     }
 }
 
-int ln_bwd_grid(const LnConfig& c, int64_t M) {
+// Workgroups of the backward, each with a partial row of 2 N floats to write
+// and read again: as many as fill the card, while those rows stay near 3% of
+// the activations' traffic (three tensors of M N elements of s bytes:
+// 16 N grid <= 0.03 * 3 M N s).
+int ln_bwd_grid(const LnConfig& c, int64_t M, int64_t elem_bytes) {
     const int64_t need = (M + ln_groups(c) - 1) / ln_groups(c);
-    // one partial row per workgroup: 512 workgroups of 256 threads fill the
-    // card while the rows stay a few per cent of the traffic
-    const int64_t cap = c.threads > 256 || c.threads == 0 ? 256 : 512;
+    const int64_t most = c.threads > 512 || c.threads == 0 ? 256 : 1024;
+    const int64_t cap = std::min(most, std::max<int64_t>(256, M * elem_bytes / 178 / 128 * 128));
     return (int)std::min(need, cap);
 }
 
@@ -71,9 +74,9 @@ int ln_shape(int64_t M, int64_t N, int xdt, int pdt) {
 
 LnPlan ln_plan(int64_t M, int64_t N, int xdt) {
     LnPlan p{};
-    const int vec = xdt == DYT_F32 ? 4 : 8;
-    p.cfg = ln_config((N + vec - 1) / vec, true);
-    p.grid = ln_bwd_grid(p.cfg, M);
+    const int bytes = (int)dtype_size(xdt);
+    p.cfg = ln_config(M, N, bytes, true);
+    p.grid = ln_bwd_grid(p.cfg, M, bytes);
     p.pitch = (2 * N + 31) / 32 * 32;
     p.bytes = (size_t)p.grid * p.pitch * sizeof(float);
     return p;
@@ -104,8 +107,7 @@ int ln_forward(const void* x, int64_t ldx, const void* r, const void* gamma, con
     LnArgs a{};
     a.x = x; a.r = res ? r : nullptr; a.h = h; a.y = y; a.gamma = gamma; a.beta = beta;
     a.mean = mean; a.rstd = rstd; a.ldx = ldx; a.ldy = ldy; a.M = M; a.N = (int32_t)N; a.pdt = pdt; a.eps = eps;
-    const int vec = xdt == DYT_F32 ? 4 : 8;
-    const LnConfig cfg = ln_config((N + vec - 1) / vec, false);
+    const LnConfig cfg = ln_config(M, N, (int)sx, false);
     with_type(xdt, [&](auto* t) {
         ln_launch_forward<std::remove_pointer_t<decltype(t)>>(cfg, a, (hipStream_t)stream);
     });

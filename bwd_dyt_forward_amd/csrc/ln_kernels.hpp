@@ -44,30 +44,73 @@ struct LnArgs {
     int64_t pitch;        // backward: floats between partial rows
 };
 
-// Elements [c, c + VEC) of the row that starts at element `row`; zeros past
-// N. `limit` is one past the tensor's last element: a whole vector is loaded
-// wherever its 16 bytes lie inside the tensor, and what belongs to the next
-// row (or the pitch's gap) is cleared afterwards.
+// The 16 bytes that hold elements [c, c + VEC) of the row that starts at
+// element `row`, without a branch: a load behind one would make every later
+// wait of the loop a wait for all loads. Lanes without elements (past the
+// row, or `on` false) read the tensor's first bytes; where the 16 bytes would
+// end past the tensor's last element (`limit`), the last 16 bytes are read.
+// The tensor has at least VEC elements.
 template <typename T>
-__device__ __forceinline__ void load_vec(const T* p, int64_t row, int c, int N, int64_t limit,
-                                         float* out) {
+__device__ __forceinline__ u32x4 load_raw(const T* p, int64_t row, int c, int N, int64_t limit, bool on) {
     constexpr int VEC = VecOf<T>::n;
-    if (c + VEC <= N) {
-        unpack16<T>(*(const u32x4_m*)(p + row + c), out);
+    const int64_t at = min(row + c, limit - VEC);
+    return *(const u32x4_m*)(p + (on && c < N ? at : 0));
+}
+
+// Those elements as float32, zeros past N: clears what belongs to the next
+// row (or the pitch's gap), and reads the tensor's last elements one by one
+// where load_raw had to stay back.
+template <typename T>
+__device__ __forceinline__ void unpack_raw(u32x4 w, const T* p, int64_t row, int c, int N, int64_t limit, bool on,
+                                           float* out) {
+    constexpr int VEC = VecOf<T>::n;
+    unpack16<T>(w, out);
+    if (N % VEC == 0) {
+        const bool in = on && c < N;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) out[i] = in ? out[i] : 0.0f;
         return;
     }
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) out[i] = 0.0f;
-    if (c >= N) return;
-    if (row + c + VEC <= limit) {
-        unpack16<T>(*(const u32x4_m*)(p + row + c), out);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) out[i] = (c + i < N) ? out[i] : 0.0f;
-    } else {
+    if (on && c < N && row + c + VEC > limit) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
             if (c + i < N) out[i] = to_f32(p[row + c + i]);
     }
+    const int n = on ? N - c : 0;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) out[i] = i < n ? out[i] : 0.0f;
+}
+
+template <typename T>
+__device__ __forceinline__ void load_vec(const T* p, int64_t row, int c, int N, float* out) {
+    constexpr int VEC = VecOf<T>::n;
+    if (c + VEC <= N) {
+        unpack16<T>(*(const u32x4_m*)(p + row + c), out);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) out[i] = c + i < N ? to_f32(p[row + c + i]) : 0.0f;
+    }
+}
+
+// Parameters of the E columns of a thread (0 past N).
+template <int V, int VEC, int TPR>
+__device__ __forceinline__ void load_columns(const void* p, int dt, int t, int N, float* out) {
+#define DYT_COLUMNS(expr)                                   \
+    _Pragma("unroll") for (int v = 0; v < V; ++v)           \
+    _Pragma("unroll") for (int i = 0; i < VEC; ++i) {       \
+        const int c = (t + v * TPR) * VEC + i;              \
+        const int k = min(c, N - 1);                        \
+        const float x = expr;                               \
+        out[v * VEC + i] = c < N ? x : 0.0f;                \
+    }
+    if (dt == DYT_F32) {
+        DYT_COLUMNS(((const float*)p)[k])
+    } else if (dt == DYT_BF16) {
+        DYT_COLUMNS(to_f32(((const bf16_t*)p)[k]))
+    } else {
+        DYT_COLUMNS(to_f32(((const f16_t*)p)[k]))
+    }
+#undef DYT_COLUMNS
 }
 
 template <typename T>
@@ -106,14 +149,8 @@ __global__ __launch_bounds__(LnShape<TPR>::threads) void ln_fwd_kernel(LnArgs a)
     const int g = (int)threadIdx.x / TPR;
     const int N = a.N;
     float gm[E], bt[E];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const int c = (t + v * TPR) * VEC + i;
-            gm[v * VEC + i] = c < N ? load_param(a.gamma, c, a.pdt) : 0.0f;
-            bt[v * VEC + i] = c < N ? load_param(a.beta, c, a.pdt) : 0.0f;
-        }
+    load_columns<V, VEC, TPR>(a.gamma, a.pdt, t, N, gm);
+    load_columns<V, VEC, TPR>(a.beta, a.pdt, t, N, bt);
     const float inv_n = 1.0f / (float)N;
     const int64_t limit = (a.M - 1) * a.ldx + N;
     const int64_t step = (int64_t)gridDim.x * S::groups * U;
@@ -122,35 +159,32 @@ __global__ __launch_bounds__(LnShape<TPR>::threads) void ln_fwd_kernel(LnArgs a)
     for (int64_t base = (int64_t)blockIdx.x * S::groups * U; base < a.M; base += step) {
         float x[U][E];
         float mean[U], m2[U];
+        u32x4 raw[U][V], rres[U][RES ? V : 1];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t m = base + u * S::groups + g;
-            if (m < a.M) {
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    load_vec<T>(xp, m * a.ldx, (t + v * TPR) * VEC, N, limit, &x[u][v * VEC]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e) x[u][e] = 0.0f;
+            for (int v = 0; v < V; ++v) {
+                const int c = (t + v * TPR) * VEC;
+                raw[u][v] = load_raw<T>(xp, m * a.ldx, c, N, limit, m < a.M);
+                if constexpr (RES) rres[u][v] = load_raw<T>((const T*)a.r, m * a.ldx, c, N, limit, m < a.M);
             }
         }
-        if constexpr (RES) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t m = base + u * S::groups + g;
-                if (m < a.M) {
+        for (int u = 0; u < U; ++u) {
+            const int64_t m = base + u * S::groups + g;
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        float r[VEC];
-                        const int c = (t + v * TPR) * VEC;
-                        load_vec<T>((const T*)a.r, m * a.ldx, c, N, limit, r);
+            for (int v = 0; v < V; ++v) {
+                const int c = (t + v * TPR) * VEC;
+                unpack_raw<T>(raw[u][v], xp, m * a.ldx, c, N, limit, m < a.M, &x[u][v * VEC]);
+                if constexpr (RES) {
+                    float r[VEC];
+                    unpack_raw<T>(rres[u][v], (const T*)a.r, m * a.ldx, c, N, limit, m < a.M, r);
 #pragma unroll
-                        for (int i = 0; i < VEC; ++i) r[i] += x[u][v * VEC + i];
-                        store_vec<T>((T*)a.h, m * a.ldx, c, N, r);
-                        // the layer's input is h as stored
-                        const u32x4 w = pack16<T>(r);
-                        unpack16<T>(w, &x[u][v * VEC]);
-                    }
+                    for (int i = 0; i < VEC; ++i) r[i] += x[u][v * VEC + i];
+                    if (m < a.M) store_vec<T>((T*)a.h, m * a.ldx, c, N, r);
+                    // the layer's input is h as stored
+                    unpack16<T>(pack16<T>(r), &x[u][v * VEC]);
                 }
             }
         }
@@ -261,17 +295,16 @@ __global__ __launch_bounds__(kLongThreads) void ln_fwd_long_kernel(LnArgs a) {
     constexpr int VEC = VecOf<T>::n;
     __shared__ float red[kLongThreads / 64];
     const int N = a.N;
-    const int64_t limit = (a.M - 1) * a.ldx + N;
     const float inv_n = 1.0f / (float)N;
     for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
         const T* src = (const T*)a.x;
         float s = 0.0f;
         for (int c = (int)threadIdx.x * VEC; c < N; c += kLongThreads * VEC) {
             float x[VEC];
-            load_vec<T>(src, m * a.ldx, c, N, limit, x);
+            load_vec<T>(src, m * a.ldx, c, N, x);
             if constexpr (RES) {
                 float r[VEC];
-                load_vec<T>((const T*)a.r, m * a.ldx, c, N, limit, r);
+                load_vec<T>((const T*)a.r, m * a.ldx, c, N, r);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) r[i] += x[i];
                 store_vec<T>((T*)a.h, m * a.ldx, c, N, r);
@@ -285,7 +318,7 @@ __global__ __launch_bounds__(kLongThreads) void ln_fwd_long_kernel(LnArgs a) {
         float q = 0.0f;
         for (int c = (int)threadIdx.x * VEC; c < N; c += kLongThreads * VEC) {
             float x[VEC];
-            load_vec<T>(src, m * a.ldx, c, N, limit, x);
+            load_vec<T>(src, m * a.ldx, c, N, x);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 const float d = x[i] - mean;
@@ -295,7 +328,7 @@ __global__ __launch_bounds__(kLongThreads) void ln_fwd_long_kernel(LnArgs a) {
         const float rs = inv_sqrt(block_sum(q, red) * inv_n + a.eps);
         for (int c = (int)threadIdx.x * VEC; c < N; c += kLongThreads * VEC) {
             float x[VEC];
-            load_vec<T>(src, m * a.ldx, c, N, limit, x);
+            load_vec<T>(src, m * a.ldx, c, N, x);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 const int k = min(c + i, N - 1);
@@ -311,7 +344,11 @@ __global__ __launch_bounds__(kLongThreads) void ln_fwd_long_kernel(LnArgs a) {
     }
 }
 
-template <typename T, int TPR, int V, bool RES>
+// U row groups at a time, and (AHEAD) the next U rows' vectors are loaded,
+// still packed, before the current ones are reduced, so that a workgroup's
+// loads do not wait for its sums. Workgroups of 1,024 threads have only 128
+// registers each and go without.
+template <typename T, int TPR, int V, int U, bool RES, bool AHEAD = (TPR < 1024)>
 __global__ __launch_bounds__(LnShape<TPR>::threads) void ln_bwd_kernel(LnArgs a) {
     using S = LnShape<TPR>;
     constexpr int VEC = VecOf<T>::n;
@@ -320,85 +357,113 @@ __global__ __launch_bounds__(LnShape<TPR>::threads) void ln_bwd_kernel(LnArgs a)
     const int g = (int)threadIdx.x / TPR;
     const int N = a.N;
     float gm[E], ag[E], ab[E];
+    load_columns<V, VEC, TPR>(a.gamma, a.pdt, t, N, gm);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const int c = (t + v * TPR) * VEC + i;
-            gm[v * VEC + i] = c < N ? load_param(a.gamma, c, a.pdt) : 0.0f;
-            ag[v * VEC + i] = 0.0f;
-            ab[v * VEC + i] = 0.0f;
-        }
+    for (int e = 0; e < E; ++e) ag[e] = ab[e] = 0.0f;
     const float inv_n = 1.0f / (float)N;
     const int64_t limit = (a.M - 1) * a.ldx + N;
     const int64_t limit_dy = (a.M - 1) * a.lddy + N;
-    const int64_t step = (int64_t)gridDim.x * S::groups;
-    for (int64_t base = (int64_t)blockIdx.x * S::groups; base < a.M; base += step) {
-        const int64_t m = base + g;
+    const int64_t step = (int64_t)gridDim.x * S::groups * U;
+    struct Raw {
+        u32x4 x[V], dy[V], res[RES ? V : 1];
+        float mean, rs;
+    };
+    const auto load = [&](int64_t m, Raw& w) {
         const bool on = m < a.M;
-        float x[E], dy[E], res[RES ? E : 1];
-        float mean = 0.0f, rs = 0.0f;
-        if (on) {
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                load_vec<T>((const T*)a.x, m * a.ldx, (t + v * TPR) * VEC, N, limit, &x[v * VEC]);
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                load_vec<T>((const T*)a.dy, m * a.lddy, (t + v * TPR) * VEC, N, limit_dy, &dy[v * VEC]);
-            if constexpr (RES) {
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    load_vec<T>((const T*)a.dres, m * a.ldx, (t + v * TPR) * VEC, N, limit, &res[v * VEC]);
-            }
-            mean = a.mean[m];
-            rs = a.rstd[m];
-        } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = dy[e] = 0.0f;
+        for (int v = 0; v < V; ++v) {
+            const int c = (t + v * TPR) * VEC;
+            w.x[v] = load_raw<T>((const T*)a.x, m * a.ldx, c, N, limit, on);
+            w.dy[v] = load_raw<T>((const T*)a.dy, m * a.lddy, c, N, limit_dy, on);
+            if constexpr (RES) w.res[v] = load_raw<T>((const T*)a.dres, m * a.ldx, c, N, limit, on);
         }
-        float s1 = 0.0f, s2 = 0.0f;
+        w.mean = a.mean[on ? m : 0];
+        w.rs = a.rstd[on ? m : 0];
+    };
+    Raw next[U];
+    int64_t base = (int64_t)blockIdx.x * S::groups * U;
+    if constexpr (AHEAD) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            // past the row's end x is 0, not the mean: dy = gamma = 0 there
-            // keeps the sums clean and the columns are never stored
-            const float n = (x[e] - mean) * rs;
-            const float d = dy[e] * gm[e];
-            ag[e] += dy[e] * n;
-            ab[e] += dy[e];
-            s1 += d;
-            s2 += d * n;
-            x[e] = n;
-        }
-        s1 = lanes_sum<S::L>(s1);
-        s2 = lanes_sum<S::L>(s2);
-        if constexpr (S::waves > 1) {
-            __shared__ float red[2][S::groups][S::waves][2];
-            const int buf = (int)((base / step) & 1);
-            if ((t & 63) == 0) {
-                red[buf][g][t >> 6][0] = s1;
-                red[buf][g][t >> 6][1] = s2;
-            }
-            __syncthreads();
-            s1 = s2 = 0.0f;
+        for (int u = 0; u < U; ++u) load(base + u * S::groups + g, next[u]);
+    }
+    for (int buf = 0; base < a.M; base += step, buf ^= 1) {
+        Raw now[U];
 #pragma unroll
-            for (int k = 0; k < S::waves; ++k) {
-                s1 += red[buf][g][k][0];
-                s2 += red[buf][g][k][1];
-            }
+        for (int u = 0; u < U; ++u) {
+            if constexpr (AHEAD) now[u] = next[u];
+            else load(base + u * S::groups + g, now[u]);
         }
-        if (on) {
-            const float c1 = s1 * inv_n, c2 = s2 * inv_n;
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) load(base + step + u * S::groups + g, next[u]);
+        }
+        float n[U][E], dy[U][E], s1[U], s2[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float o[VEC];
+                const int64_t m = base + u * S::groups + g;
+                const int c = (t + v * TPR) * VEC;
+                unpack_raw<T>(now[u].x[v], (const T*)a.x, m * a.ldx, c, N, limit, m < a.M, &n[u][v * VEC]);
+                unpack_raw<T>(now[u].dy[v], (const T*)a.dy, m * a.lddy, c, N, limit_dy, m < a.M, &dy[u][v * VEC]);
+            }
+            s1[u] = s2[u] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                // past the row's end x is 0, not the mean: dy = gamma = 0 there
+                // keeps the sums clean and the columns are never stored
+                const float x = (n[u][e] - now[u].mean) * now[u].rs;
+                const float d = dy[u][e] * gm[e];
+                ag[e] = __builtin_fmaf(dy[u][e], x, ag[e]);
+                ab[e] += dy[u][e];
+                s1[u] += d;
+                s2[u] = __builtin_fmaf(d, x, s2[u]);
+                n[u][e] = x;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            s1[u] = lanes_sum<S::L>(s1[u]);
+            s2[u] = lanes_sum<S::L>(s2[u]);
+        }
+        if constexpr (S::waves > 1) {
+            __shared__ float red[2][U][S::groups][S::waves][2];
+            if ((t & 63) == 0) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    red[buf][u][g][t >> 6][0] = s1[u];
+                    red[buf][u][g][t >> 6][1] = s2[u];
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                s1[u] = s2[u] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < S::waves; ++k) {
+                    s1[u] += red[buf][u][g][k][0];
+                    s2[u] += red[buf][u][g][k][1];
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t m = base + u * S::groups + g;
+            if (m >= a.M) continue;
+            const float c1 = s1[u] * inv_n, c2 = s2[u] * inv_n;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float o[VEC], res[VEC];
+                const int c = (t + v * TPR) * VEC;
+                if constexpr (RES) unpack_raw<T>(now[u].res[v], (const T*)a.dres, m * a.ldx, c, N, limit, true, res);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     const int e = v * VEC + i;
-                    const float d = dy[e] * gm[e];
-                    o[i] = rs * (d - c1 - x[e] * c2);
-                    if constexpr (RES) o[i] += res[e];
+                    const float d = dy[u][e] * gm[e];
+                    o[i] = now[u].rs * (d - c1 - n[u][e] * c2);
+                    if constexpr (RES) o[i] += res[i];
                 }
-                store_vec<T>((T*)a.y, m * a.ldy, (t + v * TPR) * VEC, N, o);
+                store_vec<T>((T*)a.y, m * a.ldy, c, N, o);
             }
         }
     }
@@ -444,8 +509,6 @@ __global__ __launch_bounds__(kLongThreads) void ln_bwd_long_kernel(LnArgs a) {
     constexpr int VEC = VecOf<T>::n;
     __shared__ float red[kLongThreads / 64];
     const int N = a.N;
-    const int64_t limit = (a.M - 1) * a.ldx + N;
-    const int64_t limit_dy = (a.M - 1) * a.lddy + N;
     const float inv_n = 1.0f / (float)N;
     float* row = a.part + (int64_t)blockIdx.x * a.pitch;
     for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
@@ -454,8 +517,8 @@ __global__ __launch_bounds__(kLongThreads) void ln_bwd_long_kernel(LnArgs a) {
         float s1 = 0.0f, s2 = 0.0f;
         for (int c = (int)threadIdx.x * VEC; c < N; c += kLongThreads * VEC) {
             float x[VEC], dy[VEC];
-            load_vec<T>((const T*)a.x, m * a.ldx, c, N, limit, x);
-            load_vec<T>((const T*)a.dy, m * a.lddy, c, N, limit_dy, dy);
+            load_vec<T>((const T*)a.x, m * a.ldx, c, N, x);
+            load_vec<T>((const T*)a.dy, m * a.lddy, c, N, dy);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 const int k = min(c + i, N - 1);
@@ -468,9 +531,9 @@ __global__ __launch_bounds__(kLongThreads) void ln_bwd_long_kernel(LnArgs a) {
         const float c2 = block_sum(s2, red) * inv_n;
         for (int c = (int)threadIdx.x * VEC; c < N; c += kLongThreads * VEC) {
             float x[VEC], dy[VEC], res[VEC], o[VEC];
-            load_vec<T>((const T*)a.x, m * a.ldx, c, N, limit, x);
-            load_vec<T>((const T*)a.dy, m * a.lddy, c, N, limit_dy, dy);
-            if constexpr (RES) load_vec<T>((const T*)a.dres, m * a.ldx, c, N, limit, res);
+            load_vec<T>((const T*)a.x, m * a.ldx, c, N, x);
+            load_vec<T>((const T*)a.dy, m * a.lddy, c, N, dy);
+            if constexpr (RES) load_vec<T>((const T*)a.dres, m * a.ldx, c, N, res);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 if (c + i >= N) continue;

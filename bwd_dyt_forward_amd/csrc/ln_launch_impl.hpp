@@ -47,38 +47,50 @@ void ln_launch_forward(const LnConfig& c, const LnArgs& a, hipStream_t s) {
         case 256 * 8 + 2: return ln_fwd_pick<T, 256, 2, 1>(a, s);
         case 256 * 8 + 4: return ln_fwd_pick<T, 256, 4, 1>(a, s);
         case 512 * 8 + 4: return ln_fwd_pick<T, 512, 4, 1>(a, s);
-        case 1024 * 8 + 4: return ln_fwd_pick<T, 1024, 4, 1>(a, s);
         default: break;
+    }
+    if constexpr (sizeof(T) == 4) {
+        if (c.threads == 1024) return ln_fwd_pick<T, 1024, 4, 1>(a, s);
     }
     const int grid = (int)std::min<int64_t>(a.M, 512);
     if (a.r) ln_fwd_long_kernel<T, true><<<grid, kLongThreads, 0, s>>>(a);
     else ln_fwd_long_kernel<T, false><<<grid, kLongThreads, 0, s>>>(a);
 }
 
-template <typename T, int TPR, int V>
+template <typename T, int TPR, int V, int U>
 void ln_bwd_one(int grid, const LnArgs& a, hipStream_t s) {
     using S = LnShape<TPR>;
-    if (a.dres) ln_bwd_kernel<T, TPR, V, true><<<grid, S::threads, 0, s>>>(a);
-    else ln_bwd_kernel<T, TPR, V, false><<<grid, S::threads, 0, s>>>(a);
+    if (a.dres) ln_bwd_kernel<T, TPR, V, U, true><<<grid, S::threads, 0, s>>>(a);
+    else ln_bwd_kernel<T, TPR, V, U, false><<<grid, S::threads, 0, s>>>(a);
+}
+
+// U rows per thread at a time where a row is one vector and every workgroup
+// has several rounds of them.
+template <typename T, int TPR>
+void ln_bwd_pick(int grid, const LnArgs& a, hipStream_t s) {
+    if (a.M >= (int64_t)grid * LnShape<TPR>::groups * 4) return ln_bwd_one<T, TPR, 1, 2>(grid, a, s);
+    ln_bwd_one<T, TPR, 1, 1>(grid, a, s);
 }
 
 template <typename T>
 void ln_launch_backward(const LnConfig& c, int grid, const LnArgs& a, hipStream_t s) {
     switch (c.threads * 8 + c.vecs) {
-        case 1 * 8 + 1: return ln_bwd_one<T, 1, 1>(grid, a, s);
-        case 2 * 8 + 1: return ln_bwd_one<T, 2, 1>(grid, a, s);
-        case 4 * 8 + 1: return ln_bwd_one<T, 4, 1>(grid, a, s);
-        case 8 * 8 + 1: return ln_bwd_one<T, 8, 1>(grid, a, s);
-        case 16 * 8 + 1: return ln_bwd_one<T, 16, 1>(grid, a, s);
-        case 32 * 8 + 1: return ln_bwd_one<T, 32, 1>(grid, a, s);
-        case 64 * 8 + 1: return ln_bwd_one<T, 64, 1>(grid, a, s);
-        case 64 * 8 + 2: return ln_bwd_one<T, 64, 2>(grid, a, s);
-        case 128 * 8 + 2: return ln_bwd_one<T, 128, 2>(grid, a, s);
-        case 256 * 8 + 2: return ln_bwd_one<T, 256, 2>(grid, a, s);
-        case 512 * 8 + 2: return ln_bwd_one<T, 512, 2>(grid, a, s);
-        case 1024 * 8 + 2: return ln_bwd_one<T, 1024, 2>(grid, a, s);
-        case 1024 * 8 + 4: return ln_bwd_one<T, 1024, 4>(grid, a, s);
+        case 1 * 8 + 1: return ln_bwd_pick<T, 1>(grid, a, s);
+        case 2 * 8 + 1: return ln_bwd_pick<T, 2>(grid, a, s);
+        case 4 * 8 + 1: return ln_bwd_pick<T, 4>(grid, a, s);
+        case 8 * 8 + 1: return ln_bwd_pick<T, 8>(grid, a, s);
+        case 16 * 8 + 1: return ln_bwd_pick<T, 16>(grid, a, s);
+        case 32 * 8 + 1: return ln_bwd_pick<T, 32>(grid, a, s);
+        case 64 * 8 + 1: return ln_bwd_pick<T, 64>(grid, a, s);
+        case 64 * 8 + 2: return ln_bwd_one<T, 64, 2, 1>(grid, a, s);
+        case 128 * 8 + 2: return ln_bwd_one<T, 128, 2, 1>(grid, a, s);
+        case 256 * 8 + 2: return ln_bwd_one<T, 256, 2, 1>(grid, a, s);
+        case 512 * 8 + 2: return ln_bwd_one<T, 512, 2, 1>(grid, a, s);
+        case 1024 * 8 + 2: return ln_bwd_one<T, 1024, 2, 1>(grid, a, s);
         default: break;
+    }
+    if constexpr (sizeof(T) == 4) {
+        if (c.threads == 1024) return ln_bwd_one<T, 1024, 4, 1>(grid, a, s);
     }
     if (a.dres) ln_bwd_long_kernel<T, true><<<grid, kLongThreads, 0, s>>>(a);
     else ln_bwd_long_kernel<T, false><<<grid, kLongThreads, 0, s>>>(a);
