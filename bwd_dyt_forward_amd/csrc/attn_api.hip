@@ -13,18 +13,35 @@
 
 namespace dytb {
 
-// dtable[t, head]: the workgroups' values of bucket t, batch entry by batch
-// entry. A wave per (head, bucket).
-__global__ __launch_bounds__(64) void attn_dtable_kernel(const float* part, int B, int Hq, int per_unit, int buckets,
-                                                         void* dtable, int dt) {
+// dtable[t, head]: bucket t's run of positions in the rows of the head's
+// workgroups, batch entry by batch entry. A workgroup per (head, bucket); the
+// order of the sum depends on the shape alone.
+constexpr int kTableThreads = 256;
+
+__global__ __launch_bounds__(kTableThreads) void attn_dtable_kernel(const float* part, int B, int Hq, int per_unit,
+                                                                    int buckets, Borders o, void* dtable, int dt) {
+    __shared__ float red[kTableThreads / 64];
     const int head = (int)blockIdx.x / buckets, t = (int)blockIdx.x - head * buckets;
+    int lo, hi;
+    bucket_range(o, t, lo, hi);
+    const int entries = bias_entries(o), run = max(hi - lo, 0);
     float s = 0.0f;
-    for (int x = (int)threadIdx.x; x < B * per_unit; x += 64) {
+    // rows of the head: a wave (or a part of one) along each row's run
+    const int width = run <= 8 ? 8 : run <= 32 ? 32 : 64;
+    const int lane = (int)threadIdx.x % width, side = kTableThreads / width;
+#pragma unroll 4
+    for (int x = (int)threadIdx.x / width; x < B * per_unit; x += side) {
         const int b = x / per_unit, k = x - b * per_unit;
-        s += part[(((int64_t)b * Hq + head) * per_unit + k) * buckets + t];
+        const float* row = part + (((int64_t)b * Hq + head) * per_unit + k) * entries + lo;
+        for (int i = lane; i < run; i += width) s += row[i];
     }
     s = lanes_sum<64>(s);
-    if (threadIdx.x == 0) store_param(dtable, (int64_t)t * Hq + head, dt, s);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int k = 1; k < kTableThreads / 64; ++k) s += red[k];
+        store_param(dtable, (int64_t)t * Hq + head, dt, s);
+    }
 }
 
 namespace {
@@ -90,10 +107,10 @@ bool view(const dyt_attn_desc& d, const Tensor& t, bool out, Strides& s, int64_t
 }
 
 // Whether a tensor takes 16-byte accesses: aligned base, strides and rows,
-// and (streamed tensors) a tile's rows within a 32-bit offset.
-bool vec_ok(const void* p, const Strides& s, int64_t row_bytes, int64_t pack) {
+// and a tile's rows (64 positions of up to 32 heads) within a 31-bit offset.
+bool vec_ok(const void* p, const Strides& s, int64_t row_bytes) {
     if ((uintptr_t)p % 16 || s.b % 16 || s.s % 16 || s.h % 16 || row_bytes % 16) return false;
-    return s.s < ((int64_t)1 << 24) && s.h <= ((int64_t)1 << 30) / pack;
+    return s.s < ((int64_t)1 << 24) && s.h < ((int64_t)1 << 25);
 }
 
 struct Plan {
@@ -119,19 +136,23 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 // workgroups, with the long axis cut into runs of 1,024, would fill the 256
 // CUs, and single waves below (and for up to 32 rows, one wave's). The
 // number of splits is then the power of two that minimises
-//   tiles per split * waves per SIMD (at least 1) * 0.6 us
-//   + 6 us for the join's launch and 0.1 us for each part it reads.
-void choose(int64_t units, int64_t rows, int64_t len, int tile4, int& nw, int& blocks, int& split, int& per) {
+//   tiles per split * max(lat, waves per SIMD * busy)
+//   + 6 us for the join's launch and 0.1 us for each part it reads:
+// a wave alone on its SIMD takes `lat` for 32 steps of the long axis (the
+// chain of loads, products and exponentials), and a SIMD is `busy` with them.
+void choose(int64_t units, int64_t rows, int64_t len, int pack, int tile4, double lat, double busy, AttnPick& pick,
+            int& blocks, int& split, int& per) {
     const int64_t b4 = units * ((rows + 127) / 128);
-    nw = rows > 32 && b4 * std::max<int64_t>(1, len / 1024) >= 256 ? 4 : 1;
-    const int tile = nw == 4 ? tile4 : 32;
+    int& nw = pick.nw;
+    nw = pick.vec && rows > 32 && b4 * std::max<int64_t>(1, len / 1024) >= 256 ? 4 : 1;
+    const int tile = (nw == 4 ? tile4 : 32) / pack * pack;   // whole positions of the long axis' rows
     blocks = ceil_div(rows, 32 * nw);
     const double waves = (double)units * blocks * nw;
     const int64_t tiles = std::max<int64_t>(1, ceil_div(len, tile));
     double best = 0.0;
     int64_t parts = 1;
     for (int64_t n = 1; n == 1 || (n <= 64 && n * 4 <= tiles); n *= 2) {
-        const double t = ceil_div(tiles, n) * (tile / 32) * std::max(1.0, waves * n / 1024.0) * 0.6 +
+        const double t = ceil_div(tiles, n) * ((tile + 31) / 32) * std::max(lat, waves * n / 1024.0 * busy) +
                          (n > 1 ? 6.0 + 0.1 * n : 0.0);
         if (n == 1 || t < best) {
             best = t;
@@ -144,7 +165,8 @@ void choose(int64_t units, int64_t rows, int64_t len, int tile4, int& nw, int& b
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-Plan make_plan(const dyt_attn_desc& d) {
+// vec: whether every tensor takes 16-byte accesses (single waves otherwise).
+Plan make_plan(const dyt_attn_desc& d, bool vec) {
     Plan p{};
     p.status = DYT_ERR_INVALID_ARG;
     if (d.B < 0 || d.Sq < 0 || d.Sk < 0 || d.Hq < 0 || d.Hkv < 1 || d.D < 1 || d.D > DYT_ATTN_MAX_D) return p;
@@ -160,25 +182,34 @@ Plan make_plan(const dyt_attn_desc& d) {
     if (d.table && fill_borders(d.num_buckets, d.max_distance, d.bidirectional, p.borders)) return p;
     p.nothing_out = d.B == 0 || d.Sq == 0 || d.Hq == 0;
     p.nothing_keys = d.B == 0 || d.Sk == 0;
-    // the rows of a unit: all heads of a group, unless each needs its own
-    // column of the table, or the group is too large for the row division
-    p.pack = d.table || G > 256 || G < 1 ? 1 : (int)G;
+    // the rows of a unit: all heads of a group (or a 32-row tile's worth, the
+    // largest divisor), unless each needs its own column of the table
+    p.pack = 1;
+    if (!d.table)
+        for (int n = 2; n <= 32 && n <= G; ++n)
+            if (G % n == 0) p.pack = n;
     p.units = (int)(d.B * (d.Hq / p.pack));
     p.rows = d.Sq * p.pack;
     const int dp = attn_dp(d.D), tile = d.dtype == DYT_F32 ? 32 : 64;
-    p.fwd = p.dq = p.dkv = {dp, 1, d.table != nullptr};
+    p.fwd = p.dq = p.dkv = {dp, 1, d.table != nullptr, vec};
+    // us per 32 keys (rows), measured at D = 32 (float32: the matrix cores'
+    // rate) and, 16-bit, much the same up to 128
+    const double f = d.dtype == DYT_F32 ? 2.2 * dp / 32 : 0.0;
     if (!p.nothing_out) {
-        choose(p.units, p.rows, d.Sk, tile, p.fwd.nw, p.fwd_blocks, p.fwd_split, p.fwd_per);
-        choose(p.units, p.rows, d.Sk, tile, p.dq.nw, p.dq_blocks, p.dq_split, p.dq_per);
+        choose(p.units, p.rows, d.Sk, 1, tile, std::max(f, 0.8), std::max(f, 0.4), p.fwd, p.fwd_blocks, p.fwd_split,
+               p.fwd_per);
+        choose(p.units, p.rows, d.Sk, 1, tile, std::max(1.2 * f, 0.9), std::max(1.2 * f, 0.6), p.dq, p.dq_blocks,
+               p.dq_split, p.dq_per);
     }
     if (!p.nothing_keys && d.Hq > 0)
-        choose(p.units, d.Sk, p.rows, tile, p.dkv.nw, p.dkv_blocks, p.dkv_split, p.dkv_per);
+        choose(p.units, d.Sk, p.rows, p.pack, attn_dkv_tile(d.dtype, dp), std::max(1.7 * f, 1.2), std::max(1.7 * f, 0.9),
+               p.dkv, p.dkv_blocks, p.dkv_split, p.dkv_per);
     const int64_t part_rows = p.units * p.rows * (int64_t)dp * 4;
     if (p.fwd_split > 1) p.fwd_bytes = round256((size_t)p.fwd_split * part_rows) + (size_t)p.fwd_split * p.units * p.rows * 8;
     p.per_unit = p.dkv_blocks * p.dkv_split;
     p.off_rest = round256((size_t)2 * d.B * d.Hq * d.Sq * 4);
     p.off_tpart = p.off_rest + (p.dq_split > 1 ? round256((size_t)p.dq_split * d.B * d.Hq * d.Sq * 4) : 0);
-    p.off_part = p.off_tpart + (d.table ? round256((size_t)p.units * p.per_unit * d.num_buckets * 4) : 0);
+    p.off_part = p.off_tpart + (d.table ? round256((size_t)p.units * p.per_unit * 2 * (p.borders.reach + kPad) * 4) : 0);
     p.dkv_parts = p.dkv_split * (int)(d.Hq > 0 ? G / p.pack : 1);
     size_t part = p.dq_split > 1 ? (size_t)p.dq_split * part_rows : 0;
     if (p.dkv_parts > 1) part = std::max(part, (size_t)p.dkv_parts * 2 * d.B * d.Hkv * d.Sk * dp * 4);
@@ -201,7 +232,6 @@ void fill_args(const dyt_attn_desc& d, const Plan& p, AttnArgs& a) {
     a.B = (int)d.B; a.Sq = (int)d.Sq; a.Sk = (int)d.Sk; a.Hq = (int)d.Hq; a.Hkv = (int)d.Hkv; a.D = (int)d.D;
     a.G = (int)std::max<int64_t>(d.Hq / d.Hkv, 1);
     a.pack = p.pack;
-    a.magic = ((1 << 20) + p.pack - 1) / p.pack;
     a.units = p.units;
     a.causal = d.causal;
     a.table_dt = d.table_dtype;
@@ -234,30 +264,30 @@ int dyt_attn_bucket_borders(int num_buckets, int max_distance, int bidirectional
 
 size_t dyt_attn_forward_workspace_size(const dyt_attn_desc* desc) {
     if (!desc) return 0;
-    const Plan p = make_plan(*desc);
-    return p.status || p.nothing_out ? 0 : p.fwd_bytes;
+    const Plan p = make_plan(*desc, true);
+    return p.status || p.nothing_out ? 0 : std::max(p.fwd_bytes, make_plan(*desc, false).fwd_bytes);
 }
 
 size_t dyt_attn_backward_workspace_size(const dyt_attn_desc* desc) {
     if (!desc) return 0;
-    const Plan p = make_plan(*desc);
-    return p.status ? 0 : p.bwd_bytes;
+    const Plan p = make_plan(*desc, true);
+    return p.status ? 0 : std::max(p.bwd_bytes, make_plan(*desc, false).bwd_bytes);
 }
 
 int dyt_attn_forward(const dyt_attn_desc* desc, const void* q, const void* k, const void* v, void* o, float* stats,
                      void* workspace, size_t workspace_bytes, void* stream) {
     if (!desc) return DYT_ERR_INVALID_ARG;
     const dyt_attn_desc& d = *desc;
-    const Plan p = make_plan(d);
-    if (p.status) return p.status;
+    if (int st = make_plan(d, true).status) return st;
     AttnArgs a{};
     Spans n{};
     if (!view(d, {d.Sq, d.Hq, &d.q}, false, a.qs, n.q) || !view(d, {d.Sk, d.Hkv, &d.k}, false, a.ks, n.k) ||
         !view(d, {d.Sk, d.Hkv, &d.v}, false, a.vs, n.v) || !view(d, {d.Sq, d.Hq, &d.o}, true, a.os, n.o))
         return DYT_ERR_INVALID_ARG;
+    const int64_t es = dtype_size(d.dtype), row = d.D * es;
+    const Plan p = make_plan(d, vec_ok(q, a.qs, row) && vec_ok(k, a.ks, row) && vec_ok(v, a.vs, row) && vec_ok(o, a.os, row));
     if (p.nothing_out) return DYT_OK;
     if (!q || !o || !stats || (d.Sk > 0 && (!k || !v))) return DYT_ERR_INVALID_ARG;
-    const int64_t es = dtype_size(d.dtype), row = d.D * es;
     if (d.Sk == 0) n.k = n.v = 0;
     if (!aligned({q, k, v, o}, es) || !aligned({stats}, 4) || !lists_aligned(d)) return DYT_ERR_MISALIGNED;
     if (p.fwd_bytes && (!workspace || workspace_bytes < p.fwd_bytes)) return DYT_ERR_WORKSPACE_TOO_SMALL;
@@ -268,8 +298,6 @@ int dyt_attn_forward(const dyt_attn_desc* desc, const void* q, const void* k, co
     if (!disjoint(in, 6, out, 3)) return DYT_ERR_INVALID_ARG;
     fill_args(d, p, a);
     a.q = (const char*)q; a.k = (const char*)k; a.v = (const char*)v; a.out = (char*)o; a.stats = stats;
-    a.vec_q = vec_ok(q, a.qs, row, p.pack); a.vec_k = vec_ok(k, a.ks, row, 1); a.vec_v = vec_ok(v, a.vs, row, 1);
-    a.vec_out = vec_ok(o, a.os, row, 1);
     a.blocks = p.fwd_blocks; a.nsplit = p.fwd_split; a.per_split = p.fwd_per;
     a.part = (float*)workspace;
     a.part_ml = (float*)((char*)workspace + round256((size_t)p.fwd_split * p.units * p.rows * p.fwd.dp * 4));
@@ -283,8 +311,7 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
                       void* workspace, size_t workspace_bytes, void* stream) {
     if (!desc) return DYT_ERR_INVALID_ARG;
     const dyt_attn_desc& d = *desc;
-    const Plan p = make_plan(d);
-    if (p.status) return p.status;
+    if (int st = make_plan(d, true).status) return st;
     AttnArgs a{};
     Spans n{};
     if (!view(d, {d.Sq, d.Hq, &d.q}, false, a.qs, n.q) || !view(d, {d.Sk, d.Hkv, &d.k}, false, a.ks, n.k) ||
@@ -292,12 +319,15 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
         !view(d, {d.Sq, d.Hq, &d.dout}, false, a.dos, n.dout) || !view(d, {d.Sq, d.Hq, &d.dq}, true, a.dqs, n.dq) ||
         !view(d, {d.Sk, d.Hkv, &d.dk}, true, a.dks, n.dk) || !view(d, {d.Sk, d.Hkv, &d.dv}, true, a.dvs, n.dv))
         return DYT_ERR_INVALID_ARG;
+    const int64_t es = dtype_size(d.dtype), row = d.D * es, ts = d.table ? dtype_size(d.table_dtype) : 1;
+    const Plan p = make_plan(d, vec_ok(q, a.qs, row) && vec_ok(k, a.ks, row) && vec_ok(v, a.vs, row) &&
+                                    vec_ok(o, a.os, row) && vec_ok(dout, a.dos, row) && vec_ok(dq, a.dqs, row) &&
+                                    vec_ok(dk, a.dks, row) && vec_ok(dv, a.dvs, row));
     if (p.nothing_out) n.q = n.o = n.dout = n.dq = 0;
     if (p.nothing_keys) n.k = n.v = n.dk = n.dv = 0;
     if (!p.nothing_out && (!q || !o || !dout || !stats || !dq)) return DYT_ERR_INVALID_ARG;
     if (!p.nothing_keys && (!k || !v || !dk || !dv)) return DYT_ERR_INVALID_ARG;
     if (d.table && !dtable) return DYT_ERR_INVALID_ARG;
-    const int64_t es = dtype_size(d.dtype), row = d.D * es, ts = d.table ? dtype_size(d.table_dtype) : 1;
     if (!aligned({q, k, v, o, dout, dq, dk, dv}, es) || !aligned({stats}, 4) || !lists_aligned(d) ||
         (d.table && !aligned({dtable}, ts)))
         return DYT_ERR_MISALIGNED;
@@ -324,8 +354,6 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
     a.dout = (const char*)dout; a.dq = (char*)dq; a.dk = (char*)dk; a.dv = (char*)dv;
     a.stats = const_cast<float*>(stats);
     a.dtable = dtable;
-    a.vec_q = vec_ok(q, a.qs, row, p.pack); a.vec_k = vec_ok(k, a.ks, row, 1); a.vec_v = vec_ok(v, a.vs, row, 1);
-    a.vec_o = vec_ok(o, a.os, row, 1); a.vec_do = vec_ok(dout, a.dos, row, p.pack);
     a.rows = (float*)workspace;
     a.rest = (float*)((char*)workspace + p.off_rest);
     a.tpart = (float*)((char*)workspace + p.off_tpart);
@@ -334,41 +362,38 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
         typedef std::remove_pointer_t<decltype(t)> T;
         const int dp = p.dq.dp;
         if (!p.nothing_out) {
-            a.vec_out = vec_ok(dq, a.dqs, row, 1);
             a.blocks = p.dq_blocks; a.nsplit = p.dq_split; a.per_split = p.dq_per;
             if (int st = attn_launch_dq<T>(p.dq, a, s)) return st;
             if (p.dq_split > 1) {
                 const int64_t total = (int64_t)p.units * p.rows;
-                attn_launch_sum<T>(dp, {a.part, total * dp, p.dq_split, (char*)dq, a.dqs, total, (int)p.rows, p.pack,
-                                        (int)(d.Hq / p.pack), (int)d.D, a.rows + (int64_t)d.B * d.Hq * d.Sq, a.rest}, s);
+                SumArgs sum{};
+                sum.part = a.part; sum.stride = total * dp; sum.parts = p.dq_split;
+                sum.out = (char*)dq; sum.os = a.dqs; sum.total = total; sum.rows = (int)p.rows; sum.pack = p.pack;
+                sum.hu = (int)(d.Hq / p.pack); sum.D = (int)d.D;
+                sum.delta = a.rows + (int64_t)d.B * d.Hq * d.Sq;
+                sum.rest = a.rest;
+                attn_launch_sum<T>(dp, sum, s);
             }
         }
         if (!p.nothing_keys) {
             const int64_t total = d.B * d.Hkv * d.Sk, stride = 2 * total * dp;
-            const SumArgs sk = {a.part, stride, p.dkv_parts, (char*)dk, a.dks, total, (int)d.Sk, 1, (int)d.Hkv, (int)d.D, nullptr, nullptr};
-            SumArgs sv = sk;
-            sv.part = a.part + total * dp;
-            sv.out = (char*)dv;
-            sv.os = a.dvs;
-            if (d.Hq == 0) {   // no head reads these keys: zeros
-                SumArgs zk = sk, zv = sv;
-                zk.parts = zv.parts = 0;
-                attn_launch_sum<T>(dp, zk, s);
-                attn_launch_sum<T>(dp, zv, s);
+            SumArgs sums{};
+            sums.part = a.part; sums.stride = stride; sums.parts = d.Hq ? p.dkv_parts : 0;   // no head: zeros
+            sums.out = (char*)dk; sums.os = a.dks; sums.total = total; sums.rows = (int)d.Sk; sums.pack = 1;
+            sums.hu = (int)d.Hkv; sums.D = (int)d.D;
+            sums.part2 = a.part + total * dp; sums.out2 = (char*)dv; sums.os2 = a.dvs;
+            if (d.Hq == 0) {
+                attn_launch_sum<T>(dp, sums, s);
                 return hip_status();
             }
-            a.vec_out = vec_ok(dk, a.dks, row, 1) && vec_ok(dv, a.dvs, row, 1);
             a.blocks = p.dkv_blocks; a.nsplit = p.dkv_split; a.per_split = p.dkv_per;
             if (int st = attn_launch_dkv<T>(p.dkv, a, s)) return st;
-            if (p.dkv_parts > 1) {
-                attn_launch_sum<T>(dp, sk, s);
-                attn_launch_sum<T>(dp, sv, s);
-            }
+            if (p.dkv_parts > 1) attn_launch_sum<T>(dp, sums, s);
         }
         if (d.table && d.Hq > 0)
-            attn_dtable_kernel<<<(unsigned)(d.Hq * d.num_buckets), 64, 0, s>>>(
-                a.tpart, p.nothing_keys ? 0 : (int)d.B, (int)d.Hq, p.nothing_keys ? 1 : p.per_unit, d.num_buckets, dtable,
-                d.table_dtype);
+            attn_dtable_kernel<<<(unsigned)(d.Hq * d.num_buckets), kTableThreads, 0, s>>>(
+                a.tpart, p.nothing_keys ? 0 : (int)d.B, (int)d.Hq, p.nothing_keys ? 1 : p.per_unit, d.num_buckets,
+                p.borders, dtable, d.table_dtype);
         return hip_status();
     });
 }

@@ -27,8 +27,8 @@
 // [key - query + 31][key] (the positions are the same for every tile, the
 // rest of the scratch stays zero), then lane t adds up diagonal t - 31 and
 // adds the sum to the wave's array of sums by relative position. At the end
-// the waves' arrays are joined in wave order and each bucket's range of
-// positions is summed: one float32 value per workgroup and bucket.
+// the waves' arrays are joined in wave order and left in the workspace, one
+// row per workgroup; attn_dtable_kernel sums each bucket's run of positions.
 #pragma once
 
 #include "attn_tile.hpp"
@@ -40,19 +40,34 @@ constexpr int kDiagFloats = 64 * kDiagPitch;
 
 template <typename T, int NW> struct BwdTile { static constexpr int rows = sizeof(T) == 2 && NW > 1 ? 64 : 32; };
 
+// The dk/dv kernel holds 4 DP / 32 accumulators and its keys' and values'
+// fragments. Above D = 64 that leaves room for one wave per SIMD; with the
+// values' fragments in LDS (which has bandwidth to spare) two fit, and hide
+// each other's waits. Tiles of 32 rows then keep two workgroups' LDS in a CU.
 template <typename T, int DP, int NW>
-constexpr int bwd_lds_bytes() { return 2 * 2 * BwdTile<T, NW>::rows * DP * (int)sizeof(T); }
+constexpr bool dkv_vals_in_lds() { return sizeof(T) == 2 && DP > 64; }
+template <typename T, int DP, int NW> struct DkvTile {
+    static constexpr int rows = dkv_vals_in_lds<T, DP, NW>() ? 32 : BwdTile<T, NW>::rows;
+};
+template <typename T, int DP, int NW>
+constexpr int dkv_lds_bytes() {
+    return 2 * 2 * Tile<T, DP>::bytes(DkvTile<T, DP, NW>::rows) + 1024 +
+           (dkv_vals_in_lds<T, DP, NW>() ? NW * (DP / 16) * 1024 : 0);
+}
+
+template <typename T, int DP, int NW>
+constexpr int bwd_lds_bytes() { return 2 * 2 * Tile<T, DP>::bytes(BwdTile<T, NW>::rows); }
 
 // LDS floats of the bias gradient.
 inline __host__ __device__ int dbias_floats(int entries, int nw) { return nw * (kDiagFloats + entries); }
 
-template <typename T, int DP, int NW, bool BIAS>
-__global__ __launch_bounds__(NW * 64, 1) void attn_dq_kernel(AttnArgs a) {
+template <typename T, int DP, int NW, bool BIAS, bool VEC>
+__global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dq_kernel(AttnArgs a) {
     typedef Tile<T, DP> TL;
     constexpr int KT = BwdTile<T, NW>::rows;
-    constexpr int NS = KT / 32, KB = KT * TL::row_bytes;
+    constexpr int NS = KT / 32, KB = TL::bytes(KT);
     Work w;
-    if (!find_work(a, w, a.causal != 0)) return;
+    if (!find_work(a, w, a.causal != 0, false)) return;
     const int lane = (int)threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int rows = a.Sq * a.pack;
@@ -68,16 +83,20 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dq_kernel(AttnArgs a) {
     if (a.causal) end = min(end, w.start + (min((w.block + 1) * NW * 32, rows) - 1) / a.pack + 1);
     const int begin = w.split * a.per_split;
 
-    const Rows kr = {a.k + w.b * a.ks.b + w.kv * a.ks.h, a.ks.s, 0, 1, 0, a.vec_k};
-    const Rows vr = {a.v + w.b * a.vs.b + w.kv * a.vs.h, a.vs.s, 0, 1, 0, a.vec_v};
+    const Rows kr = {a.k + w.b * a.ks.b + w.kv * a.ks.h, a.ks.s, 0, 1};
+    const Rows vr = {a.v + w.b * a.vs.b + w.kv * a.vs.h, a.vs.s, 0, 1};
     const float c = a.scale * kLog2e;
 
+    Stream<T, DP, KT, NW, VEC> ks, vs;
+    ks.start(kr, begin, KT, a.D, wave, lane);
+    vs.start(vr, begin, KT, a.D, wave, lane);
     if (begin < end) {
-        stage<T, DP, KT, NW>(0, kr, begin, begin, 0, end, a.D);
-        stage<T, DP, KT, NW>(2 * KB, vr, begin, begin, 0, end, a.D);
+        ks.fetch(0, kr, end - begin, KT, a.D, wave, lane);
+        vs.fetch(2 * KB, vr, end - begin, KT, a.D, wave, lane);
     }
-    float* bias = (float*)(smem + 4 * KB + kColBytes);
-    if constexpr (BIAS) fill_bias(bias, (float*)(smem + 4 * KB), a, w.head);
+    const int row_at = TL::row_lane(lane), col_at = TL::col_lane(lane, 0), col_at8 = TL::col_lane(lane, 8);
+    float* bias = (float*)(smem + 4 * KB);
+    if constexpr (BIAS) fill_bias(bias, a, w.head);
 
     Frag<T> q[DP / 16], dout[DP / 16];
     float delta = 0.0f;
@@ -88,9 +107,9 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dq_kernel(AttnArgs a) {
         const char* pd = a.dout + w.b * a.dos.b + (int64_t)pos_i * a.dos.s + hd * a.dos.h;
 #pragma unroll
         for (int ds = 0; ds < DP / 16; ++ds) {
-            q[ds] = global_frag<T>(pq, ds * 16 + 8 * h, a.D, a.vec_q, there);
-            dout[ds] = global_frag<T>(pd, ds * 16 + 8 * h, a.D, a.vec_do, there);
-            delta += frag_dot<T>(dout[ds], global_frag<T>(po, ds * 16 + 8 * h, a.D, a.vec_o, there));
+            q[ds] = global_frag<T, VEC>(pq, ds * 16 + 8 * h, a.D, there);
+            dout[ds] = global_frag<T, VEC>(pd, ds * 16 + 8 * h, a.D, there);
+            delta += frag_dot<T>(dout[ds], global_frag<T, VEC>(po, ds * 16 + 8 * h, a.D, there));
         }
     }
     delta = swap32_other_sum(delta);
@@ -107,26 +126,27 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dq_kernel(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) dq[dt][i] = 0.0f;
 
-    int buf = 0;
-    for (int j0 = begin; j0 < end; j0 += KT, buf ^= 1) {
+    alternate(begin, end, KT, [&](auto which, int j0) __attribute__((always_inline)) {
+        constexpr int buf = decltype(which)::value;
         loads_landed();
         __syncthreads();
         if (j0 + KT < end) {
-            stage<T, DP, KT, NW>((buf ^ 1) * KB, kr, j0 + KT, j0 + KT, 0, end, a.D);
-            stage<T, DP, KT, NW>(2 * KB + (buf ^ 1) * KB, vr, j0 + KT, j0 + KT, 0, end, a.D);
+            ks.fetch((buf ^ 1) * KB, kr, end - j0 - KT, KT, a.D, wave, lane);
+            vs.fetch(2 * KB + (buf ^ 1) * KB, vr, end - j0 - KT, KT, a.D, wave, lane);
         }
-        const int kt = buf * KB, vt = 2 * KB + buf * KB;
+        constexpr int kt = buf * KB, vt = kt + 2 * KB;
+        // (a branch around a single sub-tile would have the accumulators copied)
+        if (row0 >= rows || (a.causal && j0 > w.start + imax)) return;
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
             const int js = j0 + n * 32;
-            if (row0 >= rows || js >= end || (a.causal && js > w.start + imax)) continue;
             f32x16 s, dp;
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
 #pragma unroll
             for (int ds = 0; ds < DP / 16; ++ds) {
-                s = mma<T>(TL::row_frag(kt, n * 32 + (lane & 31), ds, h), q[ds], s);
-                dp = mma<T>(TL::row_frag(vt, n * 32 + (lane & 31), ds, h), dout[ds], dp);
+                s = mma<T>(TL::row_frag(row_at, kt, n, ds), q[ds], s);
+                dp = mma<T>(TL::row_frag(row_at, vt, n, ds), dout[ds], dp);
             }
             const int reach = a.borders.reach, after = a.borders.bidirectional ? reach : 0;
             const bool far_after = js - (w.start + imax) >= after;
@@ -163,14 +183,14 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dq_kernel(AttnArgs a) {
                 const Frag<T> pf = pack_frag<T>(p + 8 * k);
 #pragma unroll
                 for (int dt = 0; dt < DP / 32; ++dt)
-                    dq[dt] = mma<T>(TL::col_frag(kt, n * 32 + k * 16, dt, lane), pf, dq[dt]);
+                    dq[dt] = mma<T>(TL::col_frag(col_at, col_at8, kt, n * 32 + k * 16, dt), pf, dq[dt]);
             }
         }
-    }
+    });
     if (row0 < rows) {
         if (a.nsplit == 1) {
             char* out = a.dq + w.b * a.dqs.b + (int64_t)pos_i * a.dqs.s + (int64_t)(w.head + g) * a.dqs.h;
-            store_acc<T, DP>(out, dq, a.scale, a.D, a.vec_out, there, h);
+            store_acc<T, DP, VEC>(out, dq, a.scale, a.D, there, h);
         } else {
             const int64_t at = ((int64_t)w.split * a.units + w.u) * rows + row;
             store_part<DP>(a.part + at * DP, dq, a.scale, there, h);
@@ -188,13 +208,14 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dq_kernel(AttnArgs a) {
     }
 }
 
-template <typename T, int DP, int NW, bool BIAS>
-__global__ __launch_bounds__(NW * 64, 1) void attn_dkv_kernel(AttnArgs a) {
+template <typename T, int DP, int NW, bool BIAS, bool VEC>
+__global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dkv_kernel(AttnArgs a) {
     typedef Tile<T, DP> TL;
-    constexpr int RT = BwdTile<T, NW>::rows;
-    constexpr int NS = RT / 32, RB = RT * TL::row_bytes;
+    constexpr int RT = DkvTile<T, DP, NW>::rows;
+    constexpr bool VLDS = dkv_vals_in_lds<T, DP, NW>();
+    constexpr int NS = RT / 32, RB = TL::bytes(RT);
     Work w;
-    if (!find_work(a, w, false)) return;
+    if (!find_work(a, w, false, a.causal != 0)) return;
     const int lane = (int)threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int rows = a.Sq * a.pack;
@@ -203,57 +224,64 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dkv_kernel(AttnArgs a) {
     const bool there = key < w.len;
     const float c = a.scale * kLog2e;
 
-    // rows that see a key of this workgroup
+    // rows that see a key of this workgroup, in tiles of whole positions
+    const int take = RT / a.pack * a.pack;
     int begin = w.split * a.per_split, end = min(rows, (w.split + 1) * a.per_split);
     if (a.causal) {
         const int first = max(w.block * NW * 32 - w.start, 0);   // position
         if (first >= a.Sq) begin = end;
-        else begin = max(begin, first * a.pack / RT * RT);
+        else begin = max(begin, first * a.pack / take * take);
     }
     if (w.block * NW * 32 >= w.len) begin = end;
 
-    const Rows qr = {a.q + w.b * a.qs.b + w.head * a.qs.h, a.qs.s, a.qs.h, a.pack, a.magic, a.vec_q};
-    const Rows dr = {a.dout + w.b * a.dos.b + w.head * a.dos.h, a.dos.s, a.dos.h, a.pack, a.magic, a.vec_do};
+    const Rows qr = {a.q + w.b * a.qs.b + w.head * a.qs.h, a.qs.s, a.qs.h, a.pack};
+    const Rows dr = {a.dout + w.b * a.dos.b + w.head * a.dos.h, a.dos.s, a.dos.h, a.pack};
     const int64_t row_at = ((int64_t)w.b * a.Hq + w.head) * a.Sq;
     const int64_t rows_all = (int64_t)a.B * a.Hq * a.Sq;
     constexpr int kStat = 4 * RB;   // [2 buffers][lse, delta][64]
     const int entries = BIAS ? bias_entries(a.borders) : 0;
-    float* bias = (float*)(smem + kStat + 1024 + kColBytes);
+    constexpr int kVals = kStat + 1024;   // [NW][DP / 16][64 lanes] fragments
+    float* bias = (float*)(smem + dkv_lds_bytes<T, DP, NW>());
     float* diag = bias + entries + wave * kDiagFloats;
     float* sums = bias + entries + NW * kDiagFloats;   // [NW][entries]
     float far_before = 0.0f, far_behind = 0.0f;
     if constexpr (BIAS) {
-        fill_bias(bias, (float*)(smem + kStat + 1024), a, w.head);
+        fill_bias(bias, a, w.head);
         for (int x = lane; x < kDiagFloats; x += 64) diag[x] = 0.0f;
         for (int x = lane; x < entries; x += 64) sums[wave * entries + x] = 0.0f;
     }
 
-    const auto bring = [&](int r0, int to) {
-        const int i0 = r0 / a.pack, rem = r0 - i0 * a.pack;
-        stage<T, DP, RT, NW>(to * RB, qr, r0, i0, rem, end, a.D);
-        stage<T, DP, RT, NW>(2 * RB + to * RB, dr, r0, i0, rem, end, a.D);
-        // rows that are not there get log sum and delta 0: their dO and q are
-        // zeros, so they add nothing
+    Stream<T, DP, RT, NW, VEC> qs, dos;
+    int at_pos = begin / a.pack;   // position of the tile being fetched, then of the one worked on
+    qs.start(qr, at_pos, take, a.D, wave, lane);
+    dos.start(dr, at_pos, take, a.D, wave, lane);
+    const int row_lane = TL::row_lane(lane), col_at = TL::col_lane(lane, 0), col_at8 = TL::col_lane(lane, 8);
+    // log sums and delta of a tile: rows that are not there get 0, and as
+    // their dO and q are zeros they add nothing
+    const int lane_pos = lane / a.pack;
+    const uint32_t stat_off = lane < take ? (uint32_t)((lane - lane_pos * a.pack) * a.Sq + lane_pos) * 4u : kOutside;
+    const auto bring = [&](int r0, int pos0, int to) __attribute__((always_inline)) {
+        qs.fetch(to * RB, qr, end - r0, take, a.D, wave, lane);
+        dos.fetch(2 * RB + to * RB, dr, end - r0, take, a.D, wave, lane);
         if (wave < 2) {
-            for (int k = wave; k < 2; k += NW < 2 ? 1 : 2) {
-                const int di = div_pack(rem + lane, qr);
-                const int g = rem + lane - di * a.pack;
-                const uint32_t off = lane < RT && r0 + lane < end ? (uint32_t)(g * a.Sq + di) * 4u : kOutside;
-                load_to_lds4(a.rows + k * rows_all + row_at + i0, kStat + to * 512 + k * 256, off);
-            }
+            for (int k = wave; k < 2; k += NW < 2 ? 1 : 2)
+                load_to_lds4(a.rows + k * rows_all + row_at + pos0, kStat + to * 512 + k * 256,
+                             r0 + lane < end ? stat_off : kOutside);
         }
     };
-    if (begin < end) bring(begin, 0);
+    if (begin < end) bring(begin, at_pos, 0);
 
-    Frag<T> kf[DP / 16], vf[DP / 16];
+    Frag<T> kf[DP / 16], vf[VLDS ? 1 : DP / 16];
     {
         const int kk = min(key, a.Sk - 1);
         const char* pk = a.k + w.b * a.ks.b + (int64_t)kk * a.ks.s + w.kv * a.ks.h;
         const char* pv = a.v + w.b * a.vs.b + (int64_t)kk * a.vs.s + w.kv * a.vs.h;
 #pragma unroll
         for (int ds = 0; ds < DP / 16; ++ds) {
-            kf[ds] = global_frag<T>(pk, ds * 16 + 8 * h, a.D, a.vec_k, there);
-            vf[ds] = global_frag<T>(pv, ds * 16 + 8 * h, a.D, a.vec_v, there);
+            kf[ds] = global_frag<T, VEC>(pk, ds * 16 + 8 * h, a.D, there);
+            const Frag<T> f = global_frag<T, VEC>(pv, ds * 16 + 8 * h, a.D, there);
+            if constexpr (VLDS) *(Frag<T>*)(smem + kVals + (wave * (DP / 16) + ds) * 1024 + lane * 16) = f;
+            else vf[ds] = f;
         }
     }
     f32x16 dk[DP / 32], dv[DP / 32];
@@ -262,25 +290,37 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dkv_kernel(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) dk[dt][i] = dv[dt][i] = 0.0f;
 
-    int buf = 0;
-    for (int r0 = begin; r0 < end; r0 += RT, buf ^= 1) {
+    // positions of the sub-tiles' first and last rows within a tile
+    int sub_first[NS], sub_last[NS];
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        sub_first[n] = n * 32 / a.pack;
+        sub_last[n] = min(n * 32 + 31, take - 1) / a.pack;
+    }
+    const int last_pos = end / a.pack - 1;
+    alternate(begin, end, take, [&](auto which, int r0) __attribute__((always_inline)) {
+        constexpr int buf = decltype(which)::value;
         loads_landed();
         __syncthreads();
-        if (r0 + RT < end) bring(r0 + RT, buf ^ 1);
-        const int qt = buf * RB, dt0 = 2 * RB + buf * RB;
+        const int pos0 = at_pos;
+        at_pos += take / a.pack;
+        if (r0 + take < end) bring(r0 + take, at_pos, buf ^ 1);
+        constexpr int qt = buf * RB, ot = qt + 2 * RB;
+        // (a branch around a single sub-tile would have the accumulators copied)
+        if (key0 >= w.len || (a.causal && key0 > w.start + min(pos0 + sub_last[NS - 1], last_pos))) return;
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
             const int rs = r0 + n * 32;
-            if (rs >= end || key0 >= w.len) continue;
-            const int imin = w.start + rs / a.pack, imax = w.start + min(rs + 31, end - 1) / a.pack;   // positions
-            if (a.causal && key0 > imax) continue;
+            const int imin = w.start + pos0 + sub_first[n];   // positions
+            const int imax = w.start + max(min(pos0 + sub_last[n], last_pos), pos0 + sub_first[n]);
             f32x16 s, dp;
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
 #pragma unroll
             for (int ds = 0; ds < DP / 16; ++ds) {
-                s = mma<T>(TL::row_frag(qt, n * 32 + (lane & 31), ds, h), kf[ds], s);
-                dp = mma<T>(TL::row_frag(dt0, n * 32 + (lane & 31), ds, h), vf[ds], dp);
+                s = mma<T>(TL::row_frag(row_lane, qt, n, ds), kf[ds], s);
+                const Frag<T> vd = VLDS ? *(const Frag<T>*)(smem + kVals + (wave * (DP / 16) + ds) * 1024 + lane * 16) : vf[VLDS ? 0 : ds];
+                dp = mma<T>(TL::row_frag(row_lane, ot, n, ds), vd, dp);
             }
             const float* st = (const float*)(smem + kStat + buf * 512) + n * 32 + 4 * h;
             float p[16];
@@ -318,7 +358,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dkv_kernel(AttnArgs a) {
                 const Frag<T> pf = pack_frag<T>(p + 8 * k);
 #pragma unroll
                 for (int dt = 0; dt < DP / 32; ++dt)
-                    dv[dt] = mma<T>(TL::col_frag(dt0, n * 32 + k * 16, dt, lane), pf, dv[dt]);
+                    dv[dt] = mma<T>(TL::col_frag(col_at, col_at8, ot, n * 32 + k * 16, dt), pf, dv[dt]);
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) p[i] *= dp[i] - st[64 + 8 * (i / 4) + (i % 4)];
@@ -351,10 +391,10 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dkv_kernel(AttnArgs a) {
                 const Frag<T> pf = pack_frag<T>(p + 8 * k);
 #pragma unroll
                 for (int dt = 0; dt < DP / 32; ++dt)
-                    dk[dt] = mma<T>(TL::col_frag(qt, n * 32 + k * 16, dt, lane), pf, dk[dt]);
+                    dk[dt] = mma<T>(TL::col_frag(col_at, col_at8, qt, n * 32 + k * 16, dt), pf, dk[dt]);
             }
         }
-    }
+    });
     if constexpr (BIAS) {
         far_before = lanes_sum<64>(far_before);
         far_behind = lanes_sum<64>(far_behind);
@@ -366,28 +406,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dkv_kernel(AttnArgs a) {
         for (int x = (int)threadIdx.x; x < entries; x += NW * 64) {
             float s = sums[x];
             for (int k = 1; k < NW; ++k) s += sums[k * entries + x];
-            sums[x] = s;
-        }
-        __syncthreads();
-        // a bucket is a run of entries: one lane group of 64 per bucket
-        const Borders& o = a.borders;
-        const int mid = o.reach + kPad;   // entry of position 0
-        for (int t = wave; t < a.buckets; t += NW) {
-            int lo, hi;   // entries [lo, hi)
-            if (t < o.n) {
-                lo = t + 1 < o.n ? mid - o.at[t + 1] + 1 : 0;
-                hi = mid - o.at[t] + 1;
-                if (t == 0 && !o.bidirectional) hi = entries;   // every later key
-            } else {
-                // later keys: distance 0 is the other direction's
-                const int d = max(o.at[t - o.n], 1);
-                lo = mid + d;
-                hi = t - o.n + 1 < o.n ? mid + o.at[t - o.n + 1] : entries;
-            }
-            float s = 0.0f;
-            for (int x = lo + lane; x < hi; x += 64) s += sums[x];
-            s = lanes_sum<64>(s);
-            if (lane == 0) a.tpart[w.flat * a.buckets + t] = s;
+            a.tpart[w.flat * entries + x] = s;
         }
     }
     if (key0 >= a.Sk) return;
@@ -395,8 +414,8 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dkv_kernel(AttnArgs a) {
     const int parts = a.nsplit * (a.G / a.pack);   // float32 parts of each key head
     if (parts == 1) {
         const int64_t kk = min(key, a.Sk - 1);
-        store_acc<T, DP>(a.dk + w.b * a.dks.b + kk * a.dks.s + w.kv * a.dks.h, dk, a.scale, a.D, a.vec_out, in, h);
-        store_acc<T, DP>(a.dv + w.b * a.dvs.b + kk * a.dvs.s + w.kv * a.dvs.h, dv, 1.0f, a.D, a.vec_out, in, h);
+        store_acc<T, DP, VEC>(a.dk + w.b * a.dks.b + kk * a.dks.s + w.kv * a.dks.h, dk, a.scale, a.D, in, h);
+        store_acc<T, DP, VEC>(a.dv + w.b * a.dvs.b + kk * a.dvs.s + w.kv * a.dvs.h, dv, 1.0f, a.D, in, h);
     } else {
         // [part][dk, dv][B, Hkv, Sk, DP]
         const int64_t heads = (int64_t)a.B * a.Hkv, part = (w.head % a.G) / a.pack + (int64_t)(a.G / a.pack) * w.split;
@@ -413,19 +432,25 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_dkv_kernel(AttnArgs a) {
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void attn_sum_kernel(SumArgs x) {
     constexpr int TPR = DP / 4, PER = 256 / TPR;
-    const int64_t at = (int64_t)blockIdx.x * PER + (int)threadIdx.x / TPR;
+    int64_t at = (int64_t)blockIdx.x * PER + (int)threadIdx.x / TPR;
     const int d = ((int)threadIdx.x % TPR) * 4;
+    // workgroups past the first sum's rows make the second
+    const int64_t first = (x.total + PER - 1) / PER;
+    const bool second = (int64_t)blockIdx.x >= first;
+    if (second) at -= first * PER;
+    const float* part = second ? x.part2 : x.part;
     if ((int)threadIdx.x >= PER * TPR || at >= x.total) return;
     float o[4] = {0, 0, 0, 0};
 #pragma unroll 4
     for (int p = 0; p < x.parts; ++p) {
-        const f32x4 v = *(const f32x4*)(x.part + p * x.stride + at * DP + d);
+        const f32x4 v = *(const f32x4*)(part + p * x.stride + at * DP + d);
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[k] += v[k];
     }
     const int u = (int)(at / x.rows), r = (int)(at - (int64_t)u * x.rows);
     const int b = u / x.hu, i = r / x.pack, head = (u - b * x.hu) * x.pack + (r - i * x.pack);
-    T* to = (T*)(x.out + b * x.os.b + (int64_t)i * x.os.s + (int64_t)head * x.os.h);
+    const Strides os = second ? x.os2 : x.os;
+    T* to = (T*)((second ? x.out2 : x.out) + b * os.b + (int64_t)i * os.s + (int64_t)head * os.h);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         if (d + k < x.D) to[d + k] = dyt::from_f32<T>(o[k]);

@@ -29,15 +29,15 @@ namespace dytb {
 template <typename T, int NW> struct FwdTile { static constexpr int keys = sizeof(T) == 2 && NW > 1 ? 64 : 32; };
 
 template <typename T, int DP, int NW>
-constexpr int fwd_lds_bytes() { return 2 * 2 * FwdTile<T, NW>::keys * DP * (int)sizeof(T); }
+constexpr int fwd_lds_bytes() { return 2 * 2 * Tile<T, DP>::bytes(FwdTile<T, NW>::keys); }
 
-template <typename T, int DP, int NW, bool BIAS>
-__global__ __launch_bounds__(NW * 64, NW > 1 && sizeof(T) == 2 ? 2 : 1) void attn_fwd_kernel(AttnArgs a) {
+template <typename T, int DP, int NW, bool BIAS, bool VEC>
+__global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_kernel(AttnArgs a) {
     typedef Tile<T, DP> TL;
     constexpr int KT = FwdTile<T, NW>::keys;
-    constexpr int NS = KT / 32, KB = KT * TL::row_bytes;
+    constexpr int NS = KT / 32, KB = TL::bytes(KT);
     Work w;
-    if (!find_work(a, w, a.causal != 0)) return;
+    if (!find_work(a, w, a.causal != 0, false)) return;
     const int lane = (int)threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int rows = a.Sq * a.pack;
@@ -53,22 +53,26 @@ __global__ __launch_bounds__(NW * 64, NW > 1 && sizeof(T) == 2 ? 2 : 1) void att
     if (a.causal) end = min(end, w.start + (min((w.block + 1) * NW * 32, rows) - 1) / a.pack + 1);
     const int begin = w.split * a.per_split;
 
-    const Rows kr = {a.k + w.b * a.ks.b + w.kv * a.ks.h, a.ks.s, 0, 1, 0, a.vec_k};
-    const Rows vr = {a.v + w.b * a.vs.b + w.kv * a.vs.h, a.vs.s, 0, 1, 0, a.vec_v};
+    const Rows kr = {a.k + w.b * a.ks.b + w.kv * a.ks.h, a.ks.s, 0, 1};
+    const Rows vr = {a.v + w.b * a.vs.b + w.kv * a.vs.h, a.vs.s, 0, 1};
     const float c = a.scale * kLog2e;
 
+    Stream<T, DP, KT, NW, VEC> ks, vs;
+    ks.start(kr, begin, KT, a.D, wave, lane);
+    vs.start(vr, begin, KT, a.D, wave, lane);
     if (begin < end) {
-        stage<T, DP, KT, NW>(0, kr, begin, begin, 0, end, a.D);
-        stage<T, DP, KT, NW>(2 * KB, vr, begin, begin, 0, end, a.D);
+        ks.fetch(0, kr, end - begin, KT, a.D, wave, lane);
+        vs.fetch(2 * KB, vr, end - begin, KT, a.D, wave, lane);
     }
-    float* bias = (float*)(smem + 4 * KB + kColBytes);
-    if constexpr (BIAS) fill_bias(bias, (float*)(smem + 4 * KB), a, w.head);
+    const int row_at = TL::row_lane(lane), col_at = TL::col_lane(lane, 0), col_at8 = TL::col_lane(lane, 8);
+    float* bias = (float*)(smem + 4 * KB);
+    if constexpr (BIAS) fill_bias(bias, a, w.head);
 
     Frag<T> q[DP / 16];
     {
         const char* p = a.q + w.b * a.qs.b + (int64_t)pos_i * a.qs.s + (int64_t)(w.head + g) * a.qs.h;
 #pragma unroll
-        for (int ds = 0; ds < DP / 16; ++ds) q[ds] = global_frag<T>(p, ds * 16 + 8 * h, a.D, a.vec_q, there);
+        for (int ds = 0; ds < DP / 16; ++ds) q[ds] = global_frag<T, VEC>(p, ds * 16 + 8 * h, a.D, there);
     }
     f32x16 o[DP / 32];
 #pragma unroll
@@ -81,16 +85,16 @@ __global__ __launch_bounds__(NW * 64, NW > 1 && sizeof(T) == 2 ? 2 : 1) void att
     const float mc = BIAS ? 1.0f : c;
     const float grow = 8.0f / mc;
 
-    int buf = 0;
-    for (int j0 = begin; j0 < end; j0 += KT, buf ^= 1) {
+    alternate(begin, end, KT, [&](auto which, int j0) __attribute__((always_inline)) {
+        constexpr int buf = decltype(which)::value;
         loads_landed();
         __syncthreads();
         if (j0 + KT < end) {
-            stage<T, DP, KT, NW>((buf ^ 1) * KB, kr, j0 + KT, j0 + KT, 0, end, a.D);
-            stage<T, DP, KT, NW>(2 * KB + (buf ^ 1) * KB, vr, j0 + KT, j0 + KT, 0, end, a.D);
+            ks.fetch((buf ^ 1) * KB, kr, end - j0 - KT, KT, a.D, wave, lane);
+            vs.fetch(2 * KB + (buf ^ 1) * KB, vr, end - j0 - KT, KT, a.D, wave, lane);
         }
-        if (row0 >= rows || (a.causal && j0 > w.start + imax)) continue;
-        const int kt = buf * KB, vt = 2 * KB + buf * KB;
+        if (row0 >= rows || (a.causal && j0 > w.start + imax)) return;
+        constexpr int kt = buf * KB, vt = 2 * KB + buf * KB;
         f32x16 s[NS];
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
@@ -98,7 +102,7 @@ __global__ __launch_bounds__(NW * 64, NW > 1 && sizeof(T) == 2 ? 2 : 1) void att
             for (int i = 0; i < 16; ++i) s[n][i] = 0.0f;
 #pragma unroll
             for (int ds = 0; ds < DP / 16; ++ds)
-                s[n] = mma<T>(TL::row_frag(kt, n * 32 + (lane & 31), ds, h), q[ds], s[n]);
+                s[n] = mma<T>(TL::row_frag(row_at, kt, n, ds), q[ds], s[n]);
         }
         if constexpr (BIAS) {
 #pragma unroll
@@ -155,16 +159,16 @@ __global__ __launch_bounds__(NW * 64, NW > 1 && sizeof(T) == 2 ? 2 : 1) void att
                 const Frag<T> pf = pack_frag<T>(p + 8 * k);
 #pragma unroll
                 for (int dt = 0; dt < DP / 32; ++dt)
-                    o[dt] = mma<T>(TL::col_frag(vt, n * 32 + k * 16, dt, lane), pf, o[dt]);
+                    o[dt] = mma<T>(TL::col_frag(col_at, col_at8, vt, n * 32 + k * 16, dt), pf, o[dt]);
             }
         }
-    }
+    });
     if (row0 >= rows) return;
     l = swap32_other_sum(l);
     const float ml = (m == -INFINITY ? 0.0f : m) * mc;   // log2 units
     if (a.nsplit == 1) {
         char* out = a.out + w.b * a.os.b + (int64_t)pos_i * a.os.s + (int64_t)(w.head + g) * a.os.h;
-        store_acc<T, DP>(out, o, l > 0.0f ? 1.0f / l : 0.0f, a.D, a.vec_out, there, h);
+        store_acc<T, DP, VEC>(out, o, l > 0.0f ? 1.0f / l : 0.0f, a.D, there, h);
         if (there && h == 0)
             a.stats[((int64_t)w.b * a.Hq + w.head + g) * a.Sq + pos_i] =
                 l > 0.0f ? (ml + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
@@ -179,29 +183,52 @@ __global__ __launch_bounds__(NW * 64, NW > 1 && sizeof(T) == 2 ? 2 : 1) void att
 }
 
 // Joins the splits of a row: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s
-// with M the largest m_s, in split order. DP / 4 threads per row.
-template <typename T, int DP>
+// with M the largest m_s. JG groups of DP / 4 threads share a row, group g
+// taking splits g, g + JG, ..; the groups are added in order. A row of many
+// splits (a single token's) is a chain of dependent loads otherwise: 9.5 us
+// for 16 splits of 256 rows with one group.
+template <typename T, int DP, int JG>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-    constexpr int TPR = DP / 4, PER = 256 / TPR;
+    constexpr int TPR = DP / 4, PER = 256 / (TPR * JG);
     const int rows = a.Sq * a.pack;
     const int64_t total = (int64_t)a.units * rows;
-    const int64_t at = (int64_t)blockIdx.x * PER + (int)threadIdx.x / TPR;
+    const int slot = (int)threadIdx.x / (TPR * JG);
+    const int g = (int)threadIdx.x / TPR % JG;
+    const int64_t at = (int64_t)blockIdx.x * PER + slot;
     const int d = ((int)threadIdx.x % TPR) * 4;
-    if ((int)threadIdx.x >= PER * TPR || at >= total) return;
-    float M = -INFINITY;
+    const bool in = slot < PER && at < total;
+    float M = -INFINITY, l = 0.0f, mm = 0.0f, o[4] = {0, 0, 0, 0};
+    if (in) {
 #pragma unroll 8
-    for (int s = 0; s < a.nsplit; ++s) M = fmaxf(M, a.part_ml[2 * (s * total + at)]);
-    const float mm = M == -INFINITY ? 0.0f : M;
-    float l = 0.0f, o[4] = {0, 0, 0, 0};
-#pragma unroll 8
-    for (int s = 0; s < a.nsplit; ++s) {
-        // an empty split has weight 2^-inf = 0 and a part of zeros
-        const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * (s * total + at)] - mm);
-        l += f * a.part_ml[2 * (s * total + at) + 1];
-        const f32x4 v = *(const f32x4*)(a.part + (s * total + at) * DP + d);
+        for (int s = 0; s < a.nsplit; ++s) M = fmaxf(M, a.part_ml[2 * (s * total + at)]);
+        mm = M == -INFINITY ? 0.0f : M;
+#pragma unroll 4
+        for (int s = g; s < a.nsplit; s += JG) {
+            // an empty split has weight 2^-inf = 0 and a part of zeros
+            const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * (s * total + at)] - mm);
+            l += f * a.part_ml[2 * (s * total + at) + 1];
+            const f32x4 v = *(const f32x4*)(a.part + (s * total + at) * DP + d);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] += f * v[k];
+            for (int k = 0; k < 4; ++k) o[k] += f * v[k];
+        }
     }
+    if constexpr (JG > 1) {
+        __shared__ float join[256][5];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) join[threadIdx.x][k] = o[k];
+        join[threadIdx.x][4] = l;
+        __syncthreads();
+        if (g == 0) {
+#pragma unroll
+            for (int j = 1; j < JG; ++j) {
+                const int from = min((int)threadIdx.x + j * TPR, 255);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[k] += join[from][k];
+                l += join[from][4];
+            }
+        }
+    }
+    if (!in || g) return;
     const int u = (int)(at / rows), r = (int)(at - (int64_t)u * rows);
     const int hu = a.Hq / a.pack;
     const int b = u / hu, i = r / a.pack, head = (u - b * hu) * a.pack + (r - i * a.pack);

@@ -10,12 +10,12 @@ namespace dytb {
 template <typename T>
 int attn_launch_dkv(const AttnPick& p, const AttnArgs& a, hipStream_t s) {
     int st = DYT_OK;
-    with_pick(p, [&](auto dp, auto nw, auto bias) {
+    with_pick(p, [&](auto dp, auto nw, auto bias, auto vec) {
         constexpr int DP = decltype(dp)::value, NW = decltype(nw)::value;
-        constexpr bool BIAS = decltype(bias)::value != 0;
-        size_t lds = bwd_lds_bytes<T, DP, NW>() + 1024;
+        constexpr bool BIAS = decltype(bias)::value != 0, VEC = decltype(vec)::value != 0;
+        size_t lds = dkv_lds_bytes<T, DP, NW>();
         if (BIAS) lds += bias_lds_bytes(a) + sizeof(float) * dbias_floats(2 * (a.borders.reach + kPad), NW);
-        st = launch_lds((const void*)attn_dkv_kernel<T, DP, NW, BIAS>, attn_grid(a), NW * 64, lds, a, s);
+        st = launch_lds((const void*)attn_dkv_kernel<T, DP, NW, BIAS, VEC>, attn_grid(a), NW * 64, lds, a, s);
     });
     return st;
 }
@@ -24,7 +24,8 @@ template <typename T>
 void attn_launch_sum(int dp, const SumArgs& x, hipStream_t s) {
     with_dp(dp, [&](auto d) {
         constexpr int DP = decltype(d)::value, PER = 256 / (DP / 4);
-        attn_sum_kernel<T, DP><<<(unsigned)((x.total + PER - 1) / PER), 256, 0, s>>>(x);
+        const unsigned grid = (unsigned)((x.total + PER - 1) / PER) * (x.out2 ? 2 : 1);
+        attn_sum_kernel<T, DP><<<grid, 256, 0, s>>>(x);
     });
 }
 

@@ -9,17 +9,23 @@ namespace dytb {
 template <typename T>
 int attn_launch_fwd(const AttnPick& p, const AttnArgs& a, hipStream_t s) {
     int st = DYT_OK;
-    with_pick(p, [&](auto dp, auto nw, auto bias) {
+    with_pick(p, [&](auto dp, auto nw, auto bias, auto vec) {
         constexpr int DP = decltype(dp)::value, NW = decltype(nw)::value;
-        constexpr bool BIAS = decltype(bias)::value != 0;
+        constexpr bool BIAS = decltype(bias)::value != 0, VEC = decltype(vec)::value != 0;
         const size_t lds = fwd_lds_bytes<T, DP, NW>() + (BIAS ? bias_lds_bytes(a) : 0);
-        st = launch_lds((const void*)attn_fwd_kernel<T, DP, NW, BIAS>, attn_grid(a), NW * 64, lds, a, s);
+        st = launch_lds((const void*)attn_fwd_kernel<T, DP, NW, BIAS, VEC>, attn_grid(a), NW * 64, lds, a, s);
     });
     if (st || a.nsplit == 1) return st;
     with_dp(p.dp, [&](auto dp) {
-        constexpr int DP = decltype(dp)::value, PER = 256 / (DP / 4);
+        constexpr int DP = decltype(dp)::value, TPR = DP / 4;
         const int64_t rows = (int64_t)a.units * a.Sq * a.pack;
-        attn_join_kernel<T, DP><<<(unsigned)((rows + PER - 1) / PER), 256, 0, s>>>(a);
+        if (a.nsplit >= 8) {
+            constexpr int JG = 256 / TPR < 8 ? 256 / TPR : 8, PER = 256 / (TPR * JG);
+            attn_join_kernel<T, DP, JG><<<(unsigned)((rows + PER - 1) / PER), 256, 0, s>>>(a);
+        } else {
+            constexpr int PER = 256 / TPR;
+            attn_join_kernel<T, DP, 1><<<(unsigned)((rows + PER - 1) / PER), 256, 0, s>>>(a);
+        }
     });
     return hipGetLastError() == hipSuccess ? DYT_OK : DYT_ERR_HIP;
 }

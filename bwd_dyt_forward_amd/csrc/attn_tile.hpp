@@ -15,13 +15,19 @@
 // 16 s + 8 (j / 4) + 4 h + j % 4. The A side is read in that same order
 // (load_col_frag), by the LDS's transposing read for the 16-bit types.
 //
-// LDS tiles are row-major, rows of DP elements cut into 16-byte chunks; the
-// chunk at column position c of row r is stored at position c ^ f(r)
-// (swizzle()), so that the 16 rows one read instruction covers at a time
-// fall on different banks without padding: the tiles are filled by
-// direct-to-LDS loads, which write 1,024 contiguous bytes per wave
-// instruction. Columns past D and rows past the end come out as zeros: their
-// lanes ask for an offset past the buffer descriptor's end.
+// LDS tiles are row-major, rows of DP elements cut into 16-byte chunks. A read
+// of 16 bytes a lane takes 16 rows of one chunk at a time, the transposing
+// read 4 neighbouring rows of 4 neighbouring chunks; both should touch each
+// of the 64 banks once. For the 16-bit types chunk c of row r is therefore
+// stored at c ^ f(r), where f sends 16 rows to 16 different positions and 4
+// neighbouring rows to different groups of 4 (measured: no conflicts; with
+// one chunk of padding per row instead the transposing reads took four times
+// their cycles and the dk/dv kernel 14% longer). Float32 rows, read in single
+// words by the second product, are padded by one chunk. The tiles are filled
+// by direct-to-LDS loads, which write 1,024 contiguous bytes per wave
+// instruction, so each lane asks for the chunk its place belongs to; lanes on
+// padding, on columns past D or on rows past the end ask for an offset past
+// the buffer descriptor's end, which brings zeros.
 #pragma once
 
 #include "block_common.hpp"
@@ -78,69 +84,100 @@ __device__ __forceinline__ Frag<T> pack_frag(const float* v) {
 }
 
 template <typename T, int DP> struct Tile {
-    static constexpr int row_bytes = DP * (int)sizeof(T);
-    static constexpr int cpr = row_bytes / 16;   // chunks per row
+    static constexpr bool xored = sizeof(T) == 2;
+    static constexpr int cpr = DP * (int)sizeof(T) / 16;   // chunks per row
+    static constexpr int chunks = xored ? cpr : cpr + 1;
+    static constexpr int pitch = chunks * 16;
+    // Chunk bits that f changes; the row pitch is a multiple of 16 (mask + 1).
+    static constexpr int mask = !xored ? 0 : cpr == 16 ? 15 : cpr == 8 ? 7 : 3;
 
-    // f(row): see the file comment. The 256 bytes of the 64 banks hold
-    // 16 / cpr rows (or one row, or a part); 16 consecutive rows get 16
-    // different positions, 4 consecutive rows different 32-byte pairs.
+    // Bytes of a tile: whole wave instructions.
+    static constexpr int bytes(int rows) { return (rows * pitch + 1023) / 1024 * 1024; }
+
+    // f(row). The banks hold 16 chunks: one row of 16 chunks, two of 8, four
+    // of 4, and rows of 12 start at 0, 12, 8, 4 in turn.
     static __device__ __forceinline__ int swizzle(int row) {
-        if constexpr (sizeof(T) == 2) {
-            if constexpr (cpr == 16) { const int u = row & 15; return ((u & 7) << 1) | (u >> 3); }
-            else if constexpr (cpr == 8) { const int u = (row >> 1) & 7; return ((u & 3) << 1) | (u >> 2); }
-            else { const int u = (row >> 2) & 3; return ((u & 1) << 1) | (u >> 1); }
+        if constexpr (!xored) return 0;
+        else if constexpr (cpr == 16) return ((row & 3) << 2) | ((row >> 2) & 3);
+        else if constexpr (cpr == 8) return ((row & 2) << 1) | ((row >> 2) & 3);
+        else return (row >> 2) & 3;
+    }
+
+    // A lane's base for row_frag and col_frag; at() moves it to another chunk.
+    static __device__ __forceinline__ int row_lane(int lane) {
+        const int row = lane & 31, h = lane >> 5;
+        if constexpr (xored) return row * pitch + ((h ^ swizzle(row)) << 4);
+        else return row * pitch + h * 32;
+    }
+    static __device__ __forceinline__ int col_lane(int lane, int more) {
+        if constexpr (xored) {
+            // 16 lanes of the transposing read give 4 rows of 16 columns
+            const int r = lane & 15, g = lane >> 4;
+            const int row = 4 * (g >> 1) + (r >> 2) + more;
+            return row * pitch + (((((g & 1) << 1) | ((r & 3) >> 1)) ^ swizzle(row)) << 4) + (r & 1) * 8;
         } else {
-            if constexpr (cpr % 16 == 0) return row & 15;
-            else return (row >> 1) & 7;
+            return 4 * (lane >> 5) * pitch + (lane & 31) * 4 + more * pitch;
         }
     }
-
-    static __device__ __forceinline__ int offset(int row, int chunk) {
-        return row * row_bytes + ((chunk ^ swizzle(row)) << 4);
+    // chunk: a multiple of what the lane's own chunk number stays below.
+    static __device__ __forceinline__ int at(int base, int chunk) {
+        return (base ^ ((chunk & mask) << 4)) + ((chunk & ~mask) << 4);
     }
 
-    // Contraction slots ds * 16 .. + 15 of one row.
-    static __device__ __forceinline__ Frag<T> row_frag(int tile, int row, int ds, int h) {
-        if constexpr (sizeof(T) == 2) {
-            return *(const u32x4*)(smem + tile + offset(row, ds * 2 + h));
+    // Contraction slots ds * 16 .. + 15 of row n * 32 + lane % 32 of the tile
+    // at byte `tile`.
+    static __device__ __forceinline__ Frag<T> row_frag(int lane_at, int tile, int n, int ds) {
+        if constexpr (xored) {
+            return *(const u32x4*)(smem + at(lane_at, ds * 2) + (tile + n * 32 * pitch));
         } else {
-            const f32x4 lo = *(const f32x4*)(smem + tile + offset(row, ds * 4 + h * 2));
-            const f32x4 hi = *(const f32x4*)(smem + tile + offset(row, ds * 4 + h * 2 + 1));
+            const char* p = smem + lane_at + (tile + n * 32 * pitch + ds * 64);
+            const f32x4 lo = *(const f32x4*)p, hi = *(const f32x4*)(p + 16);
             return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     }
 
-    // Column dt * 32 + lane % 32, rows row0 .. row0 + 15 in accumulator order.
-    static __device__ __forceinline__ Frag<T> col_frag(int tile, int row0, int dt, int lane) {
-        if constexpr (sizeof(T) == 2) {
+    // Column dt * 32 + lane % 32, rows row0 .. row0 + 15 in accumulator order;
+    // row0 is a multiple of 16. lane_at: col_lane(lane, 0), lane_at8: (lane, 8).
+    static __device__ __forceinline__ Frag<T> col_frag(int lane_at, int lane_at8, int tile, int row0, int dt) {
+        if constexpr (xored) {
             typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-            const int r = lane & 15, g = lane >> 4;
-            const int row = 4 * (g >> 1) + (r >> 2);
-            const int chunk = dt * 4 + (g & 1) * 2 + ((r & 3) >> 1);
-            const int at = (r & 1) * 8;
             const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_ptr)(smem + tile + row0 * row_bytes + offset(row, chunk) + at));
+                (lds_ptr)(smem + at(lane_at, dt * 4) + (tile + row0 * pitch)));
             const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_ptr)(smem + tile + row0 * row_bytes + offset(row + 8, chunk) + at));
+                (lds_ptr)(smem + at(lane_at8, dt * 4) + (tile + row0 * pitch)));
             const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
             return u32x4{x[0], x[1], y[0], y[1]};
         } else {
-            const int c = dt * 32 + (lane & 31), h = lane >> 5;
+            const char* p = smem + lane_at + (tile + row0 * pitch + dt * 128);
             f32x8 f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int row = row0 + 8 * (j / 4) + 4 * h + (j % 4);
-                f[j] = *(const float*)(smem + tile + offset(row, c >> 2) + (c & 3) * 4);
-            }
+            for (int j = 0; j < 8; ++j) f[j] = *(const float*)(p + (8 * (j / 4) + (j % 4)) * pitch);
             return f;
         }
     }
 };
 
-// One 16-byte load per lane straight into LDS at `lds` + 16 lane. One wait
-// state between the write of m0 and its use.
+// Calls step(buffer, position) for begin, begin + by, .. below end, the
+// buffer 0 and 1 in turn as compile-time constants (LDS addresses then differ
+// by the instructions' own offsets).
+template <int V> struct Int { static constexpr int value = V; };
+
+template <typename F>
+__device__ __forceinline__ void alternate(int begin, int end, int by, F&& step) {
+    for (int x = begin; x < end; x += by) {
+        step(Int<0>{}, x);
+        x += by;
+        if (x >= end) break;
+        step(Int<1>{}, x);
+    }
+}
+
+// One 16-byte load per lane straight into LDS at `lds` + 16 lane. The wait
+// states stand between what may have written the operands and the load: one
+// after m0, five after a vector instruction that wrote a descriptor register
+// (a read lane, a restored spill), which the compiler does not add for asm.
 __device__ __forceinline__ void load_to_lds16(const i32x4& rsrc, uint32_t lds, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :: "s"(lds), "v"(off), "s"(rsrc) : "memory");
 }
 
@@ -160,7 +197,7 @@ __device__ __forceinline__ uint32_t lds_address(int at) {
 
 // 4 bytes per lane to `lds` + 4 lane.
 __device__ __forceinline__ void load_to_lds4(const void* base, int lds, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  :: "s"(lds_address(lds)), "v"(off), "s"(descriptor(base)) : "memory");
 }
 
@@ -169,74 +206,99 @@ __device__ __forceinline__ void load_to_lds4(const void* base, int lds, uint32_t
 __device__ __forceinline__ void loads_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // Rows of a [S, H, D] slice, `pack` heads to a position: row r is position
-// r / pack, head r % pack. magic = ceil(2^20 / pack) divides numbers below
-// 2^20 / pack exactly.
+// r / pack, head r % pack.
 struct Rows {
     const char* base;
     int64_t ss, hs;   // bytes
-    int32_t pack, magic;
-    int32_t vec;      // 16-byte accesses allowed, strides fit 32-bit offsets
+    int32_t pack;
 };
-
-__device__ __forceinline__ int div_pack(int r, const Rows& w) {
-    return w.pack == 1 ? r : (int)(((uint32_t)r * (uint32_t)w.magic) >> 20);
-}
 
 constexpr uint32_t kOutside = 0x80000000u;
 
-// Rows row0 .. row0 + ROWS - 1 (zeros from `end` on) into the tile at `lds`,
-// by NW waves. i0 = row0 / pack, rem0 = row0 % pack.
-template <typename T, int DP, int ROWS, int NW>
-__device__ __forceinline__ void stage(int lds, const Rows& w, int row0, int i0, int rem0, int end, int D) {
+// A tensor's rows on their way through LDS tiles of ROWS rows, by NW waves:
+// `take` rows to a tile (whole positions; the rest of the tile is zeros), so
+// that a lane's offsets are the same for every tile and only the base moves.
+// VEC: 16-byte loads straight into LDS (aligned, a tile's offsets in 31
+// bits); otherwise element by element.
+template <typename T, int DP, int ROWS, int NW, bool VEC> struct Stream {
     typedef Tile<T, DP> TL;
-    const int lane = (int)threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const char* base = w.base + (int64_t)i0 * w.ss;
-    if (w.vec) {
-        constexpr int NI = ROWS * TL::cpr / 64 / NW;
-        static_assert(NI * 64 * NW == ROWS * TL::cpr, "whole wave instructions");
-        const i32x4 rsrc = descriptor(base);
-        const uint32_t ss = (uint32_t)w.ss, hs = (uint32_t)w.hs;
+    static constexpr int slots = ROWS * TL::chunks;
+    static constexpr int instrs = (slots + 63) / 64;
+    static constexpr int NI = (instrs + NW - 1) / NW;
+    const char* base;
+    int64_t step;
+    uint32_t off[VEC ? NI : 1];
+
+    // Slot i of this lane: wave instruction i * NW + wave.
+    static __device__ __forceinline__ void place(int wave, int lane, int i, int& row, int& chunk) {
+        const int slot = (i * NW + wave) * 64 + lane;
+        row = slot / TL::chunks;
+        chunk = (slot - row * TL::chunks) ^ TL::swizzle(row);
+    }
+
+    __device__ __forceinline__ void start(const Rows& w, int position, int take, int D, int wave, int lane) {
+        base = w.base + (int64_t)position * w.ss;
+        step = (int64_t)(take / w.pack) * w.ss;
+        if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int slot = (wave * NI + i) * 64 + lane;
-            const int lr = slot / TL::cpr;
-            const int chunk = (slot % TL::cpr) ^ TL::swizzle(lr);
-            const int di = div_pack(rem0 + lr, w);
-            const int g = rem0 + lr - di * w.pack;
-            uint32_t off = (uint32_t)di * ss + (uint32_t)g * hs + (uint32_t)chunk * 16u;
-            off = (row0 + lr < end && chunk * (16 / (int)sizeof(T)) < D) ? off : kOutside;
-            load_to_lds16(rsrc, lds_address(lds + (wave * NI + i) * 1024), off);
-        }
-    } else {
-        constexpr int VEC = 16 / (int)sizeof(T);
-        for (int slot = (int)threadIdx.x; slot < ROWS * TL::cpr; slot += NW * 64) {
-            const int lr = slot / TL::cpr;
-            const int chunk = (slot % TL::cpr) ^ TL::swizzle(lr);
-            const int di = div_pack(rem0 + lr, w);
-            const int g = rem0 + lr - di * w.pack;
-            const T* p = (const T*)(base + (int64_t)di * w.ss + (int64_t)g * w.hs);
-            T e[VEC];
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) {
-                const int d = chunk * VEC + k;
-                e[k] = T{};
-                if (row0 + lr < end && d < D) e[k] = p[d];
+            for (int i = 0; i < NI; ++i) {
+                int row, chunk;
+                place(wave, lane, i, row, chunk);
+                const int di = row / w.pack, g = row - di * w.pack;
+                const uint32_t at = (uint32_t)di * (uint32_t)w.ss + (uint32_t)g * (uint32_t)w.hs + (uint32_t)chunk * 16u;
+                off[i] = row < take && chunk < TL::cpr && chunk * (16 / (int)sizeof(T)) < D ? at : kOutside;
             }
-            __builtin_memcpy(smem + lds + slot * 16, e, 16);
         }
     }
-}
+
+    // The next tile's rows into the tile at `lds`; `left` of them are there,
+    // the others come out as zeros.
+    __device__ __forceinline__ void fetch(int lds, const Rows& w, int left, int take, int D, int wave, int lane) {
+        if constexpr (VEC) {
+            const i32x4 rsrc = descriptor(base);
+            const uint32_t to = lds_address(lds + wave * 1024);
+            if (left >= take) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    if (instrs % NW == 0 || i * NW + wave < instrs) load_to_lds16(rsrc, to + i * NW * 1024, off[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    int row, chunk;
+                    place(wave, lane, i, row, chunk);
+                    const uint32_t at = row < left ? off[i] : kOutside;
+                    if (instrs % NW == 0 || i * NW + wave < instrs) load_to_lds16(rsrc, to + i * NW * 1024, at);
+                }
+            }
+        } else {
+            constexpr int N = 16 / (int)sizeof(T);
+            for (int x = (int)threadIdx.x; x < ROWS * TL::cpr; x += NW * 64) {
+                const int row = x / TL::cpr, chunk = x - row * TL::cpr;
+                const int di = row / w.pack, g = row - di * w.pack;
+                const T* p = (const T*)(base + (int64_t)di * w.ss + (int64_t)g * w.hs);
+                T e[N];
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const int d = chunk * N + k;
+                    e[k] = T{};
+                    if (row < min(left, take) && d < D) e[k] = p[d];
+                }
+                __builtin_memcpy(smem + lds + row * TL::pitch + ((chunk ^ TL::swizzle(row)) << 4), e, 16);
+            }
+        }
+        base += step;
+    }
+};
 
 // Fragment of columns d0 .. d0 + 7 of a row in global memory; zeros past D
 // and for rows that are not there.
-template <typename T>
-__device__ __forceinline__ Frag<T> global_frag(const char* row, int d0, int D, bool vec, bool there) {
+template <typename T, bool VEC>
+__device__ __forceinline__ Frag<T> global_frag(const char* row, int d0, int D, bool there) {
     Frag<T> f;
     if constexpr (sizeof(T) == 2) {
         f = u32x4{0, 0, 0, 0};
         if (there) {
-            if (vec) {
+            if constexpr (VEC) {
                 if (d0 < D) f = *(const u32x4*)(row + d0 * 2);
             } else {
                 const uint16_t* p = (const uint16_t*)row;
@@ -251,7 +313,7 @@ __device__ __forceinline__ Frag<T> global_frag(const char* row, int d0, int D, b
         }
     } else {
         const float* p = (const float*)row;
-        if (vec) {
+        if constexpr (VEC) {
             f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
             if (there && d0 < D) lo = *(const f32x4*)(p + d0);
             if (there && d0 + 4 < D) hi = *(const f32x4*)(p + d0 + 4);
@@ -286,9 +348,8 @@ __device__ __forceinline__ float frag_dot(const Frag<T>& a, const Frag<T>& b) {
 // Writes acc[DP / 32] (columns of the output in the accumulator's rows, one
 // output row per lane column) times `mul` to the row at `row`. The two
 // halves of the lanes trade 8-byte pieces so that each stores 16 bytes.
-template <typename T, int DP>
-__device__ __forceinline__ void store_acc(char* row, const f32x16* acc, float mul, int D, bool vec, bool there,
-                                          int h) {
+template <typename T, int DP, bool VEC>
+__device__ __forceinline__ void store_acc(char* row, const f32x16* acc, float mul, int D, bool there, int h) {
 #pragma unroll
     for (int dt = 0; dt < DP / 32; ++dt) {
 #pragma unroll
@@ -305,7 +366,7 @@ __device__ __forceinline__ void store_acc(char* row, const f32x16* acc, float mu
                 const u32x4 out = {s0[0], s1[0], s0[1], s1[1]};
                 const int d = dt * 32 + a * 16 + 8 * h;
                 if (there) {
-                    if (vec) {
+                    if constexpr (VEC) {
                         if (d < D) *(u32x4*)(row + d * 2) = out;
                     } else {
 #pragma unroll
@@ -318,7 +379,7 @@ __device__ __forceinline__ void store_acc(char* row, const f32x16* acc, float mu
                 for (int b = 0; b < 2; ++b) {
                     const int d = dt * 32 + a * 16 + b * 8 + 4 * h;
                     if (there) {
-                        if (vec) {
+                        if constexpr (VEC) {
                             if (d < D) *(f32x4*)(row + d * 4) = f32x4{v[4 * b], v[4 * b + 1], v[4 * b + 2], v[4 * b + 3]};
                         } else {
 #pragma unroll
@@ -335,7 +396,7 @@ __device__ __forceinline__ void store_acc(char* row, const f32x16* acc, float mu
 // float32 rows of DP elements in the workspace.
 template <int DP>
 __device__ __forceinline__ void store_part(float* row, const f32x16* acc, float mul, bool there, int h) {
-    store_acc<float, DP>((char*)row, acc, mul, DP, true, there, h);
+    store_acc<float, DP, true>((char*)row, acc, mul, DP, there, h);
 }
 
 // ------------------------------------------------------------- the problem
@@ -361,12 +422,11 @@ struct AttnArgs {
     float* part_ml;
     float* rows;           // backward: [2][B, Hq, Sq]: log2 of the sums, delta
     float* rest;           // backward, dq split: [nsplit][B, Hq, Sq], what delta is off by
-    float* tpart;          // backward: [units * blocks * nsplit][buckets]
+    float* tpart;          // backward: [units * blocks * nsplit][entries]
     int32_t B, Sq, Sk, Hq, Hkv, D, G;
-    int32_t pack, magic, units;   // units = B * Hq / pack
+    int32_t pack, units;   // units = B * Hq / pack
     int32_t blocks, nsplit, per_split;   // row (or key) blocks per unit, splits of the other axis
     int32_t causal, table_dt, buckets;
-    int32_t vec_q, vec_k, vec_v, vec_o, vec_do, vec_out;   // vec_out: every output
     float scale;
     Borders borders;
 };
@@ -382,6 +442,10 @@ struct SumArgs {
     int32_t rows, pack, hu, D;
     float* delta;
     const float* rest;
+    // a second sum of the same shape (dv beside dk), or null
+    const float* part2;
+    char* out2;
+    Strides os2;
 };
 
 struct Work {
@@ -389,22 +453,37 @@ struct Work {
     int64_t flat;   // index of (u, split, block)
 };
 
-// Workgroup -> (unit, split, block). Workgroups go round the 8 XCDs in turn;
-// each XCD gets a contiguous run of the work, so the blocks that read one
-// key head's keys and values share an L2. Under a causal mask the blocks
-// with most to do come first.
-__device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w, bool last_first) {
+// Workgroup -> (unit, split, block). Workgroups go round the 8 XCDs in turn,
+// each of which has an L2 of its own: of every 8 units (neighbouring heads,
+// of about the same length) each XCD takes one whole, so that the blocks
+// that read one key head's keys and values share an L2 and a batch of ragged
+// lengths still spreads evenly. Units beyond a multiple of 8, and units of
+// one block, whose keys nobody else reads, go round block by block. Under a
+// causal mask the row blocks with most to do, the last, come first
+// (last_first). Key blocks are few and all resident at once, so every second
+// unit of an XCD takes them in the other order (turn): a CU then holds a long
+// and a short one.
+__device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w, bool last_first, bool turn) {
     const int per_unit = a.blocks * a.nsplit;
-    const int64_t total = (int64_t)a.units * per_unit;
-    const int64_t chunk = (total + 7) / 8;
-    const int64_t t = (int64_t)(blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
-    if ((int64_t)(blockIdx.x >> 3) >= chunk || t >= total) return false;
-    w.flat = t;
-    w.u = (int)(t / per_unit);
-    const int rem = (int)(t - (int64_t)w.u * per_unit);
+    const int64_t bid = blockIdx.x;
+    const int whole = a.blocks > 1 ? a.units / 8 * 8 : 0;
+    int rem;
+    if (bid < (int64_t)whole * per_unit) {
+        const int i = (int)(bid >> 3);
+        const int k = i / per_unit;
+        w.u = k * 8 + (int)(bid & 7);
+        rem = i - k * per_unit;
+    } else {
+        const int i = (int)(bid - (int64_t)whole * per_unit);
+        const int k = i / per_unit;
+        w.u = whole + k;
+        rem = i - k * per_unit;
+    }
+    if (w.u >= a.units) return false;
+    w.flat = (int64_t)w.u * per_unit + rem;
     w.split = rem / a.blocks;
     w.block = rem - w.split * a.blocks;
-    if (last_first) w.block = a.blocks - 1 - w.block;
+    if (last_first || (turn && (w.u >> 3 & 1))) w.block = a.blocks - 1 - w.block;
     const int hu = a.Hq / a.pack;
     w.b = w.u / hu;
     w.head = (w.u - w.b * hu) * a.pack;
@@ -417,36 +496,37 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w, bool last_
     return true;
 }
 
-__device__ __forceinline__ int bucket_of(const Borders& o, int rel) {
-    int d = max(-rel, 0), first = 0;
-    if (o.bidirectional) {
-        d = abs(rel);
-        first = rel > 0 ? o.n : 0;
-    }
-    int b = min(d, o.e - 1);
-    for (int t = o.e; t < o.n; ++t) b += d >= o.at[t] ? 1 : 0;
-    return first + b;
-}
-
 // The bias by relative position, in log2 units, in LDS at float index
 // rel + reach + kPad for rel within reach + kPad of 0. A 32 x 32 tile that
 // touches (-reach, reach) stays inside; all others have one bias.
 constexpr int kPad = 64;
-constexpr int kColBytes = DYT_ATTN_MAX_BUCKETS * 4;   // LDS for the table's column, before the entries
-
 __device__ __forceinline__ int bias_entries(const Borders& o) { return 2 * (o.reach + kPad); }
 
-// `col` has room for the table's column: one load per bucket, then the
-// positions gather from LDS (a dependent global load per position took 6 us
-// of a small problem's kernel). Ends in a barrier's need: the caller's next
-// barrier makes the entries visible.
-__device__ __forceinline__ void fill_bias(float* lds, float* col, const AttnArgs& a, int head) {
-    const int n = bias_entries(a.borders);
-    for (int x = (int)threadIdx.x; x < a.buckets; x += (int)blockDim.x)
-        col[x] = load_param(a.table, (int64_t)x * a.Hq + head, a.table_dt) * kLog2e;
-    __syncthreads();
-    for (int x = (int)threadIdx.x; x < n; x += (int)blockDim.x)
-        lds[x] = col[bucket_of(a.borders, x - a.borders.reach - kPad)];
+// Entries [lo, hi) of bucket t.
+__device__ __forceinline__ void bucket_range(const Borders& o, int t, int& lo, int& hi) {
+    const int mid = o.reach + kPad;   // entry of position 0
+    const bool later = t >= o.n;      // bidirectional: keys after the query
+    const int u = later ? t - o.n : t;
+    const int from = o.at[u], to = o.at[min(u + 1, o.n - 1)];
+    const bool last = u + 1 == o.n;
+    if (later) {
+        lo = mid + max(from, 1);   // distance 0 is the other direction's
+        hi = last ? 2 * mid : mid + to;
+    } else {
+        lo = last ? 0 : mid - to + 1;
+        hi = t == 0 && !o.bidirectional ? 2 * mid : mid - from + 1;   // every later key
+    }
+}
+
+// A thread per bucket writes its run of entries (a search per entry through
+// the borders took 6 us of a small problem's kernel, this takes under 1).
+__device__ __forceinline__ void fill_bias(float* lds, const AttnArgs& a, int head) {
+    for (int t = (int)threadIdx.x; t < a.buckets; t += (int)blockDim.x) {
+        const float x = load_param(a.table, (int64_t)t * a.Hq + head, a.table_dt) * kLog2e;
+        int lo, hi;
+        bucket_range(a.borders, t, lo, hi);
+        for (int i = lo; i < hi; ++i) lds[i] = x;
+    }
 }
 
 __device__ __forceinline__ int acc_row(int i, int h) { return 8 * (i / 4) + 4 * h + (i % 4); }
