@@ -35,7 +35,8 @@ BLOCK_SOURCES = [os.path.join(CSRC, "block_api.hip"), os.path.join(CSRC, "attn_a
     for t in ("f32", "bf16", "f16")]
 BLOCK_DEPENDS = BLOCK_SOURCES + [os.path.join(CSRC, f) for f in (
     "block_common.hpp", "block_host.hpp", "ln_kernels.hpp", "ln_launch.hpp", "ln_launch_impl.hpp",
-    "attn_tile.hpp", "attn_fwd.hpp", "attn_bwd.hpp", "attn_launch.hpp", "dyt_math.hpp")] + [
+    "attn_tile.hpp", "attn_fwd.hpp", "attn_bwd.hpp", "attn_launch.hpp", "attn_launch_fwd.hpp",
+    "attn_launch_dq.hpp", "attn_launch_dkv.hpp", "dyt_math.hpp")] + [
     os.path.join(INCLUDE, "dyt.h"), os.path.join(INCLUDE, "dyt_block.h")]
 # Reference streaming kernels for bench.py's measured ceilings (not part of
 # the DyT ABI; nothing in the package loads them).

@@ -81,6 +81,9 @@ bool view(const dyt_attn_desc& d, const Tensor& t, bool out, Strides& s, int64_t
     const int64_t es = dtype_size(d.dtype);
     const int64_t size[3] = {d.B, t.S, t.H}, stride[3] = {t.st->b, t.st->s, t.st->h};
     int64_t bytes[3];
+    s = Strides{0, 0, 0};
+    span = 0;
+    if (!size[0] || !size[1] || !size[2]) return true;
     span = d.D * es;
     for (int i = 0; i < 3; ++i) {
         bytes[i] = 0;
@@ -347,6 +350,7 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
             if (outs[i].bytes && outs[j].bytes && outs[i].p == outs[j].p) return DYT_ERR_INVALID_ARG;
     }
     if (!disjoint(in, 9, rest, 2)) return DYT_ERR_INVALID_ARG;
+    if (p.nothing_out && p.nothing_keys && !(d.table && d.Hq > 0)) return DYT_OK;
 
     const hipStream_t s = (hipStream_t)stream;
     fill_args(d, p, a);

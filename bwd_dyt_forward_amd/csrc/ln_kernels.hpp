@@ -195,7 +195,7 @@ __global__ __launch_bounds__(LnShape<TPR>::threads) void ln_fwd_kernel(LnArgs a)
             for (int e = 0; e < E; ++e) s += x[u][e];
             s = lanes_sum<S::L>(s);
             if constexpr (S::waves == 1) {
-                mean[u] = s * inv_n;
+                mean[u] = s / (float)N;   // not times 1 / N: a row of one value gets it as its mean
             } else {
                 // columns of this wave
                 int cnt = 0;
@@ -241,7 +241,7 @@ __global__ __launch_bounds__(LnShape<TPR>::threads) void ln_fwd_kernel(LnArgs a)
                     cw[k] = (float)cnt;
                     mt += cw[k] * red[buf][u][k][0];
                 }
-                mt *= inv_n;
+                mt /= (float)N;
 #pragma unroll
                 for (int k = 0; k < S::waves; ++k) {
                     const float d = red[buf][u][k][0] - mt;
@@ -314,7 +314,7 @@ __global__ __launch_bounds__(kLongThreads) void ln_fwd_long_kernel(LnArgs a) {
             for (int i = 0; i < VEC; ++i) s += x[i];
         }
         if constexpr (RES) src = (const T*)a.h;   // each thread reads back its own stores
-        const float mean = block_sum(s, red) * inv_n;
+        const float mean = block_sum(s, red) / (float)N;
         float q = 0.0f;
         for (int c = (int)threadIdx.x * VEC; c < N; c += kLongThreads * VEC) {
             float x[VEC];
