@@ -133,37 +133,76 @@ struct Plan {
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// Waves per workgroup and splits of the long axis. Workgroups of four waves
-// share each tile of the long axis; single waves each bring their own, which
-// the L2 only keeps up with while they are few. So four waves wherever their
-// workgroups, with the long axis cut into runs of 1,024, would fill the 256
-// CUs, and single waves below (and for up to 32 rows, one wave's). The
-// number of splits is then the power of two that minimises
-//   tiles per split * max(lat, waves per SIMD * busy)
-//   + 6 us for the join's launch and 0.1 us for each part it reads:
-// a wave alone on its SIMD takes `lat` for 32 steps of the long axis (the
-// chain of loads, products and exponentials), and a SIMD is `busy` with them.
-void choose(int64_t units, int64_t rows, int64_t len, int pack, int tile4, double lat, double busy, AttnPick& pick,
-            int& blocks, int& split, int& per) {
+// How a kernel's work is cut. Workgroups of four row groups share each tile
+// of the long axis; smaller ones each bring their own, which the L2 only
+// keeps up with while they are few. So four wherever their workgroups, with
+// the long axis cut into runs of 1,024, would fill the 256 CUs, and one
+// below (and for up to 32 rows, one group's).
+//
+// Those of one row group may have 2 or 4 slices, and the long axis may be
+// cut into a power of two of splits; the pair is taken that minimises
+//   rounds * steps * max(lat, waves per SIMD * busy) + join,
+// steps of 32 per slice, rounds of the workgroups that the LDS of 256 CUs
+// holds (several slices: all of a workgroup's waves end together). A wave
+// alone on its SIMD takes `lat` for a step (the chain of loads, products and
+// exponentials), and a SIMD is `busy` with it. Slices join in LDS (0.5 us a
+// pair), splits in a launch of its own (6 us, 0.1 us for each part it reads).
+struct Shape {
+    int es, dp, pack;
+    int extra, extra_wave;   // LDS of the bias: of a workgroup, of each wave
+    bool dkv;
+    double lat, busy;
+    int tile(int nw, int sl) const {
+        return (dkv ? attn_dkv_tile_rows(es, dp, nw, sl) : attn_tile_rows(es, nw, sl)) / pack * pack;   // whole positions
+    }
+    int lds(int nw, int sl) const {
+        return (dkv ? attn_dkv_lds_bytes(es, dp, nw, sl) : attn_lds_bytes(es, dp, nw, sl)) + extra + extra_wave * nw * sl;
+    }
+};
+
+void choose(const Shape& h, int64_t units, int64_t rows, int64_t len, AttnPick& pick, int& blocks, int& split, int& per) {
     const int64_t b4 = units * ((rows + 127) / 128);
-    int& nw = pick.nw;
-    nw = pick.vec && rows > 32 && b4 * std::max<int64_t>(1, len / 1024) >= 256 ? 4 : 1;
-    const int tile = (nw == 4 ? tile4 : 32) / pack * pack;   // whole positions of the long axis' rows
+    pick.nw = pick.vec && rows > 32 && b4 * std::max<int64_t>(1, len / 1024) >= 256 ? 4 : 1;
+    const int nw = pick.nw;
     blocks = ceil_div(rows, 32 * nw);
-    const double waves = (double)units * blocks * nw;
-    const int64_t tiles = std::max<int64_t>(1, ceil_div(len, tile));
+    const double groups = (double)units * blocks;
     double best = 0.0;
     int64_t parts = 1;
-    for (int64_t n = 1; n == 1 || (n <= 64 && n * 4 <= tiles); n *= 2) {
-        const double t = ceil_div(tiles, n) * ((tile + 31) / 32) * std::max(lat, waves * n / 1024.0 * busy) +
-                         (n > 1 ? 6.0 + 0.1 * n : 0.0);
-        if (n == 1 || t < best) {
-            best = t;
-            parts = n;
+    pick.sl = 1;
+    // two slices of 16-bit dk/dv workgroups wherever they fit
+    const int lo = nw == 4 && h.dkv && h.es == 2 && h.lds(4, 2) <= kMaxLds ? 2 : 1;
+    const int hi = nw == 4 ? lo : pick.vec ? 4 : 1;
+    for (int sl = lo; sl <= hi; sl *= 2) {
+        if (h.lds(nw, sl) > kMaxLds || (sl == 4 && attn_lds_bytes(h.es, h.dp, 1, 4) > kMaxLds)) break;
+        const int tile = h.tile(nw, sl), steps = (tile + 32 * sl - 1) / (32 * sl);
+        const int64_t tiles = std::max<int64_t>(1, ceil_div(len, tile));
+        const double resident = 256.0 * (kMaxLds / h.lds(nw, sl));
+        for (int64_t n = 1; n == 1 || (n <= 64 && n * 4 <= tiles); n *= 2) {
+            double at_once = groups * n, rounds = 1.0;
+            if (nw == 1 && sl > 1 && at_once > resident) {
+                rounds = std::ceil(at_once / resident);
+                at_once = resident;
+            }
+            const double t = rounds * ceil_div(tiles, n) * steps * std::max(h.lat, at_once * nw * sl / 1024.0 * h.busy) +
+                             0.5 * (sl - 1) + (n > 1 ? 6.0 + 0.1 * n : 0.0);
+            if (best == 0.0 || t < best) {
+                best = t;
+                parts = n;
+                pick.sl = sl;
+            }
         }
     }
-    per = ceil_div(tiles, parts) * tile;
+    const int tile = h.tile(nw, pick.sl);
+    per = ceil_div(ceil_div(len, tile), parts) * tile;
+    per = std::max(per, tile);
     split = std::max(1, ceil_div(len, per));
+}
+
+// Units an XCD takes at a time under a causal mask (find_work): as many as
+// give each of its 32 CUs four workgroups.
+int units_together(const AttnArgs& a) {
+    if (!a.causal) return 1;
+    return std::max(1, std::min(a.units / 8, 128 / (a.blocks * a.nsplit)));
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -193,19 +232,20 @@ Plan make_plan(const dyt_attn_desc& d, bool vec) {
             if (G % n == 0) p.pack = n;
     p.units = (int)(d.B * (d.Hq / p.pack));
     p.rows = d.Sq * p.pack;
-    const int dp = attn_dp(d.D), tile = d.dtype == DYT_F32 ? 32 : 64;
-    p.fwd = p.dq = p.dkv = {dp, 1, d.table != nullptr, vec};
+    const int dp = attn_dp(d.D), es = (int)dtype_size(d.dtype);
+    p.fwd = p.dq = p.dkv = {dp, 1, 1, d.table != nullptr, vec};
     // us per 32 keys (rows), measured at D = 32 (float32: the matrix cores'
     // rate) and, 16-bit, much the same up to 128
     const double f = d.dtype == DYT_F32 ? 2.2 * dp / 32 : 0.0;
+    const int bias = d.table ? bias_lds_bytes(p.borders) : 0, dbias = d.table ? dbias_lds_bytes(p.borders, 1) : 0;
     if (!p.nothing_out) {
-        choose(p.units, p.rows, d.Sk, 1, tile, std::max(f, 0.8), std::max(f, 0.4), p.fwd, p.fwd_blocks, p.fwd_split,
-               p.fwd_per);
-        choose(p.units, p.rows, d.Sk, 1, tile, std::max(1.2 * f, 0.9), std::max(1.2 * f, 0.6), p.dq, p.dq_blocks,
-               p.dq_split, p.dq_per);
+        choose({es, dp, 1, bias, 0, false, std::max(f, 0.8), std::max(f, 0.4)}, p.units, p.rows, d.Sk, p.fwd,
+               p.fwd_blocks, p.fwd_split, p.fwd_per);
+        choose({es, dp, 1, bias, 0, false, std::max(1.2 * f, 0.9), std::max(1.2 * f, 0.6)}, p.units, p.rows, d.Sk, p.dq,
+               p.dq_blocks, p.dq_split, p.dq_per);
     }
     if (!p.nothing_keys && d.Hq > 0)
-        choose(p.units, d.Sk, p.rows, p.pack, attn_dkv_tile(d.dtype, dp), std::max(1.7 * f, 1.2), std::max(1.7 * f, 0.9),
+        choose({es, dp, p.pack, bias, dbias, true, std::max(1.7 * f, 1.2), std::max(1.7 * f, 0.9)}, p.units, d.Sk, p.rows,
                p.dkv, p.dkv_blocks, p.dkv_split, p.dkv_per);
     const int64_t part_rows = p.units * p.rows * (int64_t)dp * 4;
     if (p.fwd_split > 1) p.fwd_bytes = round256((size_t)p.fwd_split * part_rows) + (size_t)p.fwd_split * p.units * p.rows * 8;
@@ -302,6 +342,7 @@ int dyt_attn_forward(const dyt_attn_desc* desc, const void* q, const void* k, co
     fill_args(d, p, a);
     a.q = (const char*)q; a.k = (const char*)k; a.v = (const char*)v; a.out = (char*)o; a.stats = stats;
     a.blocks = p.fwd_blocks; a.nsplit = p.fwd_split; a.per_split = p.fwd_per;
+    a.together = units_together(a);
     a.part = (float*)workspace;
     a.part_ml = (float*)((char*)workspace + round256((size_t)p.fwd_split * p.units * p.rows * p.fwd.dp * 4));
     return with_type(d.dtype, [&](auto* t) {
@@ -367,6 +408,7 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
         const int dp = p.dq.dp;
         if (!p.nothing_out) {
             a.blocks = p.dq_blocks; a.nsplit = p.dq_split; a.per_split = p.dq_per;
+            a.together = units_together(a);
             if (int st = attn_launch_dq<T>(p.dq, a, s)) return st;
             if (p.dq_split > 1) {
                 const int64_t total = (int64_t)p.units * p.rows;
@@ -391,6 +433,7 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
                 return hip_status();
             }
             a.blocks = p.dkv_blocks; a.nsplit = p.dkv_split; a.per_split = p.dkv_per;
+            a.together = units_together(a);
             if (int st = attn_launch_dkv<T>(p.dkv, a, s)) return st;
             if (p.dkv_parts > 1) attn_launch_sum<T>(dp, sums, s);
         }

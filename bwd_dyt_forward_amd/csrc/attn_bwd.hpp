@@ -24,8 +24,7 @@
 // Bias gradient (dkv kernel): tiles beyond the reach of the last bucket add
 // to one sum per lane. In the others the pairs of one relative position form
 // a diagonal: each lane writes its 16 values of dS into a wave's scratch at
-// [key - query + 31][key] (the positions are the same for every tile, the
-// rest of the scratch stays zero), then lane t adds up diagonal t - 31 and
+// [(key - query + 31) % 32][key], then lane t adds up diagonal t - 31 and
 // adds the sum to the wave's array of sums by relative position. At the end
 // the waves' arrays are joined in wave order and left in the workspace, one
 // row per workgroup; attn_dtable_kernel sums each bucket's run of positions.
@@ -35,43 +34,19 @@
 
 namespace dytb {
 
-constexpr int kDiagPitch = 33;
-constexpr int kDiagFloats = 64 * kDiagPitch;
-
-template <typename T, int NW> struct BwdTile { static constexpr int rows = sizeof(T) == 2 && NW > 1 ? 64 : 32; };
-
-// The dk/dv kernel holds 4 DP / 32 accumulators and its keys' and values'
-// fragments. Above D = 64 that leaves room for one wave per SIMD; with the
-// values' fragments in LDS (which has bandwidth to spare) two fit, and hide
-// each other's waits. Tiles of 32 rows then keep two workgroups' LDS in a CU.
-template <typename T, int DP, int NW>
-constexpr bool dkv_vals_in_lds() { return sizeof(T) == 2 && DP > 64; }
-template <typename T, int DP, int NW> struct DkvTile {
-    static constexpr int rows = dkv_vals_in_lds<T, DP, NW>() ? 32 : BwdTile<T, NW>::rows;
-};
-template <typename T, int DP, int NW>
-constexpr int dkv_lds_bytes() {
-    return 2 * 2 * Tile<T, DP>::bytes(DkvTile<T, DP, NW>::rows) + 1024 +
-           (dkv_vals_in_lds<T, DP, NW>() ? NW * (DP / 16) * 1024 : 0);
-}
-
-template <typename T, int DP, int NW>
-constexpr int bwd_lds_bytes() { return 2 * 2 * Tile<T, DP>::bytes(BwdTile<T, NW>::rows); }
-
-// LDS floats of the bias gradient.
-inline __host__ __device__ int dbias_floats(int entries, int nw) { return nw * (kDiagFloats + entries); }
-
-template <typename T, int DP, int NW, bool BIAS, bool VEC>
-__global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dq_kernel(AttnArgs a) {
+template <typename T, int DP, int NW, int SL, bool BIAS, bool VEC>
+__global__ __launch_bounds__(NW * SL * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dq_kernel(AttnArgs a) {
+    static_assert(NW == 1 || SL == 1);
     typedef Tile<T, DP> TL;
-    constexpr int KT = BwdTile<T, NW>::rows;
-    constexpr int NS = KT / 32, KB = TL::bytes(KT);
+    constexpr int KT = attn_tile_rows(sizeof(T), NW, SL);
+    constexpr int NS = KT / 32 / SL, KB = TL::bytes(KT);
     Work w;
-    if (!find_work(a, w, a.causal != 0, false)) return;
+    if (!find_work(a, w, true)) return;
     const int lane = (int)threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int sl = SL > 1 ? wave : 0;   // this wave's slice: keys 32 sl .. 32 sl + 31 of each tile
     const int rows = a.Sq * a.pack;
-    const int row0 = (w.block * NW + wave) * 32;
+    const int row0 = (w.block * NW + (SL > 1 ? 0 : wave)) * 32;
     const int row = row0 + (lane & 31);
     const bool there = row < rows;
     const int rr = min(row, rows - 1);
@@ -87,14 +62,16 @@ __global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dq_ker
     const Rows vr = {a.v + w.b * a.vs.b + w.kv * a.vs.h, a.vs.s, 0, 1};
     const float c = a.scale * kLog2e;
 
-    Stream<T, DP, KT, NW, VEC> ks, vs;
+    Stream<T, DP, KT, NW * SL, VEC> ks, vs;
     ks.start(kr, begin, KT, a.D, wave, lane);
     vs.start(vr, begin, KT, a.D, wave, lane);
     if (begin < end) {
         ks.fetch(0, kr, end - begin, KT, a.D, wave, lane);
         vs.fetch(2 * KB, vr, end - begin, KT, a.D, wave, lane);
     }
-    const int row_at = TL::row_lane(lane), col_at = TL::col_lane(lane, 0), col_at8 = TL::col_lane(lane, 8);
+    const int mine = sl * 32 * TL::pitch;
+    const int row_at = TL::row_lane(lane) + mine, col_at = TL::col_lane(lane, 0) + mine;
+    const int col_at8 = TL::col_lane(lane, 8) + mine;
     float* bias = (float*)(smem + 4 * KB);
     if constexpr (BIAS) fill_bias(bias, a, w.head);
 
@@ -135,11 +112,12 @@ __global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dq_ker
             vs.fetch(2 * KB + (buf ^ 1) * KB, vr, end - j0 - KT, KT, a.D, wave, lane);
         }
         constexpr int kt = buf * KB, vt = kt + 2 * KB;
+        const int first = j0 + sl * 32;
         // (a branch around a single sub-tile would have the accumulators copied)
-        if (row0 >= rows || (a.causal && j0 > w.start + imax)) return;
+        if (row0 >= rows || (SL > 1 && first >= end) || (a.causal && first > w.start + imax)) return;
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-            const int js = j0 + n * 32;
+            const int js = first + n * 32;
             f32x16 s, dp;
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
@@ -187,6 +165,18 @@ __global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dq_ker
             }
         }
     });
+    // rest is what delta is too small by (rounded o): the dkv kernel takes the sum
+    rest = swap32_other_sum(rest);
+    if constexpr (SL > 1) {
+        float* stat = (float*)(smem + SL * DP * 128);   // [SL][32 rows], past the boxes
+        __syncthreads();
+        if (h == 0) stat[sl * 32 + lane] = rest;
+        join_slices<DP, 1, SL>(dq, 0, sl, 0, lane);
+        if (sl) return;
+        rest = 0.0f;
+#pragma unroll
+        for (int k = 0; k < SL; ++k) rest += stat[k * 32 + (lane & 31)];
+    }
     if (row0 < rows) {
         if (a.nsplit == 1) {
             char* out = a.dq + w.b * a.dqs.b + (int64_t)pos_i * a.dqs.s + (int64_t)(w.head + g) * a.dqs.h;
@@ -196,8 +186,6 @@ __global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dq_ker
             store_part<DP>(a.part + at * DP, dq, a.scale, there, h);
         }
     }
-    // rest is what delta is too small by (rounded o): the dkv kernel takes the sum
-    rest = swap32_other_sum(rest);
     if (there && h == 0) {
         const int64_t at = ((int64_t)w.b * a.Hq + w.head + g) * a.Sq + pos_i, all = (int64_t)a.B * a.Hq * a.Sq;
         if (w.split == 0) {
@@ -208,18 +196,20 @@ __global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dq_ker
     }
 }
 
-template <typename T, int DP, int NW, bool BIAS, bool VEC>
-__global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dkv_kernel(AttnArgs a) {
+template <typename T, int DP, int NW, int SL, bool BIAS, bool VEC>
+__global__ __launch_bounds__(NW * SL * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dkv_kernel(AttnArgs a) {
     typedef Tile<T, DP> TL;
-    constexpr int RT = DkvTile<T, DP, NW>::rows;
-    constexpr bool VLDS = dkv_vals_in_lds<T, DP, NW>();
-    constexpr int NS = RT / 32, RB = TL::bytes(RT);
+    constexpr int RT = attn_dkv_tile_rows(sizeof(T), DP, NW, SL), SR = RT > 64 ? RT : 64;
+    constexpr bool VLDS = dkv_vals_in_lds(sizeof(T), DP);
+    constexpr int NS = RT / 32 / SL, RB = TL::bytes(RT), W = NW * SL;
     Work w;
-    if (!find_work(a, w, false, a.causal != 0)) return;
+    if (!find_work(a, w, false)) return;
     const int lane = (int)threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int rows = a.Sq * a.pack;
-    const int key0 = (w.block * NW + wave) * 32;
+    const int kw = W == NW ? wave : wave % NW;   // this wave's keys of the workgroup's
+    const int sl = W == NW ? 0 : wave / NW;      // and its slice of each tile's rows
+    const int key0 = (w.block * NW + kw) * 32;
     const int key = key0 + (lane & 31);
     const bool there = key < w.len;
     const float c = a.scale * kLog2e;
@@ -238,35 +228,38 @@ __global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dkv_ke
     const Rows dr = {a.dout + w.b * a.dos.b + w.head * a.dos.h, a.dos.s, a.dos.h, a.pack};
     const int64_t row_at = ((int64_t)w.b * a.Hq + w.head) * a.Sq;
     const int64_t rows_all = (int64_t)a.B * a.Hq * a.Sq;
-    constexpr int kStat = 4 * RB;   // [2 buffers][lse, delta][64]
+    constexpr int kStat = 4 * RB;   // [2 buffers][lse, delta][SR]
     const int entries = BIAS ? bias_entries(a.borders) : 0;
-    constexpr int kVals = kStat + 1024;   // [NW][DP / 16][64 lanes] fragments
-    float* bias = (float*)(smem + dkv_lds_bytes<T, DP, NW>());
+    constexpr int kVals = kStat + SR * 16;   // [NW][DP / 16][64 lanes] fragments
+    float* bias = (float*)(smem + attn_dkv_lds_bytes(sizeof(T), DP, NW, SL));
     float* diag = bias + entries + wave * kDiagFloats;
-    float* sums = bias + entries + NW * kDiagFloats;   // [NW][entries]
+    float* sums = bias + entries + W * kDiagFloats;   // [W][entries]
     float far_before = 0.0f, far_behind = 0.0f;
     if constexpr (BIAS) {
         fill_bias(bias, a, w.head);
-        for (int x = lane; x < kDiagFloats; x += 64) diag[x] = 0.0f;
         for (int x = lane; x < entries; x += 64) sums[wave * entries + x] = 0.0f;
     }
 
-    Stream<T, DP, RT, NW, VEC> qs, dos;
+    Stream<T, DP, RT, W, VEC> qs, dos;
     int at_pos = begin / a.pack;   // position of the tile being fetched, then of the one worked on
     qs.start(qr, at_pos, take, a.D, wave, lane);
     dos.start(dr, at_pos, take, a.D, wave, lane);
-    const int row_lane = TL::row_lane(lane), col_at = TL::col_lane(lane, 0), col_at8 = TL::col_lane(lane, 8);
+    const int mine = sl * NS * 32 * TL::pitch;
+    const int row_lane = TL::row_lane(lane) + mine, col_at = TL::col_lane(lane, 0) + mine;
+    const int col_at8 = TL::col_lane(lane, 8) + mine;
     // log sums and delta of a tile: rows that are not there get 0, and as
     // their dO and q are zeros they add nothing
-    const int lane_pos = lane / a.pack;
-    const uint32_t stat_off = lane < take ? (uint32_t)((lane - lane_pos * a.pack) * a.Sq + lane_pos) * 4u : kOutside;
+    const int stat_row = (W > 1 ? (wave >> 1) * 64 : 0) + lane, stat_pos = stat_row / a.pack;
+    const uint32_t stat_off =
+        stat_row < take ? (uint32_t)((stat_row - stat_pos * a.pack) * a.Sq + stat_pos) * 4u : kOutside;
     const auto bring = [&](int r0, int pos0, int to) __attribute__((always_inline)) {
         qs.fetch(to * RB, qr, end - r0, take, a.D, wave, lane);
         dos.fetch(2 * RB + to * RB, dr, end - r0, take, a.D, wave, lane);
-        if (wave < 2) {
-            for (int k = wave; k < 2; k += NW < 2 ? 1 : 2)
-                load_to_lds4(a.rows + k * rows_all + row_at + pos0, kStat + to * 512 + k * 256,
-                             r0 + lane < end ? stat_off : kOutside);
+        // 64 rows of one of the two to a wave (both to a single wave)
+        if (W == 1 || wave < SR / 32) {
+            for (int k = wave & 1; k < 2; k += W == 1 ? 1 : 2)
+                load_to_lds4(a.rows + k * rows_all + row_at + pos0, kStat + (to * 2 + k) * SR * 4 + (wave >> 1) * 256,
+                             r0 + stat_row < end ? stat_off : kOutside);
         }
     };
     if (begin < end) bring(begin, at_pos, 0);
@@ -280,8 +273,11 @@ __global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dkv_ke
         for (int ds = 0; ds < DP / 16; ++ds) {
             kf[ds] = global_frag<T, VEC>(pk, ds * 16 + 8 * h, a.D, there);
             const Frag<T> f = global_frag<T, VEC>(pv, ds * 16 + 8 * h, a.D, there);
-            if constexpr (VLDS) *(Frag<T>*)(smem + kVals + (wave * (DP / 16) + ds) * 1024 + lane * 16) = f;
-            else vf[ds] = f;
+            if constexpr (VLDS) {
+                if (sl == 0) *(Frag<T>*)(smem + kVals + (kw * (DP / 16) + ds) * 1024 + lane * 16) = f;
+            } else {
+                vf[ds] = f;
+            }
         }
     }
     f32x16 dk[DP / 32], dv[DP / 32];
@@ -294,8 +290,8 @@ __global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dkv_ke
     int sub_first[NS], sub_last[NS];
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
-        sub_first[n] = n * 32 / a.pack;
-        sub_last[n] = min(n * 32 + 31, take - 1) / a.pack;
+        sub_first[n] = (sl * NS + n) * 32 / a.pack;
+        sub_last[n] = min((sl * NS + n) * 32 + 31, take - 1) / a.pack;
     }
     const int last_pos = end / a.pack - 1;
     alternate(begin, end, take, [&](auto which, int r0) __attribute__((always_inline)) {
@@ -310,7 +306,7 @@ __global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dkv_ke
         if (key0 >= w.len || (a.causal && key0 > w.start + min(pos0 + sub_last[NS - 1], last_pos))) return;
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-            const int rs = r0 + n * 32;
+            const int rs = r0 + (sl * NS + n) * 32;
             const int imin = w.start + pos0 + sub_first[n];   // positions
             const int imax = w.start + max(min(pos0 + sub_last[n], last_pos), pos0 + sub_first[n]);
             f32x16 s, dp;
@@ -319,10 +315,11 @@ __global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dkv_ke
 #pragma unroll
             for (int ds = 0; ds < DP / 16; ++ds) {
                 s = mma<T>(TL::row_frag(row_lane, qt, n, ds), kf[ds], s);
-                const Frag<T> vd = VLDS ? *(const Frag<T>*)(smem + kVals + (wave * (DP / 16) + ds) * 1024 + lane * 16) : vf[VLDS ? 0 : ds];
+                const Frag<T> vd = VLDS ? *(const Frag<T>*)(smem + kVals + (kw * (DP / 16) + ds) * 1024 + lane * 16)
+                                        : vf[VLDS ? 0 : ds];
                 dp = mma<T>(TL::row_frag(row_lane, ot, n, ds), vd, dp);
             }
-            const float* st = (const float*)(smem + kStat + buf * 512) + n * 32 + 4 * h;
+            const float* st = (const float*)(smem + kStat + buf * SR * 8) + (sl * NS + n) * 32 + 4 * h;
             float p[16];
             const int reach = a.borders.reach, after = a.borders.bidirectional ? reach : 0;
             const bool far_after = key0 - imax >= after;
@@ -361,19 +358,25 @@ __global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dkv_ke
                     dv[dt] = mma<T>(TL::col_frag(col_at, col_at8, ot, n * 32 + k * 16, dt), pf, dv[dt]);
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) p[i] *= dp[i] - st[64 + 8 * (i / 4) + (i % 4)];
+            for (int i = 0; i < 16; ++i) p[i] *= dp[i] - st[SR + 8 * (i / 4) + (i % 4)];
             if constexpr (BIAS) {
                 // rows past the end have q = dO = 0 and delta = 0: dS = 0
                 if (near) {
-                    float* at = diag + (31 - 4 * h + (lane & 31)) * kDiagPitch + (lane & 31);
+                    // diagonal t = key - query + 31 has its elements in columns (keys)
+                    // 0 .. t, diagonal t + 32 in t + 1 .. 31: they share row t
+                    const int t0 = 31 - 4 * h + (lane & 31);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) at[-(8 * (i / 4) + (i % 4)) * kDiagPitch] = p[i];
+                    for (int i = 0; i < 16; ++i)
+                        diag[((t0 - 8 * (i / 4) - (i % 4)) & 31) * kDiagPitch + (lane & 31)] = p[i];
                     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
                     __builtin_amdgcn_wave_barrier();
                     float d = 0.0f;
+                    const uint32_t low = (2u << (lane & 31)) - 1u, mask = h ? ~low : low;   // its columns
+                    const float* from = diag + (lane & 31) * kDiagPitch;
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) d += diag[lane * kDiagPitch + x];
-                    // lane 63 has no diagonal: its row of the scratch is never written
+                    for (int x = 0; x < 32; ++x)
+                        d += __uint_as_float(__float_as_uint(from[x]) & (uint32_t)__builtin_amdgcn_sbfe((int)mask, x, 1));
+                    // lane 63 has no diagonal: d = 0
                     float* to = sums + wave * entries + (key0 - (w.start + rs) + reach + kPad - 31 + lane);
                     if (lane < 63) *to += d;
                     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -403,25 +406,32 @@ __global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dkv_ke
             sums[wave * entries + entries - 1] += far_behind;
         }
         __syncthreads();
-        for (int x = (int)threadIdx.x; x < entries; x += NW * 64) {
+        for (int x = (int)threadIdx.x; x < entries; x += W * 64) {
             float s = sums[x];
-            for (int k = 1; k < NW; ++k) s += sums[k * entries + x];
+            for (int k = 1; k < W; ++k) s += sums[k * entries + x];
             a.tpart[w.flat * entries + x] = s;
         }
     }
+    if constexpr (SL > 1) {
+        join_slices<DP, NW, SL>(dk, kw, sl, 0, lane);
+        join_slices<DP, NW, SL>(dv, kw, sl, 1, lane);
+        if (sl > 1) return;
+    }
     if (key0 >= a.Sk) return;
     const bool in = key < a.Sk;
+    // (of several slices, the first holds dk and the second dv)
+    const bool has_dk = SL == 1 || sl == 0, has_dv = SL == 1 || sl == 1;
     const int parts = a.nsplit * (a.G / a.pack);   // float32 parts of each key head
     if (parts == 1) {
         const int64_t kk = min(key, a.Sk - 1);
-        store_acc<T, DP, VEC>(a.dk + w.b * a.dks.b + kk * a.dks.s + w.kv * a.dks.h, dk, a.scale, a.D, in, h);
-        store_acc<T, DP, VEC>(a.dv + w.b * a.dvs.b + kk * a.dvs.s + w.kv * a.dvs.h, dv, 1.0f, a.D, in, h);
+        if (has_dk) store_acc<T, DP, VEC>(a.dk + w.b * a.dks.b + kk * a.dks.s + w.kv * a.dks.h, dk, a.scale, a.D, in, h);
+        if (has_dv) store_acc<T, DP, VEC>(a.dv + w.b * a.dvs.b + kk * a.dvs.s + w.kv * a.dvs.h, dv, 1.0f, a.D, in, h);
     } else {
         // [part][dk, dv][B, Hkv, Sk, DP]
         const int64_t heads = (int64_t)a.B * a.Hkv, part = (w.head % a.G) / a.pack + (int64_t)(a.G / a.pack) * w.split;
         const int64_t at = ((part * 2 * heads + (int64_t)w.b * a.Hkv + w.kv) * a.Sk + min(key, a.Sk - 1)) * DP;
-        store_part<DP>(a.part + at, dk, a.scale, in, h);
-        store_part<DP>(a.part + at + heads * a.Sk * DP, dv, 1.0f, in, h);
+        if (has_dk) store_part<DP>(a.part + at, dk, a.scale, in, h);
+        if (has_dv) store_part<DP>(a.part + at + heads * a.Sk * DP, dv, 1.0f, in, h);
     }
 }
 

@@ -16,8 +16,10 @@
 // than 2^8 over it (then the accumulators are rescaled): probabilities stay
 // below 2^8, well inside every type, and the sums are float32.
 //
-// Few rows over many keys are split along the keys: each split leaves its
-// unnormalised float32 output and (maximum, sum) in the workspace and
+// Where there are too few blocks of rows to fill the card, SL waves (slices)
+// share the rows and take 32 keys of each tile each; they join their maxima,
+// sums and outputs through LDS at the end. Few rows over many keys are
+// also split along the keys: each split leaves its unnormalised float32 output and (maximum, sum) in the workspace and
 // attn_join_kernel joins them in split order.
 #pragma once
 
@@ -25,23 +27,19 @@
 
 namespace dytb {
 
-// Keys per LDS tile.
-template <typename T, int NW> struct FwdTile { static constexpr int keys = sizeof(T) == 2 && NW > 1 ? 64 : 32; };
-
-template <typename T, int DP, int NW>
-constexpr int fwd_lds_bytes() { return 2 * 2 * Tile<T, DP>::bytes(FwdTile<T, NW>::keys); }
-
-template <typename T, int DP, int NW, bool BIAS, bool VEC>
-__global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_kernel(AttnArgs a) {
+template <typename T, int DP, int NW, int SL, bool BIAS, bool VEC>
+__global__ __launch_bounds__(NW * SL * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_kernel(AttnArgs a) {
+    static_assert(NW == 1 || SL == 1);
     typedef Tile<T, DP> TL;
-    constexpr int KT = FwdTile<T, NW>::keys;
-    constexpr int NS = KT / 32, KB = TL::bytes(KT);
+    constexpr int KT = attn_tile_rows(sizeof(T), NW, SL);
+    constexpr int NS = KT / 32 / SL, KB = TL::bytes(KT);
     Work w;
-    if (!find_work(a, w, a.causal != 0, false)) return;
+    if (!find_work(a, w, true)) return;
     const int lane = (int)threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int sl = SL > 1 ? wave : 0;   // this wave's slice: keys 32 sl .. 32 sl + 31 of each tile
     const int rows = a.Sq * a.pack;
-    const int row0 = (w.block * NW + wave) * 32;
+    const int row0 = (w.block * NW + (SL > 1 ? 0 : wave)) * 32;
     const int row = row0 + (lane & 31);
     const bool there = row < rows;
     const int rr = min(row, rows - 1);
@@ -57,14 +55,16 @@ __global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_ke
     const Rows vr = {a.v + w.b * a.vs.b + w.kv * a.vs.h, a.vs.s, 0, 1};
     const float c = a.scale * kLog2e;
 
-    Stream<T, DP, KT, NW, VEC> ks, vs;
+    Stream<T, DP, KT, NW * SL, VEC> ks, vs;
     ks.start(kr, begin, KT, a.D, wave, lane);
     vs.start(vr, begin, KT, a.D, wave, lane);
     if (begin < end) {
         ks.fetch(0, kr, end - begin, KT, a.D, wave, lane);
         vs.fetch(2 * KB, vr, end - begin, KT, a.D, wave, lane);
     }
-    const int row_at = TL::row_lane(lane), col_at = TL::col_lane(lane, 0), col_at8 = TL::col_lane(lane, 8);
+    const int mine = sl * 32 * TL::pitch;
+    const int row_at = TL::row_lane(lane) + mine, col_at = TL::col_lane(lane, 0) + mine;
+    const int col_at8 = TL::col_lane(lane, 8) + mine;
     float* bias = (float*)(smem + 4 * KB);
     if constexpr (BIAS) fill_bias(bias, a, w.head);
 
@@ -93,7 +93,8 @@ __global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_ke
             ks.fetch((buf ^ 1) * KB, kr, end - j0 - KT, KT, a.D, wave, lane);
             vs.fetch(2 * KB + (buf ^ 1) * KB, vr, end - j0 - KT, KT, a.D, wave, lane);
         }
-        if (row0 >= rows || (a.causal && j0 > w.start + imax)) return;
+        const int first = j0 + sl * 32;
+        if (row0 >= rows || (SL > 1 && first >= end) || (a.causal && first > w.start + imax)) return;
         constexpr int kt = buf * KB, vt = 2 * KB + buf * KB;
         f32x16 s[NS];
 #pragma unroll
@@ -107,7 +108,7 @@ __global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_ke
         if constexpr (BIAS) {
 #pragma unroll
             for (int n = 0; n < NS; ++n) {
-                const int js = j0 + n * 32;
+                const int js = first + n * 32;
                 const int reach = a.borders.reach, after = a.borders.bidirectional ? reach : 0;
                 const bool far_after = js - (w.start + imax) >= after;
                 if (js + 31 - (w.start + imin) > -reach && !far_after) {
@@ -121,13 +122,13 @@ __global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_ke
                 }
             }
         }
-        if (j0 + KT > end || (a.causal && j0 + KT - 1 > w.start + imin)) {
+        if (first + NS * 32 > end || (a.causal && first + NS * 32 - 1 > w.start + imin)) {
             const int last = a.causal ? min(end - 1, pos) : end - 1;
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    s[n][i] = j0 + n * 32 + acc_row(i, h) <= last ? s[n][i] : -INFINITY;
+                    s[n][i] = first + n * 32 + acc_row(i, h) <= last ? s[n][i] : -INFINITY;
         }
         float mt = s[0][0];
 #pragma unroll
@@ -165,7 +166,33 @@ __global__ __launch_bounds__(NW * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_ke
     });
     if (row0 >= rows) return;
     l = swap32_other_sum(l);
-    const float ml = (m == -INFINITY ? 0.0f : m) * mc;   // log2 units
+    float ml = (m == -INFINITY ? 0.0f : m) * mc;   // log2 units
+    if constexpr (SL > 1) {
+        // the slices' common maximum and sum, then their outputs
+        float* stat = (float*)(smem + SL * DP * 128);   // [SL][maximum, sum][32 rows], past the boxes
+        __syncthreads();
+        if (h == 0) {
+            stat[sl * 64 + lane] = l > 0.0f ? ml : -INFINITY;
+            stat[sl * 64 + 32 + lane] = l;
+        }
+        __syncthreads();
+        float M = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < SL; ++k) M = fmaxf(M, stat[k * 64 + (lane & 31)]);
+        M = M == -INFINITY ? 0.0f : M;
+        const float f = l > 0.0f ? __builtin_amdgcn_exp2f(ml - M) : 0.0f;
+        l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < SL; ++k)
+            l += __builtin_amdgcn_exp2f(stat[k * 64 + (lane & 31)] - M) * stat[k * 64 + 32 + (lane & 31)];
+        ml = M;
+#pragma unroll
+        for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[dt][i] *= f;
+        join_slices<DP, 1, SL>(o, 0, sl, 0, lane);
+        if (sl) return;
+    }
     if (a.nsplit == 1) {
         char* out = a.out + w.b * a.os.b + (int64_t)pos_i * a.os.s + (int64_t)(w.head + g) * a.os.h;
         store_acc<T, DP, VEC>(out, o, l > 0.0f ? 1.0f / l : 0.0f, a.D, there, h);

@@ -6,16 +6,13 @@
 
 namespace dytb {
 
-// The rounded-up head dimension and waves per workgroup of an instance.
+// The rounded-up head dimension, row groups and slices of an instance.
 struct AttnPick {
-    int dp, nw;
+    int dp, nw, sl;
     bool bias, vec;
 };
 
 inline int attn_dp(int64_t D) { return D <= 32 ? 32 : D <= 64 ? 64 : D <= 96 ? 96 : 128; }
-
-// Rows to a tile of the dk/dv kernel's workgroups of four waves (DkvTile).
-inline int attn_dkv_tile(int dtype, int dp) { return dtype == DYT_F32 || dp > 64 ? 32 : 64; }
 
 inline unsigned attn_grid(const AttnArgs& a) { return (unsigned)((int64_t)a.units * a.blocks * a.nsplit); }
 
@@ -25,28 +22,38 @@ template <typename T> int attn_launch_dkv(const AttnPick&, const AttnArgs&, hipS
 
 template <typename T> void attn_launch_sum(int dp, const SumArgs&, hipStream_t);
 
-// Calls f with the compile-time (DP, NW, BIAS, VEC) of the pick. Tensors that
-// do not take 16-byte loads go element by element, in single waves.
-template <int DP, int NW, int VEC, typename F>
+// Calls f with the compile-time (DP, NW, SL, BIAS, VEC) of the pick. Tensors
+// that do not take 16-byte loads go element by element, in single waves.
+// PAIRS: the workgroups of four row groups also come with two slices.
+template <int DP, int NW, int SL, int VEC, typename F>
 void with_bias(const AttnPick& p, F&& f) {
-    if (p.bias) f(Int<DP>{}, Int<NW>{}, Int<1>{}, Int<VEC>{});
-    else f(Int<DP>{}, Int<NW>{}, Int<0>{}, Int<VEC>{});
+    if (p.bias) f(Int<DP>{}, Int<NW>{}, Int<SL>{}, Int<1>{}, Int<VEC>{});
+    else f(Int<DP>{}, Int<NW>{}, Int<SL>{}, Int<0>{}, Int<VEC>{});
 }
 
-template <int DP, typename F>
+template <int ES, bool PAIRS, int DP, typename F>
 void with_waves(const AttnPick& p, F&& f) {
-    if (!p.vec) with_bias<DP, 1, 0>(p, f);
-    else if (p.nw == 4) with_bias<DP, 4, 1>(p, f);
-    else with_bias<DP, 1, 1>(p, f);
+    if (!p.vec) return with_bias<DP, 1, 1, 0>(p, f);
+    if (p.nw == 4) {
+        if constexpr (PAIRS && ES == 2) {
+            if (p.sl == 2) return with_bias<DP, 4, 2, 1>(p, f);
+        }
+        return with_bias<DP, 4, 1, 1>(p, f);
+    }
+    if constexpr (attn_lds_bytes(ES, DP, 1, 4) <= kMaxLds) {
+        if (p.sl == 4) return with_bias<DP, 1, 4, 1>(p, f);
+    }
+    if (p.sl == 2) return with_bias<DP, 1, 2, 1>(p, f);
+    with_bias<DP, 1, 1, 1>(p, f);
 }
 
-template <typename F>
+template <int ES, bool PAIRS, typename F>
 void with_pick(const AttnPick& p, F&& f) {
     switch (p.dp) {
-        case 32: return with_waves<32>(p, f);
-        case 64: return with_waves<64>(p, f);
-        case 96: return with_waves<96>(p, f);
-        default: return with_waves<128>(p, f);
+        case 32: return with_waves<ES, PAIRS, 32>(p, f);
+        case 64: return with_waves<ES, PAIRS, 64>(p, f);
+        case 96: return with_waves<ES, PAIRS, 96>(p, f);
+        default: return with_waves<ES, PAIRS, 128>(p, f);
     }
 }
 
@@ -69,6 +76,10 @@ inline int launch_lds(const void* kernel, unsigned grid, unsigned threads, size_
     return hipLaunchKernel(kernel, dim3(grid), dim3(threads), args, lds, s) == hipSuccess ? DYT_OK : DYT_ERR_HIP;
 }
 
-inline size_t bias_lds_bytes(const AttnArgs& a) { return (size_t)2 * (a.borders.reach + kPad) * sizeof(float); }
+// LDS of the bias by relative position, and of its gradient's sums.
+inline int bias_lds_bytes(const Borders& o) { return 2 * (o.reach + kPad) * (int)sizeof(float); }
+inline int dbias_lds_bytes(const Borders& o, int waves) {
+    return dbias_floats(2 * (o.reach + kPad), waves) * (int)sizeof(float);
+}
 
 }  // namespace dytb

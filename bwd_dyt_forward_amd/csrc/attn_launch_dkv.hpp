@@ -10,12 +10,12 @@ namespace dytb {
 template <typename T>
 int attn_launch_dkv(const AttnPick& p, const AttnArgs& a, hipStream_t s) {
     int st = DYT_OK;
-    with_pick(p, [&](auto dp, auto nw, auto bias, auto vec) {
-        constexpr int DP = decltype(dp)::value, NW = decltype(nw)::value;
+    with_pick<(int)sizeof(T), true>(p, [&](auto dp, auto nw, auto sl, auto bias, auto vec) {
+        constexpr int DP = decltype(dp)::value, NW = decltype(nw)::value, SL = decltype(sl)::value;
         constexpr bool BIAS = decltype(bias)::value != 0, VEC = decltype(vec)::value != 0;
-        size_t lds = dkv_lds_bytes<T, DP, NW>();
-        if (BIAS) lds += bias_lds_bytes(a) + sizeof(float) * dbias_floats(2 * (a.borders.reach + kPad), NW);
-        st = launch_lds((const void*)attn_dkv_kernel<T, DP, NW, BIAS, VEC>, attn_grid(a), NW * 64, lds, a, s);
+        int lds = attn_dkv_lds_bytes((int)sizeof(T), DP, NW, SL);
+        if (BIAS) lds += bias_lds_bytes(a.borders) + dbias_lds_bytes(a.borders, NW * SL);
+        st = launch_lds((const void*)attn_dkv_kernel<T, DP, NW, SL, BIAS, VEC>, attn_grid(a), NW * SL * 64, lds, a, s);
     });
     return st;
 }

@@ -9,11 +9,11 @@ namespace dytb {
 template <typename T>
 int attn_launch_dq(const AttnPick& p, const AttnArgs& a, hipStream_t s) {
     int st = DYT_OK;
-    with_pick(p, [&](auto dp, auto nw, auto bias, auto vec) {
-        constexpr int DP = decltype(dp)::value, NW = decltype(nw)::value;
+    with_pick<(int)sizeof(T), false>(p, [&](auto dp, auto nw, auto sl, auto bias, auto vec) {
+        constexpr int DP = decltype(dp)::value, NW = decltype(nw)::value, SL = decltype(sl)::value;
         constexpr bool BIAS = decltype(bias)::value != 0, VEC = decltype(vec)::value != 0;
-        const size_t lds = bwd_lds_bytes<T, DP, NW>() + (BIAS ? bias_lds_bytes(a) : 0);
-        st = launch_lds((const void*)attn_dq_kernel<T, DP, NW, BIAS, VEC>, attn_grid(a), NW * 64, lds, a, s);
+        const int lds = attn_lds_bytes((int)sizeof(T), DP, NW, SL) + (BIAS ? bias_lds_bytes(a.borders) : 0);
+        st = launch_lds((const void*)attn_dq_kernel<T, DP, NW, SL, BIAS, VEC>, attn_grid(a), NW * SL * 64, lds, a, s);
     });
     return st;
 }

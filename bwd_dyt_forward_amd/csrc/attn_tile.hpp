@@ -45,6 +45,43 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 extern __shared__ __attribute__((aligned(1024))) char smem[];
 
+// ------------------------------------------- tiles and LDS of the instances
+// NW waves of a workgroup own 32 rows (dk/dv: keys) each, SL slices of them
+// share those and take different parts of each tile of the long axis.
+// es: element bytes, dp: padded head dimension.
+
+constexpr int kMaxLds = 160 * 1024;
+
+constexpr int attn_tile_bytes(int es, int dp, int rows) {
+    return (rows * (dp * es + (es == 4 ? 16 : 0)) + 1023) / 1024 * 1024;
+}
+
+// Forward and dq: keys per tile.
+constexpr int attn_tile_rows(int es, int nw, int sl) { return sl > 1 ? 32 * sl : es == 2 && nw > 1 ? 64 : 32; }
+constexpr int attn_lds_bytes(int es, int dp, int nw, int sl) {
+    return 4 * attn_tile_bytes(es, dp, attn_tile_rows(es, nw, sl));
+}
+
+// The dk/dv kernel holds 4 dp / 32 accumulators and its keys' and values'
+// fragments. Above dp = 64 that leaves room for one wave per SIMD; with the
+// values' fragments in LDS (which has bandwidth to spare) two fit, and hide
+// each other's waits. Tiles of 32 rows a slice keep its LDS small.
+constexpr bool dkv_vals_in_lds(int es, int dp) { return es == 2 && dp > 64; }
+constexpr int attn_dkv_tile_rows(int es, int dp, int nw, int sl) {
+    return sl > 1 ? 32 * sl : nw > 1 && es == 2 && dp <= 64 ? 64 : 32;
+}
+constexpr int attn_dkv_lds_bytes(int es, int dp, int nw, int sl) {
+    const int rows = attn_dkv_tile_rows(es, dp, nw, sl);
+    return 4 * attn_tile_bytes(es, dp, rows) + 16 * (rows > 64 ? rows : 64) +
+           (dkv_vals_in_lds(es, dp) ? nw * (dp / 16) * 1024 : 0);
+}
+
+// LDS floats of the bias gradient: each wave's scratch for one tile's
+// diagonals and its sums by relative position.
+constexpr int kDiagPitch = 33;
+constexpr int kDiagFloats = 32 * kDiagPitch;
+constexpr int dbias_floats(int entries, int waves) { return waves * (kDiagFloats + entries); }
+
 constexpr float kLog2e = 0x1.715476p+0f;
 constexpr float kLn2 = 0x1.62e43p-1f;
 
@@ -92,7 +129,7 @@ template <typename T, int DP> struct Tile {
     static constexpr int mask = !xored ? 0 : cpr == 16 ? 15 : cpr == 8 ? 7 : 3;
 
     // Bytes of a tile: whole wave instructions.
-    static constexpr int bytes(int rows) { return (rows * pitch + 1023) / 1024 * 1024; }
+    static constexpr int bytes(int rows) { return attn_tile_bytes((int)sizeof(T), DP, rows); }
 
     // f(row). The banks hold 16 chunks: one row of 16 chunks, two of 8, four
     // of 4, and rows of 12 start at 0, 12, 8, 4 in turn.
@@ -393,6 +430,39 @@ __device__ __forceinline__ void store_acc(char* row, const f32x16* acc, float mu
     }
 }
 
+// Adds up the accumulators of the SL slices (waves that hold the same rows of
+// the output and took different parts of the long axis) in slice order, in
+// the waves of slice `owner`. Boxes of 16 bytes per lane at the start of LDS,
+// whose tiles every wave is done with after the first barrier.
+template <int DP, int NW, int SL>
+__device__ __forceinline__ void join_slices(f32x16* acc, int g, int sl, int owner, int lane) {
+    __syncthreads();
+    char* box = smem + (g * (DP / 8) * 64 + lane) * 16;
+    constexpr int step = NW * (DP / 8) * 1024;
+    if (sl != owner) {
+        char* to = box + (sl < owner ? sl : sl - 1) * step;
+#pragma unroll
+        for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                *(f32x4*)(to + (dt * 4 + k) * 1024) =
+                    f32x4{acc[dt][4 * k], acc[dt][4 * k + 1], acc[dt][4 * k + 2], acc[dt][4 * k + 3]};
+    }
+    __syncthreads();
+    if (sl == owner) {
+#pragma unroll
+        for (int x = 0; x < SL - 1; ++x)
+#pragma unroll
+            for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const f32x4 v = *(const f32x4*)(box + x * step + (dt * 4 + k) * 1024);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[dt][4 * k + j] += v[j];
+                }
+    }
+}
+
 // float32 rows of DP elements in the workspace.
 template <int DP>
 __device__ __forceinline__ void store_part(float* row, const f32x16* acc, float mul, bool there, int h) {
@@ -426,6 +496,7 @@ struct AttnArgs {
     int32_t B, Sq, Sk, Hq, Hkv, D, G;
     int32_t pack, units;   // units = B * Hq / pack
     int32_t blocks, nsplit, per_split;   // row (or key) blocks per unit, splits of the other axis
+    int32_t together;                    // units an XCD takes at a time, see find_work
     int32_t causal, table_dt, buckets;
     float scale;
     Borders borders;
@@ -458,21 +529,31 @@ struct Work {
 // of about the same length) each XCD takes one whole, so that the blocks
 // that read one key head's keys and values share an L2 and a batch of ragged
 // lengths still spreads evenly. Units beyond a multiple of 8, and units of
-// one block, whose keys nobody else reads, go round block by block. Under a
-// causal mask the row blocks with most to do, the last, come first
-// (last_first). Key blocks are few and all resident at once, so every second
-// unit of an XCD takes them in the other order (turn): a CU then holds a long
-// and a short one.
-__device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w, bool last_first, bool turn) {
+// one block, whose keys nobody else reads, go round block by block.
+//
+// Under a causal mask the blocks' work falls from one end to the other
+// (`heavy_last`: the last block has most). An XCD then takes `together` of its
+// units at a time, the heaviest blocks of all of them first, in rows of 32
+// (its CUs) of alternating direction: a CU's workgroups add up to about the
+// same work, whether all are resident at once or follow each other. (One unit
+// after the other instead gave some CUs four of the longest and others four
+// of the shortest: 87 us for 64 units of 16 blocks, D = 64.)
+__device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w, bool heavy_last) {
     const int per_unit = a.blocks * a.nsplit;
     const int64_t bid = blockIdx.x;
     const int whole = a.blocks > 1 ? a.units / 8 * 8 : 0;
     int rem;
     if (bid < (int64_t)whole * per_unit) {
         const int i = (int)(bid >> 3);
-        const int k = i / per_unit;
-        w.u = k * 8 + (int)(bid & 7);
-        rem = i - k * per_unit;
+        const int each = a.together * per_unit, group = i / each;
+        const int n = min(a.together, whole / 8 - group * a.together);   // units of this group
+        int r = i - group * each;
+        if (a.causal) {
+            const int row = r >> 5;
+            if ((row & 1) && row * 32 + 32 <= n * per_unit) r = row * 32 + 31 - (r & 31);
+        }
+        rem = r / n;
+        w.u = (group * a.together + (r - rem * n)) * 8 + (int)(bid & 7);
     } else {
         const int i = (int)(bid - (int64_t)whole * per_unit);
         const int k = i / per_unit;
@@ -480,10 +561,15 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w, bool last_
         rem = i - k * per_unit;
     }
     if (w.u >= a.units) return false;
-    w.flat = (int64_t)w.u * per_unit + rem;
-    w.split = rem / a.blocks;
-    w.block = rem - w.split * a.blocks;
-    if (last_first || (turn && (w.u >> 3 & 1))) w.block = a.blocks - 1 - w.block;
+    if (a.causal) {
+        w.block = rem / a.nsplit;
+        w.split = rem - w.block * a.nsplit;
+        if (heavy_last) w.block = a.blocks - 1 - w.block;
+    } else {
+        w.split = rem / a.blocks;
+        w.block = rem - w.split * a.blocks;
+    }
+    w.flat = (int64_t)w.u * per_unit + w.split * a.blocks + w.block;
     const int hu = a.Hq / a.pack;
     w.b = w.u / hu;
     w.head = (w.u - w.b * hu) * a.pack;
@@ -518,14 +604,15 @@ __device__ __forceinline__ void bucket_range(const Borders& o, int t, int& lo, i
     }
 }
 
-// A thread per bucket writes its run of entries (a search per entry through
-// the borders took 6 us of a small problem's kernel, this takes under 1).
+// Eight lanes per bucket write its run of entries (a search per entry through
+// the borders took 6 us of a small problem's kernel; a single lane per
+// bucket is held up by the longest run).
 __device__ __forceinline__ void fill_bias(float* lds, const AttnArgs& a, int head) {
-    for (int t = (int)threadIdx.x; t < a.buckets; t += (int)blockDim.x) {
+    for (int t = (int)threadIdx.x / 8; t < a.buckets; t += (int)blockDim.x / 8) {
         const float x = load_param(a.table, (int64_t)t * a.Hq + head, a.table_dt) * kLog2e;
         int lo, hi;
         bucket_range(a.borders, t, lo, hi);
-        for (int i = lo; i < hi; ++i) lds[i] = x;
+        for (int i = lo + ((int)threadIdx.x & 7); i < hi; i += 8) lds[i] = x;
     }
 }
 
