@@ -50,7 +50,7 @@ __global__ __launch_bounds__(64 * kFinSlices) void ln_finish_kernel(const float*
 // 16 N grid <= 0.03 * 3 M N s).
 int ln_bwd_grid(const LnConfig& c, int64_t M, int64_t elem_bytes) {
     const int64_t need = (M + ln_groups(c) - 1) / ln_groups(c);
-    const int64_t most = c.threads > 512 || c.threads == 0 ? 256 : 1024;
+        const int64_t most = c.threads > 512 || c.threads == 0 ? 256 : 1024;
     const int64_t cap = std::min(most, std::max<int64_t>(256, M * elem_bytes / 178 / 128 * 128));
     return (int)std::min(need, cap);
 }
@@ -107,6 +107,7 @@ int ln_forward(const void* x, int64_t ldx, const void* r, const void* gamma, con
     LnArgs a{};
     a.x = x; a.r = res ? r : nullptr; a.h = h; a.y = y; a.gamma = gamma; a.beta = beta;
     a.mean = mean; a.rstd = rstd; a.ldx = ldx; a.ldy = ldy; a.M = M; a.N = (int32_t)N; a.pdt = pdt; a.eps = eps;
+    a.traffic = ln_traffic(M, N, (int)sx, false);
     const LnConfig cfg = ln_config(M, N, (int)sx, false);
     with_type(xdt, [&](auto* t) {
         ln_launch_forward<std::remove_pointer_t<decltype(t)>>(cfg, a, (hipStream_t)stream);
@@ -146,6 +147,7 @@ int ln_backward(const void* x, int64_t ldx, const void* dy, int64_t lddy, const 
     a.x = x; a.dy = dy; a.dres = res ? dres : nullptr; a.y = dx; a.gamma = gamma;
     a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd); a.part = (float*)ws;
     a.ldx = ldx; a.lddy = lddy; a.ldy = lddx; a.M = M; a.N = (int32_t)N; a.pdt = pdt; a.pitch = p.pitch;
+    a.traffic = ln_traffic(M, N, (int)sx, true);
     with_type(xdt, [&](auto* t) {
         ln_launch_backward<std::remove_pointer_t<decltype(t)>>(p.cfg, p.grid, a, s);
     });

@@ -42,6 +42,7 @@ struct LnArgs {
     int32_t pdt;
     float eps;
     int64_t pitch;        // backward: floats between partial rows
+    int32_t traffic;      // cache hints, see ln_traffic
 };
 
 // The 16 bytes that hold elements [c, c + VEC) of the row that starts at
@@ -50,11 +51,13 @@ struct LnArgs {
 // row, or `on` false) read the tensor's first bytes; where the 16 bytes would
 // end past the tensor's last element (`limit`), the last 16 bytes are read.
 // The tensor has at least VEC elements.
-template <typename T>
+template <typename T, int NT>
 __device__ __forceinline__ u32x4 load_raw(const T* p, int64_t row, int c, int N, int64_t limit, bool on) {
     constexpr int VEC = VecOf<T>::n;
     const int64_t at = min(row + c, limit - VEC);
-    return *(const u32x4_m*)(p + (on && c < N ? at : 0));
+    const u32x4_m* from = (const u32x4_m*)(p + (on && c < N ? at : 0));
+    if constexpr (NT >= 2) return __builtin_nontemporal_load(from);
+    else return *from;
 }
 
 // Those elements as float32, zeros past N: clears what belongs to the next
@@ -113,11 +116,13 @@ __device__ __forceinline__ void load_columns(const void* p, int dt, int t, int N
 #undef DYT_COLUMNS
 }
 
-template <typename T>
+template <typename T, int NT = 0>
 __device__ __forceinline__ void store_vec(T* p, int64_t row, int c, int N, const float* v) {
     constexpr int VEC = VecOf<T>::n;
     if (c + VEC <= N) {
-        *(u32x4_m*)(p + row + c) = pack16<T>(v);
+        u32x4_m* to = (u32x4_m*)(p + row + c);
+        if constexpr (NT >= 1) __builtin_nontemporal_store((u32x4_m)pack16<T>(v), to);
+        else *to = pack16<T>(v);
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
@@ -133,14 +138,18 @@ __device__ __forceinline__ float inv_sqrt(float v) {
     return (v > 0.0f && v < INFINITY) ? z : y;   // 0 and inf keep the estimate's inf and 0
 }
 
-template <int TPR> struct LnShape {
-    static constexpr int threads = TPR < 256 ? 256 : TPR;
+// TPR threads per row, TH per workgroup. NT: 1 nontemporal stores, 2 loads as
+// well (ln_traffic).
+constexpr int ln_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
+
+template <int TPR, int TH = ln_threads(TPR)> struct LnShape {
+    static constexpr int threads = TH;
     static constexpr int groups = threads / TPR;                 // rows side by side
     static constexpr int waves = TPR > 64 ? TPR / 64 : 1;        // waves of a row
     static constexpr int L = TPR > 64 ? 64 : TPR;
 };
 
-template <typename T, int TPR, int V, int U, bool RES>
+template <typename T, int TPR, int V, int U, bool RES, int NT>
 __global__ __launch_bounds__(LnShape<TPR>::threads) void ln_fwd_kernel(LnArgs a) {
     using S = LnShape<TPR>;
     constexpr int VEC = VecOf<T>::n;
@@ -166,8 +175,8 @@ __global__ __launch_bounds__(LnShape<TPR>::threads) void ln_fwd_kernel(LnArgs a)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = (t + v * TPR) * VEC;
-                raw[u][v] = load_raw<T>(xp, m * a.ldx, c, N, limit, m < a.M);
-                if constexpr (RES) rres[u][v] = load_raw<T>((const T*)a.r, m * a.ldx, c, N, limit, m < a.M);
+                raw[u][v] = load_raw<T, NT>(xp, m * a.ldx, c, N, limit, m < a.M);
+                if constexpr (RES) rres[u][v] = load_raw<T, NT>((const T*)a.r, m * a.ldx, c, N, limit, m < a.M);
             }
         }
 #pragma unroll
@@ -182,7 +191,7 @@ __global__ __launch_bounds__(LnShape<TPR>::threads) void ln_fwd_kernel(LnArgs a)
                     unpack_raw<T>(rres[u][v], (const T*)a.r, m * a.ldx, c, N, limit, m < a.M, r);
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) r[i] += x[u][v * VEC + i];
-                    if (m < a.M) store_vec<T>((T*)a.h, m * a.ldx, c, N, r);
+                    if (m < a.M) store_vec<T, NT>((T*)a.h, m * a.ldx, c, N, r);
                     // the layer's input is h as stored
                     unpack16<T>(pack16<T>(r), &x[u][v * VEC]);
                 }
@@ -264,7 +273,7 @@ __global__ __launch_bounds__(LnShape<TPR>::threads) void ln_fwd_kernel(LnArgs a)
                     const int e = v * VEC + i;
                     y[i] = __builtin_fmaf((x[u][e] - mean[u]) * rs, gm[e], bt[e]);
                 }
-                store_vec<T>((T*)a.y, m * a.ldy, (t + v * TPR) * VEC, N, y);
+                store_vec<T, NT>((T*)a.y, m * a.ldy, (t + v * TPR) * VEC, N, y);
             }
             if (t == 0) {
                 a.mean[m] = mean[u];
@@ -348,9 +357,9 @@ __global__ __launch_bounds__(kLongThreads) void ln_fwd_long_kernel(LnArgs a) {
 // still packed, before the current ones are reduced, so that a workgroup's
 // loads do not wait for its sums. Workgroups of 1,024 threads have only 128
 // registers each and go without.
-template <typename T, int TPR, int V, int U, bool RES, bool AHEAD = (TPR < 1024)>
-__global__ __launch_bounds__(LnShape<TPR>::threads) void ln_bwd_kernel(LnArgs a) {
-    using S = LnShape<TPR>;
+template <typename T, int TPR, int TH, int V, int U, bool RES, int NT, bool AHEAD = (TPR < 1024)>
+__global__ __launch_bounds__(TH) void ln_bwd_kernel(LnArgs a) {
+    using S = LnShape<TPR, TH>;
     constexpr int VEC = VecOf<T>::n;
     constexpr int E = V * VEC;
     const int t = (int)threadIdx.x % TPR;
@@ -373,9 +382,9 @@ __global__ __launch_bounds__(LnShape<TPR>::threads) void ln_bwd_kernel(LnArgs a)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = (t + v * TPR) * VEC;
-            w.x[v] = load_raw<T>((const T*)a.x, m * a.ldx, c, N, limit, on);
-            w.dy[v] = load_raw<T>((const T*)a.dy, m * a.lddy, c, N, limit_dy, on);
-            if constexpr (RES) w.res[v] = load_raw<T>((const T*)a.dres, m * a.ldx, c, N, limit, on);
+            w.x[v] = load_raw<T, NT>((const T*)a.x, m * a.ldx, c, N, limit, on);
+            w.dy[v] = load_raw<T, NT>((const T*)a.dy, m * a.lddy, c, N, limit_dy, on);
+            if constexpr (RES) w.res[v] = load_raw<T, NT>((const T*)a.dres, m * a.ldx, c, N, limit, on);
         }
         w.mean = a.mean[on ? m : 0];
         w.rs = a.rstd[on ? m : 0];
@@ -463,42 +472,44 @@ __global__ __launch_bounds__(LnShape<TPR>::threads) void ln_bwd_kernel(LnArgs a)
                     o[i] = now[u].rs * (d - c1 - n[u][e] * c2);
                     if constexpr (RES) o[i] += res[i];
                 }
-                store_vec<T>((T*)a.y, m * a.ldy, c, N, o);
+                store_vec<T, NT>((T*)a.y, m * a.ldy, c, N, o);
             }
         }
     }
     float* row = a.part + (int64_t)blockIdx.x * a.pitch;
-    if constexpr (S::groups == 1) {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const int c = (t + v * TPR) * VEC + i;
-                if (c < N) {
-                    row[c] = ag[v * VEC + i];
-                    row[N + c] = ab[v * VEC + i];
-                }
-            }
-    } else {
-        // join the row groups: columns [0, TPR * E) of every group, one
+    if constexpr (S::groups > 1) {
+        // join the row groups, the upper half onto the lower one, one
         // gradient after the other through the same LDS
-        __shared__ float join[S::groups][TPR * E];
+        __shared__ float join[E][TH / 2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            __syncthreads();
+        for (int half = S::groups / 2; half > 0; half /= 2) {
 #pragma unroll
-            for (int v = 0; v < V; ++v)
+            for (int k = 0; k < 2; ++k) {
+                float* sum = k ? ab : ag;
+                __syncthreads();
+                if (g >= half && g < 2 * half) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    join[g][(t + v * TPR) * VEC + i] = k ? ab[v * VEC + i] : ag[v * VEC + i];
-            __syncthreads();
-            for (int c = (int)threadIdx.x; c < N; c += S::threads) {
-                float s = 0.0f;
-                for (int q = 0; q < S::groups; ++q) s += join[q][c];
-                row[k * N + c] = s;
+                    for (int e = 0; e < E; ++e) join[e][(int)threadIdx.x - half * TPR] = sum[e];
+                }
+                __syncthreads();
+                if (g < half) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) sum[e] += join[e][threadIdx.x];
+                }
             }
         }
     }
+    if (g > 0) return;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int c = (t + v * TPR) * VEC + i;
+            if (c < N) {
+                row[c] = ag[v * VEC + i];
+                row[N + c] = ab[v * VEC + i];
+            }
+        }
 }
 
 // Long rows: the row sums first, then dx and the parameter gradients. Each

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ln_launch.hpp"
 
@@ -17,8 +18,13 @@ void ln_fwd_one(const LnArgs& a, hipStream_t s) {
     const int64_t per = (int64_t)S::groups * U;
     const int64_t need = (a.M + per - 1) / per;
     const int grid = (int)std::min<int64_t>(need, kFwdGridThreads / S::threads);
-    if (a.r) ln_fwd_kernel<T, TPR, V, U, true><<<grid, S::threads, 0, s>>>(a);
-    else ln_fwd_kernel<T, TPR, V, U, false><<<grid, S::threads, 0, s>>>(a);
+    const auto with = [&](auto nt) {
+        constexpr int NT = decltype(nt)::value;
+        if (a.r) ln_fwd_kernel<T, TPR, V, U, true, NT><<<grid, S::threads, 0, s>>>(a);
+        else ln_fwd_kernel<T, TPR, V, U, false, NT><<<grid, S::threads, 0, s>>>(a);
+    };
+    if (a.traffic) with(std::integral_constant<int, 1>{});
+    else with(std::integral_constant<int, 0>{});
 }
 
 // U rows per thread at a time keep enough loads in flight where a row is few
@@ -57,19 +63,31 @@ void ln_launch_forward(const LnConfig& c, const LnArgs& a, hipStream_t s) {
     else ln_fwd_long_kernel<T, false><<<grid, kLongThreads, 0, s>>>(a);
 }
 
-template <typename T, int TPR, int V, int U>
+template <typename T, int TPR, int TH, int V, int U>
 void ln_bwd_one(int grid, const LnArgs& a, hipStream_t s) {
-    using S = LnShape<TPR>;
-    if (a.dres) ln_bwd_kernel<T, TPR, V, U, true><<<grid, S::threads, 0, s>>>(a);
-    else ln_bwd_kernel<T, TPR, V, U, false><<<grid, S::threads, 0, s>>>(a);
+    const auto with = [&](auto nt) {
+        constexpr int NT = decltype(nt)::value;
+        if (a.dres) ln_bwd_kernel<T, TPR, TH, V, U, true, NT><<<grid, TH, 0, s>>>(a);
+        else ln_bwd_kernel<T, TPR, TH, V, U, false, NT><<<grid, TH, 0, s>>>(a);
+    };
+    if (a.traffic == 2) with(std::integral_constant<int, 2>{});
+    else if (a.traffic == 1) with(std::integral_constant<int, 1>{});
+    else with(std::integral_constant<int, 0>{});
+}
+
+// Several waves to a row: four or eight to a workgroup.
+template <typename T, int TPR>
+void ln_bwd_wide(const LnConfig& c, int grid, const LnArgs& a, hipStream_t s) {
+    if (c.wg == 512) ln_bwd_one<T, TPR, 512, 2, 1>(grid, a, s);
+    else ln_bwd_one<T, TPR, 256, 2, 1>(grid, a, s);
 }
 
 // U rows per thread at a time where a row is one vector and every workgroup
 // has several rounds of them.
 template <typename T, int TPR>
 void ln_bwd_pick(int grid, const LnArgs& a, hipStream_t s) {
-    if (a.M >= (int64_t)grid * LnShape<TPR>::groups * 4) return ln_bwd_one<T, TPR, 1, 2>(grid, a, s);
-    ln_bwd_one<T, TPR, 1, 1>(grid, a, s);
+    if (a.M >= (int64_t)grid * LnShape<TPR>::groups * 4) return ln_bwd_one<T, TPR, 256, 1, 2>(grid, a, s);
+    ln_bwd_one<T, TPR, 256, 1, 1>(grid, a, s);
 }
 
 template <typename T>
@@ -82,15 +100,15 @@ void ln_launch_backward(const LnConfig& c, int grid, const LnArgs& a, hipStream_
         case 16 * 8 + 1: return ln_bwd_pick<T, 16>(grid, a, s);
         case 32 * 8 + 1: return ln_bwd_pick<T, 32>(grid, a, s);
         case 64 * 8 + 1: return ln_bwd_pick<T, 64>(grid, a, s);
-        case 64 * 8 + 2: return ln_bwd_one<T, 64, 2, 1>(grid, a, s);
-        case 128 * 8 + 2: return ln_bwd_one<T, 128, 2, 1>(grid, a, s);
-        case 256 * 8 + 2: return ln_bwd_one<T, 256, 2, 1>(grid, a, s);
-        case 512 * 8 + 2: return ln_bwd_one<T, 512, 2, 1>(grid, a, s);
-        case 1024 * 8 + 2: return ln_bwd_one<T, 1024, 2, 1>(grid, a, s);
+        case 64 * 8 + 2: return ln_bwd_one<T, 64, 256, 2, 1>(grid, a, s);
+        case 128 * 8 + 2: return ln_bwd_wide<T, 128>(c, grid, a, s);
+        case 256 * 8 + 2: return ln_bwd_wide<T, 256>(c, grid, a, s);
+        case 512 * 8 + 2: return ln_bwd_one<T, 512, 512, 2, 1>(grid, a, s);
+        case 1024 * 8 + 2: return ln_bwd_one<T, 1024, 1024, 2, 1>(grid, a, s);
         default: break;
     }
     if constexpr (sizeof(T) == 4) {
-        if (c.threads == 1024) return ln_bwd_one<T, 1024, 4, 1>(grid, a, s);
+        if (c.threads == 1024) return ln_bwd_one<T, 1024, 1024, 4, 1>(grid, a, s);
     }
     if (a.dres) ln_bwd_long_kernel<T, true><<<grid, kLongThreads, 0, s>>>(a);
     else ln_bwd_long_kernel<T, false><<<grid, kLongThreads, 0, s>>>(a);
