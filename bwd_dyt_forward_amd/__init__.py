@@ -5,6 +5,11 @@ backward (dx, dgamma, dbeta, dalpha), also with the residual add fused in
 front (h = x + r, y = DyT(h)), computed by hand-written HIP kernels
 behind a C ABI (``include/dyt.h``, library ``libdyt.so`` in this package).
 The Python functions below carry the ABI's names and only marshal tensors.
+
+Around it stand the operators a transformer block needs next to its
+normalisation: layer norm (plain and residual) and attention with grouped key
+heads, masks and a learned relative position bias, forward and backward
+(``include/dyt_block.h``, library ``libdyt_block.so``).
 """
 from ._lib import (  # noqa: F401
     DYT_BF16,
@@ -45,6 +50,18 @@ from ._block import (  # noqa: E402,F401
     dyt_ln_forward_residual,
 )
 from .module import DyT, DyTFunction, DyTResidual, DyTResidualFunction, dyt, dyt_residual  # noqa: E402,F401
+from .block import (  # noqa: E402,F401
+    Attention,
+    AttentionFunction,
+    KVCache,
+    LayerNorm,
+    LayerNormFunction,
+    LayerNormResidual,
+    LayerNormResidualFunction,
+    attention,
+    layer_norm,
+    layer_norm_residual,
+)
 
 __all__ = [
     "DyT", "DyTFunction", "dyt", "DyTResidual", "DyTResidualFunction", "dyt_residual",
@@ -56,5 +73,6 @@ __all__ = [
     "dyt_get_forward_residual_plan", "dyt_xcd_hint", "dyt_set_xcd_flip_override",
     "BLOCK_LIB_FILE", "block_lib", "dyt_ln_forward", "dyt_ln_forward_residual", "dyt_ln_backward",
     "dyt_ln_backward_residual", "dyt_ln_backward_workspace_size", "dyt_attn_forward", "dyt_attn_backward",
-    "dyt_attn_bucket_borders",
+    "dyt_attn_bucket_borders", "LayerNorm", "LayerNormFunction", "layer_norm", "LayerNormResidual",
+    "LayerNormResidualFunction", "layer_norm_residual", "Attention", "AttentionFunction", "attention", "KVCache",
 ]

@@ -15,8 +15,9 @@ namespace dytb {
 
 // dtable[t, head]: bucket t's run of positions in the rows of the head's
 // workgroups, batch entry by batch entry. A workgroup per (head, bucket); the
-// order of the sum depends on the shape alone.
-constexpr int kTableThreads = 256;
+// order of the sum depends on the shape alone. Bound by the loads' latency:
+// sixteen waves take 5.8 us for 512 runs over 64 rows, four took 10.5.
+constexpr int kTableThreads = 1024;
 
 __global__ __launch_bounds__(kTableThreads) void attn_dtable_kernel(const float* part, int B, int Hq, int per_unit,
                                                                     int buckets, Borders o, void* dtable, int dt) {
@@ -57,15 +58,12 @@ int fill_borders(int num_buckets, int max_distance, int bidirectional, Borders& 
     o.e = o.n / 2;
     if (o.n < 2 || max_distance <= o.e) return DYT_ERR_INVALID_ARG;
     const int t_all = o.n - o.e;
-    const long double step = logl((long double)max_distance / o.e) / t_all;
     for (int d = 0; d < o.e; ++d) o.at[d] = d;
-    for (int t = 0; t < t_all; ++t) {
-        // smallest d with (n - e) log(d / e) >= t log(distance / e); where both
-        // sides are equal whole powers the logarithms agree to 1e-15
-        int d = std::max((int)floorl(o.e * expl(step * t)) - 1, o.e);
-        while (logl((long double)d / o.e) < step * t - 1e-13L) ++d;
-        o.at[o.e + t] = std::max(d, o.at[o.e + t - 1]);
-    }
+    // bucket e + t starts at the smallest d >= e (distance / e)^(t / (n - e)); the
+    // powers are off by 1e-17 relative, and where one is a whole number d is it
+    const long double ratio = expl(logl((long double)max_distance / o.e) / t_all);
+    long double at = o.e;
+    for (int t = 0; t < t_all; ++t, at *= ratio) o.at[o.e + t] = (int)ceill(at * (1 - 1e-13L));
     o.reach = o.at[o.n - 1];
     return DYT_OK;
 }
@@ -117,18 +115,18 @@ bool vec_ok(const void* p, const Strides& s, int64_t row_bytes) {
 }
 
 struct Plan {
-    int status;
     int64_t rows;
     AttnPick fwd, dq, dkv;
     int pack, units;
     int fwd_blocks, fwd_split, fwd_per;
     int dq_blocks, dq_split, dq_per;
     int dkv_blocks, dkv_split, dkv_per, dkv_parts;
+    int fwd_lds, dq_lds, dkv_lds;
     int per_unit;   // dkv workgroups of a head
     size_t fwd_bytes, bwd_bytes;
     size_t off_rest, off_tpart, off_part;   // backward workspace: rows, rest, tpart, part
-    bool nothing_out, nothing_keys;
-    Borders borders;
+    bool nothing_out, nothing_keys, refine;
+    Borders borders{};
 };
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
@@ -150,7 +148,7 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 struct Shape {
     int es, dp, pack;
     int extra, extra_wave;   // LDS of the bias: of a workgroup, of each wave
-    bool dkv;
+    bool dkv, whole;         // whole: no splits
     double lat, busy;
     int tile(int nw, int sl) const {
         return (dkv ? attn_dkv_tile_rows(es, dp, nw, sl) : attn_tile_rows(es, nw, sl)) / pack * pack;   // whole positions
@@ -160,7 +158,7 @@ struct Shape {
     }
 };
 
-void choose(const Shape& h, int64_t units, int64_t rows, int64_t len, AttnPick& pick, int& blocks, int& split, int& per) {
+int choose(const Shape& h, int64_t units, int64_t rows, int64_t len, AttnPick& pick, int& blocks, int& split, int& per) {
     const int64_t b4 = units * ((rows + 127) / 128);
     pick.nw = pick.vec && rows > 32 && b4 * std::max<int64_t>(1, len / 1024) >= 256 ? 4 : 1;
     const int nw = pick.nw;
@@ -169,15 +167,17 @@ void choose(const Shape& h, int64_t units, int64_t rows, int64_t len, AttnPick& 
     double best = 0.0;
     int64_t parts = 1;
     pick.sl = 1;
-    // two slices of 16-bit dk/dv workgroups wherever they fit
-    const int lo = nw == 4 && h.dkv && h.es == 2 && h.lds(4, 2) <= kMaxLds ? 2 : 1;
+    // dk/dv above dp = 64, where a CU holds eight waves: all on one block of keys
+    // at a time, so that under a causal mask the next block goes to whichever CU
+    // is free (2 x 8 key heads of 4,096, D = 128: 842 -> 655 us)
+    const int lo = nw == 4 && h.dkv && dkv_vals_in_lds(h.es, h.dp) && h.lds(4, 2) <= kMaxLds ? 2 : 1;
     const int hi = nw == 4 ? lo : pick.vec ? 4 : 1;
     for (int sl = lo; sl <= hi; sl *= 2) {
         if (h.lds(nw, sl) > kMaxLds || (sl == 4 && attn_lds_bytes(h.es, h.dp, 1, 4) > kMaxLds)) break;
         const int tile = h.tile(nw, sl), steps = (tile + 32 * sl - 1) / (32 * sl);
         const int64_t tiles = std::max<int64_t>(1, ceil_div(len, tile));
         const double resident = 256.0 * (kMaxLds / h.lds(nw, sl));
-        for (int64_t n = 1; n == 1 || (n <= 64 && n * 4 <= tiles); n *= 2) {
+        for (int64_t n = 1; n == 1 || (!h.whole && n <= 64 && n * 4 <= tiles); n *= 2) {
             double at_once = groups * n, rounds = 1.0;
             if (nw == 1 && sl > 1 && at_once > resident) {
                 rounds = std::ceil(at_once / resident);
@@ -196,34 +196,42 @@ void choose(const Shape& h, int64_t units, int64_t rows, int64_t len, AttnPick& 
     per = ceil_div(ceil_div(len, tile), parts) * tile;
     per = std::max(per, tile);
     split = std::max(1, ceil_div(len, per));
+    return h.lds(nw, pick.sl);
 }
 
-// Units an XCD takes at a time under a causal mask (find_work): as many as
-// give each of its 32 CUs four workgroups.
-int units_together(const AttnArgs& a) {
-    if (!a.causal) return 1;
-    return std::max(1, std::min(a.units / 8, 128 / (a.blocks * a.nsplit)));
+// The order of the work under a causal mask (find_work): an XCD takes as many
+// units at a time as give each of its 32 CUs four workgroups; a CU holds what
+// its LDS (`lds` bytes a workgroup) and registers allow.
+void set_order(AttnArgs& a, const AttnPick& pick, int lds, int es) {
+    const int per_cu = std::min(kMaxLds / lds, 4 * attn_waves(es) / (pick.nw * pick.sl));
+    a.together = a.causal ? std::max(1, std::min(a.units / 8, 128 / (a.blocks * a.nsplit))) : 1;
+    a.zigzag = a.causal && per_cu > 1;
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// vec: whether every tensor takes 16-byte accesses (single waves otherwise).
-Plan make_plan(const dyt_attn_desc& d, bool vec) {
-    Plan p{};
-    p.status = DYT_ERR_INVALID_ARG;
-    if (d.B < 0 || d.Sq < 0 || d.Sk < 0 || d.Hq < 0 || d.Hkv < 1 || d.D < 1 || d.D > DYT_ATTN_MAX_D) return p;
-    if (d.Hq % d.Hkv || (d.causal & ~1) || (d.bidirectional & ~1) || d.reserved) return p;
-    if (!(d.scale > 0.0f) || std::isinf(d.scale)) return p;
+int check(const dyt_attn_desc& d, Borders& borders) {
+    if (d.B < 0 || d.Sq < 0 || d.Sk < 0 || d.Hq < 0 || d.Hkv < 1 || d.D < 1 || d.D > DYT_ATTN_MAX_D)
+        return DYT_ERR_INVALID_ARG;
+    if (d.Hq % d.Hkv || (d.causal & ~1) || (d.bidirectional & ~1) || d.reserved) return DYT_ERR_INVALID_ARG;
+    if (!(d.scale > 0.0f) || std::isinf(d.scale)) return DYT_ERR_INVALID_ARG;
     const int64_t G = d.Hq / d.Hkv;
-    if (d.Sk > kMaxRows || d.Sq > kMaxRows || G > kMaxRows || d.Sq * std::max<int64_t>(G, 1) > kMaxRows) return p;
-    if (d.Hq > (1 << 20) || d.B > (1 << 24) || d.B * d.Hq > (1 << 24) || d.B * d.Hkv > (1 << 24)) return p;
-    if (!dtype_ok(d.dtype) || (d.table && !dtype_ok(d.table_dtype))) {
-        p.status = DYT_ERR_UNSUPPORTED_DTYPE;
-        return p;
-    }
-    if (d.table && fill_borders(d.num_buckets, d.max_distance, d.bidirectional, p.borders)) return p;
+    if (d.Sk > kMaxRows || d.Sq > kMaxRows || G > kMaxRows || d.Sq * std::max<int64_t>(G, 1) > kMaxRows)
+        return DYT_ERR_INVALID_ARG;
+    if (d.Hq > (1 << 20) || d.B > (1 << 24) || d.B * d.Hq > (1 << 24) || d.B * d.Hkv > (1 << 24))
+        return DYT_ERR_INVALID_ARG;
+    if (!dtype_ok(d.dtype) || (d.table && !dtype_ok(d.table_dtype))) return DYT_ERR_UNSUPPORTED_DTYPE;
+    return d.table ? fill_borders(d.num_buckets, d.max_distance, d.bidirectional, borders) : DYT_OK;
+}
+
+// vec: whether every tensor takes 16-byte accesses (single waves otherwise).
+Plan make_plan(const dyt_attn_desc& d, const Borders& borders, bool backward, bool vec) {
+    Plan p{};
+    const int64_t G = d.Hq / d.Hkv;
+    p.borders = borders;
     p.nothing_out = d.B == 0 || d.Sq == 0 || d.Hq == 0;
     p.nothing_keys = d.B == 0 || d.Sk == 0;
+    p.refine = d.dtype != DYT_F32 && d.Sk <= 256;
     // the rows of a unit: all heads of a group (or a 32-row tile's worth, the
     // largest divisor), unless each needs its own column of the table
     p.pack = 1;
@@ -238,15 +246,15 @@ Plan make_plan(const dyt_attn_desc& d, bool vec) {
     // rate) and, 16-bit, much the same up to 128
     const double f = d.dtype == DYT_F32 ? 2.2 * dp / 32 : 0.0;
     const int bias = d.table ? bias_lds_bytes(p.borders) : 0, dbias = d.table ? dbias_lds_bytes(p.borders, 1) : 0;
-    if (!p.nothing_out) {
-        choose({es, dp, 1, bias, 0, false, std::max(f, 0.8), std::max(f, 0.4)}, p.units, p.rows, d.Sk, p.fwd,
-               p.fwd_blocks, p.fwd_split, p.fwd_per);
-        choose({es, dp, 1, bias, 0, false, std::max(1.2 * f, 0.9), std::max(1.2 * f, 0.6)}, p.units, p.rows, d.Sk, p.dq,
-               p.dq_blocks, p.dq_split, p.dq_per);
-    }
-    if (!p.nothing_keys && d.Hq > 0)
-        choose({es, dp, p.pack, bias, dbias, true, std::max(1.7 * f, 1.2), std::max(1.7 * f, 0.9)}, p.units, d.Sk, p.rows,
-               p.dkv, p.dkv_blocks, p.dkv_split, p.dkv_per);
+    if (!p.nothing_out && !backward)
+        p.fwd_lds = choose({es, dp, 1, bias, 0, false, false, std::max(f, 0.8), std::max(f, 0.4)}, p.units, p.rows, d.Sk, p.fwd,
+                           p.fwd_blocks, p.fwd_split, p.fwd_per);
+    if (!p.nothing_out && backward)
+        p.dq_lds = choose({es, dp, 1, bias, 0, false, p.refine, std::max(1.2 * f, 0.9), std::max(1.2 * f, 0.6)}, p.units, p.rows,
+                          d.Sk, p.dq, p.dq_blocks, p.dq_split, p.dq_per);
+    if (!p.nothing_keys && d.Hq > 0 && backward)
+        p.dkv_lds = choose({es, dp, p.pack, bias, dbias, true, false, std::max(1.7 * f, 1.2), std::max(1.7 * f, 0.9)}, p.units,
+                           d.Sk, p.rows, p.dkv, p.dkv_blocks, p.dkv_split, p.dkv_per);
     const int64_t part_rows = p.units * p.rows * (int64_t)dp * 4;
     if (p.fwd_split > 1) p.fwd_bytes = round256((size_t)p.fwd_split * part_rows) + (size_t)p.fwd_split * p.units * p.rows * 8;
     p.per_unit = p.dkv_blocks * p.dkv_split;
@@ -257,7 +265,6 @@ Plan make_plan(const dyt_attn_desc& d, bool vec) {
     size_t part = p.dq_split > 1 ? (size_t)p.dq_split * part_rows : 0;
     if (p.dkv_parts > 1) part = std::max(part, (size_t)p.dkv_parts * 2 * d.B * d.Hkv * d.Sk * dp * 4);
     p.bwd_bytes = p.off_part + part;
-    p.status = DYT_OK;
     return p;
 }
 
@@ -307,28 +314,33 @@ int dyt_attn_bucket_borders(int num_buckets, int max_distance, int bidirectional
 
 size_t dyt_attn_forward_workspace_size(const dyt_attn_desc* desc) {
     if (!desc) return 0;
-    const Plan p = make_plan(*desc, true);
-    return p.status || p.nothing_out ? 0 : std::max(p.fwd_bytes, make_plan(*desc, false).fwd_bytes);
+    Borders borders{};
+    if (check(*desc, borders)) return 0;
+    const Plan p = make_plan(*desc, borders, false, true);
+    return p.nothing_out ? 0 : std::max(p.fwd_bytes, make_plan(*desc, borders, false, false).fwd_bytes);
 }
 
 size_t dyt_attn_backward_workspace_size(const dyt_attn_desc* desc) {
     if (!desc) return 0;
-    const Plan p = make_plan(*desc, true);
-    return p.status ? 0 : std::max(p.bwd_bytes, make_plan(*desc, false).bwd_bytes);
+    Borders borders{};
+    if (check(*desc, borders)) return 0;
+    return std::max(make_plan(*desc, borders, true, true).bwd_bytes, make_plan(*desc, borders, true, false).bwd_bytes);
 }
 
 int dyt_attn_forward(const dyt_attn_desc* desc, const void* q, const void* k, const void* v, void* o, float* stats,
                      void* workspace, size_t workspace_bytes, void* stream) {
     if (!desc) return DYT_ERR_INVALID_ARG;
     const dyt_attn_desc& d = *desc;
-    if (int st = make_plan(d, true).status) return st;
+    Borders borders{};
+    if (int st = check(d, borders)) return st;
     AttnArgs a{};
     Spans n{};
     if (!view(d, {d.Sq, d.Hq, &d.q}, false, a.qs, n.q) || !view(d, {d.Sk, d.Hkv, &d.k}, false, a.ks, n.k) ||
         !view(d, {d.Sk, d.Hkv, &d.v}, false, a.vs, n.v) || !view(d, {d.Sq, d.Hq, &d.o}, true, a.os, n.o))
         return DYT_ERR_INVALID_ARG;
     const int64_t es = dtype_size(d.dtype), row = d.D * es;
-    const Plan p = make_plan(d, vec_ok(q, a.qs, row) && vec_ok(k, a.ks, row) && vec_ok(v, a.vs, row) && vec_ok(o, a.os, row));
+    const Plan p = make_plan(d, borders, false, vec_ok(q, a.qs, row) && vec_ok(k, a.ks, row) && vec_ok(v, a.vs, row) &&
+                                                    vec_ok(o, a.os, row));
     if (p.nothing_out) return DYT_OK;
     if (!q || !o || !stats || (d.Sk > 0 && (!k || !v))) return DYT_ERR_INVALID_ARG;
     if (d.Sk == 0) n.k = n.v = 0;
@@ -342,7 +354,7 @@ int dyt_attn_forward(const dyt_attn_desc* desc, const void* q, const void* k, co
     fill_args(d, p, a);
     a.q = (const char*)q; a.k = (const char*)k; a.v = (const char*)v; a.out = (char*)o; a.stats = stats;
     a.blocks = p.fwd_blocks; a.nsplit = p.fwd_split; a.per_split = p.fwd_per;
-    a.together = units_together(a);
+    set_order(a, p.fwd, p.fwd_lds, (int)es);
     a.part = (float*)workspace;
     a.part_ml = (float*)((char*)workspace + round256((size_t)p.fwd_split * p.units * p.rows * p.fwd.dp * 4));
     return with_type(d.dtype, [&](auto* t) {
@@ -355,7 +367,8 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
                       void* workspace, size_t workspace_bytes, void* stream) {
     if (!desc) return DYT_ERR_INVALID_ARG;
     const dyt_attn_desc& d = *desc;
-    if (int st = make_plan(d, true).status) return st;
+    Borders borders{};
+    if (int st = check(d, borders)) return st;
     AttnArgs a{};
     Spans n{};
     if (!view(d, {d.Sq, d.Hq, &d.q}, false, a.qs, n.q) || !view(d, {d.Sk, d.Hkv, &d.k}, false, a.ks, n.k) ||
@@ -364,7 +377,7 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
         !view(d, {d.Sk, d.Hkv, &d.dk}, true, a.dks, n.dk) || !view(d, {d.Sk, d.Hkv, &d.dv}, true, a.dvs, n.dv))
         return DYT_ERR_INVALID_ARG;
     const int64_t es = dtype_size(d.dtype), row = d.D * es, ts = d.table ? dtype_size(d.table_dtype) : 1;
-    const Plan p = make_plan(d, vec_ok(q, a.qs, row) && vec_ok(k, a.ks, row) && vec_ok(v, a.vs, row) &&
+    const Plan p = make_plan(d, borders, true, vec_ok(q, a.qs, row) && vec_ok(k, a.ks, row) && vec_ok(v, a.vs, row) &&
                                     vec_ok(o, a.os, row) && vec_ok(dout, a.dos, row) && vec_ok(dq, a.dqs, row) &&
                                     vec_ok(dk, a.dks, row) && vec_ok(dv, a.dvs, row));
     if (p.nothing_out) n.q = n.o = n.dout = n.dq = 0;
@@ -399,6 +412,7 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
     a.dout = (const char*)dout; a.dq = (char*)dq; a.dk = (char*)dk; a.dv = (char*)dv;
     a.stats = const_cast<float*>(stats);
     a.dtable = dtable;
+    a.refine = p.refine;
     a.rows = (float*)workspace;
     a.rest = (float*)((char*)workspace + p.off_rest);
     a.tpart = (float*)((char*)workspace + p.off_tpart);
@@ -408,7 +422,7 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
         const int dp = p.dq.dp;
         if (!p.nothing_out) {
             a.blocks = p.dq_blocks; a.nsplit = p.dq_split; a.per_split = p.dq_per;
-            a.together = units_together(a);
+            set_order(a, p.dq, p.dq_lds, (int)es);
             if (int st = attn_launch_dq<T>(p.dq, a, s)) return st;
             if (p.dq_split > 1) {
                 const int64_t total = (int64_t)p.units * p.rows;
@@ -433,7 +447,7 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
                 return hip_status();
             }
             a.blocks = p.dkv_blocks; a.nsplit = p.dkv_split; a.per_split = p.dkv_per;
-            a.together = units_together(a);
+            set_order(a, p.dkv, p.dkv_lds, (int)es);
             if (int st = attn_launch_dkv<T>(p.dkv, a, s)) return st;
             if (p.dkv_parts > 1) attn_launch_sum<T>(dp, sums, s);
         }

@@ -17,6 +17,10 @@
 // o is rounded to its type, so delta is off by a little in every pair of the
 // row, which a sum over many pairs (dtable) shows: but the row's dS have to
 // add up to zero, so the dq kernel adds their sum to the delta it leaves.
+// In dq itself the error is one of three roundings of the same size, less by
+// the number of keys the softmax spreads over; with up to 256 keys in a
+// 16-bit type (`refine`) a second walk takes it out, two products over
+// a short length.
 //
 // Both take a split of their long axis where there are few blocks; the
 // splits' float32 parts are summed in split order by attn_sum_kernel.
@@ -35,7 +39,7 @@
 namespace dytb {
 
 template <typename T, int DP, int NW, int SL, bool BIAS, bool VEC>
-__global__ __launch_bounds__(NW * SL * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dq_kernel(AttnArgs a) {
+__global__ __launch_bounds__(NW * SL * 64, attn_waves(sizeof(T))) void attn_dq_kernel(AttnArgs a) {
     static_assert(NW == 1 || SL == 1);
     typedef Tile<T, DP> TL;
     constexpr int KT = attn_tile_rows(sizeof(T), NW, SL);
@@ -103,79 +107,100 @@ __global__ __launch_bounds__(NW * SL * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_d
 #pragma unroll
         for (int i = 0; i < 16; ++i) dq[dt][i] = 0.0f;
 
-    alternate(begin, end, KT, [&](auto which, int j0) __attribute__((always_inline)) {
-        constexpr int buf = decltype(which)::value;
-        loads_landed();
-        __syncthreads();
-        if (j0 + KT < end) {
-            ks.fetch((buf ^ 1) * KB, kr, end - j0 - KT, KT, a.D, wave, lane);
-            vs.fetch(2 * KB + (buf ^ 1) * KB, vr, end - j0 - KT, KT, a.D, wave, lane);
-        }
-        constexpr int kt = buf * KB, vt = kt + 2 * KB;
-        const int first = j0 + sl * 32;
-        // (a branch around a single sub-tile would have the accumulators copied)
-        if (row0 >= rows || (SL > 1 && first >= end) || (a.causal && first > w.start + imax)) return;
-#pragma unroll
-        for (int n = 0; n < NS; ++n) {
-            const int js = first + n * 32;
-            f32x16 s, dp;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
-#pragma unroll
-            for (int ds = 0; ds < DP / 16; ++ds) {
-                s = mma<T>(TL::row_frag(row_at, kt, n, ds), q[ds], s);
-                dp = mma<T>(TL::row_frag(row_at, vt, n, ds), dout[ds], dp);
+    // one pass over the keys; the second: see below
+    const auto walk = [&](auto pass) __attribute__((always_inline)) {
+        constexpr bool AGAIN = decltype(pass)::value != 0;
+        alternate(begin, end, KT, [&](auto which, int j0) __attribute__((always_inline)) {
+            constexpr int buf = decltype(which)::value;
+            loads_landed();
+            __syncthreads();
+            if (j0 + KT < end) {
+                ks.fetch((buf ^ 1) * KB, kr, end - j0 - KT, KT, a.D, wave, lane);
+                if constexpr (!AGAIN) vs.fetch(2 * KB + (buf ^ 1) * KB, vr, end - j0 - KT, KT, a.D, wave, lane);
             }
-            const int reach = a.borders.reach, after = a.borders.bidirectional ? reach : 0;
-            const bool far_after = js - (w.start + imax) >= after;
-            const bool near = js + 31 - (w.start + imin) > -reach && !far_after;
-            float p[16];
-            if constexpr (BIAS) {
-                if (near) {
-                    const float* at = bias + (js - pos + reach + kPad + 4 * h);
+            constexpr int kt = buf * KB, vt = kt + 2 * KB;
+            const int first = j0 + sl * 32;
+            // (a branch around a single sub-tile would have the accumulators copied)
+            if (row0 >= rows || (SL > 1 && first >= end) || (a.causal && first > w.start + imax)) return;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, at[8 * (i / 4) + (i % 4)]) - lse);
-                } else {
-                    const float one = bias[far_after ? 2 * (reach + kPad) - 1 : 0];
+            for (int n = 0; n < NS; ++n) {
+                const int js = first + n * 32;
+                f32x16 s, dp;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, one) - lse);
+                for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
+#pragma unroll
+                for (int ds = 0; ds < DP / 16; ++ds) {
+                    s = mma<T>(TL::row_frag(row_at, kt, n, ds), q[ds], s);
+                    if constexpr (!AGAIN) dp = mma<T>(TL::row_frag(row_at, vt, n, ds), dout[ds], dp);
                 }
-            } else {
+                const int reach = a.borders.reach, after = a.borders.bidirectional ? reach : 0;
+                const bool far_after = js - (w.start + imax) >= after;
+                const bool near = js + 31 - (w.start + imin) > -reach && !far_after;
+                float p[16];
+                if constexpr (BIAS) {
+                    if (near) {
+                        const float* at = bias + (js - pos + reach + kPad + 4 * h);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse));
+                        for (int i = 0; i < 16; ++i)
+                            p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, at[8 * (i / 4) + (i % 4)]) - lse);
+                    } else {
+                        const float one = bias[far_after ? 2 * (reach + kPad) - 1 : 0];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, one) - lse);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -lse));
+                }
+                if (js + 32 > end || (a.causal && js + 31 > w.start + imin)) {
+                    const int last = a.causal ? min(end - 1, pos) : end - 1;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) p[i] = js + acc_row(i, h) <= last ? p[i] : 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    if constexpr (AGAIN) {
+                        p[i] *= -rest;
+                    } else {
+                        p[i] *= dp[i] - delta;
+                        rest += p[i];
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const Frag<T> pf = pack_frag<T>(p + 8 * k);
+#pragma unroll
+                    for (int dt = 0; dt < DP / 32; ++dt)
+                        dq[dt] = mma<T>(TL::col_frag(col_at, col_at8, kt, n * 32 + k * 16, dt), pf, dq[dt]);
+                }
             }
-            if (js + 32 > end || (a.causal && js + 31 > w.start + imin)) {
-                const int last = a.causal ? min(end - 1, pos) : end - 1;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) p[i] = js + acc_row(i, h) <= last ? p[i] : 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                p[i] *= dp[i] - delta;
-                rest += p[i];
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const Frag<T> pf = pack_frag<T>(p + 8 * k);
-#pragma unroll
-                for (int dt = 0; dt < DP / 32; ++dt)
-                    dq[dt] = mma<T>(TL::col_frag(col_at, col_at8, kt, n * 32 + k * 16, dt), pf, dq[dt]);
-            }
-        }
-    });
+        });
+    };
+    walk(Int<0>{});
     // rest is what delta is too small by (rounded o): the dkv kernel takes the sum
     rest = swap32_other_sum(rest);
     if constexpr (SL > 1) {
-        float* stat = (float*)(smem + SL * DP * 128);   // [SL][32 rows], past the boxes
+        float* stat = (float*)smem;   // [SL][32 rows]
         __syncthreads();
         if (h == 0) stat[sl * 32 + lane] = rest;
-        join_slices<DP, 1, SL>(dq, 0, sl, 0, lane);
-        if (sl) return;
+        __syncthreads();
         rest = 0.0f;
 #pragma unroll
         for (int k = 0; k < SL; ++k) rest += stat[k * 32 + (lane & 31)];
+    }
+    if constexpr (sizeof(T) == 2) {
+        if (a.refine) {
+            // dq is too large by rest * sum_j p_j k_j
+            __syncthreads();
+            ks.start(kr, begin, KT, a.D, wave, lane);
+            if (begin < end) ks.fetch(0, kr, end - begin, KT, a.D, wave, lane);
+            walk(Int<1>{});
+        }
+    }
+    if constexpr (SL > 1) {
+        join_slices<DP, 1, SL>(dq, 0, sl, 0, lane);
+        if (sl) return;
     }
     if (row0 < rows) {
         if (a.nsplit == 1) {
@@ -197,7 +222,7 @@ __global__ __launch_bounds__(NW * SL * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_d
 }
 
 template <typename T, int DP, int NW, int SL, bool BIAS, bool VEC>
-__global__ __launch_bounds__(NW * SL * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_dkv_kernel(AttnArgs a) {
+__global__ __launch_bounds__(NW * SL * 64, attn_waves(sizeof(T))) void attn_dkv_kernel(AttnArgs a) {
     typedef Tile<T, DP> TL;
     constexpr int RT = attn_dkv_tile_rows(sizeof(T), DP, NW, SL), SR = RT > 64 ? RT : 64;
     constexpr bool VLDS = dkv_vals_in_lds(sizeof(T), DP);

@@ -28,7 +28,7 @@
 namespace dytb {
 
 template <typename T, int DP, int NW, int SL, bool BIAS, bool VEC>
-__global__ __launch_bounds__(NW * SL * 64, (sizeof(T) == 2 ? 2 : 1)) void attn_fwd_kernel(AttnArgs a) {
+__global__ __launch_bounds__(NW * SL * 64, attn_waves(sizeof(T))) void attn_fwd_kernel(AttnArgs a) {
     static_assert(NW == 1 || SL == 1);
     typedef Tile<T, DP> TL;
     constexpr int KT = attn_tile_rows(sizeof(T), NW, SL);

@@ -76,6 +76,11 @@ constexpr int attn_dkv_lds_bytes(int es, int dp, int nw, int sl) {
            (dkv_vals_in_lds(es, dp) ? nw * (dp / 16) * 1024 : 0);
 }
 
+// Waves per SIMD that an instance's registers have to leave room for. (Three or
+// four at dp <= 64 spill: forward 62 -> 82 us at 4 x 16 heads of 2,048 with four,
+// dk/dv 105 -> 187 us at 8 x 16 heads of 1,024 with three.)
+constexpr int attn_waves(int es) { return es == 4 ? 1 : 2; }
+
 // LDS floats of the bias gradient: each wave's scratch for one tile's
 // diagonals and its sums by relative position.
 constexpr int kDiagPitch = 33;
@@ -496,7 +501,8 @@ struct AttnArgs {
     int32_t B, Sq, Sk, Hq, Hkv, D, G;
     int32_t pack, units;   // units = B * Hq / pack
     int32_t blocks, nsplit, per_split;   // row (or key) blocks per unit, splits of the other axis
-    int32_t together;                    // units an XCD takes at a time, see find_work
+    int32_t refine;                      // dq: see attn_bwd.hpp
+    int32_t together, zigzag;            // units an XCD takes at a time and how, see find_work
     int32_t causal, table_dt, buckets;
     float scale;
     Borders borders;
@@ -533,11 +539,14 @@ struct Work {
 //
 // Under a causal mask the blocks' work falls from one end to the other
 // (`heavy_last`: the last block has most). An XCD then takes `together` of its
-// units at a time, the heaviest blocks of all of them first, in rows of 32
-// (its CUs) of alternating direction: a CU's workgroups add up to about the
-// same work, whether all are resident at once or follow each other. (One unit
-// after the other instead gave some CUs four of the longest and others four
-// of the shortest: 87 us for 64 units of 16 blocks, D = 64.)
+// units at a time, the heaviest blocks of all of them first, and where a CU
+// holds several workgroups (`zigzag`) every second row of 32 (its CUs) the
+// other way, so that those of a CU add up to the same work: with one unit after
+// the other, each heaviest first, some CUs got four of the longest blocks and
+// others four of the shortest (forward of 64 units of 16 blocks, D = 64: 87 us,
+// now 62). A CU with one workgroup at a time takes the heaviest left when it
+// is free (dk/dv of 16 units of 32 blocks, D = 128: 691 us with the rows
+// turned, 655 without).
 __device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w, bool heavy_last) {
     const int per_unit = a.blocks * a.nsplit;
     const int64_t bid = blockIdx.x;
@@ -548,7 +557,7 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w, bool heavy
         const int each = a.together * per_unit, group = i / each;
         const int n = min(a.together, whole / 8 - group * a.together);   // units of this group
         int r = i - group * each;
-        if (a.causal) {
+        if (a.zigzag) {
             const int row = r >> 5;
             if ((row & 1) && row * 32 + 32 <= n * per_unit) r = row * 32 + 31 - (r & 31);
         }

@@ -213,6 +213,8 @@ class Attention:
         doff = half * adelta + (self.hp + rho) * (do64.abs() * (p @ self.v.abs())).sum(-1, keepdim=True)
         voff = (do64 * self.o).square().sum(-1, keepdim=True) * (half ** 2 / 3)
         voff = voff + ((p.square() @ self.v.square()) * do64.square()).sum(-1, keepdim=True) * (self.hp ** 2 / 3)
+        if Sk <= 256:   # dq takes it out with a second walk over the keys
+            doff, voff = doff * 0, voff * 0
         dds = p * (2 * rho * (dp.abs() + delta.abs()) + (D + 8) * U * (adp + adelta))
         tiny_ds = self.tp
 

@@ -291,3 +291,49 @@ def test_the_binding_refuses_host_tensors_and_wrong_shapes(dyt):
         dyt.dyt_attn_forward(q, q, q)
     with pytest.raises(ValueError, match="device"):
         dyt.dyt_attn_backward(q, q, q, q, q, torch.zeros(1, 2, 2))
+
+
+# ---------------------------------------------------------- autograd wiring
+def test_residual_wiring_and_attention_gradients_on_stand_ins(dyt, monkeypatch):
+    """The kernels replaced by plain operations on CPU tensors: which gradient
+    goes to which input, and that x and r do not share their gradient's memory."""
+    from bwd_dyt_forward_amd import _block, block
+
+    def fwd(x, r, g, b, eps):
+        h = x + r
+        return h, h * g + b, h.mean(1), h.mean(1)
+
+    def bwd(h, dy, dres, mean, rstd, g):
+        return dres + dy * g, (dy * h).sum(0), dy.sum(0)
+
+    monkeypatch.setattr(_block, "dyt_ln_forward_residual", fwd)
+    monkeypatch.setattr(_block, "dyt_ln_backward_residual", bwd)
+    x, r = (torch.randn(4, 6, requires_grad=True) for _ in range(2))
+    g, b = torch.randn(6, requires_grad=True), torch.zeros(6, requires_grad=True)
+    for n in (1, 2):
+        h, y = block.layer_norm_residual(x, r, g, b)
+        (2 * h + 3 * y).sum().backward()
+        assert torch.allclose(x.grad, n * (2 + 3 * g.detach()).expand(4, 6)) and torch.equal(x.grad, r.grad)
+        assert x.grad.data_ptr() != r.grad.data_ptr()
+    seen = {}
+
+    def attn_fwd(q, k, v, *, table, **kw):
+        seen.update(kw, strides=q.stride())
+        return q * 2, q[..., 0]
+
+    def attn_bwd(q, k, v, o, do, stats, *, table, **kw):
+        assert do.stride(-1) == 1 and {**kw} == {n: seen[n] for n in kw}
+        out = (do * 2, k * 0 + 3, v * 0 + 5)
+        return out if table is None else (*out, table * 0 + 7)
+
+    monkeypatch.setattr(_block, "dyt_attn_forward", attn_fwd)
+    monkeypatch.setattr(_block, "dyt_attn_backward", attn_bwd)
+    q, k, v = (torch.randn(1, 3, 2, 4, requires_grad=True) for _ in range(3))
+    t = torch.randn(8, 2, requires_grad=True)
+    for table in (None, t):
+        q.grad = k.grad = v.grad = None
+        block.attention(q, k, v, causal=True, table=table).sum().backward()
+        assert (q.grad == 2).all() and (k.grad == 3).all() and (v.grad == 5).all()
+    assert (t.grad == 7).all() and seen["causal"] is True
+    block.attention(q.transpose(2, 3).contiguous().transpose(2, 3), k, v)
+    assert seen["strides"][-1] == 1
