@@ -125,7 +125,7 @@ struct Plan {
     int per_unit;   // dkv workgroups of a head
     size_t fwd_bytes, bwd_bytes;
     size_t off_rest, off_tpart, off_part;   // backward workspace: rows, rest, tpart, part
-    bool nothing_out, nothing_keys, refine;
+    bool nothing_out, nothing_keys;
     Borders borders{};
 };
 
@@ -231,7 +231,6 @@ Plan make_plan(const dyt_attn_desc& d, const Borders& borders, bool backward, bo
     p.borders = borders;
     p.nothing_out = d.B == 0 || d.Sq == 0 || d.Hq == 0;
     p.nothing_keys = d.B == 0 || d.Sk == 0;
-    p.refine = d.dtype != DYT_F32 && d.Sk <= 256;
     // the rows of a unit: all heads of a group (or a 32-row tile's worth, the
     // largest divisor), unless each needs its own column of the table
     p.pack = 1;
@@ -250,7 +249,7 @@ Plan make_plan(const dyt_attn_desc& d, const Borders& borders, bool backward, bo
         p.fwd_lds = choose({es, dp, 1, bias, 0, false, false, std::max(f, 0.8), std::max(f, 0.4)}, p.units, p.rows, d.Sk, p.fwd,
                            p.fwd_blocks, p.fwd_split, p.fwd_per);
     if (!p.nothing_out && backward)
-        p.dq_lds = choose({es, dp, 1, bias, 0, false, p.refine, std::max(1.2 * f, 0.9), std::max(1.2 * f, 0.6)}, p.units, p.rows,
+        p.dq_lds = choose({es, dp, 1, bias, 0, false, es == 2 && d.Sk <= kRefineKeys, std::max(1.2 * f, 0.9), std::max(1.2 * f, 0.6)}, p.units, p.rows,
                           d.Sk, p.dq, p.dq_blocks, p.dq_split, p.dq_per);
     if (!p.nothing_keys && d.Hq > 0 && backward)
         p.dkv_lds = choose({es, dp, p.pack, bias, dbias, true, false, std::max(1.7 * f, 1.2), std::max(1.7 * f, 0.9)}, p.units,
@@ -412,7 +411,6 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
     a.dout = (const char*)dout; a.dq = (char*)dq; a.dk = (char*)dk; a.dv = (char*)dv;
     a.stats = const_cast<float*>(stats);
     a.dtable = dtable;
-    a.refine = p.refine;
     a.rows = (float*)workspace;
     a.rest = (float*)((char*)workspace + p.off_rest);
     a.tpart = (float*)((char*)workspace + p.off_tpart);

@@ -18,9 +18,10 @@
 // row, which a sum over many pairs (dtable) shows: but the row's dS have to
 // add up to zero, so the dq kernel adds their sum to the delta it leaves.
 // In dq itself the error is one of three roundings of the same size, less by
-// the number of keys the softmax spreads over; with up to 256 keys in a
-// 16-bit type (`refine`) a second walk takes it out, two products over
-// a short length.
+// the number of keys the softmax spreads over. Blocks of rows that see up to
+// kRefineKeys keys, all in one split, take it out in a second walk over them
+// (`refine`, 16-bit types): two products over a short length, in long causal
+// sequences for the first few blocks only.
 //
 // Both take a split of their long axis where there are few blocks; the
 // splits' float32 parts are summed in split order by attn_sum_kernel.
@@ -58,8 +59,10 @@ __global__ __launch_bounds__(NW * SL * 64, attn_waves(sizeof(T))) void attn_dq_k
     const int pos = w.start + pos_i;
     const int imin = min(row0, rows - 1) / a.pack;
     const int imax = min(row0 + 31, rows - 1) / a.pack;
-    int end = min(w.len, (w.split + 1) * a.per_split);
+    int end = w.len;   // keys that the block's rows see
     if (a.causal) end = min(end, w.start + (min((w.block + 1) * NW * 32, rows) - 1) / a.pack + 1);
+    const bool refine = sizeof(T) == 2 && end <= min(kRefineKeys, a.per_split);
+    end = min(end, (w.split + 1) * a.per_split);
     const int begin = w.split * a.per_split;
 
     const Rows kr = {a.k + w.b * a.ks.b + w.kv * a.ks.h, a.ks.s, 0, 1};
@@ -190,7 +193,7 @@ __global__ __launch_bounds__(NW * SL * 64, attn_waves(sizeof(T))) void attn_dq_k
         for (int k = 0; k < SL; ++k) rest += stat[k * 32 + (lane & 31)];
     }
     if constexpr (sizeof(T) == 2) {
-        if (a.refine) {
+        if (refine) {
             // dq is too large by rest * sum_j p_j k_j
             __syncthreads();
             ks.start(kr, begin, KT, a.D, wave, lane);

@@ -81,6 +81,9 @@ constexpr int attn_dkv_lds_bytes(int es, int dp, int nw, int sl) {
 // dk/dv 105 -> 187 us at 8 x 16 heads of 1,024 with three.)
 constexpr int attn_waves(int es) { return es == 4 ? 1 : 2; }
 
+// dq's second walk, see attn_bwd.hpp.
+constexpr int kRefineKeys = 256;
+
 // LDS floats of the bias gradient: each wave's scratch for one tile's
 // diagonals and its sums by relative position.
 constexpr int kDiagPitch = 33;
@@ -501,7 +504,6 @@ struct AttnArgs {
     int32_t B, Sq, Sk, Hq, Hkv, D, G;
     int32_t pack, units;   // units = B * Hq / pack
     int32_t blocks, nsplit, per_split;   // row (or key) blocks per unit, splits of the other axis
-    int32_t refine;                      // dq: see attn_bwd.hpp
     int32_t together, zigzag;            // units an XCD takes at a time and how, see find_work
     int32_t causal, table_dt, buckets;
     float scale;

@@ -107,7 +107,7 @@ int ln_forward(const void* x, int64_t ldx, const void* r, const void* gamma, con
     LnArgs a{};
     a.x = x; a.r = res ? r : nullptr; a.h = h; a.y = y; a.gamma = gamma; a.beta = beta;
     a.mean = mean; a.rstd = rstd; a.ldx = ldx; a.ldy = ldy; a.M = M; a.N = (int32_t)N; a.pdt = pdt; a.eps = eps;
-    a.traffic = ln_traffic(M, N, (int)sx, false);
+    a.traffic = ln_traffic(M, N, (int)sx, res);
     const LnConfig cfg = ln_config(M, N, (int)sx, false);
     with_type(xdt, [&](auto* t) {
         ln_launch_forward<std::remove_pointer_t<decltype(t)>>(cfg, a, (hipStream_t)stream);

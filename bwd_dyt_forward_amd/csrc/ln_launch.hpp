@@ -48,13 +48,15 @@ inline LnConfig ln_config(int64_t M, int64_t N, int elem_bytes, bool backward) {
 // Cache hints by the bytes of one activation tensor (the last-level cache
 // holds 256 MB). From a quarter of that, what a kernel writes would only push
 // out what it reads: nontemporal stores (100,003 x 255 float32, forward and
-// backward 103 -> 93 us; 4,194,304 x 32 float16 forward 109 -> 96 us). Beyond
-// the whole of it the backward's inputs do not survive the forward either:
-// nontemporal loads there (32,768 x 4,096 bfloat16 209 -> 200 us; in the
-// forward, and for tensors that do fit, they cost up to a tenth).
-inline int ln_traffic(int64_t M, int64_t N, int elem_bytes, bool backward) {
+// backward 103 -> 93 us; 16,384 x 4,096 bfloat16 forward with the residual
+// 105 -> 84 us; a kernel that reads y straight afterwards loses 6 us of
+// that). Beyond the whole of it what the backward or the residual's four
+// tensors bring in does not survive either: nontemporal loads there (32,768 x
+// 4,096 bfloat16, backward 209 -> 200 us; in the plain forward, and for
+// tensors that do fit, they cost up to a tenth).
+inline int ln_traffic(int64_t M, int64_t N, int elem_bytes, bool many) {
     const int64_t bytes = M * N * elem_bytes;
-    if (backward && bytes >= ((int64_t)256 << 20)) return 2;
+    if (many && bytes >= ((int64_t)256 << 20)) return 2;
     return bytes >= ((int64_t)64 << 20) ? 1 : 0;
 }
 

@@ -9,20 +9,31 @@
 namespace dytb {
 
 // Workgroups of a forward launch: enough to fill 256 CUs several times over
-// and no more, since each loads gamma and beta once for all its rows.
-constexpr int kFwdGridThreads = 256 * 2048;
+// and no more, since each loads gamma and beta once for all its rows. Where
+// loads and stores are nontemporal and a row takes whole workgroups, two per
+// CU (32,768 x 4,096 bfloat16 with the residual: 203 -> 185 us; at half the
+// rows, where the tensors fit the last-level cache, the other way round: 84
+// against 92).
+constexpr int kFwdGridThreads = 256 * 2048, kFwdGridThreadsFew = 256 * 512;
 
 template <typename T, int TPR, int V, int U>
 void ln_fwd_one(const LnArgs& a, hipStream_t s) {
     using S = LnShape<TPR>;
     const int64_t per = (int64_t)S::groups * U;
     const int64_t need = (a.M + per - 1) / per;
-    const int grid = (int)std::min<int64_t>(need, kFwdGridThreads / S::threads);
     const auto with = [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
+        const int grid = (int)std::min<int64_t>(need, kFwdGridThreads / S::threads);
         if (a.r) ln_fwd_kernel<T, TPR, V, U, true, NT><<<grid, S::threads, 0, s>>>(a);
         else ln_fwd_kernel<T, TPR, V, U, false, NT><<<grid, S::threads, 0, s>>>(a);
     };
+    if constexpr (TPR >= 256) {
+        if (a.traffic == 2) {
+            const int grid = (int)std::min<int64_t>(need, kFwdGridThreadsFew / S::threads);
+            ln_fwd_kernel<T, TPR, V, U, true, 2><<<grid, S::threads, 0, s>>>(a);
+            return;
+        }
+    }
     if (a.traffic) with(std::integral_constant<int, 1>{});
     else with(std::integral_constant<int, 0>{});
 }
