@@ -96,6 +96,13 @@ def _stream_for(t: torch.Tensor, stream) -> int:
     return _lib._stream(stream)
 
 
+def _empty(like: torch.Tensor, shape) -> torch.Tensor:
+    """A contiguous tensor of like's type (empty_like is the cheapest call)."""
+    if like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(shape, dtype=like.dtype, device=like.device)
+
+
 def _on_device(name: str, t, like: torch.Tensor) -> None:
     if not isinstance(t, torch.Tensor) or t.device != like.device:
         raise ValueError(f"{name} must be a tensor on {like.device}")
@@ -153,7 +160,7 @@ def dyt_ln_forward(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, eps
     s = _stream_for(x, stream)
     made = (y is None, mean is None, rstd is None)
     if y is None:
-        y = torch.empty((M, N), dtype=x.dtype, device=x.device)
+        y = _empty(x, (M, N))
     ldy = N if made[0] else _check_rows("y", y, x)
     if mean is None:
         mean = torch.empty(M, dtype=torch.float32, device=x.device)
@@ -181,11 +188,11 @@ def dyt_ln_forward_residual(x: torch.Tensor, r: torch.Tensor, gamma: torch.Tenso
     s = _stream_for(x, stream)
     made = (h is None, y is None, mean is None, rstd is None)
     if h is None:
-        h = torch.empty((M, N), dtype=x.dtype, device=x.device)
+        h = _empty(x, (M, N))
     else:
         _check_rows("h", h, x, dense=True)
     if y is None:
-        y = torch.empty((M, N), dtype=x.dtype, device=x.device)
+        y = _empty(x, (M, N))
     else:
         _check_rows("y", y, x, dense=True)
     if mean is None:
@@ -221,7 +228,7 @@ def _ln_backward(x, dy, dres, mean, rstd, gamma, dx, dgamma, dbeta, workspace, s
     dev = x.device
     made = (dx is None, dgamma is None, dbeta is None, workspace is None)
     if dx is None:
-        dx = torch.empty((M, N), dtype=x.dtype, device=dev)
+        dx = _empty(x, (M, N))
         lddx = N
     else:
         lddx = _check_rows("dx", dx, x, dense=res)
@@ -360,7 +367,7 @@ def dyt_attn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causa
     s = _stream_for(q, stream)
     made = (o is None, stats is None, workspace is None)
     if o is None:
-        o = torch.empty((B, Sq, Hq, D), dtype=q.dtype, device=q.device)
+        o = _empty(q, (B, Sq, Hq, D))
     else:
         _check_heads("o", o, q, q.shape)
     if stats is None:
@@ -407,15 +414,15 @@ def dyt_attn_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torc
     _check_stats_tensor(stats, q, B, Hq, Sq)
     made = (dq is None, dk is None, dv is None, dtable is None, workspace is None)
     if dq is None:
-        dq = torch.empty((B, Sq, Hq, D), dtype=q.dtype, device=dev)
+        dq = _empty(q, (B, Sq, Hq, D))
     else:
         _check_heads("dq", dq, q, q.shape)
     if dk is None:
-        dk = torch.empty((B, Sk, Hkv, D), dtype=q.dtype, device=dev)
+        dk = _empty(k, (B, Sk, Hkv, D))
     else:
         _check_heads("dk", dk, q, k.shape)
     if dv is None:
-        dv = torch.empty((B, Sk, Hkv, D), dtype=q.dtype, device=dev)
+        dv = _empty(v, (B, Sk, Hkv, D))
     else:
         _check_heads("dv", dv, q, k.shape)
     if table is None:

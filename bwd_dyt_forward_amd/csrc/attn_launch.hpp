@@ -2,6 +2,8 @@
 // called by attn_api.hip, and the picking of instances.
 #pragma once
 
+#include <atomic>
+
 #include "attn_tile.hpp"
 
 namespace dytb {
@@ -67,13 +69,24 @@ void with_dp(int dp, F&& f) {
     }
 }
 
-// Launches with dynamic LDS; more than the default 64 KB is asked for.
-inline int launch_lds(const void* kernel, unsigned grid, unsigned threads, size_t lds, AttnArgs a, hipStream_t s) {
-    if (lds > 64 * 1024 &&
-        hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
-        return DYT_ERR_HIP;
-    void* args[] = {&a};
-    return hipLaunchKernel(kernel, dim3(grid), dim3(threads), args, lds, s) == hipSuccess ? DYT_OK : DYT_ERR_HIP;
+// Launches with dynamic LDS. An instance that may need more than the default 64
+// KB is given all of it, once per device (a microsecond of a small call
+// otherwise).
+template <auto Kernel>
+int launch_lds(unsigned grid, unsigned threads, size_t lds, const AttnArgs& a, hipStream_t s) {
+    if (lds > 64 * 1024) {
+        static std::atomic<uint64_t> raised{0};
+        int device = 0;
+        if (hipGetDevice(&device) != hipSuccess) return DYT_ERR_HIP;
+        const uint64_t bit = (uint64_t)1 << (device & 63);
+        if (device > 63 || !(raised.load(std::memory_order_acquire) & bit)) {
+            if (hipFuncSetAttribute((const void*)Kernel, hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds) != hipSuccess)
+                return DYT_ERR_HIP;
+            if (device <= 63) raised.fetch_or(bit, std::memory_order_release);
+        }
+    }
+    Kernel<<<grid, threads, lds, s>>>(a);
+    return hipGetLastError() == hipSuccess ? DYT_OK : DYT_ERR_HIP;
 }
 
 // LDS of the bias by relative position, and of its gradient's sums.

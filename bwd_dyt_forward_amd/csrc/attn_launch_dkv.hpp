@@ -15,7 +15,7 @@ int attn_launch_dkv(const AttnPick& p, const AttnArgs& a, hipStream_t s) {
         constexpr bool BIAS = decltype(bias)::value != 0, VEC = decltype(vec)::value != 0;
         int lds = attn_dkv_lds_bytes((int)sizeof(T), DP, NW, SL);
         if (BIAS) lds += bias_lds_bytes(a.borders) + dbias_lds_bytes(a.borders, NW * SL);
-        st = launch_lds((const void*)attn_dkv_kernel<T, DP, NW, SL, BIAS, VEC>, attn_grid(a), NW * SL * 64, lds, a, s);
+        st = launch_lds<attn_dkv_kernel<T, DP, NW, SL, BIAS, VEC>>(attn_grid(a), NW * SL * 64, lds, a, s);
     });
     return st;
 }

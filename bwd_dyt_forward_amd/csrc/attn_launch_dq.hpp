@@ -13,7 +13,7 @@ int attn_launch_dq(const AttnPick& p, const AttnArgs& a, hipStream_t s) {
         constexpr int DP = decltype(dp)::value, NW = decltype(nw)::value, SL = decltype(sl)::value;
         constexpr bool BIAS = decltype(bias)::value != 0, VEC = decltype(vec)::value != 0;
         const int lds = attn_lds_bytes((int)sizeof(T), DP, NW, SL) + (BIAS ? bias_lds_bytes(a.borders) : 0);
-        st = launch_lds((const void*)attn_dq_kernel<T, DP, NW, SL, BIAS, VEC>, attn_grid(a), NW * SL * 64, lds, a, s);
+        st = launch_lds<attn_dq_kernel<T, DP, NW, SL, BIAS, VEC>>(attn_grid(a), NW * SL * 64, lds, a, s);
     });
     return st;
 }
