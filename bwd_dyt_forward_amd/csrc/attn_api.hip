@@ -151,7 +151,7 @@ struct Shape {
     bool dkv, whole;         // whole: no splits
     double lat, busy;
     int tile(int nw, int sl) const {
-        return (dkv ? attn_dkv_tile_rows(es, dp, nw, sl) : attn_tile_rows(es, nw, sl)) / pack * pack;   // whole positions
+        return (dkv ? attn_dkv_tile_rows(es, dp, nw, sl) : attn_tile_rows(es, dp, nw, sl)) / pack * pack;   // whole positions
     }
     int lds(int nw, int sl) const {
         return (dkv ? attn_dkv_lds_bytes(es, dp, nw, sl) : attn_lds_bytes(es, dp, nw, sl)) + extra + extra_wave * nw * sl;
@@ -183,6 +183,9 @@ int choose(const Shape& h, int64_t units, int64_t rows, int64_t len, AttnPick& p
                 rounds = std::ceil(at_once / resident);
                 at_once = resident;
             }
+#ifdef NMORE
+            if (rows <= 32 && !h.dkv && groups * n < NMORE) continue;
+#endif
             const double t = rounds * ceil_div(tiles, n) * steps * std::max(h.lat, at_once * nw * sl / 1024.0 * h.busy) +
                              0.5 * (sl - 1) + (n > 1 ? 6.0 + 0.1 * n : 0.0);
             if (best == 0.0 || t < best) {
