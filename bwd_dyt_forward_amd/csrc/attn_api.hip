@@ -151,7 +151,7 @@ struct Shape {
     bool dkv, whole;         // whole: no splits
     double lat, busy;
     int tile(int nw, int sl) const {
-        return (dkv ? attn_dkv_tile_rows(es, dp, nw, sl) : attn_tile_rows(es, dp, nw, sl)) / pack * pack;   // whole positions
+        return (dkv ? attn_dkv_tile_rows(es, dp, nw, sl) : attn_tile_rows(es, nw, sl)) / pack * pack;   // whole positions
     }
     int lds(int nw, int sl) const {
         return (dkv ? attn_dkv_lds_bytes(es, dp, nw, sl) : attn_lds_bytes(es, dp, nw, sl)) + extra + extra_wave * nw * sl;
@@ -183,9 +183,6 @@ int choose(const Shape& h, int64_t units, int64_t rows, int64_t len, AttnPick& p
                 rounds = std::ceil(at_once / resident);
                 at_once = resident;
             }
-#ifdef NMORE
-            if (rows <= 32 && !h.dkv && groups * n < NMORE) continue;
-#endif
             const double t = rounds * ceil_div(tiles, n) * steps * std::max(h.lat, at_once * nw * sl / 1024.0 * h.busy) +
                              0.5 * (sl - 1) + (n > 1 ? 6.0 + 0.1 * n : 0.0);
             if (best == 0.0 || t < best) {
@@ -196,6 +193,15 @@ int choose(const Shape& h, int64_t units, int64_t rows, int64_t len, AttnPick& p
         }
     }
     const int tile = h.tile(nw, pick.sl);
+    // One block of rows (single tokens): every key is read once, and what counts
+    // are the loads in flight. Once the keys are split, they are split until
+    // every CU has all the workgroups it holds (16 x 16 heads over 4,096 keys, D =
+    // 64: 45 us with 2,048 workgroups, 41 with 4,096; where 1,280 are held, D =
+    // 128, 73 us with 2,048 and 76 with 4,096).
+    if (!h.dkv && rows <= 32 && pick.sl == 1 && parts > 1) {
+        const double held = 256.0 * (kMaxLds / h.lds(nw, 1));
+        while (groups * parts < held && parts < 64 && parts * 8 <= ceil_div(len, tile)) parts *= 2;
+    }
     per = ceil_div(ceil_div(len, tile), parts) * tile;
     per = std::max(per, tile);
     split = std::max(1, ceil_div(len, per));

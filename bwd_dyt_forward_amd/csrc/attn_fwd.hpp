@@ -31,7 +31,7 @@ template <typename T, int DP, int NW, int SL, bool BIAS, bool VEC>
 __global__ __launch_bounds__(NW * SL * 64, attn_waves(sizeof(T))) void attn_fwd_kernel(AttnArgs a) {
     static_assert(NW == 1 || SL == 1);
     typedef Tile<T, DP> TL;
-    constexpr int KT = attn_tile_rows(sizeof(T), DP, NW, SL);
+    constexpr int KT = attn_tile_rows(sizeof(T), NW, SL);
     constexpr int NS = KT / 32 / SL, KB = TL::bytes(KT);
     Work w;
     if (!find_work(a, w, true)) return;

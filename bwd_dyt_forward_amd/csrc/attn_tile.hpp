@@ -57,14 +57,9 @@ constexpr int attn_tile_bytes(int es, int dp, int rows) {
 }
 
 // Forward and dq: keys per tile.
-#ifndef T64
-#define T64 0
-#endif
-constexpr int attn_tile_rows(int es, int dp, int nw, int sl) {
-    return sl > 1 ? 32 * sl : es == 2 && (nw > 1 || dp <= T64) ? 64 : 32;
-}
+constexpr int attn_tile_rows(int es, int nw, int sl) { return sl > 1 ? 32 * sl : es == 2 && nw > 1 ? 64 : 32; }
 constexpr int attn_lds_bytes(int es, int dp, int nw, int sl) {
-    return 4 * attn_tile_bytes(es, dp, attn_tile_rows(es, dp, nw, sl));
+    return 4 * attn_tile_bytes(es, dp, attn_tile_rows(es, nw, sl));
 }
 
 // The dk/dv kernel holds 4 dp / 32 accumulators and its keys' and values'
