@@ -152,10 +152,15 @@ class KVCache:
         self.v = torch.zeros_like(self.k)
         self.length = torch.zeros(batch, dtype=torch.int32, device=device)
         self._rows = torch.arange(batch, device=device).view(-1, 1)
+        self._used = 0   # the longest length, known on the host
 
     def append(self, k: torch.Tensor, v: torch.Tensor) -> torch.Tensor:
-        """Adds [B, S, heads, head_dim] behind each sequence (S new positions,
-        which the caller sees to fit max_len); returns the lengths before."""
+        """Adds [B, S, heads, head_dim] behind each sequence; returns the
+        lengths before."""
+        if k.shape[1] > self.k.shape[1] - self._used:
+            raise ValueError(f"the cache holds {self.k.shape[1]} positions, {self._used} are taken: no room for "
+                             f"{k.shape[1]} more")
+        self._used += k.shape[1]
         start = self.length.clone()
         at = start.long().view(-1, 1) + torch.arange(k.shape[1], device=k.device)
         self.k[self._rows, at] = k

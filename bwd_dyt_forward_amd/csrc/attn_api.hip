@@ -258,8 +258,8 @@ Plan make_plan(const dyt_attn_desc& d, const Borders& borders, bool backward, bo
         p.fwd_lds = choose({es, dp, 1, bias, 0, false, false, std::max(f, 0.8), std::max(f, 0.4)}, p.units, p.rows, d.Sk, p.fwd,
                            p.fwd_blocks, p.fwd_split, p.fwd_per);
     if (!p.nothing_out && backward)
-        p.dq_lds = choose({es, dp, 1, bias, 0, false, es == 2 && d.Sk <= kRefineKeys, std::max(1.2 * f, 0.9), std::max(1.2 * f, 0.6)}, p.units, p.rows,
-                          d.Sk, p.dq, p.dq_blocks, p.dq_split, p.dq_per);
+        p.dq_lds = choose({es, dp, 1, bias, 0, false, es == 2 && d.Sk <= kRefineKeys, std::max(1.2 * f, 0.9),
+                           std::max(1.2 * f, 0.6)}, p.units, p.rows, d.Sk, p.dq, p.dq_blocks, p.dq_split, p.dq_per);
     if (!p.nothing_keys && d.Hq > 0 && backward)
         p.dkv_lds = choose({es, dp, p.pack, bias, dbias, true, false, std::max(1.7 * f, 1.2), std::max(1.7 * f, 0.9)}, p.units,
                            d.Sk, p.rows, p.dkv, p.dkv_blocks, p.dkv_split, p.dkv_per);

@@ -33,6 +33,13 @@
 // adds the sum to the wave's array of sums by relative position. At the end
 // the waves' arrays are joined in wave order and left in the workspace, one
 // row per workgroup; attn_dtable_kernel sums each bucket's run of positions.
+//
+// Measured: causal 2 x 4,096, 32 query over 8 key heads, D = 128 bf16 dq 405-440
+// us (940-1,020 TFLOP/s), dk/dv 615-655 us (840-890); over 8,192 keys in full 388
+// and 551 us (1,000). Both hold two waves per SIMD (accumulators and fragments
+// fill the registers) and wait for each other's products and exponentials half
+// the time. 8 x 16 ragged heads of up to 1,024, D = 64 with the bias: 57 and
+// 105 us, where the empty key blocks leave 1.1 rounds of workgroups.
 #pragma once
 
 #include "attn_tile.hpp"

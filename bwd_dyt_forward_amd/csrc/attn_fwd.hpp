@@ -21,6 +21,14 @@
 // sums and outputs through LDS at the end. Few rows over many keys are
 // also split along the keys: each split leaves its unnormalised float32 output and (maximum, sum) in the workspace and
 // attn_join_kernel joins them in split order.
+//
+// Measured: causal 2 x 4,096, 32 query over 8 key heads, D = 128 bf16 293-309 us
+// (890-940 TFLOP/s of the visible pairs' products; matrix cores 36% and vector
+// unit 34% busy, two waves per SIMD for the registers), 8,192 keys in full 275
+// us (1,000 TFLOP/s); at D = 64 the vector unit bounds it (an exponential and
+// six operations per pair beside 256 flop): 4 x 16 heads of 2,048 causal with the
+// bias 60 us. Single tokens are bound by HBM: 8 x 8 key heads of up to 16,384
+// keys, D = 128, 73-75 us (4.5 TB/s).
 #pragma once
 
 #include "attn_tile.hpp"

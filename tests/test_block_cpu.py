@@ -337,3 +337,13 @@ def test_residual_wiring_and_attention_gradients_on_stand_ins(dyt, monkeypatch):
     assert (t.grad == 7).all() and seen["causal"] is True
     block.attention(q.transpose(2, 3).contiguous().transpose(2, 3), k, v)
     assert seen["strides"][-1] == 1
+
+
+def test_a_full_cache_refuses_more(dyt):
+    c = dyt.KVCache(2, 5, 1, 4, torch.float32, "cpu")
+    x = torch.ones(2, 3, 1, 4)
+    assert c.append(x, x).tolist() == [0, 0] and c.length.tolist() == [3, 3]
+    with pytest.raises(ValueError, match="no room"):
+        c.append(x, x)
+    assert c.append(x[:, :2], 2 * x[:, :2]).tolist() == [3, 3] and c.length.tolist() == [5, 5]
+    assert (c.k == 1).all() and (c.v[:, 3:] == 2).all()

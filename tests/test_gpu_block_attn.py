@@ -290,6 +290,21 @@ def test_large(dyt, dt, case, causal):
         assert (g[:b] == 0).all()
 
 
+@pytest.mark.parametrize("size", [(8, 300, 1030, 16, 16, 128), (2, 40, 1200, 2, 2, 128), (1, 90, 2300, 3, 3, 64)], ids=str)
+@pytest.mark.parametrize("dt", DTYPES)
+def test_the_widest_table(dyt, dt, size):
+    """Every bucket and the longest reach: the most LDS each kernel takes."""
+    t, do, kw = make(18, DTYPES[dt], *size, buckets=128, distance=1024, causal=False)
+    b = size[0] - 1
+    only = torch.zeros_like(do)
+    only[b] = do[b]
+    o, stats = dyt.dyt_attn_forward(t["q"], t["k"], t["v"], **kw)
+    grads = dyt.dyt_attn_backward(t["q"], t["k"], t["v"], o, only, stats, **kw)
+    ref = Attention(*(t[n][b:] for n in "qkv"), **kw)
+    ref.check_forward(o[b:], stats[b:])
+    ref.check_backward(do[b:], *(g[b:] for g in grads[:3]), *grads[3:])
+
+
 @pytest.mark.parametrize("buckets", [0, 16])
 def test_gradients_against_differences(dyt, buckets):
     """f = sum(w o): its change along a direction, from the float32 forward."""

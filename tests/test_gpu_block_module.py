@@ -108,6 +108,9 @@ def test_a_cache_gives_what_the_whole_sequence_gives(dyt, buckets):
     assert (torch.cat(got, 1) - want).abs().max() <= 200 * 2.0 ** -24 * 4
     with pytest.raises(ValueError):
         m(x, seqlens=cache.length, cache=cache)
+    with pytest.raises(ValueError, match="no room"):
+        m(x[:, :1], cache=cache)
+    assert cache.length.tolist() == [30, 30, 30]
 
 
 @pytest.mark.parametrize("norm", ["dyt", "layernorm"])
