@@ -282,8 +282,8 @@ __global__ __launch_bounds__(NW * SL * 64, attn_waves(sizeof(T))) void attn_dkv_
     const int mine = sl * NS * 32 * TL::pitch;
     const int row_lane = TL::row_lane(lane) + mine, col_at = TL::col_lane(lane, 0) + mine;
     const int col_at8 = TL::col_lane(lane, 8) + mine;
-    // log sums and delta of a tile: rows that are not there get 0, and as
-    // their dO and q are zeros they add nothing
+    // log sums and delta of a tile: rows that are not there get 0, as do
+    // their dO and q
     const int stat_row = (W > 1 ? (wave >> 1) * 64 : 0) + lane, stat_pos = stat_row / a.pack;
     const uint32_t stat_off =
         stat_row < take ? (uint32_t)((stat_row - stat_pos * a.pack) * a.Sq + stat_pos) * 4u : kOutside;
@@ -379,11 +379,14 @@ __global__ __launch_bounds__(NW * SL * 64, attn_waves(sizeof(T))) void attn_dkv_
                 for (int i = 0; i < 16; ++i)
                     p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -st[8 * (i / 4) + (i % 4)]));
             }
-            if (key0 + 32 > w.len || (a.causal && key0 + 31 > imin)) {
-                // first row that sees the key
-                const int first = there ? (a.causal ? min(max(key - w.start, 0), a.Sq) * a.pack : 0) : 0x7fffffff;
+            if (key0 + 32 > w.len || (a.causal && key0 + 31 > imin) || rs + 32 > end) {
+                // rows that see the key: `count` from `first` on. Rows past the end have
+                // s = 0 and log sum 0, so with the bias e^bias as p: zeros of dO would
+                // meet an infinity where that passes the type's range.
+                const int first = a.causal ? min(max(key - w.start, 0), a.Sq) * a.pack : 0;
+                const uint32_t count = there ? (uint32_t)max(end - first, 0) : 0u;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) p[i] = rs + acc_row(i, h) >= first ? p[i] : 0.0f;
+                for (int i = 0; i < 16; ++i) p[i] = (uint32_t)(rs + acc_row(i, h) - first) < count ? p[i] : 0.0f;
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -395,7 +398,7 @@ __global__ __launch_bounds__(NW * SL * 64, attn_waves(sizeof(T))) void attn_dkv_
 #pragma unroll
             for (int i = 0; i < 16; ++i) p[i] *= dp[i] - st[SR + 8 * (i / 4) + (i % 4)];
             if constexpr (BIAS) {
-                // rows past the end have q = dO = 0 and delta = 0: dS = 0
+                // rows past the end have p = 0 and finite dP - delta: dS = 0
                 if (near) {
                     // diagonal t = key - query + 31 has its elements in columns (keys)
                     // 0 .. t, diagonal t + 32 in t + 1 .. 31: they share row t
