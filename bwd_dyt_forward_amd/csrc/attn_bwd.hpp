@@ -246,7 +246,9 @@ __global__ __launch_bounds__(NW * SL * 64, attn_waves(sizeof(T))) void attn_dkv_
     const int sl = W == NW ? 0 : wave / NW;      // and its slice of each tile's rows
     const int key0 = (w.block * NW + kw) * 32;
     const int key = key0 + (lane & 31);
-    const bool there = key < w.len;
+    // keys that some row sees: those behind them may hold anything and are never read
+    const int seen = a.causal ? min(w.len, w.start + a.Sq) : w.len;
+    const bool there = key < seen;
     const float c = a.scale * kLog2e;
 
     // rows that see a key of this workgroup, in tiles of whole positions
@@ -257,7 +259,7 @@ __global__ __launch_bounds__(NW * SL * 64, attn_waves(sizeof(T))) void attn_dkv_
         if (first >= a.Sq) begin = end;
         else begin = max(begin, first * a.pack / take * take);
     }
-    if (w.block * NW * 32 >= w.len) begin = end;
+    if (w.block * NW * 32 >= seen) begin = end;
 
     const Rows qr = {a.q + w.b * a.qs.b + w.head * a.qs.h, a.qs.s, a.qs.h, a.pack};
     const Rows dr = {a.dout + w.b * a.dos.b + w.head * a.dos.h, a.dos.s, a.dos.h, a.pack};
@@ -338,7 +340,7 @@ __global__ __launch_bounds__(NW * SL * 64, attn_waves(sizeof(T))) void attn_dkv_
         if (r0 + take < end) bring(r0 + take, at_pos, buf ^ 1);
         constexpr int qt = buf * RB, ot = qt + 2 * RB;
         // (a branch around a single sub-tile would have the accumulators copied)
-        if (key0 >= w.len || (a.causal && key0 > w.start + min(pos0 + sub_last[NS - 1], last_pos))) return;
+        if (key0 >= seen || (a.causal && key0 > w.start + min(pos0 + sub_last[NS - 1], last_pos))) return;
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
             const int rs = r0 + (sl * NS + n) * 32;
@@ -379,7 +381,7 @@ __global__ __launch_bounds__(NW * SL * 64, attn_waves(sizeof(T))) void attn_dkv_
                 for (int i = 0; i < 16; ++i)
                     p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -st[8 * (i / 4) + (i % 4)]));
             }
-            if (key0 + 32 > w.len || (a.causal && key0 + 31 > imin) || rs + 32 > end) {
+            if (key0 + 32 > seen || (a.causal && key0 + 31 > imin) || rs + 32 > end) {
                 // rows that see the key: `count` from `first` on. Rows past the end have
                 // s = 0 and log sum 0, so with the bias e^bias as p: zeros of dO would
                 // meet an infinity where that passes the type's range.

@@ -1,5 +1,6 @@
 """Attention's gradients where a masked place could leak into a sum: padding
-rows of the last tile under a large bias, against the formulas in float64
+rows of the last tile under a large bias, and keys that the causal mask hides
+from every row, against the formulas in float64
 (tests/block_ref.py) and against the same problem with whole tiles."""
 import math
 
@@ -57,3 +58,29 @@ def test_rows_of_zero_gradient_change_no_bit(dyt, dt, entry, causal, size):  # n
     got = dyt.dyt_attn_backward(q, t["k"], t["v"], o, do, stats[:, :, :Sq].contiguous(), **kw)
     for name, a, b in zip(("dq", "dk", "dv", "dtable"), got, (want[0][:, :Sq], *want[1:])):
         assert torch.isfinite(a).all() and torch.equal(a, b), name
+
+
+# where start + Sq falls inside a block of 32 keys below the length: q_start,
+# size, lengths (None: all keys)
+HIDDEN = [([10], (1, 70, 150, 2, 1, 64), None), ([0, 3, 40], (3, 64, 200, 4, 2, 72), [200, 90, 130]),
+          ([5, -20], (2, 33, 100, 6, 2, 32), None), ([100, 7], (2, 32, 1200, 1, 1, 128), [1200, 50]),
+          ([17] * 16, (16, 160, 300, 16, 16, 64), None), ([9] * 8, (8, 130, 260, 32, 8, 128), None),
+          ([1], (1, 1, 40, 8, 1, 64), None), ([2], (1, 40, 77, 3, 1, 33), None)]
+
+
+@pytest.mark.parametrize("buckets", [0, 16])
+@pytest.mark.parametrize("case", HIDDEN, ids=str)
+@pytest.mark.parametrize("dt", DTYPES)
+def test_keys_past_the_last_causal_position(dyt, dt, case, buckets):  # noqa: F811
+    """A cache's tail that no row sees yet: its memory may hold anything, and
+    its gradients are zeros."""
+    starts, size, lens = case
+    B, Sq, Sk = size[:3]
+    t, do, kw = make(43, DTYPES[dt], *size, starts=starts, lens=lens, causal=True, buckets=buckets, bidirectional=False)
+    ends = [max(0, min(n, s + Sq)) for s, n in zip(starts, lens or [Sk] * B)]
+    for b, end in enumerate(ends):
+        t["k"][b, end:] = math.inf if b % 3 == 1 else math.nan
+        t["v"][b, end:] = math.inf if b % 2 else math.nan
+    _, _, _, dk, dv, *_ = run_and_check(dyt, t, do, kw)
+    for b, end in enumerate(ends):
+        assert (dk[b, end:] == 0).all() and (dv[b, end:] == 0).all()
