@@ -104,6 +104,7 @@ __global__ __launch_bounds__(NW * SL * 64, attn_waves(sizeof(T))) void attn_dq_k
         }
     }
     delta = swap32_other_sum(delta);
+    if (a.causal && pos < 0) delta = 0.0f;   // sees no key: its do may hold anything
     float lse = INFINITY;   // a row that sees no key: every p is 2^-inf
     if (there) {
         const int64_t at = ((int64_t)w.b * a.Hq + w.head + g) * a.Sq + pos_i;
@@ -166,7 +167,11 @@ __global__ __launch_bounds__(NW * SL * 64, attn_waves(sizeof(T))) void attn_dq_k
                 if (js + 32 > end || (a.causal && js + 31 > w.start + imin)) {
                     const int last = a.causal ? min(end - 1, pos) : end - 1;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) p[i] = js + acc_row(i, h) <= last ? p[i] : 0.0f;
+                    for (int i = 0; i < 16; ++i) {
+                        const bool in = js + acc_row(i, h) <= last;
+                        p[i] = in ? p[i] : 0.0f;
+                        if constexpr (!AGAIN) dp[i] = in ? dp[i] : 0.0f;   // NaN of a row that sees no key
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -289,9 +294,11 @@ __global__ __launch_bounds__(NW * SL * 64, attn_waves(sizeof(T))) void attn_dkv_
     const int stat_row = (W > 1 ? (wave >> 1) * 64 : 0) + lane, stat_pos = stat_row / a.pack;
     const uint32_t stat_off =
         stat_row < take ? (uint32_t)((stat_row - stat_pos * a.pack) * a.Sq + stat_pos) * 4u : kOutside;
+    // rows at negative positions see no key and are left out, whatever they hold
+    const int blind = a.causal ? min(max(-w.start, 0), a.Sq) * a.pack : 0;
     const auto bring = [&](int r0, int pos0, int to) __attribute__((always_inline)) {
-        qs.fetch(to * RB, qr, end - r0, take, a.D, wave, lane);
-        dos.fetch(2 * RB + to * RB, dr, end - r0, take, a.D, wave, lane);
+        qs.template fetch<true>(to * RB, qr, end - r0, take, a.D, wave, lane, blind - r0);
+        dos.template fetch<true>(2 * RB + to * RB, dr, end - r0, take, a.D, wave, lane, blind - r0);
         // 64 rows of one of the two to a wave (both to a single wave)
         if (W == 1 || wave < SR / 32) {
             for (int k = wave & 1; k < 2; k += W == 1 ? 1 : 2)

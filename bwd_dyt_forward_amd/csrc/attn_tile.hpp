@@ -297,12 +297,14 @@ template <typename T, int DP, int ROWS, int NW, bool VEC> struct Stream {
     }
 
     // The next tile's rows into the tile at `lds`; `left` of them are there,
-    // the others come out as zeros.
-    __device__ __forceinline__ void fetch(int lds, const Rows& w, int left, int take, int D, int wave, int lane) {
+    // the others, and with SKIP the first `skip`, come out as zeros.
+    template <bool SKIP = false>
+    __device__ __forceinline__ void fetch(int lds, const Rows& w, int left, int take, int D, int wave, int lane,
+                                          int skip = 0) {
         if constexpr (VEC) {
             const i32x4 rsrc = descriptor(base);
             const uint32_t to = lds_address(lds + wave * 1024);
-            if (left >= take) {
+            if (left >= take && (!SKIP || skip <= 0)) {
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
                     if (instrs % NW == 0 || i * NW + wave < instrs) load_to_lds16(rsrc, to + i * NW * 1024, off[i]);
@@ -311,7 +313,7 @@ template <typename T, int DP, int ROWS, int NW, bool VEC> struct Stream {
                 for (int i = 0; i < NI; ++i) {
                     int row, chunk;
                     place(wave, lane, i, row, chunk);
-                    const uint32_t at = row < left ? off[i] : kOutside;
+                    const uint32_t at = (!SKIP || row >= skip) && row < left ? off[i] : kOutside;
                     if (instrs % NW == 0 || i * NW + wave < instrs) load_to_lds16(rsrc, to + i * NW * 1024, at);
                 }
             }
@@ -326,7 +328,7 @@ template <typename T, int DP, int ROWS, int NW, bool VEC> struct Stream {
                 for (int k = 0; k < N; ++k) {
                     const int d = chunk * N + k;
                     e[k] = T{};
-                    if (row < min(left, take) && d < D) e[k] = p[d];
+                    if ((!SKIP || row >= skip) && row < min(left, take) && d < D) e[k] = p[d];
                 }
                 __builtin_memcpy(smem + lds + row * TL::pitch + ((chunk ^ TL::swizzle(row)) << 4), e, 16);
             }

@@ -28,10 +28,12 @@
  *   dtable[t,h] = sum of ds over the pairs of bucket t
  *
  * A query that sees no key gives o = 0 and stats = -inf, and takes part in no
- * gradient. Keys that no query of the batch entry sees (at or past len_b, or
- * past the last causal position) are never read: their memory may hold
- * anything, NaN included. Keys and values that some query sees have to be
- * finite: a product with an exact zero of p still spreads a NaN.
+ * gradient; at a negative position, or in a batch entry of no keys, whatever
+ * its q and do hold. Keys that no query of the batch entry sees (at or past
+ * len_b, or past the last causal position) are never read: their memory may
+ * hold anything, NaN included. Keys and values that some query sees, and the q
+ * and do of queries that see a key, have to be finite: a product with an exact
+ * zero of p still spreads a NaN.
  *
  * Buckets: with `bidirectional`, num_buckets / 2 per direction (keys after
  * the query, j > pos, take the upper half) and the distance is |j - pos|;

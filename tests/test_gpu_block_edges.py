@@ -1,6 +1,6 @@
 """Attention's gradients where a masked place could leak into a sum: padding
-rows of the last tile under a large bias, and keys that the causal mask hides
-from every row, against the formulas in float64
+rows of the last tile under a large bias, keys that the causal mask hides
+from every row, and rows that see no key, against the formulas in float64
 (tests/block_ref.py) and against the same problem with whole tiles."""
 import math
 
@@ -84,3 +84,28 @@ def test_keys_past_the_last_causal_position(dyt, dt, case, buckets):  # noqa: F8
     _, _, _, dk, dv, *_ = run_and_check(dyt, t, do, kw)
     for b, end in enumerate(ends):
         assert (dk[b, end:] == 0).all() and (dv[b, end:] == 0).all()
+
+
+@pytest.mark.parametrize("buckets", [0, 16])
+@pytest.mark.parametrize("size", [(3, 70, 90, 4, 2, 64), (2, 130, 200, 6, 2, 40), (16, 160, 300, 16, 16, 128),
+                                  (2, 40, 900, 2, 2, 33), (8, 300, 256, 16, 4, 64)], ids=str)
+@pytest.mark.parametrize("dt", DTYPES)
+def test_rows_before_the_first_key(dyt, dt, size, buckets):  # noqa: F811
+    """Left-padded sequences: rows at negative positions see no key under the
+    causal mask, and neither their q nor their do may reach a gradient."""
+    B, Sq = size[:2]
+    starts = [-((7 + 13 * b) % (Sq + 5)) for b in range(B)]
+    t, do, kw = make(47, DTYPES[dt], *size, starts=starts, causal=True, buckets=buckets, bidirectional=False)
+    clean, do_clean = t["q"].clone(), do.clone()
+    for b, s in enumerate(starts):
+        clean[b, :-s] = 0
+        do_clean[b, :-s] = 0
+        t["q"][b, :-s] = math.nan if b % 2 else math.inf
+        do[b, :-s] = math.inf if b % 3 else math.nan
+    o, stats = dyt.dyt_attn_forward(t["q"], t["k"], t["v"], **kw)
+    grads = dyt.dyt_attn_backward(t["q"], t["k"], t["v"], o, do, stats, **kw)
+    ref = Attention(clean, t["k"], t["v"], **kw)
+    ref.check_forward(o, stats)
+    ref.check_backward(do_clean, *grads)
+    for b, s in enumerate(starts):
+        assert (o[b, :-s] == 0).all() and (grads[0][b, :-s] == 0).all()
