@@ -223,7 +223,7 @@ __device__ __forceinline__ void alternate(int begin, int end, int by, F&& step) 
 // (a read lane, a restored spill), which the compiler does not add for asm.
 __device__ __forceinline__ void load_to_lds16(const i32x4& rsrc, uint32_t lds, uint32_t off) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :: "s"(lds), "v"(off), "s"(rsrc) : "memory");
+                 :: "s"(lds), "v"(off), "s"(rsrc) : "memory", "m0");
 }
 
 __device__ __forceinline__ i32x4 descriptor(const void* base) {
@@ -243,7 +243,7 @@ __device__ __forceinline__ uint32_t lds_address(int at) {
 // 4 bytes per lane to `lds` + 4 lane.
 __device__ __forceinline__ void load_to_lds4(const void* base, int lds, uint32_t off) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                 :: "s"(lds_address(lds)), "v"(off), "s"(descriptor(base)) : "memory");
+                 :: "s"(lds_address(lds)), "v"(off), "s"(descriptor(base)) : "memory", "m0");
 }
 
 // Waits for this wave's direct-to-LDS loads; the barrier that follows makes
