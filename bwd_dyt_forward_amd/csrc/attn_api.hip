@@ -107,6 +107,46 @@ bool view(const dyt_attn_desc& d, const Tensor& t, bool out, Strides& s, int64_t
     return true;
 }
 
+// One output's rows: up to three dimensions that step over each other, the
+// largest stride first, and the bytes of a row.
+struct Layout {
+    struct { int64_t n, stride; } dim[3];
+    int dims;
+    int64_t row;
+    Layout(const int64_t (&size)[3], const Strides& s, int64_t row_bytes) : dims(0), row(row_bytes) {
+        const int64_t stride[3] = {s.b, s.s, s.h};
+        for (int i = 0; i < 3; ++i)
+            if (size[i] > 1) dim[dims++] = {size[i], stride[i]};
+        std::sort(dim, dim + dims, [](const auto& x, const auto& y) { return x.stride > y.stride; });
+    }
+    int64_t extent(int from) const {
+        int64_t n = row;
+        for (int i = from; i < dims; ++i) n += (dim[i].n - 1) * dim[i].stride;
+        return n;
+    }
+};
+
+// Whether x from its dimension i on and y from j on, `delta` bytes behind it,
+// share a byte. The larger stride (or both, where they are the same) is taken
+// out, and only those of its multiples are tried at which what is left can
+// meet: two or three for slices of one tensor. Layouts that need more than
+// `tries` in all count as sharing.
+bool share(const Layout& x, int i, const Layout& y, int j, int64_t delta, int& tries) {
+    const int64_t ex = x.extent(i), ey = y.extent(j);
+    if (delta >= ex || delta <= -ey) return false;
+    if (--tries < 0 || (i == x.dims && j == y.dims)) return true;
+    const int64_t sx = i < x.dims ? x.dim[i].stride : 0, sy = j < y.dims ? y.dim[j].stride : 0, step = std::max(sx, sy);
+    const int64_t nx = sx == step ? x.dim[i].n - 1 : 0, ny = sy == step ? y.dim[j].n - 1 : 0;
+    const int ii = i + (sx == step), jj = j + (sy == step);
+    // delta + k step within (-rest of y, rest of x)
+    const int64_t rx = ex - nx * step, ry = ey - ny * step;
+    const auto floor_div = [](int64_t a, int64_t b) { return a / b - (a % b < 0); };
+    const int64_t lo = std::max(-nx, floor_div(-ry - delta, step) + 1), hi = std::min(ny, -floor_div(delta - rx, step) - 1);
+    for (int64_t k = lo; k <= hi; ++k)
+        if (share(x, ii, y, jj, delta + k * step, tries)) return true;
+    return false;
+}
+
 // Whether a tensor takes 16-byte accesses: aligned base, strides and rows,
 // and a tile's rows (64 positions of up to 32 heads) within a 31-bit offset.
 bool vec_ok(const void* p, const Strides& s, int64_t row_bytes) {
@@ -396,22 +436,28 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
     if (!aligned({q, k, v, o, dout, dq, dk, dv}, es) || !aligned({stats}, 4) || !lists_aligned(d) ||
         (d.table && !aligned({dtable}, ts)))
         return DYT_ERR_MISALIGNED;
-    if (p.bwd_bytes && (!workspace || workspace_bytes < p.bwd_bytes)) return DYT_ERR_WORKSPACE_TOO_SMALL;
-    if (p.bwd_bytes && !aligned({workspace}, 16)) return DYT_ERR_MISALIGNED;
     const int64_t tb = d.table ? d.num_buckets * d.Hq * ts : 0;
     const Range in[] = {{q, n.q}, {k, n.k}, {v, n.v}, {o, n.o}, {dout, n.dout},
                         {stats, p.nothing_out ? 0 : d.B * d.Hq * d.Sq * 4},
                         {d.seqlens_k, d.B * 4}, {d.q_start, d.B * 4}, {d.table, tb}};
     // dq, dk and dv may be interleaved slices of one tensor: each is held
-    // against the inputs, the workspace and dtable, not against each other
+    // against the inputs, the workspace and dtable as a range, against each
+    // other element by element
     const Range outs[] = {{dq, n.dq}, {dk, n.dk}, {dv, n.dv}};
     const Range rest[] = {{dtable, tb}, {workspace, (int64_t)p.bwd_bytes}};
+    const int64_t of_q[] = {d.B, d.Sq, d.Hq}, of_k[] = {d.B, d.Sk, d.Hkv};
+    const Layout layouts[] = {{of_q, a.dqs, row}, {of_k, a.dks, row}, {of_k, a.dvs, row}};
     for (int i = 0; i < 3; ++i) {
         if (!disjoint(in, 9, outs + i, 1) || !disjoint(rest, 2, outs + i, 1)) return DYT_ERR_INVALID_ARG;
-        for (int j = 0; j < i; ++j)
-            if (outs[i].bytes && outs[j].bytes && outs[i].p == outs[j].p) return DYT_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j) {
+            int tries = 4096;
+            if (meet(outs[i], outs[j]) && share(layouts[i], 0, layouts[j], 0, (const char*)outs[j].p - (const char*)outs[i].p, tries))
+                return DYT_ERR_INVALID_ARG;
+        }
     }
     if (!disjoint(in, 9, rest, 2)) return DYT_ERR_INVALID_ARG;
+    if (p.bwd_bytes && (!workspace || workspace_bytes < p.bwd_bytes)) return DYT_ERR_WORKSPACE_TOO_SMALL;
+    if (p.bwd_bytes && !aligned({workspace}, 16)) return DYT_ERR_MISALIGNED;
     if (p.nothing_out && p.nothing_keys && !(d.table && d.Hq > 0)) return DYT_OK;
 
     const hipStream_t s = (hipStream_t)stream;

@@ -144,7 +144,8 @@ int dyt_attn_forward(const dyt_attn_desc* desc, const void* q, const void* k, co
 
 /* dq, dk, dv and, with a table, dtable [num_buckets, Hq] of table_dtype are
  * written whole (zeros where nothing contributes). o and stats are the
- * forward's. */
+ * forward's. dq, dk and dv may be interleaved (slices of one tensor); sharing
+ * an element with each other, or memory with anything else, is refused. */
 int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, const void* v,
                       const void* o, const void* dout, const float* stats, void* dq, void* dk,
                       void* dv, void* dtable, void* workspace, size_t workspace_bytes,

@@ -3,9 +3,10 @@ of the ranges, the cache's and the autograd functions' bookkeeping. Pointers
 are made up; every call comes back before it would use them."""
 import glob
 import os
+import random
 import re
 
-from test_block_cpu import CSRC
+from test_block_cpu import CSRC, bwd, codes, desc, dyt  # noqa: F401
 
 
 def test_every_asm_statement_that_writes_m0_names_it():
@@ -17,3 +18,73 @@ def test_every_asm_statement_that_writes_m0_names_it():
                 found += 1
                 assert '"m0"' in asm.rsplit(":", 1)[1], (path, asm)
     assert found == 2
+
+
+def places(base, size, stride):
+    """Elements of a [B, S, H, D] tensor by their address."""
+    B, S, H, D = size
+    return {base + b * stride[0] + s * stride[1] + h * stride[2] + x
+            for b in range(B) for s in range(S) for h in range(H) for x in range(D)}
+
+
+def overlap_status(dyt, at, sizes, strides):
+    """The backward's answer for outputs at these element offsets, without a
+    workspace: DYT_ERR_WORKSPACE_TOO_SMALL where they pass."""
+    (B, Sq, Hq, D), (_, Sk, Hkv, _) = sizes[:2]
+    d = desc(B=B, Sq=Sq, Sk=Sk, Hq=Hq, Hkv=Hkv, D=D, **dict(zip(("dq", "dk", "dv"), strides)))
+    base = 1 << 40
+    return bwd(dyt, d, n=0, ws=None, **{t: base + 2 * x for t, x in zip(("dq", "dk", "dv"), at)})
+
+
+def test_gradients_that_share_elements_are_refused(dyt, codes):  # noqa: F811
+    bad, ok = codes["DYT_ERR_INVALID_ARG"], codes["DYT_ERR_WORKSPACE_TOO_SMALL"]
+    B, S, Hq, Hkv, D = 2, 33, 4, 2, 64
+    q, k = (B, S, Hq, D), (B, S, Hkv, D)
+    n = Hq + 2 * Hkv
+    fused = (S * n * D, n * D, D)
+    own = lambda s: (s[1] * s[2] * s[3], s[2] * s[3], s[3])
+    far = 1 << 24
+    # slices of one projection, each after the other and with one head too far
+    assert overlap_status(dyt, (0, Hq * D, (Hq + Hkv) * D), (q, k, k), (fused,) * 3) == ok
+    assert overlap_status(dyt, (0, (Hq - 1) * D, (Hq + Hkv) * D), (q, k, k), (fused,) * 3) == bad
+    assert overlap_status(dyt, (0, Hq * D, (Hq + Hkv - 1) * D), (q, k, k), (fused,) * 3) == bad
+    assert overlap_status(dyt, (0, Hq * D + 1, (Hq + Hkv) * D), (q, k, k), (fused,) * 3) == bad
+    # [B, n, S, D]
+    heads = (n * S * D, D, S * D)
+    assert overlap_status(dyt, (0, Hq * S * D, (Hq + Hkv) * S * D), (q, k, k), (heads,) * 3) == ok
+    assert overlap_status(dyt, (0, Hq * S * D - 1, (Hq + Hkv) * S * D), (q, k, k), (heads,) * 3) == bad
+    # tensors of their own, one behind the other and one element over it
+    m = B * S * Hkv * D
+    assert overlap_status(dyt, (far, 0, m), (q, k, k), (own(q), own(k), own(k))) == ok
+    assert overlap_status(dyt, (far, 0, m - 1), (q, k, k), (own(q), own(k), own(k))) == bad
+    assert overlap_status(dyt, (far, 0, 64), (q, k, k), (own(q), own(k), own(k))) == bad
+    assert overlap_status(dyt, (0, B * S * Hq * D - 1, far), (q, k, k), (own(q), own(k), own(k))) == bad
+    # batch entries in turn
+    assert overlap_status(dyt, (far, 0, S * Hkv * D), (q, k, k), (own(q), (2 * S * Hkv * D, Hkv * D, D), (2 * S * Hkv * D, Hkv * D, D))) == ok
+
+
+def test_shared_elements_of_random_layouts(dyt, codes):  # noqa: F811
+    """Against sets of addresses."""
+    bad, ok = codes["DYT_ERR_INVALID_ARG"], codes["DYT_ERR_WORKSPACE_TOO_SMALL"]
+    rng = random.Random(11)
+    met = 0
+
+    def layout(size):
+        order, at, stride = rng.sample(range(3), 3), size[3] + rng.choice([0, 0, 1, 8]), [0, 0, 0]
+        for i in order:
+            stride[i] = at * rng.choice([1, 1, 2, 3])
+            at = stride[i] * size[i]
+        return tuple(stride)
+
+    for _ in range(400):
+        B, Sq, Sk, Hkv, D = (rng.randint(1, n) for n in (3, 5, 5, 3, 9))
+        q, k = (B, Sq, Hkv * rng.randint(1, 2), D), (B, Sk, Hkv, D)
+        strides = [layout(q), layout(k), layout(k)]
+        if rng.random() < 0.5:
+            strides[2] = strides[1]
+        at = [rng.randint(0, rng.choice([60, 600])) for _ in range(3)]
+        sets = [places(a, s, st) for a, s, st in zip(at, (q, k, k), strides)]
+        want = bad if sets[0] & sets[1] or sets[0] & sets[2] or sets[1] & sets[2] else ok
+        met += want == bad
+        assert overlap_status(dyt, at, (q, k, k), strides) == want, (q, k, strides, at)
+    assert 50 < met < 350
