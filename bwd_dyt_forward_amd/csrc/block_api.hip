@@ -18,29 +18,35 @@ namespace dytb {
 // workgroup, kFinSlices slices of rows side by side, each summed in row
 // order, then the slices in slice order. The loads of a slice do not depend
 // on each other; 16 slices of up to 64 rows each took 4-6 us at every width.
+// A grid may have 2^32 threads; from 2^15 workgroups on (over a million columns)
+// they walk.
 constexpr int kFinSlices = 16;
+constexpr int64_t kFinGrid = 1 << 15;
 
 __global__ __launch_bounds__(64 * kFinSlices) void ln_finish_kernel(const float* part, int64_t pitch,
                                                                     int rows, int64_t N, void* dgamma,
                                                                     void* dbeta, int pdt) {
     __shared__ float red[kFinSlices][64];
     const int lane = (int)threadIdx.x & 63, slice = (int)threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-    float s = 0.0f;
-    if (c < 2 * N) {
-        const int per = (rows + kFinSlices - 1) / kFinSlices;
-        const int lo = slice * per, hi = min(lo + per, rows);
+    const int per = (rows + kFinSlices - 1) / kFinSlices;
+    const int lo = slice * per, hi = min(lo + per, rows);
+    for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < 2 * N; c0 += (int64_t)gridDim.x * 64) {
+        const int64_t c = c0 + lane;
+        float s = 0.0f;
+        if (c < 2 * N) {
 #pragma unroll 8
-        for (int r = lo; r < hi; ++r) s += part[r * pitch + c];
-    }
-    red[slice][lane] = s;
-    __syncthreads();
-    if (slice == 0 && c < 2 * N) {
-        s = 0.0f;
+            for (int r = lo; r < hi; ++r) s += part[r * pitch + c];
+        }
+        __syncthreads();   // the previous columns' sums have been read
+        red[slice][lane] = s;
+        __syncthreads();
+        if (slice == 0 && c < 2 * N) {
+            s = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kFinSlices; ++k) s += red[k][lane];
-        if (c < N) store_param(dgamma, c, pdt, s);
-        else store_param(dbeta, c - N, pdt, s);
+            for (int k = 0; k < kFinSlices; ++k) s += red[k][lane];
+            if (c < N) store_param(dgamma, c, pdt, s);
+            else store_param(dbeta, c - N, pdt, s);
+        }
     }
 }
 
@@ -50,7 +56,7 @@ __global__ __launch_bounds__(64 * kFinSlices) void ln_finish_kernel(const float*
 // 16 N grid <= 0.03 * 3 M N s).
 int ln_bwd_grid(const LnConfig& c, int64_t M, int64_t elem_bytes) {
     const int64_t need = (M + ln_groups(c) - 1) / ln_groups(c);
-        const int64_t most = c.threads > 512 || c.threads == 0 ? 256 : 1024;
+    const int64_t most = c.threads > 512 || c.threads == 0 ? 256 : 1024;
     const int64_t cap = std::min(most, std::max<int64_t>(256, M * elem_bytes / 178 / 128 * 128));
     return (int)std::min(need, cap);
 }
@@ -127,7 +133,7 @@ int ln_backward(const void* x, int64_t ldx, const void* dy, int64_t lddy, const 
     if (!dgamma || !dbeta) return DYT_ERR_INVALID_ARG;
     const int64_t sx = dtype_size(xdt), sp = dtype_size(pdt);
     const hipStream_t s = (hipStream_t)stream;
-    const int fin_grid = (int)((2 * N + 63) / 64);
+    const int fin_grid = (int)std::min((2 * N + 63) / 64, kFinGrid);
     if (M == 0) {
         if (!aligned({dgamma, dbeta}, sp)) return DYT_ERR_MISALIGNED;
         ln_finish_kernel<<<fin_grid, 64 * kFinSlices, 0, s>>>(nullptr, 0, 0, N, dgamma, dbeta, pdt);

@@ -109,3 +109,22 @@ def test_rows_before_the_first_key(dyt, dt, size, buckets):  # noqa: F811
     ref.check_backward(do_clean, *grads)
     for b, s in enumerate(starts):
         assert (o[b, :-s] == 0).all() and (grads[0][b, :-s] == 0).all()
+
+
+def test_layer_norm_of_a_row_of_2_to_the_27(dyt):  # noqa: F811
+    """The parameters' gradients of more columns than one launch has threads
+    for: the second pass walks. One row, so dbeta is dy and dgamma is one
+    product."""
+    N = (1 << 27) + 3
+    g = torch.Generator(device="cuda").manual_seed(53)
+    x, dy = (torch.randn(1, N, device="cuda", generator=g, dtype=torch.float16) for _ in range(2))
+    gamma = torch.ones(N, device="cuda", dtype=torch.float16)
+    y, mean, rstd = dyt.dyt_ln_forward(x, gamma, torch.zeros_like(gamma))
+    dx, dgamma, dbeta = dyt.dyt_ln_backward(x, dy, mean, rstd, gamma)
+    assert torch.equal(dbeta, dy[0])
+    n = (x[0].double() - mean.double()) * rstd.double()
+    want = n * dy[0].double()
+    # n is rounded twice and the product once in float32, the result to float16
+    bound = want.abs() * (2.0 ** -11 + 4 * 2.0 ** -24) + 2.0 ** -24
+    assert ((dgamma.double() - want).abs() <= bound).all()
+    assert torch.isfinite(dx).all() and torch.isfinite(y).all()
