@@ -267,7 +267,7 @@ int check(const dyt_attn_desc& d, Borders& borders) {
     const int64_t G = d.Hq / d.Hkv;
     if (d.Sk > kMaxRows || d.Sq > kMaxRows || G > kMaxRows || d.Sq * std::max<int64_t>(G, 1) > kMaxRows)
         return DYT_ERR_INVALID_ARG;
-    if (d.Hq > (1 << 20) || d.B > (1 << 24) || d.B * d.Hq > (1 << 24) || d.B * d.Hkv > (1 << 24))
+    if (d.Hq > (1 << 20) || d.Hkv > (1 << 20) || d.B > (1 << 24) || d.B * d.Hq > (1 << 24) || d.B * d.Hkv > (1 << 24))
         return DYT_ERR_INVALID_ARG;
     if (!dtype_ok(d.dtype) || (d.table && !dtype_ok(d.table_dtype))) return DYT_ERR_UNSUPPORTED_DTYPE;
     return d.table ? fill_borders(d.num_buckets, d.max_distance, d.bidirectional, borders) : DYT_OK;
@@ -314,6 +314,18 @@ Plan make_plan(const dyt_attn_desc& d, const Borders& borders, bool backward, bo
     if (p.dkv_parts > 1) part = std::max(part, (size_t)p.dkv_parts * 2 * d.B * d.Hkv * d.Sk * dp * 4);
     p.bwd_bytes = p.off_part + part;
     return p;
+}
+
+// A launch has fewer than 2^32 threads. (The sums of float32 parts walk.)
+bool launches_fit(const dyt_attn_desc& d, const Plan& p, bool backward) {
+    const auto fit = [](int64_t groups, int threads) { return groups * threads < ((int64_t)1 << 32); };
+    const auto main = [&](const AttnPick& pick, int blocks, int split) {
+        return fit((int64_t)p.units * blocks * split, pick.nw * pick.sl * 64);
+    };
+    if (!backward)
+        return main(p.fwd, p.fwd_blocks, p.fwd_split) && (p.fwd_split == 1 || fit(p.units * p.rows, p.fwd.dp / 4 * 8));
+    return main(p.dq, p.dq_blocks, p.dq_split) && main(p.dkv, p.dkv_blocks, p.dkv_split) &&
+           (!d.table || fit(d.Hq * d.num_buckets, kTableThreads));
 }
 
 template <typename F>
@@ -364,15 +376,18 @@ size_t dyt_attn_forward_workspace_size(const dyt_attn_desc* desc) {
     if (!desc) return 0;
     Borders borders{};
     if (check(*desc, borders)) return 0;
-    const Plan p = make_plan(*desc, borders, false, true);
-    return p.nothing_out ? 0 : std::max(p.fwd_bytes, make_plan(*desc, borders, false, false).fwd_bytes);
+    const Plan p = make_plan(*desc, borders, false, true), each = make_plan(*desc, borders, false, false);
+    if (p.nothing_out || !launches_fit(*desc, p, false) || !launches_fit(*desc, each, false)) return 0;
+    return std::max(p.fwd_bytes, each.fwd_bytes);
 }
 
 size_t dyt_attn_backward_workspace_size(const dyt_attn_desc* desc) {
     if (!desc) return 0;
     Borders borders{};
     if (check(*desc, borders)) return 0;
-    return std::max(make_plan(*desc, borders, true, true).bwd_bytes, make_plan(*desc, borders, true, false).bwd_bytes);
+    const Plan p = make_plan(*desc, borders, true, true), each = make_plan(*desc, borders, true, false);
+    if (!launches_fit(*desc, p, true) || !launches_fit(*desc, each, true)) return 0;
+    return std::max(p.bwd_bytes, each.bwd_bytes);
 }
 
 int dyt_attn_forward(const dyt_attn_desc* desc, const void* q, const void* k, const void* v, void* o, float* stats,
@@ -390,6 +405,7 @@ int dyt_attn_forward(const dyt_attn_desc* desc, const void* q, const void* k, co
     const Plan p = make_plan(d, borders, false, vec_ok(q, a.qs, row) && vec_ok(k, a.ks, row) && vec_ok(v, a.vs, row) &&
                                                     vec_ok(o, a.os, row));
     if (p.nothing_out) return DYT_OK;
+    if (!launches_fit(d, p, false)) return DYT_ERR_INVALID_ARG;
     if (!q || !o || !stats || (d.Sk > 0 && (!k || !v))) return DYT_ERR_INVALID_ARG;
     if (d.Sk == 0) n.k = n.v = 0;
     if (!aligned({q, k, v, o}, es) || !aligned({stats}, 4) || !lists_aligned(d)) return DYT_ERR_MISALIGNED;
@@ -428,6 +444,7 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
     const Plan p = make_plan(d, borders, true, vec_ok(q, a.qs, row) && vec_ok(k, a.ks, row) && vec_ok(v, a.vs, row) &&
                                     vec_ok(o, a.os, row) && vec_ok(dout, a.dos, row) && vec_ok(dq, a.dqs, row) &&
                                     vec_ok(dk, a.dks, row) && vec_ok(dv, a.dvs, row));
+    if (!launches_fit(d, p, true)) return DYT_ERR_INVALID_ARG;
     if (p.nothing_out) n.q = n.o = n.dout = n.dq = 0;
     if (p.nothing_keys) n.k = n.v = n.dk = n.dv = 0;
     if (!p.nothing_out && (!q || !o || !dout || !stats || !dq)) return DYT_ERR_INVALID_ARG;

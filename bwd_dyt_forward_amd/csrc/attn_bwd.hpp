@@ -489,33 +489,35 @@ __global__ __launch_bounds__(NW * SL * 64, attn_waves(sizeof(T))) void attn_dkv_
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void attn_sum_kernel(SumArgs x) {
     constexpr int TPR = DP / 4, PER = 256 / TPR;
-    int64_t at = (int64_t)blockIdx.x * PER + (int)threadIdx.x / TPR;
+    if ((int)threadIdx.x >= PER * TPR) return;
     const int d = ((int)threadIdx.x % TPR) * 4;
     // workgroups past the first sum's rows make the second
     const int64_t first = (x.total + PER - 1) / PER;
-    const bool second = (int64_t)blockIdx.x >= first;
-    if (second) at -= first * PER;
-    const float* part = second ? x.part2 : x.part;
-    if ((int)threadIdx.x >= PER * TPR || at >= x.total) return;
-    float o[4] = {0, 0, 0, 0};
+    for (int64_t group = blockIdx.x; group < (x.out2 ? 2 : 1) * first; group += gridDim.x) {
+        const bool second = group >= first;
+        const int64_t at = (second ? group - first : group) * PER + (int)threadIdx.x / TPR;
+        const float* part = second ? x.part2 : x.part;
+        if (at >= x.total) continue;
+        float o[4] = {0, 0, 0, 0};
 #pragma unroll 4
-    for (int p = 0; p < x.parts; ++p) {
-        const f32x4 v = *(const f32x4*)(part + p * x.stride + at * DP + d);
+        for (int p = 0; p < x.parts; ++p) {
+            const f32x4 v = *(const f32x4*)(part + p * x.stride + at * DP + d);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] += v[k];
-    }
-    const int u = (int)(at / x.rows), r = (int)(at - (int64_t)u * x.rows);
-    const int b = u / x.hu, i = r / x.pack, head = (u - b * x.hu) * x.pack + (r - i * x.pack);
-    const Strides os = second ? x.os2 : x.os;
-    T* to = (T*)((second ? x.out2 : x.out) + b * os.b + (int64_t)i * os.s + (int64_t)head * os.h);
+            for (int k = 0; k < 4; ++k) o[k] += v[k];
+        }
+        const int u = (int)(at / x.rows), r = (int)(at - (int64_t)u * x.rows);
+        const int b = u / x.hu, i = r / x.pack, head = (u - b * x.hu) * x.pack + (r - i * x.pack);
+        const Strides os = second ? x.os2 : x.os;
+        T* to = (T*)((second ? x.out2 : x.out) + b * os.b + (int64_t)i * os.s + (int64_t)head * os.h);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (d + k < x.D) to[d + k] = dyt::from_f32<T>(o[k]);
-    if (x.delta && d == 0) {
-        const int64_t n = ((int64_t)b * x.hu * x.pack + head) * (x.rows / x.pack) + i;
-        float s = 0.0f;
-        for (int p = 0; p < x.parts; ++p) s += x.rest[p * x.total + n];
-        x.delta[n] += s;
+        for (int k = 0; k < 4; ++k)
+            if (d + k < x.D) to[d + k] = dyt::from_f32<T>(o[k]);
+        if (x.delta && d == 0) {
+            const int64_t n = ((int64_t)b * x.hu * x.pack + head) * (x.rows / x.pack) + i;
+            float s = 0.0f;
+            for (int p = 0; p < x.parts; ++p) s += x.rest[p * x.total + n];
+            x.delta[n] += s;
+        }
     }
 }
 

@@ -2,6 +2,8 @@
 // and of the sums of float32 parts.
 #pragma once
 
+#include <algorithm>
+
 #include "attn_bwd.hpp"
 #include "attn_launch.hpp"
 
@@ -20,12 +22,16 @@ int attn_launch_dkv(const AttnPick& p, const AttnArgs& a, hipStream_t s) {
     return st;
 }
 
+// From here on a sum's workgroups walk: far above what fills the card, and
+// below the 2^32 threads of a launch.
+constexpr int64_t kSumGrid = 1 << 22;
+
 template <typename T>
 void attn_launch_sum(int dp, const SumArgs& x, hipStream_t s) {
     with_dp(dp, [&](auto d) {
         constexpr int DP = decltype(d)::value, PER = 256 / (DP / 4);
-        const unsigned grid = (unsigned)((x.total + PER - 1) / PER) * (x.out2 ? 2 : 1);
-        attn_sum_kernel<T, DP><<<grid, 256, 0, s>>>(x);
+        const int64_t groups = (x.total + PER - 1) / PER * (x.out2 ? 2 : 1);
+        attn_sum_kernel<T, DP><<<(unsigned)std::min(groups, kSumGrid), 256, 0, s>>>(x);
     });
 }
 

@@ -117,6 +117,8 @@ typedef struct dyt_attn_strides {
  *   table      [num_buckets, Hq] of table_dtype, contiguous, or NULL: no bias
  *   causal, bidirectional: 0 or 1
  *   scale      finite
+ * Sk and Sq Hq / Hkv are at most 2^28, Hq and Hkv 2^20, B Hq and B Hkv 2^24, and
+ * no launch may need 2^32 threads (two a row and head, backward two a key and head).
  * num_buckets is even when bidirectional, and >= 2 (>= 4 when
  * bidirectional); max_distance is larger than a direction's exact buckets.
  */

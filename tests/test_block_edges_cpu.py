@@ -6,7 +6,7 @@ import os
 import random
 import re
 
-from test_block_cpu import CSRC, bwd, codes, desc, dyt  # noqa: F401
+from test_block_cpu import AT, CSRC, bwd, codes, desc, dyt, fwd  # noqa: F401
 
 
 def test_every_asm_statement_that_writes_m0_names_it():
@@ -88,3 +88,28 @@ def test_shared_elements_of_random_layouts(dyt, codes):  # noqa: F811
         met += want == bad
         assert overlap_status(dyt, at, (q, k, k), strides) == want, (q, k, strides, at)
     assert 50 < met < 350
+
+
+def test_problems_that_one_launch_cannot_hold(dyt, codes):  # noqa: F811
+    """A launch has fewer than 2^32 threads: refused before anything is
+    enqueued, not by a launch in the middle."""
+    bad = codes["DYT_ERR_INVALID_ARG"]
+    at = {t: (i + 1) << 48 for i, t in enumerate(AT)}
+    table = dict(table=1 << 60, buckets=128, distance=1024)
+    sizes = dyt.block_lib
+    for kw in (dict(B=1, Hq=64, Hkv=64, Sq=1 << 28, Sk=16, D=1), dict(B=64, Hq=64, Hkv=64, Sq=1 << 22, Sk=16, D=1),
+               dict(table, B=1, Hq=1 << 20, Hkv=1 << 20, Sq=1 << 11, Sk=4, D=1)):
+        d = desc(**kw)
+        assert fwd(dyt, d, n=1 << 60, **at) == bad, kw
+        assert bwd(dyt, d, n=1 << 60, **at) == bad, kw
+        assert sizes.dyt_attn_forward_workspace_size(d) == 0
+        assert sizes.dyt_attn_backward_workspace_size(d) == 0
+    # many keys, and many heads' buckets: the backward alone
+    for kw in (dict(B=1, Hq=64, Hkv=64, Sq=16, Sk=1 << 28, D=1), dict(table, B=1, Hq=1 << 16, Hkv=1 << 16, Sq=4, Sk=4, D=1)):
+        d = desc(**kw)
+        assert bwd(dyt, d, n=1 << 60, **at) == bad, kw
+        assert sizes.dyt_attn_backward_workspace_size(d) == 0
+    # no query head, and more key heads than a problem may have
+    d = desc(B=4, Hq=0, Hkv=1 << 62, k=(0, 0, 0), v=(0, 0, 0), dk=(0, 0, 0), dv=(0, 0, 0))
+    assert fwd(dyt, d, **at) == bad and bwd(dyt, d, **at) == bad
+    assert sizes.dyt_attn_backward_workspace_size(desc(B=1, Hq=64, Hkv=64, Sq=1 << 20, Sk=1 << 20, D=128)) > 0
