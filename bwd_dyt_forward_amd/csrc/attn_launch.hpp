@@ -26,7 +26,7 @@ template <typename T> void attn_launch_sum(int dp, const SumArgs&, hipStream_t);
 
 // Calls f with the compile-time (DP, NW, SL, BIAS, VEC) of the pick. Tensors
 // that do not take 16-byte loads go element by element, in single waves.
-// PAIRS: the workgroups of four row groups also come with two slices.
+// PAIRS: the workgroups of four row groups come with two slices above dp = 64.
 template <int DP, int NW, int SL, int VEC, typename F>
 void with_bias(const AttnPick& p, F&& f) {
     if (p.bias) f(Int<DP>{}, Int<NW>{}, Int<SL>{}, Int<1>{}, Int<VEC>{});
@@ -37,10 +37,14 @@ template <int ES, bool PAIRS, int DP, typename F>
 void with_waves(const AttnPick& p, F&& f) {
     if (!p.vec) return with_bias<DP, 1, 1, 0>(p, f);
     if (p.nw == 4) {
-        if constexpr (PAIRS && ES == 2) {
+        if constexpr (PAIRS && dkv_vals_in_lds(ES, DP)) {
+            // (one slice only where a wide table's sums leave no LDS for two)
+            static_assert(attn_dkv_lds_bytes(ES, DP, 4, 2) <= kMaxLds);
             if (p.sl == 2) return with_bias<DP, 4, 2, 1>(p, f);
+            return f(Int<DP>{}, Int<4>{}, Int<1>{}, Int<1>{}, Int<1>{});
+        } else {
+            return with_bias<DP, 4, 1, 1>(p, f);
         }
-        return with_bias<DP, 4, 1, 1>(p, f);
     }
     if constexpr (attn_lds_bytes(ES, DP, 1, 4) <= kMaxLds) {
         if (p.sl == 4) return with_bias<DP, 1, 4, 1>(p, f);

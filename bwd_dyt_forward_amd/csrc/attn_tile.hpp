@@ -589,7 +589,7 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w, bool heavy
     w.kv = w.head / a.G;
     w.len = a.Sk;
     if (a.lens) w.len = min(max(a.lens[w.b], 0), a.Sk);
-    // positions beyond +-2^30 see and measure what those do (Sq, Sk <= 2^29)
+    // positions beyond +-2^30 see and measure what those do (Sq, Sk <= 2^28)
     w.start = a.Sk - a.Sq;
     if (a.starts) w.start = min(max(a.starts[w.b], -(1 << 30)), 1 << 30);
     return true;

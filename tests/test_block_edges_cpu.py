@@ -5,6 +5,7 @@ import glob
 import os
 import random
 import re
+import subprocess
 
 from test_block_cpu import AT, CSRC, bwd, codes, desc, dyt, fwd  # noqa: F401
 
@@ -113,3 +114,16 @@ def test_problems_that_one_launch_cannot_hold(dyt, codes):  # noqa: F811
     d = desc(B=4, Hq=0, Hkv=1 << 62, k=(0, 0, 0), v=(0, 0, 0), dk=(0, 0, 0), dv=(0, 0, 0))
     assert fwd(dyt, d, **at) == bad and bwd(dyt, d, **at) == bad
     assert sizes.dyt_attn_backward_workspace_size(desc(B=1, Hq=64, Hkv=64, Sq=1 << 20, Sk=1 << 20, D=128)) > 0
+
+
+def test_every_dkv_instance_of_four_row_groups_can_be_picked(dyt):  # noqa: F811
+    """Two slices above a padded head dimension of 64 in the 16-bit types, and
+    there one only with the bias, where a wide table's sums leave no room."""
+    names = subprocess.run(["nm", "-C", dyt.BLOCK_LIB_FILE], capture_output=True, text=True, check=True).stdout
+    found = {(t, int(dp), int(sl), b == "true") for t, dp, sl, b in re.findall(
+        r"attn_dkv_kernel<(?:dyt::)?(\w+), (\d+), 4, (\d), (true|false), true>\(", names)}
+    want = {("float", dp, 1, b) for dp in (32, 64, 96, 128) for b in (True, False)}
+    for t in ("bf16_t", "f16_t"):
+        want |= {(t, dp, 1, b) for dp in (32, 64) for b in (True, False)}
+        want |= {(t, dp, 2, b) for dp in (96, 128) for b in (True, False)} | {(t, dp, 1, True) for dp in (96, 128)}
+    assert found == want
