@@ -147,11 +147,29 @@ bool share(const Layout& x, int i, const Layout& y, int j, int64_t delta, int& t
     return false;
 }
 
-// Whether a tensor takes 16-byte accesses: aligned base, strides and rows,
-// and a tile's rows (64 positions of up to 32 heads) within a 31-bit offset.
+// Whether a tensor takes 16-byte accesses: aligned base, strides and rows.
 bool vec_ok(const void* p, const Strides& s, int64_t row_bytes) {
-    if ((uintptr_t)p % 16 || s.b % 16 || s.s % 16 || s.h % 16 || row_bytes % 16) return false;
-    return s.s < ((int64_t)1 << 24) && s.h < ((int64_t)1 << 25);
+    return (uintptr_t)p % 16 == 0 && s.b % 16 == 0 && s.s % 16 == 0 && s.h % 16 == 0 && row_bytes % 16 == 0;
+}
+
+// Whether the rows of a tile, up to 128 of `pack` heads to a position, lie
+// within the 31-bit offsets of the direct-to-LDS loads. Keys and values (pack
+// 1) go head by head: how far apart their heads are does not matter.
+bool tile_ok(const Strides& s, int pack, int64_t row_bytes) {
+    constexpr int64_t limit = (int64_t)1 << 31;
+    if (s.s >= limit || (pack > 1 && s.h >= limit)) return false;
+    return 127 / pack * s.s + (pack > 1 ? (pack - 1) * s.h : 0) + row_bytes < limit;
+}
+
+// The rows of a unit: all heads of a group (or a 32-row tile's worth, the
+// largest divisor), unless each needs its own column of the table.
+int pack_of(const dyt_attn_desc& d) {
+    int pack = 1;
+    const int64_t G = d.Hq / d.Hkv;
+    if (!d.table)
+        for (int n = 2; n <= 32 && n <= G; ++n)
+            if (G % n == 0) pack = n;
+    return pack;
 }
 
 struct Plan {
@@ -280,12 +298,7 @@ Plan make_plan(const dyt_attn_desc& d, const Borders& borders, bool backward, bo
     p.borders = borders;
     p.nothing_out = d.B == 0 || d.Sq == 0 || d.Hq == 0;
     p.nothing_keys = d.B == 0 || d.Sk == 0;
-    // the rows of a unit: all heads of a group (or a 32-row tile's worth, the
-    // largest divisor), unless each needs its own column of the table
-    p.pack = 1;
-    if (!d.table)
-        for (int n = 2; n <= 32 && n <= G; ++n)
-            if (G % n == 0) p.pack = n;
+    p.pack = pack_of(d);
     p.units = (int)(d.B * (d.Hq / p.pack));
     p.rows = d.Sq * p.pack;
     const int dp = attn_dp(d.D), es = (int)dtype_size(d.dtype);
@@ -403,7 +416,7 @@ int dyt_attn_forward(const dyt_attn_desc* desc, const void* q, const void* k, co
         return DYT_ERR_INVALID_ARG;
     const int64_t es = dtype_size(d.dtype), row = d.D * es;
     const Plan p = make_plan(d, borders, false, vec_ok(q, a.qs, row) && vec_ok(k, a.ks, row) && vec_ok(v, a.vs, row) &&
-                                                    vec_ok(o, a.os, row));
+                                                    vec_ok(o, a.os, row) && tile_ok(a.ks, 1, row) && tile_ok(a.vs, 1, row));
     if (p.nothing_out) return DYT_OK;
     if (!launches_fit(d, p, false)) return DYT_ERR_INVALID_ARG;
     if (!q || !o || !stats || (d.Sk > 0 && (!k || !v))) return DYT_ERR_INVALID_ARG;
@@ -441,9 +454,12 @@ int dyt_attn_backward(const dyt_attn_desc* desc, const void* q, const void* k, c
         !view(d, {d.Sk, d.Hkv, &d.dk}, true, a.dks, n.dk) || !view(d, {d.Sk, d.Hkv, &d.dv}, true, a.dvs, n.dv))
         return DYT_ERR_INVALID_ARG;
     const int64_t es = dtype_size(d.dtype), row = d.D * es, ts = d.table ? dtype_size(d.table_dtype) : 1;
+    const int pack = pack_of(d);
     const Plan p = make_plan(d, borders, true, vec_ok(q, a.qs, row) && vec_ok(k, a.ks, row) && vec_ok(v, a.vs, row) &&
                                     vec_ok(o, a.os, row) && vec_ok(dout, a.dos, row) && vec_ok(dq, a.dqs, row) &&
-                                    vec_ok(dk, a.dks, row) && vec_ok(dv, a.dvs, row));
+                                    vec_ok(dk, a.dks, row) && vec_ok(dv, a.dvs, row) &&
+                                    tile_ok(a.ks, 1, row) && tile_ok(a.vs, 1, row) && tile_ok(a.qs, pack, row) &&
+                                    tile_ok(a.dos, pack, row));
     if (!launches_fit(d, p, true)) return DYT_ERR_INVALID_ARG;
     if (p.nothing_out) n.q = n.o = n.dout = n.dq = 0;
     if (p.nothing_keys) n.k = n.v = n.dk = n.dv = 0;

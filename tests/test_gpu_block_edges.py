@@ -128,3 +128,28 @@ def test_layer_norm_of_a_row_of_2_to_the_27(dyt):  # noqa: F811
     bound = want.abs() * (2.0 ** -11 + 4 * 2.0 ** -24) + 2.0 ** -24
     assert ((dgamma.double() - want).abs() <= bound).all()
     assert torch.isfinite(dx).all() and torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("size", [(1, 200, 300, 4, 2, 64), (2, 1, 3000, 4, 2, 128), (1, 257, 130, 2, 2, 72),
+                                  (8, 160, 300, 16, 16, 64)], ids=str)
+def test_head_strides_of_long_caches(dyt, size):  # noqa: F811
+    """[B, H, S, D] tensors whose heads lie 2^25 bytes and more apart (131,072
+    positions of D = 128) take the same kernels as contiguous ones: equal bits."""
+    B, Sq, Sk, Hq, Hkv, D = size
+    t, do, kw = make(59, torch.bfloat16, *size, causal=True)
+    apart = (1 << 24) + 64
+
+    def far(x):
+        S, H = x.shape[1:3]
+        y = torch.zeros((B * H - 1) * apart + S * D, dtype=x.dtype, device="cuda").as_strided(x.shape, (H * apart, D, apart, 1))
+        return y.copy_(x)
+
+    o, stats = dyt.dyt_attn_forward(t["q"], t["k"], t["v"], **kw)
+    want = (o, stats, *dyt.dyt_attn_backward(t["q"], t["k"], t["v"], o, do, stats, **kw))
+    q, k, v = (far(t[n]) for n in "qkv")
+    o2 = far(torch.zeros_like(o))
+    o2, stats = dyt.dyt_attn_forward(q, k, v, o=o2, **kw)
+    outs = {n: far(torch.zeros_like(x)) for n, x in (("dq", q), ("dk", k), ("dv", v))}
+    got = (o2, stats, *dyt.dyt_attn_backward(q, k, v, o2, far(do), stats, **outs, **kw))
+    for name, a, b in zip(("o", "stats", "dq", "dk", "dv"), got, want):
+        assert torch.equal(a, b), name
