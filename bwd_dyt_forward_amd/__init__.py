@@ -37,31 +37,51 @@ from ._lib import (  # noqa: F401
     lib,
 )
 
-from ._block import (  # noqa: E402,F401
-    BLOCK_LIB_FILE,
-    block_lib,
-    dyt_attn_backward,
-    dyt_attn_bucket_borders,
-    dyt_attn_forward,
-    dyt_ln_backward,
-    dyt_ln_backward_residual,
-    dyt_ln_backward_workspace_size,
-    dyt_ln_forward,
-    dyt_ln_forward_residual,
-)
 from .module import DyT, DyTFunction, DyTResidual, DyTResidualFunction, dyt, dyt_residual  # noqa: E402,F401
-from .block import (  # noqa: E402,F401
-    Attention,
-    AttentionFunction,
-    KVCache,
-    LayerNorm,
-    LayerNormFunction,
-    LayerNormResidual,
-    LayerNormResidualFunction,
-    attention,
-    layer_norm,
-    layer_norm_residual,
-)
+
+_BLOCK_ALL = [
+    "BLOCK_LIB_FILE", "block_lib", "dyt_ln_forward", "dyt_ln_forward_residual", "dyt_ln_backward",
+    "dyt_ln_backward_residual", "dyt_ln_backward_workspace_size", "dyt_attn_forward", "dyt_attn_backward",
+    "dyt_attn_bucket_borders", "LayerNorm", "LayerNormFunction", "layer_norm", "LayerNormResidual",
+    "LayerNormResidualFunction", "layer_norm_residual", "Attention", "AttentionFunction", "attention", "KVCache",
+]
+
+# DyT needs its own library only: where the block operators' is missing or from
+# other sources, their names say so when they are used.
+try:
+    from ._block import (  # noqa: E402,F401
+        BLOCK_LIB_FILE,
+        block_lib,
+        dyt_attn_backward,
+        dyt_attn_bucket_borders,
+        dyt_attn_forward,
+        dyt_ln_backward,
+        dyt_ln_backward_residual,
+        dyt_ln_backward_workspace_size,
+        dyt_ln_forward,
+        dyt_ln_forward_residual,
+    )
+    from .block import (  # noqa: E402,F401
+        Attention,
+        AttentionFunction,
+        KVCache,
+        LayerNorm,
+        LayerNormFunction,
+        LayerNormResidual,
+        LayerNormResidualFunction,
+        attention,
+        layer_norm,
+        layer_norm_residual,
+    )
+except ImportError as _e:
+    _block_missing = str(_e)
+
+    def __getattr__(name):
+        if name in _BLOCK_ALL:
+            raise ImportError(_block_missing)
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+else:
+    _block_missing = None
 
 __all__ = [
     "DyT", "DyTFunction", "dyt", "DyTResidual", "DyTResidualFunction", "dyt_residual",
@@ -71,8 +91,5 @@ __all__ = [
     "dyt_backward_residual_partials",
     "dyt_status_string", "dyt_abi_version", "dyt_get_plan", "dyt_get_forward_plan",
     "dyt_get_forward_residual_plan", "dyt_xcd_hint", "dyt_set_xcd_flip_override",
-    "BLOCK_LIB_FILE", "block_lib", "dyt_ln_forward", "dyt_ln_forward_residual", "dyt_ln_backward",
-    "dyt_ln_backward_residual", "dyt_ln_backward_workspace_size", "dyt_attn_forward", "dyt_attn_backward",
-    "dyt_attn_bucket_borders", "LayerNorm", "LayerNormFunction", "layer_norm", "LayerNormResidual",
-    "LayerNormResidualFunction", "layer_norm_residual", "Attention", "AttentionFunction", "attention", "KVCache",
+    *([] if _block_missing else _BLOCK_ALL),
 ]

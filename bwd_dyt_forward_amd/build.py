@@ -108,18 +108,19 @@ OBJ_CACHE = os.path.join(PKG_DIR, "_build")
 
 def build(out: str = LIB_PATH, extra_flags: list[str] | None = None, verbose: bool = False,
           with_stream_ref: bool = True, cache: bool = False) -> str:
-    """Compile the library (and, by default, the block operators' library and
-    the reference streaming kernels next to the default library path);
-    returns the library's path. Always
-    recompiles every source, unless cache=True, which reuses the object of
-    a translation unit whose source, headers and flags are unchanged. Only
-    the host translation unit carries the build id."""
+    """Compile the library; at the default path also the block operators'
+    library and, by default, the reference streaming kernels next to it.
+    Returns the library's path. Always recompiles every source, unless
+    cache=True, which reuses the object of a translation unit whose source,
+    headers and flags are unchanged. Only the host translation unit carries
+    the build id."""
     extra = list(extra_flags or [])
     per_source = {SOURCES[0]: [f'-DDYT_BUILD_ID="{source_hash(extra)}"']}
     _compile(out, SOURCES, extra, verbose, per_source, OBJ_CACHE if cache else None)
-    if with_stream_ref and out == LIB_PATH:
-        _compile(STREAM_REF_PATH, [STREAM_REF_SOURCE], None, verbose)
+    if out == LIB_PATH:
         build_block(verbose=verbose, cache=cache)
+        if with_stream_ref:
+            _compile(STREAM_REF_PATH, [STREAM_REF_SOURCE], None, verbose)
     return out
 
 

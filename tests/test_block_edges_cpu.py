@@ -5,9 +5,13 @@ import glob
 import os
 import random
 import re
+import shutil
 import subprocess
+import sys
 
-from test_block_cpu import AT, CSRC, bwd, codes, desc, dyt, fwd  # noqa: F401
+import pytest
+
+from test_block_cpu import AT, CSRC, ROOT, bwd, codes, desc, dyt, fwd  # noqa: F401
 
 
 def test_every_asm_statement_that_writes_m0_names_it():
@@ -127,3 +131,52 @@ def test_every_dkv_instance_of_four_row_groups_can_be_picked(dyt):  # noqa: F811
         want |= {(t, dp, 1, b) for dp in (32, 64) for b in (True, False)}
         want |= {(t, dp, 2, b) for dp in (96, 128) for b in (True, False)} | {(t, dp, 1, True) for dp in (96, 128)}
     assert found == want
+
+
+@pytest.mark.parametrize("state", ["missing", "other sources"])
+def test_the_package_without_the_block_library(dyt, tmp_path, state):  # noqa: F811
+    """DyT needs its own library only; the block operators' names fail loudly."""
+    package = "bwd_dyt_forward_amd"
+    os.mkdir(tmp_path / package)
+    for name in os.listdir(os.path.join(ROOT, package)):
+        if name.endswith((".py", ".so", ".json")) and name != "libdyt_block.so" or name == "csrc":
+            os.symlink(os.path.join(ROOT, package, name), tmp_path / package / name)
+    # build.py finds the sources next to itself
+    os.remove(tmp_path / package / "build.py")
+    shutil.copy(os.path.join(ROOT, package, "build.py"), tmp_path / package / "build.py")
+    os.symlink(os.path.join(ROOT, "include"), tmp_path / "include")
+    if state == "other sources":
+        lib = open(dyt.BLOCK_LIB_FILE, "rb").read()
+        mark = lib.index(b"DYT_BUILD_ID=") + 13
+        open(tmp_path / package / "libdyt_block.so", "wb").write(lib[:mark] + b"0" * 16 + lib[mark + 16:])
+    word = "not found" if state == "missing" else "other sources"
+    code = f"""
+import sys
+sys.path.insert(0, {str(tmp_path)!r})
+import {package} as m
+from {package} import *
+assert m.__file__.startswith({str(tmp_path)!r}) and m.dyt_abi_version() and DyT(8).num_features == 8
+for name in ("Attention", "layer_norm", "block_lib"):
+    assert name not in globals()
+    try:
+        getattr(m, name)
+    except ImportError as e:
+        assert {word!r} in str(e), e
+    else:
+        raise SystemExit(name)
+assert not hasattr(m, "no_such_name")
+"""
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=tmp_path)
+    assert run.returncode == 0, run.stderr
+
+
+def test_a_build_at_the_default_path_brings_the_block_library(monkeypatch):
+    from bwd_dyt_forward_amd import build
+    for stream_ref in (True, False):
+        made = []
+        monkeypatch.setattr(build, "_compile", lambda out, *a, **kw: made.append(out))
+        build.build(with_stream_ref=stream_ref)
+        assert build.BLOCK_LIB_PATH in made and (build.STREAM_REF_PATH in made) == stream_ref
+        made.clear()
+        build.build(out="/elsewhere.so", with_stream_ref=stream_ref)
+        assert made == ["/elsewhere.so"]
