@@ -113,6 +113,9 @@ def _unit_last(t: torch.Tensor) -> torch.Tensor:
     return t if t.shape[-1] <= 1 or t.stride(-1) == 1 else t.contiguous()
 
 
+_LISTS = ("seqlens_k", "q_start")
+
+
 class AttentionFunction(torch.autograd.Function):
     """Saves q, k, v, the output and the rows' log sums; the probabilities are
     recomputed in the backward."""
@@ -121,23 +124,24 @@ class AttentionFunction(torch.autograd.Function):
     def forward(ctx, q, k, v, table, options: dict):
         q, k, v = _unit_last(q), _unit_last(k), _unit_last(v)
         o, stats = _block.dyt_attn_forward(q, k, v, table=table, **options)
-        ctx.save_for_backward(q, k, v, o, stats, table)
-        ctx.options = options
+        # the lists are saved like the others: a change before the backward is an error
+        ctx.save_for_backward(q, k, v, o, stats, table, *(options.get(n) for n in _LISTS))
+        ctx.options = {n: x for n, x in options.items() if n not in _LISTS}
         return o
 
     @staticmethod
     @once_differentiable
     def backward(ctx, do: torch.Tensor):
-        q, k, v, o, stats, table = ctx.saved_tensors
-        grads = _block.dyt_attn_backward(q, k, v, o, _unit_last(do.to(q.dtype)), stats, table=table, **ctx.options)
+        q, k, v, o, stats, table, *lists = ctx.saved_tensors
+        grads = _block.dyt_attn_backward(q, k, v, o, _unit_last(do.to(q.dtype)), stats, table=table,
+                                         **dict(zip(_LISTS, lists)), **ctx.options)
         return (*grads, None) if table is not None else (*grads, None, None)
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool = False, scale: float | None = None,
               seqlens_k: torch.Tensor | None = None, q_start: torch.Tensor | None = None,
               table: torch.Tensor | None = None, max_distance: int = 128, bidirectional: bool = True) -> torch.Tensor:
-    """dyt_attn_forward with autograd support (q, k, v and table); returns o.
-    seqlens_k and q_start must keep their values until the backward."""
+    """dyt_attn_forward with autograd support (q, k, v and table); returns o."""
     options = dict(causal=causal, scale=scale, seqlens_k=seqlens_k, q_start=q_start, max_distance=max_distance,
                    bidirectional=bidirectional)
     return AttentionFunction.apply(q, k, v, table, options)

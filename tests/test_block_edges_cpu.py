@@ -10,6 +10,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 from test_block_cpu import AT, CSRC, ROOT, bwd, codes, desc, dyt, fwd  # noqa: F401
 
@@ -180,3 +181,29 @@ def test_a_build_at_the_default_path_brings_the_block_library(monkeypatch):
         made.clear()
         build.build(out="/elsewhere.so", with_stream_ref=stream_ref)
         assert made == ["/elsewhere.so"]
+
+
+@pytest.mark.parametrize("name", ["seqlens_k", "q_start"])
+def test_lists_that_change_before_the_backward_are_an_error(dyt, monkeypatch, name):  # noqa: F811
+    """The kernels replaced by plain operations on CPU tensors."""
+    from bwd_dyt_forward_amd import _block, block
+    seen = []
+
+    def backward(q, k, v, o, do, stats, *, table, seqlens_k, q_start, **kw):
+        seen.append((seqlens_k, q_start))
+        return (do, k, v) if table is None else (do, k, v, table)
+
+    monkeypatch.setattr(_block, "dyt_attn_forward", lambda q, k, v, **kw: (q * 2, q[..., 0]))
+    monkeypatch.setattr(_block, "dyt_attn_backward", backward)
+    q, k, v = (torch.randn(2, 3, 2, 4, requires_grad=True) for _ in range(3))
+    table = torch.randn(8, 2, requires_grad=True)
+    for t in (None, table):
+        lists = {name: torch.tensor([1, 2], dtype=torch.int32)}
+        block.attention(q, k, v, table=t, **lists).sum().backward()
+        got = dict(zip(("seqlens_k", "q_start"), seen[-1]))
+        assert got.pop(name).tolist() == [1, 2] and list(got.values()) == [None]
+        o = block.attention(q, k, v, table=t, **lists)
+        lists[name] += 1
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            o.sum().backward()
+    assert len(seen) == 2 and table.grad is not None
