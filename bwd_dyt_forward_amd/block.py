@@ -164,12 +164,12 @@ class KVCache:
         if k.shape[1] > self.k.shape[1] - self._used:
             raise ValueError(f"the cache holds {self.k.shape[1]} positions, {self._used} are taken: no room for "
                              f"{k.shape[1]} more")
-        self._used += k.shape[1]
         start = self.length.clone()
         at = start.long().view(-1, 1) + torch.arange(k.shape[1], device=k.device)
         self.k[self._rows, at] = k
         self.v[self._rows, at] = v
         self.length += k.shape[1]
+        self._used += k.shape[1]   # last: what fails above takes no room
         return start
 
 
@@ -201,6 +201,8 @@ class Attention(nn.Module):
         if cache is not None:
             if seqlens is not None:
                 raise ValueError("a cache keeps its own lengths: seqlens must be None")
+            if B != cache.k.shape[0]:
+                raise ValueError(f"the cache holds {cache.k.shape[0]} sequences, x has {B}")
             start = cache.append(k, v)
             k, v, seqlens = cache.k, cache.v, cache.length.clone()
         o = attention(q, k, v, causal=self.causal, seqlens_k=seqlens, q_start=start, table=self.table,

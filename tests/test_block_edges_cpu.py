@@ -207,3 +207,23 @@ def test_lists_that_change_before_the_backward_are_an_error(dyt, monkeypatch, na
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             o.sum().backward()
     assert len(seen) == 2 and table.grad is not None
+
+
+def test_an_append_that_fails_takes_no_room(dyt):  # noqa: F811
+    c = dyt.KVCache(2, 5, 1, 4, torch.float32, "cpu")
+    x = torch.ones(2, 3, 1, 4)
+    for k, v in ((x.double(), x), (x, x.double()), (x[..., :3], x), (x, x[:, :2]), (torch.ones(3, 3, 1, 4), x)):
+        with pytest.raises((RuntimeError, IndexError)):
+            c.append(k, v)
+        assert c.length.tolist() == [0, 0]
+    assert c.append(x, x).tolist() == [0, 0] and c.append(x[:, :2], x[:, :2]).tolist() == [3, 3]
+    with pytest.raises(ValueError, match="no room"):
+        c.append(x[:, :1], x[:, :1])
+
+
+def test_a_batch_that_is_not_the_caches_changes_nothing(dyt):  # noqa: F811
+    m = dyt.Attention(8, 2, 2, device="cpu")
+    c = dyt.KVCache(3, 5, 2, 4, torch.float32, "cpu")
+    with pytest.raises(ValueError, match="sequences"):
+        m(torch.ones(1, 2, 8), cache=c)
+    assert c.length.tolist() == [0, 0, 0] and (c.k == 0).all()
