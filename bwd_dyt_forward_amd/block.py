@@ -149,27 +149,38 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool
 
 class KVCache:
     """Keys and values of a batch of growing sequences: k, v [B, max_len,
-    heads, head_dim] and the sequences' lengths (int32, on the device)."""
+    heads, head_dim] and the sequences' lengths (int32, on the device).
+
+    An append may be captured into a graph. Its replays move the device's
+    lengths only, which stop at max_len: what finds no room is dropped there (a
+    position behind the last takes it) and refused by the next eager append."""
 
     def __init__(self, batch: int, max_len: int, num_kv_heads: int, head_dim: int, dtype=torch.bfloat16, device="cuda"):
-        self.k = torch.zeros(batch, max_len, num_kv_heads, head_dim, dtype=dtype, device=device)
-        self.v = torch.zeros_like(self.k)
+        self._k = torch.zeros(batch, max_len + 1, num_kv_heads, head_dim, dtype=dtype, device=device)
+        self._v = torch.zeros_like(self._k)
+        self.k, self.v = self._k[:, :max_len], self._v[:, :max_len]
         self.length = torch.zeros(batch, dtype=torch.int32, device=device)
         self._rows = torch.arange(batch, device=device).view(-1, 1)
-        self._used = 0   # the longest length, known on the host
+        self._steps = torch.arange(max_len, device=device)
+        self._used = 0            # the longest length, known on the host
+        self._captured = False    # replays may have moved the lengths since
 
     def append(self, k: torch.Tensor, v: torch.Tensor) -> torch.Tensor:
         """Adds [B, S, heads, head_dim] behind each sequence; returns the
         lengths before."""
-        if k.shape[1] > self.k.shape[1] - self._used:
-            raise ValueError(f"the cache holds {self.k.shape[1]} positions, {self._used} are taken: no room for "
-                             f"{k.shape[1]} more")
+        S, max_len = k.shape[1], self.k.shape[1]
+        if self.k.is_cuda and torch.cuda.is_current_stream_capturing():
+            self._captured = True
+        elif self._captured and self.length.numel():
+            self._used = int(self.length.max())
+        if S > max_len - self._used:
+            raise ValueError(f"the cache holds {max_len} positions, {self._used} are taken: no room for {S} more")
         start = self.length.clone()
-        at = start.long().view(-1, 1) + torch.arange(k.shape[1], device=k.device)
-        self.k[self._rows, at] = k
-        self.v[self._rows, at] = v
-        self.length += k.shape[1]
-        self._used += k.shape[1]   # last: what fails above takes no room
+        at = (start.view(-1, 1) + self._steps[:S]).clamp_(max=max_len)
+        self._k[self._rows, at] = k
+        self._v[self._rows, at] = v
+        self.length.add_(S).clamp_(max=max_len)
+        self._used += S   # last: what fails above takes no room
         return start
 
 

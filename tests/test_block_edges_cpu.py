@@ -227,3 +227,20 @@ def test_a_batch_that_is_not_the_caches_changes_nothing(dyt):  # noqa: F811
     with pytest.raises(ValueError, match="sequences"):
         m(torch.ones(1, 2, 8), cache=c)
     assert c.length.tolist() == [0, 0, 0] and (c.k == 0).all()
+
+
+def test_appends_behind_the_end_write_nothing_out_of_range(dyt):  # noqa: F811
+    """What a captured append's replays do once the cache is full: the host's
+    check does not run again."""
+    c = dyt.KVCache(3, 4, 1, 2, torch.float32, "cpu")
+    c.length.copy_(torch.tensor([1, 3, 4]))
+    x = torch.arange(1.0, 13).view(3, 2, 1, 2)
+    starts = [c.append(x, -x).tolist()]
+    for _ in range(2):
+        c._used = 0
+        starts.append(c.append(x + 100, x + 100).tolist())
+    assert starts == [[1, 3, 4], [3, 4, 4], [4, 4, 4]] and c.length.tolist() == [4, 4, 4]
+    assert c.k.shape == (3, 4, 1, 2)
+    want = torch.zeros(3, 4, 1, 2)
+    want[0, 1:3], want[0, 3], want[1, 3] = x[0], x[0, 0] + 100, x[1, 0]
+    assert torch.equal(c.k, want)

@@ -153,3 +153,44 @@ def test_head_strides_of_long_caches(dyt, size):  # noqa: F811
     got = (o2, stats, *dyt.dyt_attn_backward(q, k, v, o2, far(do), stats, **outs, **kw))
     for name, a, b in zip(("o", "stats", "dq", "dk", "dv"), got, want):
         assert torch.equal(a, b), name
+
+
+def test_a_captured_append_replayed_past_the_end(dyt):  # noqa: F811
+    """A decoding step as a graph: each replay is the next token, checked
+    against the whole sequence; past the end it changes nothing, and an eager
+    append sees that the cache is full."""
+    torch.manual_seed(61)
+    B, prompt, room = 2, 5, 11
+    m = dyt.Attention(64, 4, 2, num_buckets=16, max_distance=40, device="cuda")
+    torch.nn.init.normal_(m.table)
+    x = torch.randn(B, room, 64, device="cuda")
+    token = x[:, prompt:prompt + 1].clone()
+    with torch.no_grad():
+        want = m(x)
+        warm = dyt.KVCache(B, room, 2, 16, torch.float32)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(2):
+                m(token, cache=warm)
+        torch.cuda.current_stream().wait_stream(side)
+        cache = dyt.KVCache(B, room, 2, 16, torch.float32)
+        m(x[:, :prompt], cache=cache)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = m(token, cache=cache)
+        for i in range(prompt, room):
+            token.copy_(x[:, i:i + 1])
+            graph.replay()
+            torch.cuda.synchronize()
+            # the same 64 and room terms of order one in other orders
+            assert (out - want[:, i:i + 1]).abs().max() <= 200 * 2.0 ** -24 * 4, i
+            assert cache.length.tolist() == [i + 1] * B
+            m(token, cache=dyt.KVCache(B, 1, 2, 16, torch.float32))   # eager work in between
+        k, v = cache.k.clone(), cache.v.clone()
+        for _ in range(3):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(cache.k, k) and torch.equal(cache.v, v) and cache.length.tolist() == [room] * B
+        with pytest.raises(ValueError, match="no room"):
+            m(token, cache=cache)
