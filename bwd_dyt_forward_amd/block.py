@@ -151,6 +151,9 @@ class KVCache:
     """Keys and values of a batch of growing sequences: k, v [B, max_len,
     heads, head_dim] and the sequences' lengths (int32, on the device).
 
+    A cache holds values: gradients reach the keys and values of the call that
+    adds them, not those of the calls before.
+
     An append may be captured into a graph. Its replays move the device's
     lengths only, which stop at max_len: what finds no room is dropped there (a
     position behind the last takes it) and refused by the next eager append."""
@@ -176,12 +179,24 @@ class KVCache:
         if S > max_len - self._used:
             raise ValueError(f"the cache holds {max_len} positions, {self._used} are taken: no room for {S} more")
         start = self.length.clone()
-        at = (start.view(-1, 1) + self._steps[:S]).clamp_(max=max_len)
-        self._k[self._rows, at] = k
-        self._v[self._rows, at] = v
+        at = self._places(start, S)
+        with torch.no_grad():
+            self._k[self._rows, at] = k
+            self._v[self._rows, at] = v
         self.length.add_(S).clamp_(max=max_len)
         self._used += S   # last: what fails above takes no room
         return start
+
+    def _places(self, start: torch.Tensor, count: int) -> torch.Tensor:
+        return (start.view(-1, 1) + self._steps[:count]).clamp_(max=self.k.shape[1])
+
+    def with_gradient(self, k: torch.Tensor, v: torch.Tensor, start: torch.Tensor):
+        """The cache's keys and values, those of an append of k and v at
+        `start` as part of their graph (a copy where one is needed)."""
+        if not torch.is_grad_enabled() or not (k.requires_grad or v.requires_grad):
+            return self.k, self.v
+        at = (self._rows, self._places(start, k.shape[1]))
+        return tuple(all_.index_put(at, new)[:, :-1] for all_, new in ((self._k, k), (self._v, v)))
 
 
 class Attention(nn.Module):
@@ -215,7 +230,8 @@ class Attention(nn.Module):
             if B != cache.k.shape[0]:
                 raise ValueError(f"the cache holds {cache.k.shape[0]} sequences, x has {B}")
             start = cache.append(k, v)
-            k, v, seqlens = cache.k, cache.v, cache.length.clone()
+            k, v = cache.with_gradient(k, v, start)
+            seqlens = cache.length.clone()
         o = attention(q, k, v, causal=self.causal, seqlens_k=seqlens, q_start=start, table=self.table,
                       max_distance=self.max_distance, bidirectional=not self.causal)
         return self.out(o.reshape(B, S, H * self.head_dim))

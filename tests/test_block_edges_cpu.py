@@ -244,3 +244,20 @@ def test_appends_behind_the_end_write_nothing_out_of_range(dyt):  # noqa: F811
     want = torch.zeros(3, 4, 1, 2)
     want[0, 1:3], want[0, 3], want[1, 3] = x[0], x[0, 0] + 100, x[1, 0]
     assert torch.equal(c.k, want)
+
+
+def test_a_cache_holds_values_and_no_graph(dyt):  # noqa: F811
+    c = dyt.KVCache(2, 6, 1, 4, torch.float32, "cpu")
+    k, v = (torch.randn(2, 2, 1, 4, requires_grad=True) for _ in range(2))
+    for n in (0, 2):
+        start = c.append(k, v)
+        assert not c.k.requires_grad and not c.v.requires_grad and not c.length.requires_grad
+        all_k, all_v = c.with_gradient(k, v, start)
+        assert torch.equal(all_k, c.k) and torch.equal(all_v, c.v) and all_k.shape == c.k.shape
+        k.grad = v.grad = None
+        (all_k * 2 + all_v * 3).sum().backward()
+        assert (k.grad == 2).all() and (v.grad == 3).all()
+    with torch.no_grad():
+        start = c.append(k, v)
+        assert all(a is b for a, b in zip(c.with_gradient(k, v, start), (c.k, c.v)))
+    assert c.with_gradient(k.detach(), v.detach(), start)[0] is c.k

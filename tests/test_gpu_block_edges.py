@@ -194,3 +194,45 @@ def test_a_captured_append_replayed_past_the_end(dyt):  # noqa: F811
             assert torch.equal(cache.k, k) and torch.equal(cache.v, v) and cache.length.tolist() == [room] * B
         with pytest.raises(ValueError, match="no room"):
             m(token, cache=cache)
+
+
+def test_gradients_through_a_cache(dyt):  # noqa: F811
+    """A prompt's gradients are those without a cache; the next token's call
+    takes the prompt's keys and values as they are, and holds no graph of it."""
+    torch.manual_seed(67)
+    m = dyt.Attention(64, 4, 2, num_buckets=16, max_distance=40, device="cuda")
+    torch.nn.init.normal_(m.table)
+    x = torch.randn(2, 40, 64, device="cuda")
+    w = torch.randn(2, 40, 64, device="cuda")
+
+    def gradients(out, w):
+        m.zero_grad()
+        (out * w).sum().backward()
+        return [p.grad.clone() for p in m.parameters()]
+
+    want = gradients(m(x), w)
+    cache = dyt.KVCache(2, 42, 2, 16, torch.float32)
+    got = gradients(m(x, cache=cache), w)
+    for a, b in zip(got, want):
+        # sums of 80 rows' and 64 columns' float32 terms, a few operators deep
+        assert (a - b).norm() <= 500 * 2.0 ** -24 * b.norm()
+    for _ in range(2):
+        before = cache.k.clone(), cache.v.clone()
+        assert not cache.k.requires_grad and not cache.v.requires_grad
+        token = torch.randn(2, 1, 64, device="cuda")
+        out = m(token, cache=cache)
+        got = gradients(out, w[:, :1])
+        # the same in float64: the keys before are constants
+        n = int(cache.length[0])
+        p = [t.detach().double().requires_grad_() for t in (m.table, m.qkv.weight, m.out.weight)]
+        q, k, v = (token.double() @ p[1].t()).view(2, 1, 8, 16).split([4, 2, 2], 2)
+        k, v = (torch.cat([b[:, :n - 1].double(), t], 1).repeat_interleave(2, 2) for b, t in zip(before, (k, v)))
+        far = torch.arange(n - 1, -1, -1, device="cuda")
+        bucket = torch.searchsorted(torch.tensor(dyt.dyt_attn_bucket_borders(16, 40, False), device="cuda"), far, right=True) - 1
+        s = (q * k).sum(-1) / 4 + p[0][bucket]
+        o = (torch.softmax(s, 1).unsqueeze(-1) * v).sum(1, keepdim=True).reshape(2, 1, 64) @ p[2].t()
+        (o * w[:, :1].double()).sum().backward()
+        names = [x for x, _ in m.named_parameters()]
+        for a, b in ((got[names.index("table")], p[0].grad), (got[names.index("qkv.weight")], p[1].grad),
+                     (got[names.index("out.weight")], p[2].grad)):
+            assert (a - b).norm() <= 500 * 2.0 ** -24 * b.norm()
