@@ -3,12 +3,13 @@ rows of the last tile under a large bias, keys that the causal mask hides
 from every row, and rows that see no key, against the formulas in float64
 (tests/block_ref.py) and against the same problem with whole tiles."""
 import math
+import random
 
 import pytest
 import torch
 
 from block_ref import Attention
-from test_gpu_block_attn import DTYPES, dyt, make, run_and_check  # noqa: F401
+from test_gpu_block_attn import DTYPES, LARGE, dyt, make, run_and_check  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -236,3 +237,62 @@ def test_gradients_through_a_cache(dyt):  # noqa: F811
         for a, b in ((got[names.index("table")], p[0].grad), (got[names.index("qkv.weight")], p[1].grad),
                      (got[names.index("out.weight")], p[2].grad)):
             assert (a - b).norm() <= 500 * 2.0 ** -24 * b.norm()
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("case", LARGE, ids=str)
+@pytest.mark.parametrize("dt", DTYPES)
+def test_batch_entries_of_the_large_sizes(dyt, dt, case, causal):  # noqa: F811
+    """The first and a middle batch entry of the sizes with four waves to a
+    workgroup (the last is test_large's): their outputs from the one forward,
+    their gradients with the others' upstream gradient zero."""
+    size, more = case
+    B = size["B"]
+    t, do, kw = make(71, DTYPES[dt], **size, causal=causal, lens=[size["Sk"] - 3 * b for b in range(B)], **more)
+    o, stats = dyt.dyt_attn_forward(t["q"], t["k"], t["v"], **kw)
+    for b in (0, B // 2):
+        only = torch.zeros_like(do)
+        only[b] = do[b]
+        grads = dyt.dyt_attn_backward(t["q"], t["k"], t["v"], o, only, stats, **kw)
+        one = slice(b, b + 1)
+        ref = Attention(*(t[n][one] for n in "qkv"), **dict(kw, seqlens_k=kw["seqlens_k"][one]))
+        ref.check_forward(o[one], stats[one])
+        ref.check_backward(do[one], *(g[one] for g in grads[:3]), *grads[3:])
+        others = [i for i in range(B) if i != b]
+        assert all((g[others] == 0).all() for g in grads[:3])
+
+
+def test_random_problems_whose_unseen_places_are_nan(dyt):  # noqa: F811
+    """Forty problems with lengths, positions and the causal mask drawn, and
+    everything that no pair reaches filled with NaN: keys that no row sees,
+    rows at negative positions, and all of a batch entry without keys."""
+    rng = random.Random(73)
+    for i in range(40):
+        D = rng.randint(1, 128)
+        Hkv = rng.choice([1, 1, 2, 3])
+        Hq = Hkv * rng.choice([1, 2, 3, 4, 6])
+        Sq, Sk = (int(math.exp(rng.uniform(0, math.log(600)))) for _ in range(2))
+        B = rng.randint(1, 4)
+        causal = rng.random() < 0.7
+        lens = [rng.randint(0, Sk + 5) for _ in range(B)]
+        starts = [rng.randint(-Sq, max(0, Sk - Sq // 2)) for _ in range(B)]
+        more = {}
+        if rng.random() < 0.5:
+            bidi = rng.random() < 0.5
+            buckets = rng.choice([4, 10, 32, 64])
+            more = dict(buckets=buckets, bidirectional=bidi, distance=rng.randint(buckets // 2 + 1, 300))
+        dt = rng.choice(list(DTYPES))
+        print(i, dt, (B, Sq, Sk, Hq, Hkv, D), causal, lens, starts, more, flush=True)
+        t, do, kw = make(i, DTYPES[dt], B, Sq, Sk, Hq, Hkv, D, causal=causal, lens=lens, starts=starts, **more)
+        q, clean_do = t["q"].clone(), do.clone()
+        for b in range(B):
+            end = max(0, min(lens[b], Sk, starts[b] + Sq if causal else Sk))
+            t["k"][b, end:] = t["v"][b, end:] = math.nan
+            blind = Sq if end == 0 else max(0, -starts[b]) if causal else 0
+            q[b, :blind] = clean_do[b, :blind] = 0
+            t["q"][b, :blind] = do[b, :blind] = math.nan
+        o, stats = dyt.dyt_attn_forward(t["q"], t["k"], t["v"], **kw)
+        grads = dyt.dyt_attn_backward(t["q"], t["k"], t["v"], o, do, stats, **kw)
+        ref = Attention(q, t["k"], t["v"], **kw)
+        ref.check_forward(o, stats)
+        ref.check_backward(clean_do, *grads)
