@@ -48,7 +48,11 @@
  * floating-point atomics: results are bitwise reproducible and depend on the
  * arguments only). In the 16-bit types the probabilities and their gradients
  * are rounded to that type for the second matrix products, as the operands of
- * the matrix cores are; the sums are float32.
+ * the matrix cores are (in float16 |p (do . v - do . o)| stays below 65,504 and
+ * loses digits under 2^-14); the sums are float32. The backward takes p from the
+ * float32 stats: its relative error grows with |stats| 2^-23, and a row whose
+ * visible scores all lie beyond +-10^7 (a table's entries of -10^9 and no other
+ * key in sight) has p of that row's largest score's keys only, not normalised.
  */
 #ifndef DYT_BLOCK_H_
 #define DYT_BLOCK_H_
@@ -116,7 +120,7 @@ typedef struct dyt_attn_strides {
  *              may be negative
  *   table      [num_buckets, Hq] of table_dtype, contiguous, or NULL: no bias
  *   causal, bidirectional: 0 or 1
- *   scale      finite
+ *   scale      positive and finite
  * Sk and Sq Hq / Hkv are at most 2^28, Hq and Hkv 2^20, B Hq and B Hkv 2^24, and
  * no launch may need 2^32 threads (two a row and head, backward two a key and head).
  * num_buckets is even when bidirectional, and >= 2 (>= 4 when

@@ -296,3 +296,37 @@ def test_random_problems_whose_unseen_places_are_nan(dyt):  # noqa: F811
         ref = Attention(q, t["k"], t["v"], **kw)
         ref.check_forward(o, stats)
         ref.check_backward(clean_do, *grads)
+
+
+@pytest.mark.parametrize("size", [(3, 160, 160, 2, 2, 64), (3, 90, 200, 4, 2, 40)], ids=str)
+@pytest.mark.parametrize("hide", [-1e4, -1e8, -1e9, -3e38, -math.inf])
+@pytest.mark.parametrize("dt", DTYPES)
+def test_rows_that_see_hidden_buckets_only(dyt, dt, hide, size):  # noqa: F811
+    """A window made by hiding the farthest buckets, over a padded batch: rows
+    of the padding see only hidden keys. Their log sums are too large for a
+    float32 probability to mean anything; with an upstream gradient of zero
+    they must add nothing all the same."""
+    B, S, Sk = size[:3]
+    lens = [[Sk, 40, 7][b % 3] for b in range(B)]
+    t, do, kw = make(79, DTYPES[dt], *size, buckets=16, distance=30, lens=lens, starts=[0] * B, table_dt=torch.float32)
+    for b, n in enumerate(lens):
+        do[b, n:] = 0
+    kw["table"][7] = kw["table"][15] = hide
+    o, stats = dyt.dyt_attn_forward(t["q"], t["k"], t["v"], **kw)
+    grads = dyt.dyt_attn_backward(t["q"], t["k"], t["v"], o, do, stats, **kw)
+    kw["table"] = kw["table"].clamp(min=-1e4)   # exp(-1e4) = 0 as well
+    ref = Attention(t["q"], t["k"], t["v"], **kw)
+    # the rows before the padding, which see an ordinary key each: what their
+    # hidden pairs' size adds to rho is no error of theirs
+    ref.rho = ref.rho.clamp(max=1e-4)
+    for b, n in enumerate(lens):
+        n = min(n, S)
+        err = (o[b, :n].double().cpu().transpose(0, 1) - ref.o[b, :, :n]).abs()
+        half = {"f32": 0, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[dt]
+        pv = ref.p[b, :, :n] @ ref.v[b].abs()
+        assert (err <= 1.05 * (2 * half + 1e-4) * pv + 2.0 ** -24).all()
+        ref.p[b, :, n:] = 0
+        ref.o[b, :, n:] = 0
+    for x in grads:
+        assert torch.isfinite(x).all()
+    ref.check_backward(do, *grads)
