@@ -18,26 +18,27 @@ namespace dytb {
 // workgroup, kFinSlices slices of rows side by side, each summed in row
 // order, then the slices in slice order. The loads of a slice do not depend
 // on each other; 16 slices of up to 64 rows each took 4-6 us at every width.
-// A grid may have 2^32 threads; from 2^15 workgroups on (over a million columns)
-// they walk.
+// A grid may have 2^32 threads: from 2^15 workgroups on (over a million columns)
+// they walk (WALK).
 constexpr int kFinSlices = 16;
 constexpr int64_t kFinGrid = 1 << 15;
 
+template <bool WALK>
 __global__ __launch_bounds__(64 * kFinSlices) void ln_finish_kernel(const float* part, int64_t pitch,
                                                                     int rows, int64_t N, void* dgamma,
                                                                     void* dbeta, int pdt) {
     __shared__ float red[kFinSlices][64];
     const int lane = (int)threadIdx.x & 63, slice = (int)threadIdx.x >> 6;
-    const int per = (rows + kFinSlices - 1) / kFinSlices;
-    const int lo = slice * per, hi = min(lo + per, rows);
     for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < 2 * N; c0 += (int64_t)gridDim.x * 64) {
         const int64_t c = c0 + lane;
         float s = 0.0f;
         if (c < 2 * N) {
+            const int per = (rows + kFinSlices - 1) / kFinSlices;
+            const int lo = slice * per, hi = min(lo + per, rows);
 #pragma unroll 8
             for (int r = lo; r < hi; ++r) s += part[r * pitch + c];
         }
-        __syncthreads();   // the previous columns' sums have been read
+        if constexpr (WALK) __syncthreads();   // the columns before have been read
         red[slice][lane] = s;
         __syncthreads();
         if (slice == 0 && c < 2 * N) {
@@ -47,7 +48,14 @@ __global__ __launch_bounds__(64 * kFinSlices) void ln_finish_kernel(const float*
             if (c < N) store_param(dgamma, c, pdt, s);
             else store_param(dbeta, c - N, pdt, s);
         }
+        if constexpr (!WALK) return;
     }
+}
+
+void ln_finish(const float* part, int64_t pitch, int rows, int64_t N, void* dgamma, void* dbeta, int pdt, hipStream_t s) {
+    const int64_t need = (2 * N + 63) / 64;
+    if (need <= kFinGrid) ln_finish_kernel<false><<<(unsigned)need, 64 * kFinSlices, 0, s>>>(part, pitch, rows, N, dgamma, dbeta, pdt);
+    else ln_finish_kernel<true><<<(unsigned)kFinGrid, 64 * kFinSlices, 0, s>>>(part, pitch, rows, N, dgamma, dbeta, pdt);
 }
 
 // Workgroups of the backward, each with a partial row of 2 N floats to write
@@ -133,10 +141,9 @@ int ln_backward(const void* x, int64_t ldx, const void* dy, int64_t lddy, const 
     if (!dgamma || !dbeta) return DYT_ERR_INVALID_ARG;
     const int64_t sx = dtype_size(xdt), sp = dtype_size(pdt);
     const hipStream_t s = (hipStream_t)stream;
-    const int fin_grid = (int)std::min((2 * N + 63) / 64, kFinGrid);
     if (M == 0) {
         if (!aligned({dgamma, dbeta}, sp)) return DYT_ERR_MISALIGNED;
-        ln_finish_kernel<<<fin_grid, 64 * kFinSlices, 0, s>>>(nullptr, 0, 0, N, dgamma, dbeta, pdt);
+        ln_finish(nullptr, 0, 0, N, dgamma, dbeta, pdt, s);
         return hip_status();
     }
     if (!x || !dy || !mean || !rstd || !gamma || !dx || (res && !dres)) return DYT_ERR_INVALID_ARG;
@@ -157,7 +164,7 @@ int ln_backward(const void* x, int64_t ldx, const void* dy, int64_t lddy, const 
     with_type(xdt, [&](auto* t) {
         ln_launch_backward<std::remove_pointer_t<decltype(t)>>(p.cfg, p.grid, a, s);
     });
-    ln_finish_kernel<<<fin_grid, 64 * kFinSlices, 0, s>>>(a.part, a.pitch, p.grid, N, dgamma, dbeta, pdt);
+    ln_finish(a.part, a.pitch, p.grid, N, dgamma, dbeta, pdt, s);
     return hip_status();
 }
 
