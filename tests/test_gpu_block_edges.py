@@ -330,3 +330,27 @@ def test_rows_that_see_hidden_buckets_only(dyt, dt, hide, size):  # noqa: F811
     for x in grads:
         assert torch.isfinite(x).all()
     ref.check_backward(do, *grads)
+
+
+def test_prompts_of_unequal_lengths_in_a_cache(dyt):  # noqa: F811
+    """Appended padded, then the lengths set: the next tokens see each
+    sequence as if it stood alone, whatever the padding held."""
+    torch.manual_seed(83)
+    m = dyt.Attention(64, 4, 2, num_buckets=16, max_distance=40, device="cuda")
+    torch.nn.init.normal_(m.table)
+    lens = [9, 3, 6]
+    x = torch.randn(3, 13, 64, device="cuda")
+    padded = torch.full((3, 9, 64), 1e3, device="cuda")
+    for b, n in enumerate(lens):
+        padded[b, :n] = x[b, :n]
+    with torch.no_grad():
+        cache = dyt.KVCache(3, 13, 2, 16, torch.float32)
+        m(padded, cache=cache)
+        cache.length.copy_(torch.tensor(lens))
+        for i in range(4):
+            got = m(torch.stack([x[b, n + i:n + i + 1] for b, n in enumerate(lens)]), cache=cache)
+            for b, n in enumerate(lens):
+                want = m(x[b:b + 1, :n + i + 1])[:, -1]
+                # both sides sum the same 64 and 13 terms of order one in other orders
+                assert (got[b] - want).abs().max() <= 200 * 2.0 ** -24 * 4, (b, i)
+    assert cache.length.tolist() == [n + 4 for n in lens]
