@@ -34,12 +34,17 @@
 // the waves' arrays are joined in wave order and left in the workspace, one
 // row per workgroup; attn_dtable_kernel sums each bucket's run of positions.
 //
-// Measured: causal 2 x 4,096, 32 query over 8 key heads, D = 128 bf16 dq 405-440
-// us (940-1,020 TFLOP/s), dk/dv 615-655 us (840-890); over 8,192 keys in full 388
-// and 551 us (1,000). Both hold two waves per SIMD (accumulators and fragments
-// fill the registers) and wait for each other's products and exponentials half
-// the time. 8 x 16 ragged heads of up to 1,024, D = 64 with the bias: 57 and
-// 105 us, where the empty key blocks leave 1.1 rounds of workgroups.
+// Measured (traced, box to box): causal 2 x 4,096, 32 query over 8 key heads, D = 128
+// bf16 dq 426-445 us (930-970 TFLOP/s), dk/dv 602-624 us (880-910); over 8,192 keys in
+// full 374-396 and 542-569 us (970-1,100). Both hold two waves per SIMD (accumulators
+// and fragments fill the registers; the 16-bit dk/dv instances of D over 96 spill
+// 28 bytes a lane without the bias, 100-148 with it, single row groups 76-216) and
+// have matrix cores and vector unit busy one after the other, 36-38% and 22-30% of
+// the time. With the bias at D = 128, 8 x 16 heads of 1,024: 131 and 278-287 us,
+// without it 118 and 179-187. 8 x 16 ragged heads of up to 1,024, D = 64 with the
+// bias: 59 and 105-107 us, where the empty key blocks leave 1.1 rounds of
+// workgroups. Head dimensions off 16 bytes: D = 100 1,170 and 1,920 us where 104
+// takes 127 and 197.
 #pragma once
 
 #include "attn_tile.hpp"

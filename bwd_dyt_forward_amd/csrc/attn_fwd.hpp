@@ -19,16 +19,19 @@
 // Where there are too few blocks of rows to fill the card, SL waves (slices)
 // share the rows and take 32 keys of each tile each; they join their maxima,
 // sums and outputs through LDS at the end. Few rows over many keys are
-// also split along the keys: each split leaves its unnormalised float32 output and (maximum, sum) in the workspace and
-// attn_join_kernel joins them in split order.
+// also split along the keys: each split leaves its unnormalised float32 output
+// and (maximum, sum) in the workspace and attn_join_kernel joins them in split
+// order.
 //
-// Measured: causal 2 x 4,096, 32 query over 8 key heads, D = 128 bf16 293-309 us
-// (890-940 TFLOP/s of the visible pairs' products; matrix cores 36% and vector
-// unit 34% busy, two waves per SIMD for the registers), 8,192 keys in full 275
-// us (1,000 TFLOP/s); at D = 64 the vector unit bounds it (an exponential and
-// six operations per pair beside 256 flop): 4 x 16 heads of 2,048 causal with the
-// bias 60 us. Single tokens are bound by HBM: 8 x 8 key heads of up to 16,384
-// keys, D = 128, 73-75 us (4.5 TB/s).
+// Measured (traced, box to box): causal 2 x 4,096, 32 query over 8 key heads, D = 128
+// bf16 305-316 us (870-900 TFLOP/s of the visible pairs' products), 8,192 keys in
+// full 270-282 us (970-1,020 TFLOP/s); two waves per SIMD for the registers, whose
+// matrix cores (36% busy) and vector unit (34%) work one after the other within a
+// wave. At D = 64 (an exponential and six operations per pair beside 256 flop) the
+// vector unit is 49% and the matrix cores 22% busy: 4 x 16 heads of 2,048 causal with
+// the bias 63 us. Single tokens are bound by HBM: 8 x 8 key heads of up to 16,384
+// keys, D = 128, 75 us (4.5 TB/s). Head dimensions off 16 bytes go element by
+// element in single waves: 8 x 16 heads of 1,024, D = 100, 1,060 us (104: 92).
 #pragma once
 
 #include "attn_tile.hpp"

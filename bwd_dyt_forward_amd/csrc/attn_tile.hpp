@@ -76,9 +76,10 @@ constexpr int attn_dkv_lds_bytes(int es, int dp, int nw, int sl) {
            (dkv_vals_in_lds(es, dp) ? nw * (dp / 16) * 1024 : 0);
 }
 
-// Waves per SIMD that an instance's registers have to leave room for. (Three or
-// four at dp <= 64 spill: forward 62 -> 82 us at 4 x 16 heads of 2,048 with four,
-// dk/dv 105 -> 187 us at 8 x 16 heads of 1,024 with three.)
+// Waves per SIMD that an instance's registers have to leave room for; instances
+// that need less, such as the forward's at dp <= 64, hold more. (Asking for three
+// or four at dp <= 64 makes some spill: forward 62 -> 82 us at 4 x 16 heads of
+// 2,048 with four, dk/dv 105 -> 187 us at 8 x 16 heads of 1,024 with three.)
 constexpr int attn_waves(int es) { return es == 4 ? 1 : 2; }
 
 // dq's second walk, see attn_bwd.hpp.

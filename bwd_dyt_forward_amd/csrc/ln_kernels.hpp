@@ -19,10 +19,15 @@
 // [dgamma | dbeta] per workgroup goes to the workspace; a second kernel sums
 // those rows in a fixed order. No atomics.
 //
-// Measured: 32,768 x 4,096 bf16 forward 86 us (6.2 TB/s), with the residual 185-
-// 195 us (5.6), backward with the residual 174-178 us (6.1); 4,194,304 x 32 f16
-// forward 89-95 us (6.2); 100,003 x 255 f32, whose rows are no whole vectors, 35
-// and 49 us (5.8 and 6.2). A 1,024 x 64 problem takes 3-4 us a kernel.
+// Measured (traced, box to box): 32,768 x 4,096 bf16 forward 98-101 us (5.4 TB/s),
+// with the residual 188-212 us (5.1-5.7), backward 118 (6.8) and with the
+// residual 171-185 us (5.8-6.3); 4,194,304 x 32 f16 forward 89-90 us (6.0); 100,003 x
+// 255 f32, whose rows are no whole vectors, 35 and 50 us (5.8 and 6.1). A 1,024 x 64
+// problem takes 3-4 us a kernel. The backward's rows of sixteen waves spill: 8,192
+// x 16,384 bf16 168 us (4.8 TB/s) and with the residual 435 us (2.5), f32 268 (6.0)
+// and 563 us (3.8). Rows past 16,384 columns, 4,096 x 33,000 bf16: forward 542 us (1.0
+// TB/s), backward 1,774 us (0.5): they are walked again for every sum, gamma is
+// read element by element and the column sums are kept in memory.
 #pragma once
 
 #include "block_common.hpp"
@@ -367,7 +372,8 @@ __global__ __launch_bounds__(kLongThreads) void ln_fwd_long_kernel(LnArgs a) {
 // U row groups at a time, and (AHEAD) the next U rows' vectors are loaded,
 // still packed, before the current ones are reduced, so that a workgroup's
 // loads do not wait for its sums. Workgroups of 1,024 threads have only 128
-// registers each and go without.
+// registers a lane, spill even so (with the residual 194 of them in the 16-bit
+// types, 12 without) and go without.
 template <typename T, int TPR, int TH, int V, int U, bool RES, int NT, bool AHEAD = (TPR < 1024)>
 __global__ __launch_bounds__(TH) void ln_bwd_kernel(LnArgs a) {
     using S = LnShape<TPR, TH>;

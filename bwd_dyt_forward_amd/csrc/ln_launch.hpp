@@ -35,8 +35,8 @@ inline LnConfig ln_row(int64_t M, int64_t N, int elem_bytes, bool backward) {
 // Rows of 128 and 256 threads come four waves to a workgroup, and in the
 // backward, where every workgroup has a partial row of sums to write and
 // more workgroups mean more of them, eight: at 32,768 x 4,096 bfloat16 with
-// the residual 200 -> 176 us (6.1 TB/s). Workgroups of sixteen waves get 64
-// registers a lane and spill. With fewer than four rounds of rows the smaller
+// the residual 200 -> 176 us (6.1 TB/s). Workgroups of sixteen waves, which get 128
+// registers a lane and spill, are left to rows that need them. With fewer than four rounds of rows the smaller
 // workgroups spread better.
 inline LnConfig ln_config(int64_t M, int64_t N, int elem_bytes, bool backward) {
     LnConfig c = ln_row(M, N, elem_bytes, backward);

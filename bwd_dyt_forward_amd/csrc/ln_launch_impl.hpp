@@ -10,8 +10,8 @@ namespace dytb {
 
 // Workgroups of a forward launch: enough to fill 256 CUs several times over
 // and no more, since each loads gamma and beta once for all its rows. Where
-// loads and stores are nontemporal and a row takes whole workgroups, two per
-// CU (32,768 x 4,096 bfloat16 with the residual: 203 -> 185 us; at half the
+// loads and stores are nontemporal and a row takes whole workgroups, two of 256
+// threads per CU, or one of 512, or half of 1,024 (32,768 x 4,096 bfloat16 with the residual: 203 -> 185 us; at half the
 // rows, where the tensors fit the last-level cache, the other way round: 84
 // against 92).
 constexpr int kFwdGridThreads = 256 * 2048, kFwdGridThreadsFew = 256 * 512;
