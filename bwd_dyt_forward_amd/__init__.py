@@ -9,7 +9,10 @@ The Python functions below carry the ABI's names and only marshal tensors.
 Around it stand the operators a transformer block needs next to its
 normalisation: layer norm (plain and residual) and attention with grouped key
 heads, masks and a learned relative position bias, forward and backward
-(``include/dyt_block.h``, library ``libdyt_block.so``).
+(``include/dyt_block.h``, library ``libdyt_block.so``); and what a decoder needs
+around such blocks: root-mean-square norm (also with an 8-bit output),
+embedding, log probabilities of tokens, AdamW (``include/dyt_lm.h``, library
+``libdyt_lm.so``).
 """
 from ._lib import (  # noqa: F401
     DYT_BF16,
@@ -46,6 +49,15 @@ _BLOCK_ALL = [
     "LayerNormResidualFunction", "layer_norm_residual", "Attention", "AttentionFunction", "attention", "KVCache",
 ]
 
+_LM_ALL = [
+    "LM_LIB_FILE", "lm_lib", "DYT_LOGPROB_MAX_TOP", "DYT_ADAMW_BLOCK", "dyt_rms_forward", "dyt_rms_forward_residual",
+    "dyt_rms_forward_q8", "dyt_rms_forward_residual_q8", "dyt_rms_backward", "dyt_rms_backward_residual",
+    "dyt_rms_backward_workspace_size", "dyt_embed_forward", "dyt_embed_backward", "dyt_embed_backward_workspace_size",
+    "dyt_logprob_forward", "dyt_logprob_backward", "dyt_logprob_forward_workspace_size", "dyt_adamw_step",
+    "dyt_adamw_values", "RMSNorm", "RMSNormFunction", "rms_norm", "RMSNormResidual", "RMSNormResidualFunction",
+    "rms_norm_residual", "Embedding", "EmbeddingFunction", "embedding", "LogProbFunction", "token_log_probs", "AdamW",
+]
+
 # DyT needs its own library only: where the block operators' is missing or from
 # other sources, their names say so when they are used.
 try:
@@ -75,13 +87,59 @@ try:
     )
 except ImportError as _e:
     _block_missing = str(_e)
-
-    def __getattr__(name):
-        if name in _BLOCK_ALL:
-            raise ImportError(_block_missing)
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 else:
     _block_missing = None
+
+# Likewise the operators around a decoder's blocks (their binding shares the
+# block operators' checks).
+try:
+    from ._lm import (  # noqa: E402,F401
+        DYT_ADAMW_BLOCK,
+        DYT_LOGPROB_MAX_TOP,
+        LM_LIB_FILE,
+        dyt_adamw_step,
+        dyt_adamw_values,
+        dyt_embed_backward,
+        dyt_embed_backward_workspace_size,
+        dyt_embed_forward,
+        dyt_logprob_backward,
+        dyt_logprob_forward,
+        dyt_logprob_forward_workspace_size,
+        dyt_rms_backward,
+        dyt_rms_backward_residual,
+        dyt_rms_backward_workspace_size,
+        dyt_rms_forward,
+        dyt_rms_forward_q8,
+        dyt_rms_forward_residual,
+        dyt_rms_forward_residual_q8,
+        lm_lib,
+    )
+    from .lm import (  # noqa: E402,F401
+        AdamW,
+        Embedding,
+        EmbeddingFunction,
+        LogProbFunction,
+        RMSNorm,
+        RMSNormFunction,
+        RMSNormResidual,
+        RMSNormResidualFunction,
+        embedding,
+        rms_norm,
+        rms_norm_residual,
+        token_log_probs,
+    )
+except ImportError as _e:
+    _lm_missing = str(_e)
+else:
+    _lm_missing = None
+
+if _block_missing or _lm_missing:
+    def __getattr__(name):
+        if _block_missing and name in _BLOCK_ALL:
+            raise ImportError(_block_missing)
+        if _lm_missing and name in _LM_ALL:
+            raise ImportError(_lm_missing)
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 __all__ = [
     "DyT", "DyTFunction", "dyt", "DyTResidual", "DyTResidualFunction", "dyt_residual",
@@ -92,4 +150,5 @@ __all__ = [
     "dyt_status_string", "dyt_abi_version", "dyt_get_plan", "dyt_get_forward_plan",
     "dyt_get_forward_residual_plan", "dyt_xcd_hint", "dyt_set_xcd_flip_override",
     *([] if _block_missing else _BLOCK_ALL),
+    *([] if _lm_missing else _LM_ALL),
 ]

@@ -38,6 +38,18 @@ BLOCK_DEPENDS = BLOCK_SOURCES + [os.path.join(CSRC, f) for f in (
     "attn_tile.hpp", "attn_fwd.hpp", "attn_bwd.hpp", "attn_launch.hpp", "attn_launch_fwd.hpp",
     "attn_launch_dq.hpp", "attn_launch_dkv.hpp", "dyt_math.hpp")] + [
     os.path.join(INCLUDE, "dyt.h"), os.path.join(INCLUDE, "dyt_block.h")]
+# The operators around a decoder's blocks (RMS norm, embedding, token log
+# probabilities, AdamW): again a library of their own, for the same reason.
+LM_LIB_PATH = os.path.join(PKG_DIR, "libdyt_lm.so")
+LM_SOURCES = [os.path.join(CSRC, f) for f in (
+    "lm_api.hip", "embed.hip", "logprob_api.hip", "adamw_api.hip", "adamw32.hip", "adamw8.hip")] + [
+    os.path.join(CSRC, f"{k}_{t}.hip") for k in ("rms_fwd", "rms_q8", "rms_bwd", "logprob")
+    for t in ("f32", "bf16", "f16")]
+LM_DEPENDS = LM_SOURCES + [os.path.join(CSRC, f) for f in (
+    "block_common.hpp", "block_host.hpp", "ln_kernels.hpp", "ln_launch.hpp", "rms_kernels.hpp", "rms_launch.hpp",
+    "rms_launch_impl.hpp", "embed_kernels.hpp", "logprob_kernels.hpp", "logprob_launch.hpp",
+    "logprob_launch_impl.hpp", "adamw_kernels.hpp", "adamw_launch.hpp", "dyt_math.hpp")] + [
+    os.path.join(INCLUDE, "dyt.h"), os.path.join(INCLUDE, "dyt_lm.h")]
 # Reference streaming kernels for bench.py's measured ceilings (not part of
 # the DyT ABI; nothing in the package loads them).
 STREAM_REF_SOURCE = os.path.join(CSRC, "stream_ref.hip")
@@ -108,8 +120,8 @@ OBJ_CACHE = os.path.join(PKG_DIR, "_build")
 
 def build(out: str = LIB_PATH, extra_flags: list[str] | None = None, verbose: bool = False,
           with_stream_ref: bool = True, cache: bool = False) -> str:
-    """Compile the library; at the default path also the block operators'
-    library and, by default, the reference streaming kernels next to it.
+    """Compile the library; at the default path also the block operators' and
+    the decoder operators' libraries and, by default, the reference streaming kernels next to it.
     Returns the library's path. Always recompiles every source, unless
     cache=True, which reuses the object of a translation unit whose source,
     headers and flags are unchanged. Only the host translation unit carries
@@ -119,6 +131,7 @@ def build(out: str = LIB_PATH, extra_flags: list[str] | None = None, verbose: bo
     _compile(out, SOURCES, extra, verbose, per_source, OBJ_CACHE if cache else None)
     if out == LIB_PATH:
         build_block(verbose=verbose, cache=cache)
+        build_lm(verbose=verbose, cache=cache)
         if with_stream_ref:
             _compile(STREAM_REF_PATH, [STREAM_REF_SOURCE], None, verbose)
     return out
@@ -131,6 +144,20 @@ def build_block(out: str = BLOCK_LIB_PATH, extra_flags: list[str] | None = None,
     per_source = {BLOCK_SOURCES[0]: [f'-DDYT_BUILD_ID="{source_hash(extra, BLOCK_DEPENDS)}"']}
     _compile(out, BLOCK_SOURCES, extra, verbose, per_source, OBJ_CACHE if cache else None, BLOCK_DEPENDS)
     return out
+
+
+def build_lm(out: str = LM_LIB_PATH, extra_flags: list[str] | None = None, verbose: bool = False,
+             cache: bool = False) -> str:
+    """Compile the decoder operators' library; returns its path."""
+    extra = list(extra_flags or [])
+    per_source = {LM_SOURCES[0]: [f'-DDYT_BUILD_ID="{source_hash(extra, LM_DEPENDS)}"']}
+    _compile(out, LM_SOURCES, extra, verbose, per_source, OBJ_CACHE if cache else None, LM_DEPENDS)
+    return out
+
+
+def lm_is_stale(path: str = LM_LIB_PATH) -> bool:
+    """True if the decoder operators' library is missing or from other sources."""
+    return built_id(path) != source_hash((), LM_DEPENDS)
 
 
 def block_is_stale(path: str = BLOCK_LIB_PATH) -> bool:
