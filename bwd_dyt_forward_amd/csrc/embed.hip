@@ -18,10 +18,12 @@ int embed_shape(int64_t T, int64_t V, int64_t D) {
     return DYT_OK;
 }
 
+// Threads of a row: its vectors, or an even share of them where they are more
+// than 256. Not rounded up to a power of two: no step exchanges lanes, and 40
+// vectors in 64 threads leave a third of the loads undone.
 int threads_per_row(int64_t D) {
-    int t = 1;
-    while (t < 256 && (int64_t)t * kEmbVec < D) t *= 2;
-    return t;
+    const int64_t vecs = (D + kEmbVec - 1) / kEmbVec, tiles = (vecs + 255) / 256;
+    return (int)((vecs + tiles - 1) / std::max<int64_t>(tiles, 1));
 }
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -37,7 +39,7 @@ struct EmbedPlan {
 
 EmbedPlan embed_plan(int64_t T, int64_t V, int64_t D) {
     EmbedPlan p{};
-    p.tpr = threads_per_row(D);
+    p.tpr = std::max(1, threads_per_row(D));
     p.groups = 256 / p.tpr;
     p.col_tiles = (int)((D + p.tpr * kEmbVec - 1) / (p.tpr * kEmbVec));
     const int64_t want = std::max<int64_t>(1, (int64_t)1024 * p.groups / p.col_tiles);
@@ -48,7 +50,7 @@ EmbedPlan embed_plan(int64_t T, int64_t V, int64_t D) {
     p.sorted = p.passes & 1;
     p.tiles = (T + kSortTile - 1) / kSortTile;
     p.keys = (size_t)up(T * 4, 16);
-    p.counts = T > kSortOne ? (size_t)p.tiles * kRadix * 4 : 0;
+    p.counts = T > kSortOne ? (size_t)(p.tiles + 1) * kRadix * 4 : 0;
     p.part = (size_t)p.chunks * 2 * D * 4;
     p.bytes = 4 * p.keys + p.counts + p.part;
     return p;
@@ -111,7 +113,7 @@ int embed_backward(const void* dy, int64_t lddy, const void* tokens, void* dw, i
     const int64_t sw = dtype_size(wdt), sy = dtype_size(ydt);
     if (!aligned({dw}, sw) || !aligned({dy}, sy) || !aligned({tokens}, bits / 8)) return DYT_ERR_MISALIGNED;
     const EmbedPlan p = embed_plan(T, V, D);
-    const int64_t zero_wgs = accumulate ? 0 : (V + 255) / 256;
+    const int64_t zero_wgs = accumulate ? 0 : (V + kZeroRows - 1) / kZeroRows;
     const int64_t sum_wgs = (p.chunks + p.groups - 1) / p.groups * p.col_tiles;
     if (sum_wgs + zero_wgs >= ((int64_t)1 << 24)) return DYT_ERR_INVALID_ARG;   // 2^32 threads of a launch
     if (T > 0 && (ws_bytes < p.bytes || !ws)) return DYT_ERR_WORKSPACE_TOO_SMALL;
@@ -126,16 +128,18 @@ int embed_backward(const void* dy, int64_t lddy, const void* tokens, void* dw, i
     for (int k = 0; k < 2; ++k, at += p.keys) a.places[k] = (uint32_t*)at;
     a.counts = (uint32_t*)at;
     a.part = (float*)(at + p.counts);
+    a.tiles = (uint32_t)p.tiles;
     a.token_bits = bits; a.tpr = p.tpr; a.chunk = (int32_t)p.chunk; a.chunks = (int32_t)p.chunks;
     a.col_tiles = p.col_tiles; a.sum_wgs = (int32_t)sum_wgs; a.accumulate = accumulate; a.scale = scale;
     const hipStream_t s = (hipStream_t)stream;
     if (T > 0 && T <= kSortOne) {
-        embed_sort_one_kernel<<<1, kSortThreads, 0, s>>>(a, p.passes);
+        embed_sort_one_kernel<<<1, kSortOneWaves * 64, 0, s>>>(a, p.passes);
     } else if (T > 0) {
+        const unsigned tiles = (unsigned)p.tiles, threads = kSortManyWaves * 64;
         for (int pass = 0; pass < p.passes; ++pass) {
-            embed_count_kernel<<<(unsigned)p.tiles, kSortThreads, 0, s>>>(a, pass);
-            embed_scan_kernel<<<1, kSortThreads, 0, s>>>(a.counts, p.tiles * kRadix);
-            embed_scatter_kernel<<<(unsigned)p.tiles, kSortThreads, 0, s>>>(a, pass);
+            embed_count_kernel<<<tiles, threads, 0, s>>>(a, pass);
+            if (p.tiles > kScanTiles) embed_scan_kernel<<<kRadix / 4, 256, 0, s>>>(a.counts, a.tiles);
+            embed_move_kernel<<<tiles, threads, 0, s>>>(a, pass);
         }
     }
     with_type(wdt, [&](auto* w) {
@@ -147,7 +151,7 @@ int embed_backward(const void* dy, int64_t lddy, const void* tokens, void* dw, i
             else embed_sum_kernel<TY, TW, 1><<<grid, 256, 0, s>>>(a, p.sorted);
         });
         if (p.chunks > 1) {
-            const dim3 grid((unsigned)(p.chunks - 1), (unsigned)std::min<int64_t>((D + 255) / 256, 1024));
+            const dim3 grid((unsigned)((p.chunks - 1 + kJoinChunks - 1) / kJoinChunks), (unsigned)std::min<int64_t>((D + 255) / 256, 1024));
             embed_join_kernel<TW><<<grid, 64 * kJoinWaves, 0, s>>>(a, p.sorted);
         }
     });

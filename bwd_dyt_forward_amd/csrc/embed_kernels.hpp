@@ -22,10 +22,16 @@
 namespace dytb {
 
 constexpr int kRadixBits = 9, kRadix = 1 << kRadixBits;
-constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-constexpr int kSortTile = 16384;        // tokens of a workgroup where several share a pass
-constexpr int64_t kSortOne = 65536;     // up to here one workgroup sorts alone, in one launch
+// One workgroup of 16 waves sorts up to kSortOne tokens alone, in one launch;
+// beyond, workgroups of 4 waves take a tile each and a pass is a launch. (A
+// round of 64 tokens is some 70 instructions of a wave: 16,384 tokens keep one
+// CU's vector units 8 us a pass.)
+constexpr int kSortOneWaves = 16, kSortManyWaves = 4;
+constexpr int64_t kSortOne = 16384;
+constexpr int kSortTile = 2048;
+constexpr int kScanTiles = 64;          // up to here every workgroup adds up the tiles before it itself
 constexpr int kEmbVec = 8;              // columns of a thread
+constexpr int kZeroRows = 64;           // rows that a workgroup looks up and clears
 
 // The token at place t, or V where there is none.
 __device__ __forceinline__ uint32_t token_at(const void* tokens, int bits, int64_t t, int64_t V) {
@@ -68,15 +74,12 @@ __device__ __forceinline__ void unpack_cols(const RawCols<T>& r, const T* p, int
     for (int i = 0; i < kEmbVec / W; ++i) unpack_raw<T>(r.w[i], p, row, c + i * W, D, limit, on, out + i * W);
 }
 
-template <typename T, bool NT = false>
+template <typename T>
 __device__ __forceinline__ void store_cols(T* p, int n, const float* v) {
     constexpr int W = VecOf<T>::n;
     if (n >= kEmbVec) {
 #pragma unroll
-        for (int i = 0; i < kEmbVec; i += W) {
-            if constexpr (NT) __builtin_nontemporal_store((u32x4_m)pack16<T>(v + i), (u32x4_m*)(p + i));
-            else *(u32x4_m*)(p + i) = pack16<T>(v + i);
-        }
+        for (int i = 0; i < kEmbVec; i += W) *(u32x4_m*)(p + i) = pack16<T>(v + i);
     } else {
 #pragma unroll
         for (int i = 0; i < kEmbVec; ++i)
@@ -91,13 +94,14 @@ struct EmbedArgs {
     void* out;            // y or dweight
     uint32_t* keys[2];    // sorted tokens and places, two of each
     uint32_t* places[2];
-    uint32_t* counts;     // [kRadix][tiles]
+    uint32_t* counts;     // [kRadix][tiles], then the digits' totals [kRadix]
+    uint32_t tiles;
     float* part;          // [chunks][2][D]
     int64_t ldw, ldy;     // pitch of weight or dweight, of y or dy
     int64_t T, V;
     int32_t D;
     int32_t token_bits;
-    int32_t tpr;          // threads of a row, a power of two up to 256
+    int32_t tpr;          // threads of a row or of a column tile of it, up to 256
     int32_t chunk;        // sorted tokens of a chunk
     int32_t chunks;
     int32_t col_tiles;    // of tpr * kEmbVec columns
@@ -113,8 +117,9 @@ template <typename TW, typename TY, int U>
 __global__ __launch_bounds__(256) void embed_fwd_kernel(EmbedArgs a) {
     const int64_t limit = (a.V - 1) * a.ldw + a.D;
     const TW* wp = (const TW*)a.weight;
-    const int t = (int)threadIdx.x & (a.tpr - 1), g = (int)threadIdx.x / a.tpr, groups = 256 / a.tpr;
+    const int g = (int)threadIdx.x / a.tpr, t = (int)threadIdx.x - g * a.tpr, groups = 256 / a.tpr;
     const int64_t step = (int64_t)gridDim.x * groups * U;
+    if (g >= groups) return;   // what is left over of 256 threads
     for (int64_t base = (int64_t)blockIdx.x * groups * U + g; base < a.T; base += step) {
         uint32_t tok[U];
 #pragma unroll
@@ -162,53 +167,79 @@ __device__ __forceinline__ uint64_t same_digit(uint32_t digit, bool on) {
     return same;
 }
 
-// The key and place that pass `pass` reads at i.
-__device__ __forceinline__ uint32_t sort_key(const EmbedArgs& a, int pass, int64_t i) {
-    return pass ? a.keys[pass & 1][i] : token_at(a.tokens, a.token_bits, i, a.V);
+__device__ __forceinline__ uint32_t digit_of(uint32_t key, int pass) {
+    return (key >> (pass * kRadixBits)) & (kRadix - 1);
 }
 
-// Counts of the digits of this wave's tokens [lo, hi).
-__device__ __forceinline__ void count_digits(const EmbedArgs& a, int pass, int64_t lo, int64_t hi, uint32_t* cnt) {
-    const int lane = (int)threadIdx.x & 63;
-    for (int64_t i = lo + lane; i < hi; i += 64)
-        atomicAdd(&cnt[(sort_key(a, pass, i) >> (pass * kRadixBits)) & (kRadix - 1)], 1u);
-}
+// Four rounds of a wave's tokens [from, to): 64 neighbours each, all loads on
+// their way before the first is used.
+constexpr int kRounds = 4;
 
-// Moves this wave's tokens [lo, hi) to their places; cnt[digit]: the place of
-// the wave's next token of that digit.
-__device__ __forceinline__ void scatter_digits(const EmbedArgs& a, int pass, int64_t lo, int64_t hi, uint32_t* cnt) {
-    const int lane = (int)threadIdx.x & 63;
-    uint32_t* to_key = a.keys[(pass + 1) & 1];
-    uint32_t* to_place = a.places[(pass + 1) & 1];
-    for (int64_t at = lo; at < hi; at += 64) {
-        const int64_t i = at + lane;
-        const bool on = i < hi;
-        const uint32_t key = on ? sort_key(a, pass, i) : 0u;
-        const uint32_t place = on ? (pass ? a.places[pass & 1][i] : (uint32_t)i) : 0u;
-        const uint32_t digit = (key >> (pass * kRadixBits)) & (kRadix - 1);
-        const uint64_t same = same_digit(digit, on);
-        const uint64_t below = same & ((1ull << lane) - 1);
-        const uint32_t first = on ? cnt[digit] : 0u;
-        wave_fence();   // every lane has read before the first of each digit writes
-        if (on && below == 0) cnt[digit] = first + (uint32_t)__popcll(same);
-        wave_fence();
-        if (on) {
-            const uint32_t to = first + (uint32_t)__popcll(below);
-            to_key[to] = key;
-            to_place[to] = place;
-        }
+__device__ __forceinline__ void load_keys(const EmbedArgs& a, int pass, uint32_t from, uint32_t to, uint32_t* key) {
+    const uint32_t* keys = a.keys[pass & 1];
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const uint32_t i = min(from + r * 64 + (threadIdx.x & 63), to - 1);
+        key[r] = pass ? keys[i] : token_at(a.tokens, a.token_bits, i, a.V);
     }
 }
 
 // The wave's part of the tokens [lo, hi).
-__device__ __forceinline__ void wave_part(int64_t lo, int64_t hi, int64_t& from, int64_t& to) {
-    const int64_t per = ((hi - lo + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
-    from = min(lo + ((int64_t)threadIdx.x >> 6) * per, hi);
+template <int WAVES>
+__device__ __forceinline__ void wave_part(uint32_t lo, uint32_t hi, uint32_t& from, uint32_t& to) {
+    const uint32_t per = ((hi - lo + WAVES - 1) / WAVES + 63) / 64 * 64;
+    from = min(lo + (threadIdx.x >> 6) * per, hi);
     to = min(from + per, hi);
 }
 
-// Exclusive sums over the workgroup's values in thread order.
-__device__ __forceinline__ uint32_t exclusive_sum(uint32_t v, uint32_t* waves) {
+__device__ __forceinline__ void count_digits(const EmbedArgs& a, int pass, uint32_t from, uint32_t to, uint32_t* cnt) {
+    for (uint32_t at = from; at < to; at += 64 * kRounds) {
+        uint32_t key[kRounds];
+        load_keys(a, pass, at, to, key);
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r)
+            if (at + r * 64 + (threadIdx.x & 63) < to) atomicAdd(&cnt[digit_of(key[r], pass)], 1u);
+    }
+}
+
+// Moves the wave's tokens to their places; cnt[digit]: the place of its next
+// token of that digit.
+__device__ __forceinline__ void move_tokens(const EmbedArgs& a, int pass, uint32_t from, uint32_t to, uint32_t* cnt) {
+    const uint32_t lane = threadIdx.x & 63;
+    const uint32_t* places = a.places[pass & 1];
+    uint32_t* to_key = a.keys[(pass + 1) & 1];
+    uint32_t* to_place = a.places[(pass + 1) & 1];
+    for (uint32_t at = from; at < to; at += 64 * kRounds) {
+        uint32_t key[kRounds], place[kRounds];
+        load_keys(a, pass, at, to, key);
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const uint32_t i = min(at + r * 64 + lane, to - 1);
+            place[r] = pass ? places[i] : i;
+        }
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            if (at + r * 64 >= to) break;   // for the whole wave
+            const bool on = at + r * 64 + lane < to;
+            const uint32_t digit = digit_of(key[r], pass);
+            const uint64_t same = same_digit(digit, on);
+            const uint64_t below = same & ((1ull << lane) - 1);
+            const uint32_t first = cnt[digit];
+            wave_fence();   // every lane has read before the first of each digit writes
+            if (on && below == 0) cnt[digit] = first + (uint32_t)__popcll(same);
+            wave_fence();
+            if (on) {
+                const uint32_t p = first + (uint32_t)__popcll(below);
+                to_key[p] = key[r];
+                to_place[p] = place[r];
+            }
+        }
+    }
+}
+
+// Exclusive sums over the workgroup's values in thread order, and their total.
+template <int WAVES>
+__device__ __forceinline__ uint32_t exclusive_sum(uint32_t v, uint32_t* waves, uint32_t& total) {
     const int lane = (int)threadIdx.x & 63, w = (int)threadIdx.x >> 6;
     uint32_t s = v;
 #pragma unroll
@@ -220,87 +251,121 @@ __device__ __forceinline__ uint32_t exclusive_sum(uint32_t v, uint32_t* waves) {
     if (lane == 63) waves[w] = s;
     __syncthreads();
     uint32_t before = 0;
-    for (int k = 0; k < w; ++k) before += waves[k];
+    total = 0;
+#pragma unroll
+    for (int k = 0; k < WAVES; ++k) {
+        before += k < w ? waves[k] : 0u;
+        total += waves[k];
+    }
     return before + s - v;
 }
 
-// All passes by one workgroup.
-__global__ __launch_bounds__(kSortThreads) void embed_sort_one_kernel(EmbedArgs a, int passes) {
-    __shared__ uint32_t cnt[kSortWaves][kRadix];
-    __shared__ uint32_t sums[kSortWaves];
-    int64_t lo, hi;
-    wave_part(0, a.T, lo, hi);
+// All passes by one workgroup. Its digits are counted with LDS atomics (whole
+// numbers: no order).
+__global__ __launch_bounds__(kSortOneWaves * 64) void embed_sort_one_kernel(EmbedArgs a, int passes) {
+    __shared__ uint32_t cnt[kSortOneWaves][kRadix];
+    __shared__ uint32_t sums[kSortOneWaves];
+    uint32_t from, to;
+    wave_part<kSortOneWaves>(0, (uint32_t)a.T, from, to);
+    uint32_t* mine = cnt[threadIdx.x >> 6];
     for (int pass = 0; pass < passes; ++pass) {
-        for (int i = (int)threadIdx.x; i < kSortWaves * kRadix; i += kSortThreads) cnt[0][i] = 0;
+        for (int i = (int)threadIdx.x; i < kSortOneWaves * kRadix; i += kSortOneWaves * 64) cnt[0][i] = 0;
         __syncthreads();
-        count_digits(a, pass, lo, hi, cnt[threadIdx.x >> 6]);
+        count_digits(a, pass, from, to, mine);
         __syncthreads();
         const int d = (int)threadIdx.x;
-        uint32_t total = 0;
+        uint32_t n = 0, total;
         if (d < kRadix)
-            for (int w = 0; w < kSortWaves; ++w) total += cnt[w][d];
-        uint32_t at = exclusive_sum(total, sums);
+            for (int w = 0; w < kSortOneWaves; ++w) n += cnt[w][d];
+        uint32_t at = exclusive_sum<kSortOneWaves>(n, sums, total);
         if (d < kRadix)
-            for (int w = 0; w < kSortWaves; ++w) {
-                const uint32_t n = cnt[w][d];
+            for (int w = 0; w < kSortOneWaves; ++w) {
+                const uint32_t x = cnt[w][d];
                 cnt[w][d] = at;
-                at += n;
+                at += x;
             }
         __syncthreads();
-        scatter_digits(a, pass, lo, hi, cnt[threadIdx.x >> 6]);
+        move_tokens(a, pass, from, to, mine);
         __threadfence_block();
-        __syncthreads();
+        __syncthreads();   // the next pass reads what all waves wrote
     }
 }
 
-// One pass by many workgroups: counts of each tile, their sums in the order
-// (digit, tile), and the moves.
-__global__ __launch_bounds__(kSortThreads) void embed_count_kernel(EmbedArgs a, int pass) {
+// A pass's digits of each tile. (Counting them for the next pass where the
+// tokens are moved to would save this launch, but the atomics meet: most tokens
+// share their upper digit. 62 us a pass of 32,768 tokens.)
+__global__ __launch_bounds__(kSortManyWaves * 64) void embed_count_kernel(EmbedArgs a, int pass) {
     __shared__ uint32_t cnt[kRadix];
-    if (threadIdx.x < kRadix) cnt[threadIdx.x] = 0;
+    for (int d = (int)threadIdx.x; d < kRadix; d += kSortManyWaves * 64) cnt[d] = 0;
     __syncthreads();
-    const int64_t lo = (int64_t)blockIdx.x * kSortTile, hi = min(lo + kSortTile, a.T);
-    int64_t from, to;
-    wave_part(lo, hi, from, to);
+    const uint32_t lo = blockIdx.x * kSortTile, hi = min(lo + kSortTile, (uint32_t)a.T);
+    uint32_t from, to;
+    wave_part<kSortManyWaves>(lo, hi, from, to);
     count_digits(a, pass, from, to, cnt);
     __syncthreads();
-    if (threadIdx.x < kRadix) a.counts[(int64_t)threadIdx.x * gridDim.x + blockIdx.x] = cnt[threadIdx.x];
+    for (int d = (int)threadIdx.x; d < kRadix; d += kSortManyWaves * 64) a.counts[(size_t)d * a.tiles + blockIdx.x] = cnt[d];
 }
 
-__global__ __launch_bounds__(kSortThreads) void embed_scan_kernel(uint32_t* counts, int64_t n) {
-    __shared__ uint32_t sums[kSortWaves];
-    const int64_t per = (n + kSortThreads - 1) / kSortThreads;
-    const int64_t lo = min((int64_t)threadIdx.x * per, n), hi = min(lo + per, n);
-    uint32_t s = 0;
-    for (int64_t i = lo; i < hi; ++i) s += counts[i];
-    uint32_t at = exclusive_sum(s, sums);
-    for (int64_t i = lo; i < hi; ++i) {
-        const uint32_t c = counts[i];
-        counts[i] = at;
-        at += c;
+// Each digit's sums over the tiles before, a wave for each digit.
+__global__ __launch_bounds__(256) void embed_scan_kernel(uint32_t* counts, uint32_t tiles) {
+    const uint32_t lane = threadIdx.x & 63;
+    const size_t d = (size_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    uint32_t* row = counts + d * tiles;
+    uint32_t total = 0;
+    for (uint32_t i0 = 0; i0 < tiles; i0 += 64) {
+        const uint32_t i = i0 + lane;
+        const uint32_t v = i < tiles ? row[i] : 0u;
+        uint32_t s = v;
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) {
+            const uint32_t x = (uint32_t)__shfl_up((int)s, o);
+            if ((int)lane >= o) s += x;
+        }
+        if (i < tiles) row[i] = total + s - v;
+        total += (uint32_t)__shfl((int)s, 63);
     }
+    if (lane == 0) counts[(size_t)kRadix * tiles + d] = total;
 }
 
-__global__ __launch_bounds__(kSortThreads) void embed_scatter_kernel(EmbedArgs a, int pass) {
-    __shared__ uint32_t cnt[kSortWaves][kRadix];
-    const int64_t lo = (int64_t)blockIdx.x * kSortTile, hi = min(lo + kSortTile, a.T);
-    int64_t from, to;
-    wave_part(lo, hi, from, to);
-    for (int i = (int)threadIdx.x; i < kSortWaves * kRadix; i += kSortThreads) cnt[0][i] = 0;
+// One pass.
+__global__ __launch_bounds__(kSortManyWaves * 64) void embed_move_kernel(EmbedArgs a, int pass) {
+    __shared__ uint32_t cnt[kSortManyWaves][kRadix];
+    __shared__ uint32_t sums[kSortManyWaves];
+    constexpr int TH = kSortManyWaves * 64;
+    const uint32_t lo = blockIdx.x * kSortTile, hi = min(lo + kSortTile, (uint32_t)a.T);
+    uint32_t from, to;
+    wave_part<kSortManyWaves>(lo, hi, from, to);
+    uint32_t* mine = cnt[threadIdx.x >> 6];
+    for (int i = (int)threadIdx.x; i < kSortManyWaves * kRadix; i += TH) cnt[0][i] = 0;
     __syncthreads();
-    count_digits(a, pass, from, to, cnt[threadIdx.x >> 6]);
-    __syncthreads();
-    const int d = (int)threadIdx.x;
-    if (d < kRadix) {
-        uint32_t at = a.counts[(int64_t)d * gridDim.x + blockIdx.x];
-        for (int w = 0; w < kSortWaves; ++w) {
-            const uint32_t n = cnt[w][d];
+    count_digits(a, pass, from, to, mine);
+    const uint32_t* counts = a.counts;
+    uint32_t smaller = 0;   // tokens of the digits of the rounds before
+    for (int d = (int)threadIdx.x; d < kRadix; d += TH) {
+        const uint32_t* row = counts + (size_t)d * a.tiles;
+        uint32_t before = 0, all = 0, total;
+        if (a.tiles <= kScanTiles) {
+#pragma unroll 8
+            for (uint32_t i = 0; i < a.tiles; ++i) {
+                const uint32_t n = row[i];
+                all += n;
+                before += i < blockIdx.x ? n : 0u;
+            }
+        } else {
+            before = row[blockIdx.x];
+            all = counts[(size_t)kRadix * a.tiles + d];
+        }
+        uint32_t at = smaller + before + exclusive_sum<kSortManyWaves>(all, sums, total);
+        smaller += total;
+        // (the barriers of the sum stand between the waves' counts and this)
+        for (int w = 0; w < kSortManyWaves; ++w) {
+            const uint32_t x = cnt[w][d];
             cnt[w][d] = at;
-            at += n;
+            at += x;
         }
     }
     __syncthreads();
-    scatter_digits(a, pass, from, to, cnt[threadIdx.x >> 6]);
+    move_tokens(a, pass, from, to, mine);
 }
 
 // ------------------------------------------------------------------- sums
@@ -320,36 +385,41 @@ __device__ __forceinline__ void put_row(const EmbedArgs& a, uint32_t key, int c,
 }
 
 // Sums of the runs of chunks, tpr threads to a chunk and column tile, U rows
-// of dy on their way (U = 1: also for a dy of fewer elements than a vector); and (workgroups from sum_wgs on, 256 rows each) zeros
-// for the rows of tokens that do not occur.
+// of dy on their way (U = 1: also for a dy of fewer elements than a vector);
+// and (workgroups from sum_wgs on, kZeroRows rows each) zeros for the rows of
+// tokens that do not occur.
 template <typename TY, typename TW, int U>
 __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs a, int sorted) {
     const uint32_t* keys = a.keys[sorted];
     const uint32_t V = (uint32_t)a.V;
     if ((int)blockIdx.x >= a.sum_wgs) {
-        __shared__ uint8_t absent[256];
-        const int64_t v0 = (int64_t)((int)blockIdx.x - a.sum_wgs) * 256, v = v0 + threadIdx.x;
-        int64_t lo = 0, hi = a.T;   // the first key of at least v
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) / 2;
-            if ((int64_t)keys[mid] < v) lo = mid + 1;
-            else hi = mid;
+        __shared__ uint8_t absent[kZeroRows];
+        const int64_t v0 = (int64_t)((int)blockIdx.x - a.sum_wgs) * kZeroRows, v = v0 + threadIdx.x;
+        if (threadIdx.x < kZeroRows) {
+            int64_t lo = 0, hi = a.T;   // the first key of at least v
+            while (lo < hi) {
+                const int64_t mid = (lo + hi) / 2;
+                if ((int64_t)keys[mid] < v) lo = mid + 1;
+                else hi = mid;
+            }
+            absent[threadIdx.x] = v < a.V && (lo == a.T || (int64_t)keys[lo] != v);
         }
-        absent[threadIdx.x] = v < a.V && (lo == a.T || (int64_t)keys[lo] != v);
         __syncthreads();
-        const int t = (int)threadIdx.x & (a.tpr - 1), g = (int)threadIdx.x / a.tpr, groups = 256 / a.tpr;
-        const float zero[kEmbVec] = {};
-        for (int r = g; r < 256; r += groups) {
+        // 16 bytes to a lane: whole lines to a wave
+        constexpr int W = VecOf<TW>::n;
+        const int lanes = min((a.D + W - 1) / W, 256), groups = 256 / lanes;
+        const int g = (int)threadIdx.x / lanes, t = (int)threadIdx.x - g * lanes;
+        const float zero[W] = {};
+        for (int r = g < groups ? g : kZeroRows; r < kZeroRows; r += groups) {
             if (!absent[r]) continue;
-            for (int c = t * kEmbVec; c < a.D; c += a.tpr * kEmbVec)
-                store_cols<TW, true>((TW*)a.out + (v0 + r) * a.ldw + c, a.D - c, zero);
+            for (int c = t * W; c < a.D; c += lanes * W) store_vec<TW, 0>((TW*)a.out, (v0 + r) * a.ldw, c, a.D, zero);
         }
         return;
     }
-    const int t = (int)threadIdx.x & (a.tpr - 1), g = (int)threadIdx.x / a.tpr, groups = 256 / a.tpr;
+    const int g = (int)threadIdx.x / a.tpr, t = (int)threadIdx.x - g * a.tpr, groups = 256 / a.tpr;
     const int chunk = (int)(blockIdx.x / a.col_tiles) * groups + g;
     const int c = ((int)(blockIdx.x % a.col_tiles) * a.tpr + t) * kEmbVec;
-    if (chunk >= a.chunks || c >= a.D) return;
+    if (g >= groups || chunk >= a.chunks || c >= a.D) return;
     const int64_t lo = (int64_t)chunk * a.chunk, hi = min(lo + a.chunk, a.T);
     const uint32_t* places = a.places[sorted];
     const uint32_t before = lo > 0 ? keys[lo - 1] : V, after = hi < a.T ? keys[hi] : V;
@@ -403,51 +473,71 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs a, int sorted)
     else put_row<TW>(a, run, c, acc);
 }
 
-// A run that begins in chunk blockIdx.x and goes on: its tail and the heads of
-// the chunks after it. 256 columns to a workgroup, 4 a lane; its waves take
-// slices of the heads, joined in order.
-constexpr int kJoinWaves = 16;
+// Runs that begin in a chunk and go on: the tail and the heads of the chunks
+// after it. A workgroup looks at kJoinChunks borders between chunks (a launch
+// of one each would take longer to hand out than to run: 65 us of 1,023
+// borders, 8 column tiles and 16 waves) and takes 256 columns of each such run, 4 a
+// lane; its waves take slices of the heads, joined in order.
+constexpr int kJoinWaves = 8, kJoinChunks = 4;
 
 template <typename TW>
 __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedArgs a, int sorted) {
     __shared__ float red[kJoinWaves][256];
     const uint32_t* keys = a.keys[sorted];
-    const int64_t lo = (int64_t)blockIdx.x * a.chunk, hi = lo + a.chunk;   // never the last chunk
-    const uint32_t run = keys[hi - 1];
-    if (run >= (uint32_t)a.V || keys[hi] != run) return;   // it does not go on
-    if (lo > 0 && keys[lo] == run && keys[lo - 1] == run) return;   // it began before
-    int64_t x = hi, y = a.T;   // the end of the run
-    while (x < y) {
-        const int64_t mid = (x + y) / 2;
-        if (keys[mid] <= run) x = mid + 1;
-        else y = mid;
-    }
-    const int last = (int)((x - 1) / a.chunk);   // the last chunk with a part of it
-    const int n = last - (int)blockIdx.x;        // heads
     const int lane = (int)threadIdx.x & 63, w = (int)threadIdx.x >> 6;
-    const int per = (n + kJoinWaves - 1) / kJoinWaves;
-    const int from = (int)blockIdx.x + 1 + min(w * per, n), to = (int)blockIdx.x + 1 + min((w + 1) * per, n);
-    for (int c0 = (int)blockIdx.y * 256; c0 < a.D; c0 += (int)gridDim.y * 256) {
-        float s[4] = {};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = c0 + j * 64 + lane;
-            if (c >= a.D) continue;
-            if (w == 0) s[j] = a.part[((int64_t)blockIdx.x * 2 + 1) * a.D + c];
-#pragma unroll 8
-            for (int k = from; k < to; ++k) s[j] += a.part[(int64_t)k * 2 * a.D + c];
+    // lane i: whether a run of chunk first + i goes on there, which, and in how
+    // many chunks (found from both ends of a doubling step: most runs are short)
+    const int first = (int)blockIdx.x * kJoinChunks;
+    uint32_t run = 0;
+    int heads = 0;
+    bool some = false;
+    if (lane < kJoinChunks && first + lane < a.chunks - 1) {
+        const int64_t lo = (int64_t)(first + lane) * a.chunk, hi = lo + a.chunk;
+        run = keys[hi - 1];
+        const bool began_before = lo > 0 && keys[lo] == run && keys[lo - 1] == run;
+        some = run < (uint32_t)a.V && keys[hi] == run && !began_before;
+        if (some) {
+            const int left = a.chunks - 1 - (first + lane);   // chunks after this one
+            const auto goes = [&](int n) { return n <= left && keys[(int64_t)(first + lane + n) * a.chunk] == run; };
+            int no = 2;
+            while (goes(no)) no *= 2;
+            heads = no / 2;
+            while (heads + 1 < no) {
+                const int mid = (heads + no) / 2;
+                if (goes(mid)) heads = mid;
+                else no = mid;
+            }
         }
-        __syncthreads();   // the columns before have been read
+    }
+    for (uint64_t todo = __ballot(some); todo; todo &= todo - 1) {   // the same in every wave
+        const int i = __ffsll((unsigned long long)todo) - 1;
+        const uint32_t key = (uint32_t)__shfl((int)run, i);
+        const int chunk = first + i;
+        const int n = __shfl(heads, i);
+        const int per = (n + kJoinWaves - 1) / kJoinWaves;
+        const int from = chunk + 1 + min(w * per, n), to = chunk + 1 + min((w + 1) * per, n);
+        for (int c0 = (int)blockIdx.y * 256; c0 < a.D; c0 += (int)gridDim.y * 256) {
+            const int c = min(c0 + lane * 4, a.D);
+            float s[4] = {}, v[4];
+            if (w == 0) load_vec<float>(a.part, ((int64_t)chunk * 2 + 1) * a.D, c, a.D, s);
+#pragma unroll 8
+            for (int k = from; k < to; ++k) {
+                load_vec<float>(a.part, (int64_t)k * 2 * a.D, c, a.D, v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) red[w][j * 64 + lane] = s[j];
-        __syncthreads();
-        if (threadIdx.x < 256 && c0 + (int)threadIdx.x < a.D) {
-            const int c = c0 + (int)threadIdx.x;
-            float v = 0.0f;
+                for (int j = 0; j < 4; ++j) s[j] += v[j];
+            }
+            __syncthreads();   // the sums before have been read
 #pragma unroll
-            for (int k = 0; k < kJoinWaves; ++k) v += red[k][threadIdx.x];
-            TW* p = (TW*)a.out + (int64_t)run * a.ldw + c;
-            *p = dyt::from_f32<TW>(a.accumulate ? __builtin_fmaf(v, a.scale, to_f32(*p)) : v * a.scale);
+            for (int j = 0; j < 4; ++j) red[w][lane * 4 + j] = s[j];
+            __syncthreads();
+            const int col = c0 + (int)threadIdx.x;
+            if (threadIdx.x < 256 && col < a.D) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kJoinWaves; ++k) sum += red[k][threadIdx.x];
+                TW* p = (TW*)a.out + (int64_t)key * a.ldw + col;
+                *p = dyt::from_f32<TW>(a.accumulate ? __builtin_fmaf(sum, a.scale, to_f32(*p)) : sum * a.scale);
+            }
         }
     }
 }
