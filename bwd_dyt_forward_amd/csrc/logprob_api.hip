@@ -13,10 +13,17 @@ namespace {
 
 static_assert(kLpMaxTop == DYT_LOGPROB_MAX_TOP, "the kernels' limit is the header's");
 constexpr int64_t kMaxV = (int64_t)1 << 26;
-constexpr int64_t kMaxPart = (int64_t)1 << 18;   // columns of a part with alternatives: 4,096 lines' maxima in LDS
+// With alternatives: lines of a part and parts of a row, for what of both is in
+// LDS (51 KB of maxima and candidates of a part, 32 KB of candidates of a row),
+// and the longest row that they leave.
+constexpr int64_t kMaxLines = 4096, kMaxTopParts = 64;
+constexpr int64_t kMaxTopV = (int64_t)1 << 23;
+static_assert(kMaxTopV <= kMaxTopParts * kMaxLines * 8 * 4, "float32 lines have 32 elements");
 
 int lp_shape(int64_t T, int64_t V, int top, int dt) {
-    if (T < 0 || V < 0 || T > 0x7fffffff || V > kMaxV || top < 0 || top > kLpMaxTop || top > V) return DYT_ERR_INVALID_ARG;
+    if (T < 0 || V < 0 || T > 0x7fffffff || V > kMaxV || top < 0 || top > kLpMaxTop || top > V ||
+        (top > 0 && V > kMaxTopV))
+        return DYT_ERR_INVALID_ARG;
     return dtype_ok(dt) ? DYT_OK : DYT_ERR_UNSUPPORTED_DTYPE;
 }
 
@@ -31,7 +38,7 @@ struct LpPlan {
     size_t shared, join_shared, part_bytes, bytes;
 };
 
-LpPlan lp_plan(int64_t T, int64_t V, int top, int dt) {
+LpPlan lp_plan(int64_t T, int64_t V, int top, int dt, bool backward = false) {
     LpPlan p{};
     const int64_t vec = 16 / dtype_size(dt), nv = (V + vec - 1) / vec;
     p.tpr = 256;
@@ -42,16 +49,25 @@ LpPlan lp_plan(int64_t T, int64_t V, int top, int dt) {
     int64_t parts = 1;
     const int64_t step = 256 * vec;   // one vector of every thread
     if (p.tpr == 256 && T < 512) parts = std::min((1024 + T - 1) / T, (nv + 1023) / 1024);
-    if (top) parts = std::max(parts, (V + kMaxPart - 1) / kMaxPart);
+    if (top) parts = std::min(std::max(parts, (V + kMaxLines * 8 * vec - 1) / (kMaxLines * 8 * vec)), kMaxTopParts);
     parts = std::min<int64_t>(parts, 256);
-    p.part_len = p.tpr == 256 ? ((V + parts - 1) / parts + step - 1) / step * step : V;
-    p.parts = (int)((V + p.part_len - 1) / p.part_len);
+    if (backward && p.tpr == 256) {
+        // tiles that follow each other in memory: 290 us for 320 of a workgroup for each row
+        p.part_len = kLpBwdVecs * step;
+        p.parts = (int)((V + vec - 1 + p.part_len - 1) / p.part_len);
+        p.grid = T * p.parts;
+        return p;
+    }
+    // a row may begin up to vec - 1 places after the 16-byte grid
+    const int64_t places = V + vec - 1;
+    p.part_len = p.tpr == 256 ? ((places + parts - 1) / parts + step - 1) / step * step : places;
+    p.parts = (int)((places + p.part_len - 1) / p.part_len);
     const int64_t per = 256 / p.tpr;
     p.grid = (T * p.parts + per - 1) / per;
     if (top) {
         const int64_t lines = p.part_len / (8 * vec);
-        p.shared = (size_t)((lines + 2) / 2 + top * std::max((lines + 255) / 256, 2 * vec)) * 8;
-        p.join_shared = (size_t)(top * ((p.parts * top + 255) / 256)) * 8;
+        p.shared = (size_t)((lines + 1) / 2 + top * 4 * std::max((lines + 255) / 256, 2 * vec)) * 8;
+        p.join_shared = (size_t)(top * 4 * ((p.parts * top + 255) / 256)) * 8;
     }
     if (p.parts > 1) {
         p.part_bytes = (size_t)T * p.parts * 16;
@@ -95,6 +111,11 @@ int lp_forward(const void* logits, int64_t ld, const void* tokens, float* logp, 
     a.part_top = (uint64_t*)((uint8_t*)ws + p.part_bytes);
     a.ld = ld; a.T = T; a.V = V; a.part_len = p.part_len; a.parts = p.parts; a.top = top; a.token_bits = bits;
     a.tpr = p.tpr; a.scale = scale;
+    // Logits past the last-level cache (256 MB) leave it to what was written before
+    // them: nontemporal loads (8,192 x 50,257 bfloat16: 187 -> 147 us; 8,192 x 4,096,
+    // which fit, 22 -> 26). The backward, whose reads and writes both pass through
+    // it, is slower with such loads or stores (289 -> 305).
+    a.stream = T * V * s >= ((int64_t)256 << 20);
     with_type(dt, [&](auto* t) {
         lp_launch_forward<std::remove_pointer_t<decltype(t)>>(a, p.grid, p.shared, p.join_shared, (hipStream_t)stream);
     });
@@ -114,7 +135,7 @@ int lp_backward(const void* logits, int64_t ld, const void* tokens, const float*
     const int64_t s = dtype_size(dt);
     if (!aligned({logits, dlogits}, s) || !aligned({tokens}, bits / 8) || !aligned({entropy, lse, dlogp, dentropy}, 4))
         return DYT_ERR_MISALIGNED;
-    const LpPlan p = lp_plan(T, V, 0, dt);
+    const LpPlan p = lp_plan(T, V, 0, dt, true);
     if (p.grid >= ((int64_t)1 << 24)) return DYT_ERR_INVALID_ARG;
     const bool same = dlogits == logits && ldd == ld;   // in place
     const Range in[] = {{same ? nullptr : logits, ((T - 1) * ld + V) * s}, {tokens, T * (bits / 8)}, {entropy, T * 4},
@@ -124,7 +145,8 @@ int lp_backward(const void* logits, int64_t ld, const void* tokens, const float*
     LpArgs a{};
     a.logits = logits; a.tokens = tokens; a.entropy = const_cast<float*>(entropy); a.lse = const_cast<float*>(lse);
     a.dlogp = dlogp; a.dentropy = dentropy; a.dlogits = dlogits; a.ld = ld; a.ldd = ldd; a.T = T; a.V = V;
-    a.part_len = p.part_len; a.parts = p.parts; a.token_bits = bits; a.tpr = p.tpr; a.scale = scale;
+    a.part_len = p.part_len; a.parts = p.parts; a.token_bits = bits; a.tpr = p.tpr;
+    a.scale = scale;
     with_type(dt, [&](auto* t) {
         lp_launch_backward<std::remove_pointer_t<decltype(t)>>(a, p.grid, (hipStream_t)stream);
     });

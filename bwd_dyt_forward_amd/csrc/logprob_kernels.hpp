@@ -7,23 +7,26 @@
 //   entropy = lse - sum_j p[j] z[j]  p[j] = exp(z[j] - lse)
 //   dx[j] = scale (dlogp ([j = c] - p[j]) - dentropy p[j] (z[j] - lse + entropy))
 //
-// Bound by HBM: the forward reads a row once, the backward reads it and writes
-// its gradient; nothing of a row's length is kept in between. A thread keeps a
-// running maximum m of what it has read and, relative to it,
-//   s = sum exp(scale (x - m)),  t = sum (x - m) exp(scale (x - m))
-// so that entropy = log s - scale t / s, without the cancellation of lse
-// against a sum of raw logits; threads, and parts of a row where few rows are
-// split over workgroups, are joined the same way. One exponential and about
-// seven operations an element keep the vector unit four fifths as long busy as
-// HBM.
+// The forward reads a row once, the backward reads it and writes its gradient;
+// nothing of a row's length is kept in between. A thread works in powers of two:
+// with y = k x, k = scale log2(e), it keeps a running maximum m of the y it has
+// read and, relative to it, s = sum 2^(y - m), t = sum (y - m) 2^(y - m), so that
+//   lse = (m + log2 s) ln 2        entropy = (log2 s - t / s) ln 2
+// without the cancellation of lse against a sum of raw logits; threads, and parts
+// of a row where few rows are split over workgroups, are joined the same way.
+//
+// The backward is bound by HBM. In the forward the vector unit is as busy as
+// HBM: one exponential (a quarter of the rate) and six other operations an
+// element. Hence y - m in one fused operation, maxima of three, 32-bit places,
+// and checks for a row's ends outside of the vectors that lie within it.
 //
 // Alternatives: the best k by (value, lowest index), as one 64-bit key each.
 // Neighbouring eight lanes share a line of memory; its maximum (three lane
 // exchanges a vector) goes to LDS. The k best lines hold the k best elements,
-// so only they are read again. A set's k best keys are found without a sort:
-// every thread's best key is ranked among all threads' by counting, the k-th is
-// a bound that at least k keys reach and, since the threads beyond it are out,
-// at most k threads' keys; those few are then ranked exactly. No step depends
+// so only they are read again. The k best of many keys are found without a sort:
+// the best keys of 64 sets are ranked among each other by counting, the k-th is
+// a bound that at least k keys reach and, since the sets beyond it are out, at
+// most the keys of k sets; those few are then ranked exactly. No step depends
 // on the values, so rows of equal or masked logits cost the same.
 #pragma once
 
@@ -33,6 +36,7 @@ namespace dytb {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpMaxTop = 64;
+constexpr int kLpBwdVecs = 4;   // vectors of a thread in the backward: no loop
 constexpr float kLog2e = 0x1.715476p+0f;
 
 struct LpArgs {
@@ -50,11 +54,12 @@ struct LpArgs {
     uint64_t* part_top;   // [T][parts][top]
     int64_t ld, ldd;
     int64_t T, V;
-    int64_t part_len;     // columns of a part
+    int64_t part_len;     // places of a part, see RowPart
     int32_t parts;
     int32_t top;
     int32_t token_bits;
     int32_t tpr;          // threads of a row, a power of two up to 64, or 256
+    int32_t stream;       // 1: nontemporal loads
     float scale;
 };
 
@@ -62,96 +67,127 @@ struct Lse {
     float m, s, t;
 };
 
+// The least maximum is finite: a y of -inf (a logit of -inf, or below -2.3e38 /
+// scale) then has an exponential of 0.
 __device__ __forceinline__ Lse lse_none() { return {-3.402823466e+38f, 0.0f, 0.0f}; }
 
-// a and b relative to the larger maximum.
-__device__ __forceinline__ Lse lse_join(Lse a, Lse b, float k2) {
-    const float m = fmaxf(a.m, b.m);
-    const float da = a.m - m, db = b.m - m;   // 0 or below; -inf next to an infinite maximum
-    const float fa = __builtin_amdgcn_exp2f(da * k2), fb = __builtin_amdgcn_exp2f(db * k2);
-    Lse r;
-    r.m = m;
-    r.s = fa * a.s + fb * b.s;
-    // a side that is far below has a factor of 0: so has its share, whatever da
-    r.t = fa * (a.t + fmaxf(da, -1e30f) * a.s) + fb * (b.t + fmaxf(db, -1e30f) * b.s);
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
     return r;
 }
 
-template <int CTRL>
-__device__ __forceinline__ Lse lse_dpp(Lse v) { return {dpp_mov<CTRL>(v.m), dpp_mov<CTRL>(v.s), dpp_mov<CTRL>(v.t)}; }
-
-__device__ __forceinline__ Lse lse_lane(Lse v, int from) {
-    return {__shfl(v.m, from), __shfl(v.s, from), __shfl(v.t, from)};
+// Over aligned groups of `lanes` lanes, in every lane: the maximum, then the
+// sums relative to it.
+__device__ __forceinline__ float lp_max(float v, int lanes) {
+    if (lanes >= 2) v = fmaxf(v, dpp_mov<0xB1>(v));     // lane ^ 1
+    if (lanes >= 4) v = fmaxf(v, dpp_mov<0x4E>(v));     // lane ^ 2
+    if (lanes >= 8) v = fmaxf(v, dpp_mov<0x141>(v));    // mirrored within 8
+    if (lanes >= 16) v = fmaxf(v, dpp_mov<0x140>(v));   // mirrored within 16
+    if (lanes >= 32) {
+        const u32x2 s = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(
+            __float_as_uint(v), __float_as_uint(v), false, false));
+        v = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+    }
+    if (lanes >= 64) v = swap32_max(v);
+    return v;
 }
 
-// Joined over aligned groups of `lanes` lanes, in every lane (the same bits:
-// the join is symmetric).
-__device__ __forceinline__ Lse lse_lanes(Lse v, int lanes, float k2) {
-    if (lanes >= 2) v = lse_join(v, lse_dpp<0xB1>(v), k2);
-    if (lanes >= 4) v = lse_join(v, lse_dpp<0x4E>(v), k2);
-    if (lanes >= 8) v = lse_join(v, lse_dpp<0x141>(v), k2);
-    if (lanes >= 16) v = lse_join(v, lse_dpp<0x140>(v), k2);
-    const int lane = (int)threadIdx.x & 63;
-    if (lanes >= 32) v = lse_join(v, lse_lane(v, lane ^ 16), k2);
-    if (lanes >= 64) v = lse_join(v, lse_lane(v, lane ^ 32), k2);
+__device__ __forceinline__ float lp_sum(float v, int lanes) {
+    if (lanes >= 2) v += dpp_mov<0xB1>(v);
+    if (lanes >= 4) v += dpp_mov<0x4E>(v);
+    if (lanes >= 8) v += dpp_mov<0x141>(v);
+    if (lanes >= 16) v += dpp_mov<0x140>(v);
+    if (lanes >= 32) v = swap16_other_sum(v);
+    if (lanes >= 64) v = swap32_other_sum(v);
     return v;
+}
+
+__device__ __forceinline__ Lse lse_lanes(Lse v, int lanes) {
+    const float m = lp_max(v.m, lanes), d = v.m - m;   // 0 or below; NaN next to an infinite maximum
+    const float f = __builtin_amdgcn_exp2f(d);
+    // a lane that is far below has a factor of 0: so has its share, whatever d
+    return {m, lp_sum(f * v.s, lanes), lp_sum(f * (v.t + fmaxf(d, -1e30f) * v.s), lanes)};
+}
+
+// Over a workgroup, in every thread.
+__device__ __forceinline__ Lse lse_group(Lse v, Lse* waves) {
+    v = lse_lanes(v, 64);
+    if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return lse_lanes(waves[threadIdx.x & 3], 4);
 }
 
 // One vector's elements (-inf where there are none); returns their maximum.
 template <int VEC>
 __device__ __forceinline__ float lse_add(Lse& a, const float* x, float k2) {
-    float mv = fmaxf(x[0], x[1]);
-#pragma unroll
-    for (int i = 2; i < VEC; ++i) mv = fmaxf(mv, x[i]);
-    if (mv > a.m) {
-        const float d = a.m - mv, f = __builtin_amdgcn_exp2f(d * k2);
+    float mv;
+    if constexpr (VEC == 8) mv = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
+    else mv = max3(x[0], x[1], fmaxf(x[2], x[3]));
+    const float m = mv * k2;
+    if (m > a.m) {
+        const float d = a.m - m, f = __builtin_amdgcn_exp2f(d);
         a.t = f * (a.t + fmaxf(d, -1e30f) * a.s);
         a.s *= f;
-        a.m = mv;
+        a.m = m;
     }
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-        const float z = x[i] - a.m;
-        const float e = __builtin_amdgcn_exp2f(z * k2);
+        const float z = __builtin_fmaf(x[i], k2, -a.m);
+        const float e = __builtin_amdgcn_exp2f(z);
         a.s += e;
         a.t = __builtin_fmaf(fmaxf(z, -1e30f), e, a.t);   // -inf times an exact 0 would be NaN
     }
     return mv;
 }
 
+// A part of a row on the 16-byte grid: its vectors are the aligned 16 bytes of
+// memory, whatever the row's first address, so that rows of odd length are read
+// like others (50,257 bfloat16 logits: unaligned vectors cost a tenth). Place e
+// is column e - skew, of the row's V + skew places. The vectors at places lo to
+// hi lie within the row; the others, at its ends, are read element by element.
 template <typename T>
-__device__ __forceinline__ void logits_at(u32x4 raw, const T* p, int64_t row, int64_t c, int64_t end, float* x) {
-    constexpr int VEC = VecOf<T>::n;
-    unpack16<T>(raw, x);
-    if (c + VEC > end) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) x[i] = c + i < end ? to_f32(p[row + c + i]) : -INFINITY;
+struct RowPart {
+    static constexpr int VEC = VecOf<T>::n;
+    const T* p;           // place 0 (before the row by `skew` elements)
+    const T* from;        // what vectors are loaded from: p, or 16 bytes of nothing where there is no whole one
+    int V, skew;
+    int first, end;       // places of the part
+    int lo, hi, most;     // whole vectors' places, and the last one that is loaded
+
+    __device__ __forceinline__ RowPart(const T* logits, uint32_t m, uint32_t part, const LpArgs& a) {
+        static __device__ const u32x4 none = {0, 0, 0, 0};
+        const bool on = m < a.T;
+        const T* row = logits + (on ? (int64_t)m * a.ld : 0);
+        V = (int)a.V;
+        skew = (int)(((uintptr_t)row / sizeof(T)) % VEC);
+        p = row - skew;
+        first = (int)part * (int)a.part_len;
+        end = on ? min(first + (int)a.part_len, V + skew) : first;
+        lo = max(first, skew ? VEC : 0);
+        hi = min(end, (V + skew) / VEC * VEC);
+        const bool some = lo < hi;
+        from = some ? p : (const T*)&none;
+        most = some ? hi - VEC : 0;
     }
-}
 
-// The 16 bytes at column c, or the tensor's first or last ones where there are
-// none (see load_raw). A tensor of fewer elements than a vector is not read
-// here: its only vector ends past its row and is read one by one.
-__device__ const u32x4 kNoLogits = {0, 0, 0, 0};
-
-template <typename T>
-__device__ __forceinline__ u32x4 logits_raw(const T* p, int64_t row, int64_t c, int64_t end, int64_t limit) {
-    constexpr int VEC = VecOf<T>::n;
-    const T* from = p + (c < end ? min(row + c, limit - VEC) : 0);
-    return *(const u32x4_m*)(limit < VEC ? (const T*)&kNoLogits : from);
-}
-
-template <typename T>
-__device__ __forceinline__ void store_part(T* p, int64_t row, int64_t c, int64_t end, const float* v) {
-    constexpr int VEC = VecOf<T>::n;
-    if (c + VEC <= end) {
-        *(u32x4_m*)(p + row + c) = pack16<T>(v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            if (c + i < end) p[row + c + i] = dyt::from_f32<T>(v[i]);
+    // The vector at e; another one where that is not whole.
+    template <bool NT>
+    __device__ __forceinline__ u32x4 load(int e) const {
+        const u32x4* at = (const u32x4*)(from + min(max(e, min(lo, most)), most));
+        if constexpr (NT) return __builtin_nontemporal_load(at);
+        else return *at;
     }
-}
+
+    // The elements of a vector that is not whole as float32, -inf where there are none.
+    __device__ __forceinline__ void elements(int e, float* x) const {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) x[i] = in_row(e, i) ? to_f32(p[e + i]) : -INFINITY;
+    }
+
+    __device__ __forceinline__ bool in_row(int e, int i) const { return e < end && e + i >= skew && e + i < V + skew; }
+    __device__ __forceinline__ bool whole(int e) const { return e >= lo && e < hi; }
+};
 
 // Maximum over aligned groups of eight lanes.
 __device__ __forceinline__ float lanes_max8(float v) {
@@ -160,20 +196,34 @@ __device__ __forceinline__ float lanes_max8(float v) {
     return fmaxf(v, dpp_mov<0x141>(v));
 }
 
-__device__ __forceinline__ void lp_write(const LpArgs& a, int64_t m, Lse v, float x, bool real) {
-    const float log_s = logf(v.s);
-    const bool none = v.s == 0.0f;   // every logit is -inf
-    a.lse[m] = none ? -INFINITY : __builtin_fmaf(v.m, a.scale, log_s);
-    a.entropy[m] = none ? 0.0f : log_s - a.scale * v.t / v.s;
-    a.logp[m] = !real ? 0.0f : none ? -INFINITY : (x - v.m) * a.scale - log_s;
+constexpr float kLn2 = 0x1.62e43p-1f;
+
+// log p of a logit.
+__device__ __forceinline__ float lp_of(Lse v, float log2_s, float x, float k2) {
+    return v.s == 0.0f ? -INFINITY : (__builtin_fmaf(x, k2, -v.m) - log2_s) * kLn2;
 }
 
-template <typename T>
-__device__ __forceinline__ void lp_finish(const LpArgs& a, int64_t m, Lse v) {
-    const int64_t c = a.token_bits == 64 ? ((const int64_t*)a.tokens)[m] : (int64_t)((const int32_t*)a.tokens)[m];
-    const bool real = c >= 0 && c < a.V;
-    lp_write(a, m, v, real ? to_f32(((const T*)a.logits)[m * a.ld + c]) : 0.0f, real);
+__device__ __forceinline__ void lp_write(const LpArgs& a, int64_t m, Lse v, float x, bool real, float k2) {
+    const float log2_s = log2f(v.s);
+    const bool none = v.s == 0.0f;   // every logit is -inf
+    a.lse[m] = none ? -INFINITY : (v.m + log2_s) * kLn2;
+    a.entropy[m] = none ? 0.0f : (log2_s - v.t / v.s) * kLn2;
+    a.logp[m] = real ? lp_of(v, log2_s, x, k2) : 0.0f;
 }
+
+// The row's token, whether there is one, and its logit.
+template <typename T>
+struct RowToken {
+    float x = 0.0f;
+    bool real = false;
+
+    __device__ __forceinline__ RowToken(const LpArgs& a, int64_t m) {
+        if (m >= a.T) return;
+        const int64_t c = a.token_bits == 64 ? ((const int64_t*)a.tokens)[m] : (int64_t)((const int32_t*)a.tokens)[m];
+        real = c >= 0 && c < a.V;
+        x = to_f32(((const T*)a.logits)[m * a.ld + (real ? c : 0)]);
+    }
+};
 
 // ------------------------------------------------------------- alternatives
 // Order of the values (negative zero counts as zero, NaN as the least), then
@@ -191,26 +241,42 @@ __device__ __forceinline__ float key_value(uint64_t key) {
 
 __device__ __forceinline__ uint32_t key_at(uint64_t key) { return 0xffffffffu - (uint32_t)key; }
 
+constexpr int kTopSets = 64;   // of four neighbouring threads each
+
 struct TopShared {
-    uint64_t best[kLpThreads];
+    uint64_t best[kTopSets];
     uint64_t bound;
     uint32_t count;
 };
 
-// The k-th largest of the threads' best keys (0: none), 0 if fewer threads
-// have one. All threads call it; clears `count`.
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp_key(uint64_t v) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, 0xf, 0xf, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, 0xf, 0xf, true);
+    return ((uint64_t)hi << 32) | lo;
+}
+
+// The k-th largest of the sets' best keys (0: none), 0 if fewer sets have one.
+// All threads call it; clears `count`. (One wave ranks 64 sets: all waves
+// ranking 256 threads took 13 of a row's 18 us.)
 __device__ __forceinline__ uint64_t top_bound(uint64_t mine, int k, TopShared& sh) {
+    static_assert(kLpMaxTop <= kTopSets, "k sets are needed for a bound that k keys reach");
+    mine = max(mine, dpp_key<0xB1>(mine));
+    mine = max(mine, dpp_key<0x4E>(mine));
     __syncthreads();   // what was shared before has been read
-    sh.best[threadIdx.x] = mine;
+    if ((threadIdx.x & 3) == 0) sh.best[threadIdx.x >> 2] = mine;
     if (threadIdx.x == 0) {
         sh.bound = 0;
         sh.count = 0;
     }
     __syncthreads();
-    int above = 0;
-#pragma unroll 8
-    for (int i = 0; i < kLpThreads; ++i) above += sh.best[i] > mine ? 1 : 0;
-    if (mine != 0 && above == k - 1) sh.bound = mine;   // keys are unique
+    if (threadIdx.x < kTopSets) {
+        const uint64_t key = sh.best[threadIdx.x];
+        int above = 0;
+#pragma unroll 16
+        for (int i = 0; i < kTopSets; ++i) above += sh.best[i] > key ? 1 : 0;
+        if (key != 0 && above == k - 1) sh.bound = key;   // keys are unique
+    }
     __syncthreads();
     return sh.bound;
 }
@@ -227,6 +293,7 @@ __device__ __forceinline__ void top_rank(const uint64_t* list, int k, const TopS
     for (int i = (int)threadIdx.x; i < n; i += kLpThreads) {
         const uint64_t key = list[i];
         int above = 0;
+#pragma unroll 8
         for (int j = 0; j < n; ++j) above += list[j] > key ? 1 : 0;
         if (above < k) out(above, key);
     }
@@ -234,54 +301,58 @@ __device__ __forceinline__ void top_rank(const uint64_t* list, int k, const TopS
 
 // --------------------------------------------------------------- forward
 // A row to tpr lanes, several rows to a workgroup (V up to a few vectors a
-// lane), or a row or a part of one to the workgroup (tpr == 256).
-template <typename T, bool TOP>
+// lane), or a row or a part of one to the workgroup (tpr == 256). U vectors of
+// a thread at a time, the next ones loaded before the current ones are used.
+template <typename T, bool TOP, bool NT, int U>
 __global__ __launch_bounds__(kLpThreads) void lp_fwd_kernel(LpArgs a) {
     constexpr int VEC = VecOf<T>::n;
     constexpr int LINE = 8 * VEC;   // elements of a line: eight lanes' vectors
-    constexpr int U = 4;
     extern __shared__ uint64_t dyn[];
-    const T* p = (const T*)a.logits;
     const float k2 = a.scale * kLog2e;
-    const int64_t limit = (a.T - 1) * a.ld + a.V;
     const int tpr = TOP ? kLpThreads : a.tpr;
     const int t = (int)threadIdx.x & (tpr - 1), g = (int)threadIdx.x / tpr;
-    const int64_t item = (int64_t)blockIdx.x * (kLpThreads / tpr) + g;   // (row, part)
-    const int64_t m = item / a.parts, part = item - m * a.parts;
-    const bool on = m < a.T;
-    const int64_t row = on ? m * a.ld : 0;
-    const int64_t c0 = part * a.part_len, end = on ? min(c0 + a.part_len, a.V) : 0;
+    const uint32_t item = blockIdx.x * (uint32_t)(kLpThreads / tpr) + (uint32_t)g;   // (row, part)
+    const uint32_t m = item / (uint32_t)a.parts, part = item - m * (uint32_t)a.parts;
+    const RowPart<T> r((const T*)a.logits, m, part, a);
     float* line_max = (float*)dyn;
     Lse v = lse_none();
-    for (int64_t c = c0 + (int64_t)t * VEC; c - (int64_t)t * VEC < end; c += (int64_t)U * tpr * VEC) {
-        u32x4 raw[U];
+    const int step = tpr * VEC;
+    int base = r.first;   // the row's first lane's place: the same for all its lanes
+    u32x4 next[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) raw[u] = logits_raw<T>(p, row, c + (int64_t)u * tpr * VEC, end, limit);
+    for (int u = 0; u < U; ++u) next[u] = r.template load<NT>(base + t * VEC + u * step);
+    const RowToken<T> token(a, m);
+    for (; base < r.end; base += U * step) {
+        u32x4 now[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t cu = c + (int64_t)u * tpr * VEC;
-            if (cu - (int64_t)t * VEC >= end) continue;   // for all lanes of the row
+            now[u] = next[u];
+            next[u] = r.template load<NT>(base + t * VEC + (U + u) * step);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int b = base + u * step, e = b + t * VEC;
+            if (b >= r.end) continue;
             float x[VEC];
-            logits_at<T>(raw[u], p, row, cu, end, x);
+            unpack16<T>(now[u], x);
+            if (b < r.lo || b + step > r.hi) {   // a vector of some lane is not whole
+                if (!r.whole(e)) r.elements(e, x);
+            }
             float mv = lse_add<VEC>(v, x, k2);
             if constexpr (TOP) {
                 mv = lanes_max8(mv);
-                if ((t & 7) == 0 && cu < end) line_max[(cu - c0) / LINE] = mv;
+                if ((t & 7) == 0 && e < r.end) line_max[(uint32_t)(e - r.first) / LINE] = mv;
             }
         }
     }
-    v = lse_lanes(v, tpr >= 64 ? 64 : tpr, k2);
-    if (tpr == kLpThreads) {
-        __shared__ Lse red[kLpThreads / 64];
-        if ((t & 63) == 0) red[t >> 6] = v;
-        __syncthreads();
-        v = lse_join(lse_join(red[0], red[1], k2), lse_join(red[2], red[3], k2), k2);
-    }
-    if (t == 0 && on) {
+    __shared__ Lse red[kLpThreads / 64];
+    if (tpr == kLpThreads) v = lse_group(v, red);
+    else v = lse_lanes(v, tpr);
+    if (t == 0 && m < a.T) {
         if (a.parts == 1) {
-            lp_finish<T>(a, m, v);
+            lp_write(a, m, v, token.x, token.real, k2);
         } else {
-            float* to = a.part + item * 4;
+            float* to = a.part + (int64_t)item * 4;
             to[0] = v.m;
             to[1] = v.s;
             to[2] = v.t;
@@ -291,47 +362,58 @@ __global__ __launch_bounds__(kLpThreads) void lp_fwd_kernel(LpArgs a) {
         __shared__ TopShared sh;
         __shared__ uint64_t lines[kLpMaxTop];
         const int k = a.top;
-        const int n_lines = (int)((end - c0 + LINE - 1) / LINE);
-        uint64_t* list = dyn + (a.part_len / LINE + 2) / 2;   // behind the lines' maxima
+        // (none of a row's last part whose places end before it)
+        const int n_lines = (max(r.end - r.first, 0) + LINE - 1) / LINE;
+        uint64_t* list = dyn + (a.part_len / LINE + 1) / 2;   // behind the lines' maxima
         // the k best lines: each thread has every 256th
         uint64_t best = 0;
+#pragma unroll 4
         for (int i = (int)threadIdx.x; i < n_lines; i += kLpThreads) best = max(best, top_key(line_max[i], (uint32_t)i));
         uint64_t bound = top_bound(best, k, sh);
+#pragma unroll 4
         for (int i = (int)threadIdx.x; i < n_lines; i += kLpThreads)
             top_keep(top_key(line_max[i], (uint32_t)i), bound, list, sh);
         if (threadIdx.x < kLpMaxTop) lines[threadIdx.x] = 0;
         top_rank(list, k, sh, [&](int place, uint64_t key) { lines[place] = key; });
         __syncthreads();
-        // their elements, a vector to a lane: 32 lines at a time
-        uint64_t key[kLpMaxTop / 32][VEC];
-        best = 0;
+        // their elements, a vector to a lane, 32 lines at a time, packed: their
+        // keys would take the registers of two more waves
+        constexpr int H = kLpMaxTop / 32;
+        int place[H];
+        u32x4 raw[H];
 #pragma unroll
-        for (int h = 0; h < kLpMaxTop / 32; ++h) {
+        for (int h = 0; h < H; ++h) {
             const int at = h * 32 + ((int)threadIdx.x >> 3);
             const uint64_t line = at < k ? lines[at] : 0;
-            const int64_t c = c0 + (int64_t)key_at(line) * LINE + ((int)threadIdx.x & 7) * VEC;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                key[h][i] = line != 0 && c + i < end ? top_key(to_f32(p[row + c + i]), (uint32_t)(c + i)) : 0;
-                best = max(best, key[h][i]);
-            }
+            place[h] = line == 0 ? -1 : r.first + (int)key_at(line) * LINE + ((int)threadIdx.x & 7) * VEC;
+            if (place[h] >= 0) raw[h] = r.template load<false>(place[h]);
         }
+        const auto each = [&](auto&& f) {
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                if (place[h] < 0) continue;
+                float x[VEC];
+                unpack16<T>(raw[h], x);
+                if (!r.whole(place[h])) r.elements(place[h], x);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (r.in_row(place[h], i)) f(top_key(x[i], (uint32_t)(place[h] + i - r.skew)));
+            }
+        };
+        best = 0;
+        each([&](uint64_t key) { best = max(best, key); });
         bound = top_bound(best, k, sh);
-#pragma unroll
-        for (int h = 0; h < kLpMaxTop / 32; ++h)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) top_keep(key[h][i], bound, list, sh);
+        each([&](uint64_t key) { top_keep(key, bound, list, sh); });
         top_rank(list, k, sh, [&](int place, uint64_t best_key) {
             if (a.parts > 1) {
-                a.part_top[item * k + place] = best_key;
+                a.part_top[(int64_t)item * k + place] = best_key;
             } else {
-                const float log_s = logf(v.s);
-                a.top_tokens[m * k + place] = key_at(best_key);
-                a.top_logp[m * k + place] = v.s == 0.0f ? -INFINITY : (key_value(best_key) - v.m) * a.scale - log_s;
+                a.top_tokens[(int64_t)m * k + place] = key_at(best_key);
+                a.top_logp[(int64_t)m * k + place] = lp_of(v, log2f(v.s), key_value(best_key), k2);
             }
         });
         // a part of fewer than k elements
-        if (a.parts > 1 && (int)threadIdx.x < k && threadIdx.x >= sh.count) a.part_top[item * k + threadIdx.x] = 0;
+        if (a.parts > 1 && (int)threadIdx.x < k && threadIdx.x >= sh.count) a.part_top[(int64_t)item * k + threadIdx.x] = 0;
     }
 }
 
@@ -342,16 +424,14 @@ __global__ __launch_bounds__(kLpThreads) void lp_join_kernel(LpArgs a) {
     const int64_t m = blockIdx.x;
     const int t = (int)threadIdx.x;
     const float k2 = a.scale * kLog2e;
+    const RowToken<T> token(a, m);
     Lse v = lse_none();
     if (t < a.parts) {
         const float* from = a.part + (m * a.parts + t) * 4;
         v = {from[0], from[1], from[2]};
     }
-    v = lse_lanes(v, 64, k2);
-    if ((t & 63) == 0) red[t >> 6] = v;
-    __syncthreads();
-    v = lse_join(lse_join(red[0], red[1], k2), lse_join(red[2], red[3], k2), k2);
-    if (t == 0) lp_finish<T>(a, m, v);
+    v = lse_group(v, red);
+    if (t == 0) lp_write(a, m, v, token.x, token.real, k2);
     if constexpr (TOP) {
         extern __shared__ uint64_t list[];
         __shared__ TopShared sh;
@@ -361,64 +441,71 @@ __global__ __launch_bounds__(kLpThreads) void lp_join_kernel(LpArgs a) {
         for (int i = t; i < n; i += kLpThreads) best = max(best, keys[i]);
         const uint64_t bound = top_bound(best, k, sh);
         for (int i = t; i < n; i += kLpThreads) top_keep(keys[i], bound, list, sh);
-        const float log_s = logf(v.s);
+        const float log2_s = log2f(v.s);
         top_rank(list, k, sh, [&](int place, uint64_t key) {
             a.top_tokens[m * k + place] = key_at(key);
-            a.top_logp[m * k + place] = v.s == 0.0f ? -INFINITY : (key_value(key) - v.m) * a.scale - log_s;
+            a.top_logp[m * k + place] = lp_of(v, log2_s, key_value(key), k2);
         });
     }
 }
 
 // -------------------------------------------------------------- backward
-// Items as in the forward. A row without an upstream gradient is not read.
+// A tile of kLpBwdVecs vectors a thread of one row (or, of short rows, all of
+// several): neighbouring workgroups read and write neighbouring memory. A row
+// without an upstream gradient counts as zeros.
 template <typename T>
 __global__ __launch_bounds__(kLpThreads) void lp_bwd_kernel(LpArgs a) {
     constexpr int VEC = VecOf<T>::n;
-    constexpr int U = 4;
-    const T* p = (const T*)a.logits;
-    T* out = (T*)a.dlogits;
-    const int64_t limit = (a.T - 1) * a.ld + a.V;
+    constexpr int U = kLpBwdVecs;
     const int tpr = a.tpr;
     const int t = (int)threadIdx.x & (tpr - 1), g = (int)threadIdx.x / tpr;
-    const int64_t item = (int64_t)blockIdx.x * (kLpThreads / tpr) + g;
-    const int64_t m = item / a.parts, part = item - m * a.parts;
+    const uint32_t item = blockIdx.x * (uint32_t)(kLpThreads / tpr) + (uint32_t)g;
+    const uint32_t m = item / (uint32_t)a.parts, part = item - m * (uint32_t)a.parts;
     if (m >= a.T) return;
-    const int64_t row = m * a.ld, to = m * a.ldd;
-    const int64_t c0 = part * a.part_len, end = min(c0 + a.part_len, a.V);
+    const RowPart<T> r((const T*)a.logits, m, part, a);
+    T* out = (T*)a.dlogits + (int64_t)m * a.ldd - r.skew;   // place 0
+    const int e0 = r.first + t * VEC;
+    u32x4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u] = r.template load<false>(e0 + u * tpr * VEC);
     const int64_t token = a.token_bits == 64 ? ((const int64_t*)a.tokens)[m] : (int64_t)((const int32_t*)a.tokens)[m];
     const bool real = token >= 0 && token < a.V;
+    const int at = real ? (int)token + r.skew : -VEC;
     const float lse = a.lse[m], h = a.entropy[m];
     const float up = real && a.dlogp ? a.dlogp[m] : 0.0f;
     const float ue = a.dentropy ? a.dentropy[m] : 0.0f;
-    if ((up == 0.0f && ue == 0.0f) || lse == -INFINITY) {
-        const float zero[VEC] = {};
-        for (int64_t c = c0 + (int64_t)t * VEC; c < end; c += (int64_t)tpr * VEC) store_part<T>(out, to, c, end, zero);
-        return;
-    }
+    const bool dead = (up == 0.0f && ue == 0.0f) || lse == -INFINITY;
     // dx = -scale p (up + ue (z - lse + h)), and scale up more at the token
     const float base = -a.scale * (up + ue * h), slope = -a.scale * ue;
-    for (int64_t c = c0 + (int64_t)t * VEC; c < end; c += (int64_t)U * tpr * VEC) {
-        u32x4 raw[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) raw[u] = logits_raw<T>(p, row, c + (int64_t)u * tpr * VEC, end, limit);
+    for (int u = 0; u < U; ++u) {
+        const int e = e0 + u * tpr * VEC;
+        if (e >= r.end) break;
+        const bool whole = r.whole(e);
+        float x[VEC];
+        unpack16<T>(raw[u], x);
+        if (!whole) r.elements(e, x);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t cu = c + (int64_t)u * tpr * VEC;
-            if (cu >= end) continue;
-            float x[VEC];
-            logits_at<T>(raw[u], p, row, cu, end, x);
+        for (int i = 0; i < VEC; ++i) {
+            const float z = __builtin_fmaf(x[i], a.scale, -lse);
+            const float p = __builtin_amdgcn_exp2f(z * kLog2e);
+            x[i] = p * __builtin_fmaf(fmaxf(z, -1e30f), slope, base);
+        }
+        if ((uint32_t)(at - e) < (uint32_t)VEC) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float z = __builtin_fmaf(x[i], a.scale, -lse);
-                const float e = __builtin_amdgcn_exp2f(z * kLog2e);
-                x[i] = e * __builtin_fmaf(fmaxf(z, -1e30f), slope, base);
-            }
-            if (real && (uint64_t)(token - cu) < (uint64_t)VEC) {
+            for (int i = 0; i < VEC; ++i)
+                if (at == e + i) x[i] = __builtin_fmaf(a.scale, up, x[i]);
+        }
+        if (dead) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    if (token == cu + i) x[i] = __builtin_fmaf(a.scale, up, x[i]);
-            }
-            store_part<T>(out, to, cu, end, x);
+            for (int i = 0; i < VEC; ++i) x[i] = 0.0f;
+        }
+        if (whole) {
+            *(u32x4_m*)(out + e) = pack16<T>(x);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (r.in_row(e, i)) out[e + i] = dyt::from_f32<T>(x[i]);
         }
     }
 }

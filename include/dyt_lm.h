@@ -114,10 +114,12 @@ int dyt_embed_backward(const void* dy, int64_t lddy, const void* tokens, void* d
  * V). tokens: [T] of `token_bits` (32 or 64); one outside [0, V) (an ignored
  * place) has logp = 0 and no gradient of it. logp, entropy, lse, dlogp,
  * dentropy: [T] float32. scale (an inverse temperature): positive and finite.
- * V is at most 2^26, T 2^31 - 1.
+ * V is at most 2^26 (with alternatives 2^23), T 2^31 - 1.
  *
- * A logit of -inf is a masked place: p = 0 and gradient 0. A row of nothing
- * else has lse = -inf, logp = -inf, entropy 0 and gradient 0. A NaN or +inf
+ * A logit of -inf, or with scale x below -2.35e38 (float32's range as a power of
+ * two: the lowest float32 and bfloat16 values), is a masked place: p = 0 and
+ * gradient 0. A row of nothing else has lse = -inf, logp = -inf, entropy 0 and
+ * gradient 0. A NaN or +inf
  * makes its row's results NaN.
  *
  * top_logp, top_tokens: [T, top] (top 0: NULL), the log probabilities

@@ -113,7 +113,10 @@ class LogProb:
 
     def __init__(self, logits, tokens, scale=1.0):
         x = d(logits)
-        self.x, self.scale = x, scale
+        self.raw, self.scale = x, scale
+        # beyond float32 as a power of two: masked, as -inf
+        x = x.masked_fill(x * scale < -3.402823466e38 * math.log(2), -math.inf)
+        self.x = x
         T, V = x.shape
         self.t, self.real = _real(tokens, V)
         m = x.amax(1, keepdim=True)
@@ -152,7 +155,8 @@ class LogProb:
         self._finite("entropy", entropy, self.entropy, self.rel * (1 + 2 * self.away) + 6 * U * (ls + self.away))
 
     def check_top(self, k, top_logp, top_tokens):
-        value, place = torch.sort(self.x, dim=1, descending=True, stable=True)
+        place = torch.sort(self.raw, dim=1, descending=True, stable=True).indices
+        value = self.x.gather(1, place)
         assert torch.equal(top_tokens.cpu(), place[:, :k]), "top_tokens"
         # from the maximum: next to a logit of -3.4e38 float64 keeps no digit of log s
         want = (value[:, :k] - self.top) * self.scale - self.log_s.masked_fill(self.none, 0).view(-1, 1)
