@@ -7,10 +7,15 @@ void adamw_launch8(const AdamArgs& a, int pdt, int gdt, bool master, unsigned gr
     adamw_types(pdt, gdt, [&](auto* p, auto* g) {
         using TP = std::remove_pointer_t<decltype(p)>;
         using TG = std::remove_pointer_t<decltype(g)>;
+        const auto run = [&](auto with_master) {
+            constexpr bool MASTER = decltype(with_master)::value;
+            if (a.seeded) adamw8_kernel<TP, TG, MASTER, true><<<grid, kAdamThreads, 0, s>>>(a);
+            else adamw8_kernel<TP, TG, MASTER, false><<<grid, kAdamThreads, 0, s>>>(a);
+        };
         if constexpr (!std::is_same_v<TP, float>) {
-            if (master) return adamw8_kernel<TP, TG, true><<<grid, kAdamThreads, 0, s>>>(a);
+            if (master) return run(std::true_type{});
         }
-        adamw8_kernel<TP, TG, false><<<grid, kAdamThreads, 0, s>>>(a);
+        run(std::false_type{});
     });
 }
 

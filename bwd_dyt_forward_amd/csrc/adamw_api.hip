@@ -40,7 +40,7 @@ void add(std::vector<Span>& spans, const void* p, int64_t bytes, bool written) {
 // Launches in batches of kAdamTensors tensors that `pick` takes; returns
 // whether there were any.
 template <typename Pick, typename Launch>
-bool in_batches(AdamArgs& a, int64_t count, Pick&& pick, Launch&& launch) {
+bool in_batches(AdamArgs& a, int64_t count, int64_t chunk, Pick&& pick, Launch&& launch) {
     uint32_t grid = 0;
     bool any = false;
     a.count = 0;
@@ -55,7 +55,7 @@ bool in_batches(AdamArgs& a, int64_t count, Pick&& pick, Launch&& launch) {
     for (int64_t i = 0; i < count; ++i) {
         AdamTensor t{};
         if (!pick(i, t) || t.n == 0) continue;
-        const int64_t need = (t.n + kAdamChunk - 1) / kAdamChunk;
+        const int64_t need = (t.n + chunk - 1) / chunk;
         if (a.count == kAdamTensors || grid + need > kMaxGrid) flush();
         t.first = grid;
         a.t[a.count++] = t;
@@ -100,8 +100,11 @@ int adamw_step(const dyt_adamw_tensor* list, int64_t count, const dyt_adamw_opti
         add(spans, t.sq_scale, blocks * 4, true);
         add(spans, t.master, t.n * 4, true);
     }
+    int64_t bytes = 0;
+    for (const Span& t : spans) bytes += (int64_t)(t.hi - t.lo);
     if (!apart(spans)) return DYT_ERR_INVALID_ARG;
     AdamArgs a{};
+    const bool stream_past = bytes >= ((int64_t)256 << 20);   // the last-level cache
     a.seeded = o->seeded; a.seed = o->seed;
     a.beta1 = (float)o->beta1; a.one_beta1 = (float)(1.0 - o->beta1);
     a.beta2 = (float)o->beta2; a.one_beta2 = (float)(1.0 - o->beta2);
@@ -110,7 +113,7 @@ int adamw_step(const dyt_adamw_tensor* list, int64_t count, const dyt_adamw_opti
     a.step = o->step; a.lr_dev = o->lr_dev; a.step_dev = o->step_dev; a.grad_scale = o->grad_scale;
     a.keep = (float)(1.0 - o->lr * o->weight_decay);
     a.rate = (float)(o->lr / -std::expm1((double)o->step * a.log_beta1));
-    a.inv_corr2 = (float)(1.0 / -std::expm1((double)o->step * a.log_beta2));
+    a.root_corr2 = (float)(1.0 / std::sqrt(-std::expm1((double)o->step * a.log_beta2)));
     // the types of a parameter, its gradient and whether it has a master: a kernel each
     bool any = false;
     for (int pdt : {DYT_F32, DYT_BF16, DYT_F16})
@@ -118,7 +121,7 @@ int adamw_step(const dyt_adamw_tensor* list, int64_t count, const dyt_adamw_opti
             for (int master = 0; master < (pdt == DYT_F32 ? 1 : 2); ++master) {
                 const int gdt = own ? pdt : DYT_F32;
                 any |= in_batches(
-                    a, count,
+                    a, count, bits8 ? kAdamChunk8 : kAdamChunk,
                     [&](int64_t i, AdamTensor& t) {
                         const dyt_adamw_tensor& x = list[i];
                         if (x.param_dtype != pdt || x.grad_dtype != gdt || (x.master != nullptr) != (master != 0)) return false;
@@ -127,7 +130,7 @@ int adamw_step(const dyt_adamw_tensor* list, int64_t count, const dyt_adamw_opti
                     },
                     [&](unsigned grid) {
                         if (bits8) adamw_launch8(a, pdt, gdt, master != 0, grid, (hipStream_t)stream);
-                        else adamw_launch32(a, pdt, gdt, master != 0, grid, (hipStream_t)stream);
+                        else adamw_launch32(a, pdt, gdt, master != 0, stream_past, grid, (hipStream_t)stream);
                     });
             }
     return any ? hip_status() : DYT_OK;
@@ -151,7 +154,7 @@ int adamw_values(const dyt_adamw_codes* list, int64_t count, int vdt, void* stre
     if (!apart(spans)) return DYT_ERR_INVALID_ARG;
     AdamArgs a{};
     const bool any = in_batches(
-        a, count,
+        a, count, kAdamChunk8,
         [&](int64_t i, AdamTensor& t) {
             const dyt_adamw_codes& x = list[i];
             t.param = x.values;

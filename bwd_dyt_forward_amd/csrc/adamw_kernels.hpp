@@ -25,13 +25,17 @@
 // the bits, where a NaN is larger than all else: a NaN spoils its block.
 #pragma once
 
+#include <type_traits>
+
 #include "ln_kernels.hpp"
 
 namespace dytb {
 
 constexpr int kAdamThreads = 256;
 constexpr int kAdamTensors = 44;          // of a launch: their table stays under 4 KB of arguments
-constexpr int kAdamChunk = 8192;          // elements of a workgroup, a multiple of 256 x 8
+// Elements of a workgroup: what 256 threads hold at once; with 8-bit states,
+// where the arithmetic is the bound, more (8,192 for 2,048: 798 us for 815).
+constexpr int kAdamChunk = 2048, kAdamChunk8 = 8192;
 constexpr int kAdamBlock = 128;
 constexpr float kScaleTiny = 0x1p-126f;
 
@@ -54,7 +58,7 @@ struct AdamArgs {
     int32_t seeded;
     uint32_t seed;
     float beta1, one_beta1, beta2, one_beta2, eps;
-    float keep, rate, inv_corr2;  // 1 - lr weight_decay, lr / (1 - beta1^step), 1 / (1 - beta2^step)
+    float keep, rate, root_corr2; // 1 - lr weight_decay, lr / (1 - beta1^step), 1 / sqrt(1 - beta2^step)
     double lr, weight_decay;      // for those three where the device holds lr or step
     double log_beta1, log_beta2;
     int64_t step;
@@ -84,18 +88,44 @@ __device__ __forceinline__ uint32_t next_random(uint32_t x) {
     return x ^ (x << 5);
 }
 
+// 8 and 16 bytes at an element's (or a code's) alignment.
+typedef uint32_t u32x2_m __attribute__((ext_vector_type(2), aligned(1)));
+
+template <bool NT>
+__device__ __forceinline__ u32x4 load16(const void* p) {
+    if constexpr (NT) return __builtin_nontemporal_load((const u32x4_m*)p);
+    else return *(const u32x4_m*)p;
+}
+
+template <bool NT>
+__device__ __forceinline__ u32x2 load8(const void* p) {
+    if constexpr (NT) return __builtin_nontemporal_load((const u32x2_m*)p);
+    else return *(const u32x2_m*)p;
+}
+
+template <bool NT>
+__device__ __forceinline__ void store16(void* p, u32x4 v) {
+    if constexpr (NT) __builtin_nontemporal_store((u32x4_m)v, (u32x4_m*)p);
+    else *(u32x4_m*)p = v;
+}
+
+template <bool NT>
+__device__ __forceinline__ void store8(void* p, u32x2 v) {
+    if constexpr (NT) __builtin_nontemporal_store((u32x2_m)v, (u32x2_m*)p);
+    else *(u32x2_m*)p = v;
+}
+
 // V elements at p, n of them there (zeros for the rest).
-template <typename T, int V>
+template <typename T, int V, int NT = 0>
 __device__ __forceinline__ void load_some(const T* p, int64_t n, float* out) {
     if (n >= V) {
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < V; i += 4) unpack16<T>(*(const u32x4_m*)(p + i), out + i);
+            for (int i = 0; i < V; i += 4) unpack16<T>(load16<(NT & 2) != 0>(p + i), out + i);
         } else if constexpr (V == 8) {
-            unpack16<T>(*(const u32x4_m*)p, out);
+            unpack16<T>(load16<(NT & 2) != 0>(p), out);
         } else {
-            uint32_t w[2];
-            __builtin_memcpy(w, p, 8);
+            const u32x2 w = load8<(NT & 2) != 0>(p);
 #pragma unroll
             for (int i = 0; i < 4; ++i) out[i] = to_f32(T{(uint16_t)(w[i / 2] >> (16 * (i % 2)))});
         }
@@ -105,17 +135,16 @@ __device__ __forceinline__ void load_some(const T* p, int64_t n, float* out) {
     }
 }
 
-template <typename T, int V>
+template <typename T, int V, int NT = 0>
 __device__ __forceinline__ void store_some(T* p, int64_t n, const float* v) {
     if (n >= V) {
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < V; i += 4) *(u32x4_m*)(p + i) = pack16<T>(v + i);
+            for (int i = 0; i < V; i += 4) store16<(NT & 1) != 0>(p + i, pack16<T>(v + i));
         } else if constexpr (V == 8) {
-            *(u32x4_m*)p = pack16<T>(v);
+            store16<(NT & 1) != 0>(p, pack16<T>(v));
         } else {
-            const uint32_t w[2] = {pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])};
-            __builtin_memcpy(p, w, 8);
+            store8<(NT & 1) != 0>(p, u32x2{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])});
         }
     } else {
 #pragma unroll
@@ -125,64 +154,79 @@ __device__ __forceinline__ void store_some(T* p, int64_t n, const float* v) {
 }
 
 struct AdamStep {
-    float beta1, one_beta1, beta2, one_beta2, eps, keep, rate, inv_corr2;
+    float beta1, one_beta1, beta2, one_beta2, eps, keep, rate, root_corr2;
 
-    __device__ __forceinline__ void operator()(float& p, float& m, float& v, float g) const {
+    // Returns the second moment's root.
+    __device__ __forceinline__ float operator()(float& p, float& m, float& v, float g) const {
         m = __builtin_fmaf(m, beta1, g * one_beta1);
         v = __builtin_fmaf(v, beta2, g * g * one_beta2);
-        const float root = __builtin_amdgcn_sqrtf(v * inv_corr2) + eps;
-        p = __builtin_fmaf(p, keep, -rate * m * __builtin_amdgcn_rcpf(root));
+        const float root = __builtin_amdgcn_sqrtf(v);
+        const float inv = __builtin_amdgcn_rcpf(__builtin_fmaf(root, root_corr2, eps));
+        p = __builtin_fmaf(-rate * m, inv, p * keep);
+        return root;
     }
 };
 
 __device__ __forceinline__ AdamStep adam_step(const AdamArgs& a) {
-    AdamStep r{a.beta1, a.one_beta1, a.beta2, a.one_beta2, a.eps, a.keep, a.rate, a.inv_corr2};
+    AdamStep r{a.beta1, a.one_beta1, a.beta2, a.one_beta2, a.eps, a.keep, a.rate, a.root_corr2};
     if (a.lr_dev || a.step_dev) {
         const double step = (double)(a.step_dev ? *a.step_dev : a.step);
         const double lr = a.lr_dev ? (double)*a.lr_dev : a.lr;
         r.keep = (float)(1.0 - lr * a.weight_decay);
         r.rate = (float)(lr / -expm1(step * a.log_beta1));
-        r.inv_corr2 = (float)(1.0 / -expm1(step * a.log_beta2));
+        r.root_corr2 = (float)(1.0 / sqrt(-expm1(step * a.log_beta2)));
     }
     return r;
 }
 
+// The tensor of a workgroup: the last that begins at or before it, found by all
+// lanes at once.
 __device__ __forceinline__ int adam_tensor(const AdamArgs& a, uint32_t wg) {
-    int lo = 0, hi = a.count - 1;   // the last tensor that begins at or before wg
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (a.t[mid].first <= wg) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
+    static_assert(kAdamTensors <= 64, "a lane for each");
+    const int lane = (int)threadIdx.x & 63;
+    const bool before = lane < a.count && a.t[min(lane, kAdamTensors - 1)].first <= wg;
+    return __builtin_amdgcn_readfirstlane(__popcll(__ballot(before)) - 1);
 }
 
-// float32 states, four elements a lane: every access of a wave is one run.
-template <typename TP, typename TG, bool MASTER>
+// float32 states, four elements a lane: every access of a wave is one run. All
+// loads of a workgroup's chunk are on their way before its first store (the
+// compiler may not move one before a store: the tensors could be the same).
+// STREAM: nontemporal loads and stores where the tensors pass the last-level
+// cache. 332 million bfloat16 parameters with masters: 1,803 us with a loop of
+// two loads ahead, 1,754 so, 1,653 nontemporal (5.6 TB/s of eight streams).
+template <typename TP, typename TG, bool MASTER, bool STREAM>
 __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamArgs) {
+    constexpr int NT = STREAM ? 3 : 0, V = 4, U = kAdamChunk / (kAdamThreads * V);
     const AdamArgs& a = adam_args();
-    constexpr int V = 4;
     const AdamTensor& x = a.t[adam_tensor(a, blockIdx.x)];
+    const int64_t base = (int64_t)(blockIdx.x - x.first) * kAdamChunk + (int64_t)threadIdx.x * V;
     const AdamStep step = adam_step(a);
     const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
-    const int64_t base = (int64_t)(blockIdx.x - x.first) * kAdamChunk;
-    const int64_t end = min(base + kAdamChunk, x.n);
-#pragma unroll 2
-    for (int64_t i = base + (int64_t)threadIdx.x * V; i < end; i += kAdamThreads * V) {
-        const int64_t n = end - i;
-        float p[V], g[V], m[V], v[V];
-        if constexpr (MASTER) load_some<float, V>(x.master + i, n, p);
-        else load_some<TP, V>((const TP*)x.param + i, n, p);
-        load_some<TG, V>((const TG*)x.grad + i, n, g);
-        load_some<float, V>((const float*)x.avg + i, n, m);
-        load_some<float, V>((const float*)x.sq + i, n, v);
+    // whole: no element past the end, known for the workgroup
+    const auto run = [&](auto whole) {
+        float p[U][V], g[U][V], m[U][V], v[U][V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) step(p[j], m[j], v[j], g[j] * gs);
-        if constexpr (MASTER) store_some<float, V>(x.master + i, n, p);
-        store_some<TP, V>((TP*)x.param + i, n, p);
-        store_some<float, V>((float*)x.avg + i, n, m);
-        store_some<float, V>((float*)x.sq + i, n, v);
-    }
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = base + u * kAdamThreads * V, n = decltype(whole)::value ? V : x.n - i;
+            if constexpr (MASTER) load_some<float, V, NT>(x.master + i, n, p[u]);
+            else load_some<TP, V, NT>((const TP*)x.param + i, n, p[u]);
+            load_some<TG, V, NT>((const TG*)x.grad + i, n, g[u]);
+            load_some<float, V, NT>((const float*)x.avg + i, n, m[u]);
+            load_some<float, V, NT>((const float*)x.sq + i, n, v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = base + u * kAdamThreads * V, n = decltype(whole)::value ? V : x.n - i;
+#pragma unroll
+            for (int j = 0; j < V; ++j) step(p[u][j], m[u][j], v[u][j], g[u][j] * gs);
+            if constexpr (MASTER) store_some<float, V, NT>(x.master + i, n, p[u]);
+            store_some<TP, V, NT>((TP*)x.param + i, n, p[u]);
+            store_some<float, V, NT>((float*)x.avg + i, n, m[u]);
+            store_some<float, V, NT>((float*)x.sq + i, n, v[u]);
+        }
+    };
+    if ((int64_t)(blockIdx.x - x.first + 1) * kAdamChunk <= x.n) run(std::true_type{});
+    else run(std::false_type{});
 }
 
 // Maximum of the bits over aligned groups of 16 lanes.
@@ -199,57 +243,59 @@ __device__ __forceinline__ float block_max(uint32_t v) {
     return __uint_as_float(max(v, __float_as_uint(kScaleTiny)));
 }
 
-// The codes' values. c: the code as a float.
-__device__ __forceinline__ float avg_value(float c, float a) { return c * __builtin_fabsf(c) * (1.0f / 16129.0f) * a; }
-
-__device__ __forceinline__ float sq_value(float c, float a) {
-    const float r = c * c * (1.0f / 65025.0f);   // c * c is exact
-    return r * r * a;
-}
-
 __device__ __forceinline__ int avg_code(uint32_t w, int i) { return (int)(int8_t)(w >> (8 * i)); }
 
-// The code for y = 127^2 |m| / a: of the two around it the upper one if the
-// random number is below y's place between them.
+__device__ __forceinline__ float sq_code(uint32_t w, int i) { return (float)((w >> (8 * i)) & 255u); }
+
+// Of the two codes around y = 127^2 |m| / a the upper one if the random number,
+// (random + 0.5) / 65536, is below y's place between them. (y may pass 127^2 by
+// a rounding.)
 __device__ __forceinline__ float avg_round(float y, float random) {
     const float low = fminf(__builtin_floorf(__builtin_amdgcn_sqrtf(y)), 126.0f);
     const float above = __builtin_fmaf(-low, low, y);
-    return random * __builtin_fmaf(2.0f, low, 1.0f) < above ? low + 1.0f : low;
+    const float gap = __builtin_fmaf(0x1p-15f, low, 0x1p-16f);   // (2 low + 1) / 65536
+    return random * gap < above ? low + 1.0f : low;
 }
 
-// The same for y = 255^4 v / a; a moment that is not zero gets no code 0.
-__device__ __forceinline__ float sq_round(float y, float random, bool some) {
-    const float low = fminf(__builtin_floorf(__builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(y))), 254.0f);
+// The same for y = z^2 = 255^4 v / a; a moment that is not zero gets no code 0.
+__device__ __forceinline__ float sq_round(float z, float random) {
+    const float low = fminf(__builtin_floorf(__builtin_amdgcn_sqrtf(z)), 254.0f);
     const float l2 = low * low;
-    const float above = __builtin_fmaf(-l2, l2, y);
-    const float gap = __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(4.0f, low, 6.0f), low, 4.0f), low, 1.0f);
+    const float above = __builtin_fmaf(-l2, l2, z * z);
+    // (4 low^3 + 6 low^2 + 4 low + 1) / 65536
+    const float gap = __builtin_fmaf(__builtin_fmaf(__builtin_fmaf(0x1p-14f, low, 0x1.8p-14f), low, 0x1p-14f), low, 0x1p-16f);
     const float c = random * gap < above ? low + 1.0f : low;
-    return some ? fmaxf(c, 1.0f) : c;
+    return fmaxf(c, __builtin_amdgcn_fmed3f(z * 0x1p100f, 0.0f, 1.0f));
 }
 
-template <typename TP, typename TG, bool MASTER>
+// Bound by arithmetic: about 66 operations and four of a quarter of the rate an
+// element. Hence one root of v for the step and for its code, factors of a block
+// in front of the loop over its elements (a lane's eight), codes of both signs
+// as c + 128 until they are packed, and an instance of its own for rounding at
+// random.
+template <typename TP, typename TG, bool MASTER, bool SEEDED>
 __global__ __launch_bounds__(kAdamThreads) void adamw8_kernel(AdamArgs) {
+    constexpr int V = 8, NT = 2;   // nontemporal loads, see adamw_kernel
     const AdamArgs& a = adam_args();
-    constexpr int V = 8;
     const AdamTensor& x = a.t[adam_tensor(a, blockIdx.x)];
     const AdamStep step = adam_step(a);
     const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
-    const int64_t base = (int64_t)(blockIdx.x - x.first) * kAdamChunk;
-    const int64_t end = min(base + kAdamChunk, x.n);
+    const int64_t base = (int64_t)(blockIdx.x - x.first) * kAdamChunk8;
+    const int64_t end = min(base + kAdamChunk8, x.n);
     const uint32_t at_step = (uint32_t)(a.step_dev ? *a.step_dev : a.step);
     const uint32_t key = mix32(a.seed + 0x9E3779B9u * at_step) ^ mix32(0x85EBCA77u * (x.number + 1u));
-    // whole blocks: the lanes past the end take part in the maxima
+    // whole blocks: the lanes past the end take part in the maxima, with zeros
     const int64_t stop = base + (end - base + kAdamBlock - 1) / kAdamBlock * kAdamBlock;
     for (int64_t i = base + (int64_t)threadIdx.x * V; i < stop; i += kAdamThreads * V) {
         const int64_t n = end - i;
-        float p[V], g[V], m[V], v[V];
-        uint32_t cm[2] = {0, 0}, cv[2] = {0, 0};
-        if constexpr (MASTER) load_some<float, V>(x.master + i, n, p);
-        else load_some<TP, V>((const TP*)x.param + i, n, p);
-        load_some<TG, V>((const TG*)x.grad + i, n, g);
+        float p[V], g[V], m[V], root[V];
+        u32x2 cm = {0, 0}, cv = {0, 0};
+        if constexpr (MASTER) load_some<float, V, NT>(x.master + i, n, p);
+        else load_some<TP, V, NT>((const TP*)x.param + i, n, p);
+        load_some<TG, V, NT>((const TG*)x.grad + i, n, g);
         if (n >= V) {
-            __builtin_memcpy(cm, (const uint8_t*)x.avg + i, 8);
-            __builtin_memcpy(cv, (const uint8_t*)x.sq + i, 8);
+            cm = load8<(NT & 2) != 0>((const uint8_t*)x.avg + i);
+            cv = load8<(NT & 2) != 0>((const uint8_t*)x.sq + i);
         } else {
 #pragma unroll
             for (int j = 0; j < V; ++j)
@@ -258,37 +304,37 @@ __global__ __launch_bounds__(kAdamThreads) void adamw8_kernel(AdamArgs) {
                     cv[j / 4] |= (uint32_t)((const uint8_t*)x.sq)[i + j] << (8 * (j % 4));
                 }
         }
-        const float am = x.avg_scale[i / kAdamBlock], av = x.sq_scale[i / kAdamBlock];
+        const float am = x.avg_scale[i / kAdamBlock] * (1.0f / 16129.0f);
+        const float av = __builtin_amdgcn_sqrtf(x.sq_scale[i / kAdamBlock]) * (1.0f / 65025.0f);
         uint32_t top_m = 0, top_v = 0;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            m[j] = avg_value((float)avg_code(cm[j / 4], j % 4), am);
-            v[j] = sq_value((float)((cv[j / 4] >> (8 * (j % 4))) & 255u), av);
-            step(p[j], m[j], v[j], g[j] * gs);
-            if (j < n) {
-                top_m = max(top_m, __float_as_uint(m[j]) & 0x7fffffffu);
-                top_v = max(top_v, __float_as_uint(v[j]) & 0x7fffffffu);
-            }
+            const float c = (float)avg_code(cm[j / 4], j % 4), c2 = sq_code(cv[j / 4], j % 4);
+            m[j] = c * __builtin_fabsf(c) * am;
+            const float r = c2 * c2 * av;
+            float v = r * r;
+            root[j] = step(p[j], m[j], v, g[j] * gs);
+            top_m = max(top_m, __float_as_uint(m[j]) & 0x7fffffffu);
+            top_v = max(top_v, __float_as_uint(v));
         }
         const float new_m = block_max(top_m), new_v = block_max(top_v);
-        const float inv_m = 1.0f / new_m, inv_v = 1.0f / new_v;
+        const float inv_m = __builtin_amdgcn_rcpf(new_m), inv_v = 65025.0f * __builtin_amdgcn_rsqf(new_v);
         const uint64_t vec = (uint64_t)i / V;
-        uint32_t r = mix32((uint32_t)vec ^ key ^ mix32((uint32_t)(vec >> 32))) | 1u;
-        cm[0] = cm[1] = cv[0] = cv[1] = 0;
+        uint32_t r = SEEDED ? mix32((uint32_t)vec ^ key ^ mix32((uint32_t)(vec >> 32))) | 1u : 0u;
+        cm = cv = u32x2{0, 0};
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            if (j) r = next_random(r);
-            const float r1 = a.seeded ? ((float)(r >> 16) + 0.5f) * 0x1p-16f : 0.5f;
-            const float r2 = a.seeded ? ((float)(r & 0xffffu) + 0.5f) * 0x1p-16f : 0.5f;
-            float c = avg_round(__builtin_fabsf(m[j]) * inv_m * 16129.0f, r1);
-            c = m[j] < 0.0f && c > 0.0f ? 256.0f - c : c;   // two's complement
-            cm[j / 4] = __builtin_amdgcn_cvt_pk_u8_f32(c, j % 4, cm[j / 4]);
-            c = sq_round(v[j] * inv_v * 4228250625.0f, r2, v[j] > 0.0f);
-            cv[j / 4] = __builtin_amdgcn_cvt_pk_u8_f32(c, j % 4, cv[j / 4]);
+            if (SEEDED && j) r = next_random(r);
+            const float r1 = SEEDED ? (float)(r >> 16) + 0.5f : 32768.0f;
+            const float r2 = SEEDED ? (float)(r & 0xffffu) + 0.5f : 32768.0f;
+            const float c = avg_round(__builtin_fabsf(m[j]) * inv_m * 16129.0f, r1);
+            cm[j / 4] = __builtin_amdgcn_cvt_pk_u8_f32(__builtin_copysignf(c, m[j]) + 128.0f, j % 4, cm[j / 4]);
+            cv[j / 4] = __builtin_amdgcn_cvt_pk_u8_f32(sq_round(root[j] * inv_v, r2), j % 4, cv[j / 4]);
         }
+        cm ^= 0x80808080u;   // c + 128 to two's complement
         if (n >= V) {
-            __builtin_memcpy((uint8_t*)x.avg + i, cm, 8);
-            __builtin_memcpy((uint8_t*)x.sq + i, cv, 8);
+            store8<(NT & 1) != 0>((uint8_t*)x.avg + i, cm);
+            store8<(NT & 1) != 0>((uint8_t*)x.sq + i, cv);
         } else {
 #pragma unroll
             for (int j = 0; j < V; ++j)
@@ -301,8 +347,8 @@ __global__ __launch_bounds__(kAdamThreads) void adamw8_kernel(AdamArgs) {
             x.avg_scale[i / kAdamBlock] = new_m;
             x.sq_scale[i / kAdamBlock] = new_v;
         }
-        if constexpr (MASTER) store_some<float, V>(x.master + i, n, p);
-        store_some<TP, V>((TP*)x.param + i, n, p);
+        if constexpr (MASTER) store_some<float, V, NT>(x.master + i, n, p);
+        store_some<TP, V, NT>((TP*)x.param + i, n, p);
     }
 }
 
@@ -313,8 +359,8 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_values_kernel(AdamArgs) {
     const AdamArgs& a = adam_args();
     constexpr int V = 8;
     const AdamTensor& x = a.t[adam_tensor(a, blockIdx.x)];
-    const int64_t base = (int64_t)(blockIdx.x - x.first) * kAdamChunk;
-    const int64_t end = min(base + kAdamChunk, x.n);
+    const int64_t base = (int64_t)(blockIdx.x - x.first) * kAdamChunk8;
+    const int64_t end = min(base + kAdamChunk8, x.n);
 #pragma unroll 2
     for (int64_t i = base + (int64_t)threadIdx.x * V; i < end; i += kAdamThreads * V) {
         const int64_t n = end - i;
@@ -329,9 +375,11 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_values_kernel(AdamArgs) {
         const float s = x.avg_scale[i / kAdamBlock];
         float v[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            v[j] = x.number ? sq_value((float)((c[j / 4] >> (8 * (j % 4))) & 255u), s)
-                            : avg_value((float)avg_code(c[j / 4], j % 4), s);
+        for (int j = 0; j < V; ++j) {
+            const float cm = (float)avg_code(c[j / 4], j % 4), cv = sq_code(c[j / 4], j % 4);
+            const float r = cv * cv * (1.0f / 65025.0f);   // the square is exact
+            v[j] = x.number ? r * r * s : cm * __builtin_fabsf(cm) * (1.0f / 16129.0f) * s;
+        }
         store_some<TO, V>((TO*)x.param + i, n, v);
     }
 }

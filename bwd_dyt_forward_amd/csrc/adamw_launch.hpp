@@ -7,8 +7,9 @@
 
 namespace dytb {
 
-// One launch of `grid` workgroups over tensors of the same types.
-void adamw_launch32(const AdamArgs&, int param_dtype, int grad_dtype, bool master, unsigned grid, hipStream_t);
+// One launch of `grid` workgroups over tensors of the same types; stream_past:
+// the call's tensors do not fit the last-level cache.
+void adamw_launch32(const AdamArgs&, int param_dtype, int grad_dtype, bool master, bool stream_past, unsigned grid, hipStream_t);
 void adamw_launch8(const AdamArgs&, int param_dtype, int grad_dtype, bool master, unsigned grid, hipStream_t);
 
 // Calls f with the types of a parameter and its gradient (the parameter's or

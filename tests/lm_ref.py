@@ -239,9 +239,9 @@ def adamw(p, g, m, v, *, lr, betas, eps, weight_decay, step, grad_scale=1.0):
     root = (v1 / c2).sqrt() + eps
     update = lr / c1 * m1 / root
     p1 = p - lr * weight_decay * p - update
-    # the root: half of v's error, its factor, the square root and the sum; its
+    # the root: half of v's error, the square root, its factor and the sum; its
     # reciprocal; two products
-    ep = 3 * U * p.abs() + 1.01 * (update.abs() * (2.5 * U + 2 * U + EXP2 + 2 * U + EXP2 + 4 * U) + lr / c1 * em / root)
+    ep = 3 * U * p.abs() + 1.01 * (update.abs() * (2.5 * U + EXP2 + 2 * U + 2 * U + EXP2 + 4 * U) + lr / c1 * em / root)
     return (p1, m1, v1), (ep + U * p1.abs(), em, ev)
 
 
@@ -253,9 +253,12 @@ def check_codes(name, codes, scale, want, off, power, most, random):
     offs = torch.nn.functional.pad(off, (0, -n % 128)).view(-1, 128).amax(1)
     check(f"{name} scale", scale, blocks, offs + U * blocks)
     at = want.abs() / _each(scale, n)
-    # the place of the value, as the codes count; the quotient has three roundings
-    # and the powers around it a few more, at the size of the value
-    slack = (off / _each(scale, n) + 12 * U * at) * most ** power + 1e-30
+    # the place of the value, as the codes count: for the first moment the
+    # scale's reciprocal (2 U) and two products; for the second the moment's root
+    # (2 U) times the scale's reciprocal root (2 U and its factor, U), squared
+    # (6 U twice and one more). Then the distance from the lower code and the
+    # random number's product with the gap
+    slack = (off / _each(scale, n) + 16 * U * at) * most ** power + 1e-30
     y = at * most ** power
     low = torch.floor(y.clamp(min=0).pow(1 / power) + 1e-9).clamp(0, most - 1)
     low = torch.where(low.pow(power) > y, low - 1, low).clamp(min=0)

@@ -75,11 +75,13 @@ class Tensors:
             if self.bits8:
                 n = p.numel()
                 one, two = dice(n, i, seed, step) if seed is not None else (torch.full((n,), 0.5).double(),) * 2
-                # the codes' values before the step: five roundings of what the betas keep
+                # the codes' values before the step, of which the betas keep a share: the
+                # scale's factor and two products (4 U), or the root of the scale (2 U), its
+                # factor (2 U) and a product, squared (5 U twice and one more)
                 b1, b2 = {**KW, **kw}["betas"]
-                check_codes("avg", self.m[i], self.sm[i], want[1], off[1] + 5 * U * b1 * m.abs(), 2, 127, one)
+                check_codes("avg", self.m[i], self.sm[i], want[1], off[1] + 4 * U * b1 * m.abs(), 2, 127, one)
                 assert ((d(self.m[i]) * want[1]) >= 0).all()
-                check_codes("sq", self.v[i], self.sv[i], want[2], off[2] + 6 * U * b2 * v, 4, 255, two)
+                check_codes("sq", self.v[i], self.sv[i], want[2], off[2] + 11 * U * b2 * v, 4, 255, two)
             else:
                 check("avg", self.m[i], want[1], off[1] + U * want[1].abs())
                 check("sq", self.v[i], want[2], off[2] + U * want[2].abs())
