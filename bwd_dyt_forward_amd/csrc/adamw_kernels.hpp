@@ -258,8 +258,9 @@ __device__ __forceinline__ float avg_round(float y, float random) {
 }
 
 // The same for y = z^2 = 255^4 v / a; a moment that is not zero gets no code 0.
+// (256, where a rounding takes y past 255^4, becomes 255 as it is packed.)
 __device__ __forceinline__ float sq_round(float z, float random) {
-    const float low = fminf(__builtin_floorf(__builtin_amdgcn_sqrtf(z)), 254.0f);
+    const float low = __builtin_floorf(__builtin_amdgcn_sqrtf(z));
     const float l2 = low * low;
     const float above = __builtin_fmaf(-l2, l2, z * z);
     // (4 low^3 + 6 low^2 + 4 low + 1) / 65536

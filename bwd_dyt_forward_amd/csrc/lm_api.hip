@@ -74,7 +74,7 @@ RmsPlan rms_plan(int64_t M, int64_t N, int xdt) {
     const int64_t bytes = dtype_size(xdt);
     p.cfg = rms_config(M, N, (int)bytes, true);
     const int64_t need = (M + ln_groups(p.cfg) - 1) / ln_groups(p.cfg);
-    const int64_t most = p.cfg.threads > 512 || p.cfg.threads == 0 ? 256 : 1024;
+    const int64_t most = p.cfg.threads > 512 || p.cfg.threads == 0 ? 256 : 1024;   // what a CU holds of them
     const int64_t cap = std::min(most, std::max<int64_t>(256, M * bytes / 89 / 128 * 128));
     p.grid = (int)std::min(need, cap);
     p.pitch = (N + 31) / 32 * 32;
@@ -112,7 +112,7 @@ int rms_forward(const void* x, int64_t ldx, const void* r, const void* gamma, vo
     RmsArgs a{};
     a.x = x; a.r = res ? r : nullptr; a.h = h; a.y = y; a.gamma = gamma; a.rstd = stats; a.scales = stats;
     a.ldx = ldx; a.ldy = ldy; a.M = M; a.N = (int32_t)N; a.pdt = pdt; a.eps = eps; a.group = group;
-    a.traffic = ln_traffic(M, N, (int)sx, res);
+    a.traffic = rms_traffic(M, N, (int)sx, res ? 4 : 2);
     const LnConfig cfg = rms_config(M, N, (int)sx, false);
     with_type(xdt, [&](auto* t) {
         using T = std::remove_pointer_t<decltype(t)>;
@@ -153,9 +153,11 @@ int rms_backward(const void* x, int64_t ldx, const void* dy, int64_t lddy, const
     a.rstd = const_cast<float*>(rstd); a.part = (float*)ws;
     a.ldx = ldx; a.lddy = lddy; a.ldy = lddx; a.M = M; a.N = (int32_t)N; a.pdt = pdt; a.pitch = p.pitch;
     a.traffic = ln_traffic(M, N, (int)sx, true);
+    int e = DYT_OK;
     with_type(xdt, [&](auto* t) {
-        rms_launch_backward<std::remove_pointer_t<decltype(t)>>(p.cfg, p.grid, a, s);
+        e = rms_launch_backward<std::remove_pointer_t<decltype(t)>>(p.cfg, p.grid, a, s);
     });
+    if (e) return e;
     rms_finish(a.part, a.pitch, p.grid, N, dgamma, pdt, s);
     return hip_status();
 }

@@ -91,7 +91,7 @@ __global__ __launch_bounds__(LnShape<TPR>::threads) void rms_fwd_kernel(RmsArgs 
     using S = LnShape<TPR>;
     constexpr int VEC = VecOf<T>::n;
     constexpr int E = V * VEC;
-    constexpr bool HOLD = E <= 32;
+    constexpr bool HOLD = E <= 32, AHEAD = TPR >= 256 && V <= 2;
     const int t = (int)threadIdx.x % TPR;
     const int g = (int)threadIdx.x / TPR;
     const int N = a.N;
@@ -101,19 +101,35 @@ __global__ __launch_bounds__(LnShape<TPR>::threads) void rms_fwd_kernel(RmsArgs 
     const int64_t limit = (a.M - 1) * a.ldx + N;
     const int64_t step = (int64_t)gridDim.x * S::groups * U;
     const T* xp = (const T*)a.x;
-    int buf = 0;
-    for (int64_t base = (int64_t)blockIdx.x * S::groups * U; base < a.M; base += step, buf ^= 1) {
+    struct Raw {
+        u32x4 x[V], r[RES ? V : 1];
+    };
+    const auto load = [&](int64_t m, Raw& w) {
+        const bool on = m < a.M;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = (t + v * TPR) * VEC;
+            w.x[v] = load_raw<T, NT>(xp, m * a.ldx, c, N, limit, on);
+            if constexpr (RES) w.r[v] = load_raw<T, NT>((const T*)a.r, m * a.ldx, c, N, limit, on);
+        }
+    };
+    Raw next[AHEAD ? U : 1];
+    int64_t base = (int64_t)blockIdx.x * S::groups * U;
+    if constexpr (AHEAD) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) load(base + u * S::groups + g, next[u]);
+    }
+    for (int buf = 0; base < a.M; base += step, buf ^= 1) {
         float x[U][E], ss[U];
-        u32x4 raw[U][V], rres[U][RES ? V : 1];
+        Raw now[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t m = base + u * S::groups + g;
+            if constexpr (AHEAD) now[u] = next[u];
+            else load(base + u * S::groups + g, now[u]);
+        }
+        if constexpr (AHEAD) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = (t + v * TPR) * VEC;
-                raw[u][v] = load_raw<T, NT>(xp, m * a.ldx, c, N, limit, m < a.M);
-                if constexpr (RES) rres[u][v] = load_raw<T, NT>((const T*)a.r, m * a.ldx, c, N, limit, m < a.M);
-            }
+            for (int u = 0; u < U; ++u) load(base + step + u * S::groups + g, next[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -123,10 +139,10 @@ __global__ __launch_bounds__(LnShape<TPR>::threads) void rms_fwd_kernel(RmsArgs 
             for (int v = 0; v < V; ++v) {
                 const int c = (t + v * TPR) * VEC;
                 float* xv = &x[u][v * VEC];
-                unpack_raw<T>(raw[u][v], xp, m * a.ldx, c, N, limit, m < a.M, xv);
+                unpack_raw<T>(now[u].x[v], xp, m * a.ldx, c, N, limit, m < a.M, xv);
                 if constexpr (RES) {
                     float r[VEC];
-                    unpack_raw<T>(rres[u][v], (const T*)a.r, m * a.ldx, c, N, limit, m < a.M, r);
+                    unpack_raw<T>(now[u].r[v], (const T*)a.r, m * a.ldx, c, N, limit, m < a.M, r);
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) r[i] += xv[i];
                     if (m < a.M) store_vec<T, NT>((T*)a.h, m * a.ldx, c, N, r);
@@ -286,21 +302,21 @@ __global__ __launch_bounds__(kLongThreads) void rms_fwd_long_kernel(RmsArgs a) {
 }
 
 // As the layer norm's backward: U row groups at a time, the next rows' vectors
-// loaded before the current ones are reduced (AHEAD), a thread's columns of
-// dgamma summed in registers over the rows its workgroup walks, one float32
-// row of sums per workgroup. LEAN (rows of 1,024 threads, 128 registers a
-// lane): x and dy stay packed and gamma is read again for each row.
-template <typename T, int TPR, int TH, int V, int U, bool RES, int NT, bool LEAN = (TPR >= 1024)>
+// loaded before the current ones are reduced (AHEAD; four vectors a thread would
+// spill for it), a thread's columns of dgamma summed in
+// registers over the rows its workgroup walks, one float32 row of sums per
+// workgroup.
+template <typename T, int TPR, int TH, int V, int U, bool RES, int NT>
 __global__ __launch_bounds__(TH) void rms_bwd_kernel(RmsArgs a) {
     using S = LnShape<TPR, TH>;
     constexpr int VEC = VecOf<T>::n;
     constexpr int E = V * VEC;
-    constexpr bool AHEAD = !LEAN;
+    constexpr bool AHEAD = E < 32;
     const int t = (int)threadIdx.x % TPR;
     const int g = (int)threadIdx.x / TPR;
     const int N = a.N;
-    float gm[LEAN ? VEC : E], ag[E];
-    if constexpr (!LEAN) load_columns<V, VEC, TPR>(a.gamma, a.pdt, t, N, gm);
+    float gm[E], ag[E];
+    load_columns<V, VEC, TPR>(a.gamma, a.pdt, t, N, gm);
 #pragma unroll
     for (int e = 0; e < E; ++e) ag[e] = 0.0f;
     const float inv_n = 1.0f / (float)N;
@@ -308,7 +324,7 @@ __global__ __launch_bounds__(TH) void rms_bwd_kernel(RmsArgs a) {
     const int64_t limit_dy = (a.M - 1) * a.lddy + N;
     const int64_t step = (int64_t)gridDim.x * S::groups * U;
     struct Raw {
-        u32x4 x[V], dy[V], res[RES && !LEAN ? V : 1];
+        u32x4 x[V], dy[V], res[RES ? V : 1];
         float rs;
     };
     const auto load = [&](int64_t m, Raw& w) {
@@ -318,11 +334,11 @@ __global__ __launch_bounds__(TH) void rms_bwd_kernel(RmsArgs a) {
             const int c = (t + v * TPR) * VEC;
             w.x[v] = load_raw<T, NT>((const T*)a.x, m * a.ldx, c, N, limit, on);
             w.dy[v] = load_raw<T, NT>((const T*)a.dy, m * a.lddy, c, N, limit_dy, on);
-            if constexpr (RES && !LEAN) w.res[v] = load_raw<T, NT>((const T*)a.dres, m * a.ldx, c, N, limit, on);
+            if constexpr (RES) w.res[v] = load_raw<T, NT>((const T*)a.dres, m * a.ldx, c, N, limit, on);
         }
         w.rs = a.rstd[on ? m : 0];
     };
-    Raw next[U];
+    Raw next[AHEAD ? U : 1];
     int64_t base = (int64_t)blockIdx.x * S::groups * U;
     if constexpr (AHEAD) {
 #pragma unroll
@@ -339,29 +355,23 @@ __global__ __launch_bounds__(TH) void rms_bwd_kernel(RmsArgs a) {
 #pragma unroll
             for (int u = 0; u < U; ++u) load(base + step + u * S::groups + g, next[u]);
         }
-        float n[U][LEAN ? VEC : E], dy[U][LEAN ? VEC : E], s[U];
-        // n and dy of vector v
-        const auto open = [&](int u, int v, float* nv, float* dv) {
-            const int64_t m = base + u * S::groups + g;
-            const int c = (t + v * TPR) * VEC;
-            unpack_raw<T>(now[u].x[v], (const T*)a.x, m * a.ldx, c, N, limit, m < a.M, nv);
-            unpack_raw<T>(now[u].dy[v], (const T*)a.dy, m * a.lddy, c, N, limit_dy, m < a.M, dv);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) nv[i] *= now[u].rs;
-        };
+        float n[U][E], dy[U][E], s[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            const int64_t m = base + u * S::groups + g;
             s[u] = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int at = LEAN ? 0 : v * VEC;
-                if constexpr (LEAN) load_params<VEC>(a.gamma, a.pdt, (t + v * TPR) * VEC, N, gm);
-                open(u, v, &n[u][at], &dy[u][at]);
+                const int c = (t + v * TPR) * VEC;
+                unpack_raw<T>(now[u].x[v], (const T*)a.x, m * a.ldx, c, N, limit, m < a.M, &n[u][v * VEC]);
+                unpack_raw<T>(now[u].dy[v], (const T*)a.dy, m * a.lddy, c, N, limit_dy, m < a.M, &dy[u][v * VEC]);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    const float dn = dy[u][at + i] * n[u][at + i];
-                    ag[v * VEC + i] += dn;
-                    s[u] = __builtin_fmaf(dn, gm[at + i], s[u]);
+                    const int e = v * VEC + i;
+                    n[u][e] *= now[u].rs;
+                    const float dn = dy[u][e] * n[u][e];
+                    ag[e] += dn;
+                    s[u] = __builtin_fmaf(dn, gm[e], s[u]);
                 }
             }
             s[u] = lanes_sum<S::L>(s[u]);
@@ -389,17 +399,20 @@ __global__ __launch_bounds__(TH) void rms_bwd_kernel(RmsArgs a) {
             for (int v = 0; v < V; ++v) {
                 float o[VEC], res[VEC];
                 const int c = (t + v * TPR) * VEC;
-                const int at = LEAN ? 0 : v * VEC;
-                if constexpr (LEAN) {
-                    load_params<VEC>(a.gamma, a.pdt, c, N, gm);
-                    open(u, v, n[u], dy[u]);
-                    if constexpr (RES) load_vec<T>((const T*)a.dres, m * a.ldx, c, N, res);
-                } else if constexpr (RES) {
-                    unpack_raw<T>(now[u].res[v], (const T*)a.dres, m * a.ldx, c, N, limit, true, res);
+                if constexpr (RES) unpack_raw<T>(now[u].res[v], (const T*)a.dres, m * a.ldx, c, N, limit, true, res);
+                if constexpr (!AHEAD && VEC > 4 && !RES) {
+                    // The compiler spills 132 bytes for the floats kept over the reduction (with
+                    // the residual it keeps them, and spills 100 for this): unpacked again.
+                    asm volatile("" : "+v"(now[u].x[v]), "+v"(now[u].dy[v]));
+                    unpack_raw<T>(now[u].x[v], (const T*)a.x, m * a.ldx, c, N, limit, true, &n[u][v * VEC]);
+                    unpack_raw<T>(now[u].dy[v], (const T*)a.dy, m * a.lddy, c, N, limit_dy, true, &dy[u][v * VEC]);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) n[u][v * VEC + i] *= now[u].rs;
                 }
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    o[i] = now[u].rs * (dy[u][at + i] * gm[at + i] - n[u][at + i] * c2);
+                    const int e = v * VEC + i;
+                    o[i] = now[u].rs * (dy[u][e] * gm[e] - n[u][e] * c2);
                     if constexpr (RES) o[i] += res[i];
                 }
                 store_vec<T, NT>((T*)a.y, m * a.ldy, c, N, o);
@@ -431,6 +444,111 @@ __global__ __launch_bounds__(TH) void rms_bwd_kernel(RmsArgs a) {
         for (int i = 0; i < VEC; ++i) {
             const int c = (t + v * TPR) * VEC + i;
             if (c < N) row[c] = ag[v * VEC + i];
+        }
+}
+
+// Rows of up to 32,768 columns: a workgroup's 1,024 threads have 128 registers
+// each, which hold a row's vectors, packed, and the next one's where those are few
+// (AHEAD; of 4 vectors they would spill: 4,096 x 30,000 bfloat16 484 us, without
+// 294); the columns' sums live in LDS (128 KB), four floats of a thread at a time so
+// that neighbouring lanes meet no bank twice, and gamma is read again for each row.
+constexpr int kWideColumns = 32768;
+
+template <typename T, int V, bool RES, int NT>
+__global__ __launch_bounds__(kLongThreads) void rms_bwd_wide_kernel(RmsArgs a) {
+    constexpr int VEC = VecOf<T>::n, Q = VEC / 4;
+    static_assert(V * VEC * kLongThreads <= kWideColumns, "the sums' LDS");
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    extern __shared__ f32x4 sums[];   // [V * Q][kLongThreads]
+    __shared__ float red[2][kLongThreads / 64];
+    int t = (int)threadIdx.x;
+    const int N = a.N;
+    const int64_t limit = (a.M - 1) * a.ldx + N, limit_dy = (a.M - 1) * a.lddy + N;
+#pragma unroll
+    for (int q = 0; q < V * Q; ++q) sums[q * kLongThreads + t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 next_x[V], next_dy[V];
+    const auto load = [&](int64_t m) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = (t + v * kLongThreads) * VEC;
+            next_x[v] = load_raw<T, NT>((const T*)a.x, m * a.ldx, c, N, limit, m < a.M);
+            next_dy[v] = load_raw<T, NT>((const T*)a.dy, m * a.lddy, c, N, limit_dy, m < a.M);
+        }
+    };
+    constexpr bool AHEAD = VEC * V <= 16;
+    if constexpr (AHEAD) load(blockIdx.x);
+    int buf = 0;
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, buf ^= 1) {
+        u32x4 x[V], dy[V];
+        if constexpr (!AHEAD) load(m);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            x[v] = next_x[v];
+            dy[v] = next_dy[v];
+        }
+        if constexpr (AHEAD) load(m + gridDim.x);
+        // What depends on a thread's columns only (gamma, addresses, which of them are
+        // in the row) would be kept from row to row, in registers that are not there.
+        asm volatile("" : "+v"(t));
+        const float rs = a.rstd[m];
+        float s = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = (t + v * kLongThreads) * VEC;
+            float gm[VEC], n[VEC], d[VEC];
+            load_params<VEC>(a.gamma, a.pdt, c, N, gm);
+            unpack_raw<T>(x[v], (const T*)a.x, m * a.ldx, c, N, limit, true, n);
+            unpack_raw<T>(dy[v], (const T*)a.dy, m * a.lddy, c, N, limit_dy, true, d);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) s = __builtin_fmaf(d[i] * (n[i] * rs), gm[i], s);
+            __builtin_amdgcn_sched_barrier(0);   // one vector's floats at a time
+        }
+        s = lanes_sum<64>(s);
+        if ((t & 63) == 0) red[buf][t >> 6] = s;
+        __syncthreads();
+        s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kLongThreads / 64; ++k) s += red[buf][k];
+        const float c2 = s / (float)N;
+        // nor is there room for the floats of the first walk: unpack them again
+        asm volatile("" : "+v"(t));
+#pragma unroll
+        for (int v = 0; v < V; ++v) asm volatile("" : "+v"(x[v]), "+v"(dy[v]));
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = (t + v * kLongThreads) * VEC;
+            float gm[VEC], n[VEC], d[VEC], res[VEC], o[VEC];
+            if constexpr (RES) load_vec<T>((const T*)a.dres, m * a.ldx, c, N, res);
+            load_params<VEC>(a.gamma, a.pdt, c, N, gm);
+            unpack_raw<T>(x[v], (const T*)a.x, m * a.ldx, c, N, limit, true, n);
+            unpack_raw<T>(dy[v], (const T*)a.dy, m * a.lddy, c, N, limit_dy, true, d);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                f32x4 w = sums[(v * Q + q) * kLongThreads + t];
+#pragma unroll
+                for (int i = 4 * q; i < 4 * q + 4; ++i) {
+                    n[i] *= rs;
+                    w[i % 4] = __builtin_fmaf(d[i], n[i], w[i % 4]);
+                    o[i] = rs * (d[i] * gm[i] - n[i] * c2);
+                    if constexpr (RES) o[i] += res[i];
+                }
+                sums[(v * Q + q) * kLongThreads + t] = w;
+            }
+            store_vec<T, NT>((T*)a.y, m * a.ldy, c, N, o);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    float* row = a.part + (int64_t)blockIdx.x * a.pitch;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const f32x4 w = sums[(v * Q + q) * kLongThreads + t];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = (t + v * kLongThreads) * VEC + 4 * q + i;
+                if (c < N) row[c] = w[i];
+            }
         }
 }
 

@@ -7,21 +7,34 @@
 
 namespace dytb {
 
-// The layer norm's shapes, and wider rows: without a mean and its second sum
-// 1,024 threads hold 8 vectors each in the forward and 4 in the backward.
+// The layer norm's shapes, and wider rows. Without a mean and its second sum
+// 1,024 threads hold 8 vectors each in the forward, and 512 threads, which may
+// have twice the registers of 1,024, hold 4 in the backward (8,192 x 16,384
+// bfloat16 172 us, with the residual 196; of 1,024 threads that spill 289 and 422).
+// Beyond, the backward keeps the columns' sums in LDS up to kWideColumns.
 inline LnConfig rms_config(int64_t M, int64_t N, int elem_bytes, bool backward) {
-    LnConfig c = ln_config(M, N, elem_bytes, backward);
+    const LnConfig c = ln_config(M, N, elem_bytes, backward);
     const int vec = 16 / elem_bytes;
     const int64_t nv = (N + vec - 1) / vec;
-    if (c.threads == 0 && M * N >= vec) {
-        if (nv <= 4096) return {1024, 4, 1024};
-        if (!backward && nv <= 8192) return {1024, 8, 1024};
-    }
-    return c;
+    if (M * N < vec || nv <= 1024 || (!backward && nv <= 2048)) return c;
+    if (!backward) return nv <= 4096 ? LnConfig{1024, 4, 1024} : nv <= 8192 ? LnConfig{1024, 8, 1024} : LnConfig{0, 0, 0};
+    if (nv <= 2048) return {512, 4, 512};
+    if (nv <= 4096) return {1024, 4, 1024};
+    return N <= kWideColumns ? LnConfig{1024, 8, 1024} : LnConfig{0, 0, 0};
+}
+
+// Cache hints of the forward: nontemporal stores from 64 MB tensors on, and
+// nontemporal loads where its two or four tensors together pass the last-level
+// cache (8,192 x 4,096 bfloat16 with the residual: 48 us for 50 with such stores
+// only; 100,003 x 255 float32, which stays under it, 44 us with and 40 without).
+inline int rms_traffic(int64_t M, int64_t N, int elem_bytes, int tensors) {
+    const int64_t bytes = M * N * elem_bytes;
+    if (bytes * tensors >= ((int64_t)256 << 20)) return 2;
+    return bytes >= ((int64_t)64 << 20) ? 1 : 0;
 }
 
 template <typename T> void rms_launch_forward(const LnConfig&, const RmsArgs&, hipStream_t);
 template <typename T> void rms_launch_forward_q8(const LnConfig&, const RmsArgs&, hipStream_t);
-template <typename T> void rms_launch_backward(const LnConfig&, int grid, const RmsArgs&, hipStream_t);
+template <typename T> int rms_launch_backward(const LnConfig&, int grid, const RmsArgs&, hipStream_t);   // dyt_status
 
 }  // namespace dytb

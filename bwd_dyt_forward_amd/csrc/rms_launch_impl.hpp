@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "rms_launch.hpp"
@@ -10,8 +11,9 @@
 namespace dytb {
 
 // Workgroups of a forward launch: enough to fill 256 CUs several times over
-// and no more, since each loads gamma once for all its rows; fewer where loads
-// are nontemporal (as in the layer norm's forward).
+// and no more, since each loads gamma once for all its rows; two of 256 threads
+// per CU where the tensors do not stay in the caches (32,768 x 4,096 bfloat16: 92
+// us for 103; 131,072 x 1,024 with the residual 192 for 200).
 constexpr int kRmsGridThreads = 256 * 2048, kRmsGridThreadsFew = 256 * 512;
 
 template <typename T, bool Q8, int TPR, int V, int U>
@@ -27,10 +29,8 @@ void rms_fwd_one(const RmsArgs& a, hipStream_t s) {
     };
     // the codes are half a 16-bit row: left to the caches for what reads them next
     if constexpr (Q8) return with(std::integral_constant<int, 0>{}, kRmsGridThreads);
-    if constexpr (TPR >= 256) {
-        if (a.traffic == 2) return with(std::integral_constant<int, 2>{}, kRmsGridThreadsFew);
-    }
-    if (a.traffic) with(std::integral_constant<int, 1>{}, kRmsGridThreads);
+    if (a.traffic == 2) with(std::integral_constant<int, 2>{}, kRmsGridThreadsFew);
+    else if (a.traffic) with(std::integral_constant<int, 1>{}, kRmsGridThreadsFew);
     else with(std::integral_constant<int, 0>{}, kRmsGridThreads);
 }
 
@@ -103,7 +103,7 @@ void rms_bwd_pick(int grid, const RmsArgs& a, hipStream_t s) {
 }
 
 template <typename T>
-void rms_launch_backward(const LnConfig& c, int grid, const RmsArgs& a, hipStream_t s) {
+void rms_bwd_any(const LnConfig& c, int grid, const RmsArgs& a, hipStream_t s) {
     switch (c.threads * 16 + c.vecs) {
         case 1 * 16 + 1: return rms_bwd_pick<T, 1>(grid, a, s);
         case 2 * 16 + 1: return rms_bwd_pick<T, 2>(grid, a, s);
@@ -116,12 +116,51 @@ void rms_launch_backward(const LnConfig& c, int grid, const RmsArgs& a, hipStrea
         case 128 * 16 + 2: return rms_bwd_wide<T, 128>(c, grid, a, s);
         case 256 * 16 + 2: return rms_bwd_wide<T, 256>(c, grid, a, s);
         case 512 * 16 + 2: return rms_bwd_one<T, 512, 512, 2, 1>(grid, a, s);
-        case 1024 * 16 + 2: return rms_bwd_one<T, 1024, 1024, 2, 1>(grid, a, s);
-        case 1024 * 16 + 4: return rms_bwd_one<T, 1024, 1024, 4, 1>(grid, a, s);
+        case 512 * 16 + 4: return rms_bwd_one<T, 512, 512, 4, 1>(grid, a, s);
         default: break;
     }
     if (a.dres) rms_bwd_long_kernel<T, true><<<grid, kLongThreads, 0, s>>>(a);
     else rms_bwd_long_kernel<T, false><<<grid, kLongThreads, 0, s>>>(a);
+}
+
+// The wide rows' kernel, with more than the default 64 KB of dynamic LDS: an
+// instance is given it once per device (a microsecond of a small call otherwise).
+template <auto Kernel>
+int launch_wide(int grid, size_t lds, const RmsArgs& a, hipStream_t s) {
+    static std::atomic<uint64_t> raised{0};
+    int device = 0;
+    if (hipGetDevice(&device) != hipSuccess) return DYT_ERR_HIP;
+    const uint64_t bit = (uint64_t)1 << (device & 63);
+    if (device > 63 || !(raised.load(std::memory_order_acquire) & bit)) {
+        if (hipFuncSetAttribute((const void*)Kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                kWideColumns * sizeof(float)) != hipSuccess)
+            return DYT_ERR_HIP;
+        if (device <= 63) raised.fetch_or(bit, std::memory_order_release);
+    }
+    Kernel<<<grid, kLongThreads, lds, s>>>(a);
+    return DYT_OK;
+}
+
+template <typename T, int V>
+int rms_bwd_wide_rows(int grid, const RmsArgs& a, hipStream_t s) {
+    constexpr size_t lds = (size_t)V * VecOf<T>::n * kLongThreads * sizeof(float);
+    const bool past = a.traffic == 2;
+    if (a.dres) return past ? launch_wide<rms_bwd_wide_kernel<T, V, true, 2>>(grid, lds, a, s)
+                            : launch_wide<rms_bwd_wide_kernel<T, V, true, 0>>(grid, lds, a, s);
+    return past ? launch_wide<rms_bwd_wide_kernel<T, V, false, 2>>(grid, lds, a, s)
+                : launch_wide<rms_bwd_wide_kernel<T, V, false, 0>>(grid, lds, a, s);
+}
+
+template <typename T>
+int rms_launch_backward(const LnConfig& c, int grid, const RmsArgs& a, hipStream_t s) {
+    if (c.threads == 1024) {
+        if constexpr (sizeof(T) == 4) {
+            if (c.vecs == 8) return rms_bwd_wide_rows<T, 8>(grid, a, s);
+        }
+        return rms_bwd_wide_rows<T, 4>(grid, a, s);
+    }
+    rms_bwd_any<T>(c, grid, a, s);
+    return DYT_OK;
 }
 
 }  // namespace dytb
