@@ -188,8 +188,9 @@ class LogProbFunction(torch.autograd.Function):
         ctx.scale, ctx.shape = scale, logits.shape
         best = tuple(t.view(*tokens.shape, top) for t in best)
         ctx.mark_non_differentiable(*best)
-        # the caller may change its results, the backward needs the entropy
-        return (logp.view(tokens.shape), entropy.clone().view(tokens.shape), *best)
+        if ctx.needs_input_grad[0]:
+            entropy = entropy.clone()   # the caller may change its results, the backward needs the entropy
+        return (logp.view(tokens.shape), entropy.view(tokens.shape), *best)
 
     @staticmethod
     @once_differentiable
