@@ -153,6 +153,11 @@ int rms_backward(const void* x, int64_t ldx, const void* dy, int64_t lddy, const
     a.rstd = const_cast<float*>(rstd); a.part = (float*)ws;
     a.ldx = ldx; a.lddy = lddy; a.ldy = lddx; a.M = M; a.N = (int32_t)N; a.pdt = pdt; a.pitch = p.pitch;
     a.traffic = ln_traffic(M, N, (int)sx, true);
+    a.dgamma = dgamma;
+    if (rms_few(M, N, (int)sx)) {
+        with_type(xdt, [&](auto* t) { rms_launch_backward_few<std::remove_pointer_t<decltype(t)>>(a, s); });
+        return hip_status();
+    }
     int e = DYT_OK;
     with_type(xdt, [&](auto* t) {
         e = rms_launch_backward<std::remove_pointer_t<decltype(t)>>(p.cfg, p.grid, a, s);

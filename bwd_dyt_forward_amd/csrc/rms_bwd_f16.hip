@@ -2,5 +2,6 @@
 #include "rms_launch_impl.hpp"
 
 namespace dytb {
+template void rms_launch_backward_few<f16_t>(const RmsArgs&, hipStream_t);
 template int rms_launch_backward<f16_t>(const LnConfig&, int, const RmsArgs&, hipStream_t);
 }  // namespace dytb

@@ -32,6 +32,7 @@ struct RmsArgs {
     float* rstd;
     float* scales;        // 8-bit output: [M, groups]
     float* part;          // backward: partial rows
+    void* dgamma;         // backward of few elements
     int64_t ldx, ldy, lddy;
     int64_t M;
     int32_t N;
@@ -445,6 +446,88 @@ __global__ __launch_bounds__(TH) void rms_bwd_kernel(RmsArgs a) {
             const int c = (t + v * TPR) * VEC + i;
             if (c < N) row[c] = ag[v * VEC + i];
         }
+}
+
+// Few elements, where a second launch costs more than reading x and dy twice
+// (rms_few): the workgroups from row_wgs on sum the columns themselves, which needs
+// no row's sum. TPR threads to a row; a column's rows go to 64 groups of 4 lanes.
+template <typename T, int TPR, bool RES>
+__global__ __launch_bounds__(256) void rms_bwd_few_kernel(RmsArgs a, int row_wgs) {
+    constexpr int VEC = VecOf<T>::n, U = 8;
+    __shared__ float red[4][4 * VEC];
+    const int N = a.N, lane = (int)threadIdx.x & 63, w = (int)threadIdx.x >> 6;
+    const int64_t limit = (a.M - 1) * a.ldx + N, limit_dy = (a.M - 1) * a.lddy + N;
+    const T* x = (const T*)a.x;
+    const T* dy = (const T*)a.dy;
+    if ((int)blockIdx.x >= row_wgs) {
+        const int c = (((int)blockIdx.x - row_wgs) * 4 + ((int)threadIdx.x & 3)) * VEC;
+        float sum[VEC] = {};
+        for (int64_t base = (int)threadIdx.x >> 2; base < a.M; base += 64 * U) {
+            u32x4 rx[U], rdy[U];
+            float rs[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t m = base + u * 64;
+                rx[u] = load_raw<T, 0>(x, m * a.ldx, c, N, limit, m < a.M);
+                rdy[u] = load_raw<T, 0>(dy, m * a.lddy, c, N, limit_dy, m < a.M);
+                rs[u] = a.rstd[m < a.M ? m : 0];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t m = base + u * 64;
+                float n[VEC], d[VEC];
+                unpack_raw<T>(rx[u], x, m * a.ldx, c, N, limit, m < a.M, n);
+                unpack_raw<T>(rdy[u], dy, m * a.lddy, c, N, limit_dy, m < a.M, d);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) sum[i] = __builtin_fmaf(d[i], n[i] * rs[u], sum[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+            for (int l = 4; l < 64; l *= 2) sum[i] += __shfl_xor(sum[i], l);
+            if (lane < 4) red[w][lane * VEC + i] = sum[i];
+        }
+        __syncthreads();
+        const int i = (int)threadIdx.x, at = ((int)blockIdx.x - row_wgs) * 4 * VEC + i;
+        if (i < 4 * VEC && at < N) store_param(a.dgamma, at, a.pdt, red[0][i] + red[1][i] + red[2][i] + red[3][i]);
+        return;
+    }
+    const int t = (int)threadIdx.x % TPR;
+    const int64_t m = (int64_t)blockIdx.x * (256 / TPR) + (int)threadIdx.x / TPR;
+    const bool on = m < a.M;   // for the whole wave
+    const float rs = a.rstd[on ? m : 0];
+    float s = 0.0f;
+#pragma unroll 2
+    for (int c = t * VEC; on && c < N; c += TPR * VEC) {
+        float n[VEC], d[VEC], gm[VEC];
+        load_vec<T>(x, m * a.ldx, c, N, n);
+        load_vec<T>(dy, m * a.lddy, c, N, d);
+        load_params<VEC>(a.gamma, a.pdt, c, N, gm);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s = __builtin_fmaf(d[i] * (n[i] * rs), gm[i], s);
+    }
+    s = lanes_sum<64>(s);
+    if constexpr (TPR == 256) {
+        if (lane == 0) red[w][0] = s;
+        __syncthreads();
+        s = red[0][0] + red[1][0] + red[2][0] + red[3][0];
+    }
+    const float c2 = s / (float)N;
+#pragma unroll 2
+    for (int c = t * VEC; on && c < N; c += TPR * VEC) {
+        float n[VEC], d[VEC], gm[VEC], res[VEC], o[VEC];
+        load_vec<T>(x, m * a.ldx, c, N, n);
+        load_vec<T>(dy, m * a.lddy, c, N, d);
+        load_params<VEC>(a.gamma, a.pdt, c, N, gm);
+        if constexpr (RES) load_vec<T>((const T*)a.dres, m * a.ldx, c, N, res);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            o[i] = rs * (d[i] * gm[i] - n[i] * rs * c2);
+            if constexpr (RES) o[i] += res[i];
+        }
+        store_vec<T>((T*)a.y, m * a.ldy, c, N, o);
+    }
 }
 
 // Rows of up to 32,768 columns: a workgroup's 1,024 threads have 128 registers

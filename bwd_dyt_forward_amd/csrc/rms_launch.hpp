@@ -33,8 +33,18 @@ inline int rms_traffic(int64_t M, int64_t N, int elem_bytes, int tensors) {
     return bytes >= ((int64_t)64 << 20) ? 1 : 0;
 }
 
+// Whether the backward takes one launch (rms_bwd_few_kernel). On the device, in one
+// and in two launches: 1,024 x 64 float32 5.3 and 7.8 us, 512 x 1,024 5.7 and 8.8,
+// 64 x 8,192 10.0 and 10.9, 16 x 4,096 4.7 and 8.6, but 2,048 x 64 9.7 and 8.2,
+// 1,024 x 1,024 10.4 and 9.6, 512 x 4,096 13.8 and 12.1; the launch itself is some
+// 3 us of the calling thread.
+inline bool rms_few(int64_t M, int64_t N, int elem_bytes) {
+    return M <= 1024 && M * N <= (1 << 19) && M * N * elem_bytes >= 16;
+}
+
 template <typename T> void rms_launch_forward(const LnConfig&, const RmsArgs&, hipStream_t);
 template <typename T> void rms_launch_forward_q8(const LnConfig&, const RmsArgs&, hipStream_t);
+template <typename T> void rms_launch_backward_few(const RmsArgs&, hipStream_t);
 template <typename T> int rms_launch_backward(const LnConfig&, int grid, const RmsArgs&, hipStream_t);   // dyt_status
 
 }  // namespace dytb

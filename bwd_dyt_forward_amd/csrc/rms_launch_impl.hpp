@@ -152,6 +152,19 @@ int rms_bwd_wide_rows(int grid, const RmsArgs& a, hipStream_t s) {
 }
 
 template <typename T>
+void rms_launch_backward_few(const RmsArgs& a, hipStream_t s) {
+    constexpr int cols = 4 * VecOf<T>::n;
+    const auto with = [&](auto tpr) {
+        constexpr int TPR = decltype(tpr)::value;
+        const int rows = (int)((a.M + 256 / TPR - 1) / (256 / TPR)), grid = rows + (a.N + cols - 1) / cols;
+        if (a.dres) rms_bwd_few_kernel<T, TPR, true><<<grid, 256, 0, s>>>(a, rows);
+        else rms_bwd_few_kernel<T, TPR, false><<<grid, 256, 0, s>>>(a, rows);
+    };
+    if (a.N <= 64 * 4 * VecOf<T>::n) with(std::integral_constant<int, 64>{});
+    else with(std::integral_constant<int, 256>{});
+}
+
+template <typename T>
 int rms_launch_backward(const LnConfig& c, int grid, const RmsArgs& a, hipStream_t s) {
     if (c.threads == 1024) {
         if constexpr (sizeof(T) == 4) {

@@ -77,6 +77,20 @@ def test_many_rows(dyt, dt, M, N):
         check_rms_q8(x, gm, EPS, group, *dyt.dyt_rms_forward_q8(x, gm, EPS, group))
 
 
+@pytest.mark.parametrize("M,N", [(1024, 512), (1024, 513), (1025, 1), (1025, 3), (1025, 17), (1025, 64), (1025, 127), (1025, 200),
+                                 (1025, 500), (1100, 1000), (1030, 2047), (64, 8192), (64, 8193), (7, 70001), (1, 524288),
+                                 (1, 524289), (1024, 4), (1000, 15)])
+@pytest.mark.parametrize("dt,pdt", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16"), ("f16", "f16")])
+def test_around_the_border_of_one_launch(dyt, dt, pdt, M, N):
+    x, gm, dy, r = make(M + N, M, N, DTYPES[dt], DTYPES[pdt])
+    run_plain(dyt, x, gm, dy)
+    h, y, rstd = dyt.dyt_rms_forward_residual(x, r, gm, EPS)
+    dx, dg = dyt.dyt_rms_backward_residual(h, dy, r, rstd, gm)
+    check_rms_backward(h, dy, rstd, gm, dx, dg, dres=r)
+    again = dyt.dyt_rms_backward_residual(h, dy, r, rstd, gm)
+    assert torch.equal(dx, again[0]) and torch.equal(dg, again[1])
+
+
 @pytest.mark.parametrize("M,N", [(9000, 8192), (600, 131072)])
 def test_rows_of_large_tensors(dyt, M, N):
     """Nontemporal instances: 64 MB tensors and more; first and last rows."""
