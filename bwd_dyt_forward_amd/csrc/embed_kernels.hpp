@@ -473,6 +473,121 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs a, int sorted)
     else put_row<TW>(a, run, c, acc);
 }
 
+// Few tokens and a small dweight, in one launch in place of three: a workgroup has
+// every gridDim.x-th row (the frequent tokens are often neighbours) and 128 columns
+// (blockIdx.y), looks all tokens through, lists those of its rows in the order of
+// their places, and sums 16 threads to a token. Rows of more than kFewAlone tokens
+// are cut into 16 slices, joined in order.
+constexpr int kFewTokens = 2048, kFewRows = 64, kFewAlone = 8;
+
+template <typename TY, typename TW>
+__global__ __launch_bounds__(256) void embed_few_kernel(EmbedArgs a) {
+    constexpr int K = kFewTokens / 256, U = 8;
+    __shared__ uint32_t list[kFewTokens];     // row << 16 | place, in the order of the places
+    __shared__ uint16_t order[kFewTokens];    // the places, row by row
+    __shared__ uint32_t count[kFewRows], first[kFewRows + 1], waves[K][4];
+    __shared__ float red[16][16 * kEmbVec];
+    const int tid = (int)threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const uint64_t below = (1ull << lane) - 1;
+    const uint32_t v0 = blockIdx.x, apart = gridDim.x, none = kFewRows;
+    const int mine = (int)(((uint32_t)a.V - v0 + apart - 1) / apart);
+    uint32_t tok[K];
+    uint64_t in[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) tok[k] = k * 256 + tid < a.T ? token_at(a.tokens, a.token_bits, k * 256 + tid, a.V) : (uint32_t)a.V;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const uint32_t r = tok[k] / apart;
+        tok[k] = tok[k] < (uint32_t)a.V && tok[k] - r * apart == v0 ? r : none;
+        in[k] = __ballot(tok[k] != none);
+        if (lane == 0) waves[k][w] = (uint32_t)__popcll(in[k]);
+    }
+    if (tid < kFewRows) count[tid] = 0;
+    __syncthreads();
+    uint32_t n = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        uint32_t at = n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            at += i < w ? waves[k][i] : 0u;
+            n += waves[k][i];
+        }
+        if (tok[k] != none) {
+            list[at + (uint32_t)__popcll(in[k] & below)] = tok[k] << 16 | (uint32_t)(k * 256 + tid);
+            atomicAdd(&count[tok[k]], 1u);
+        }
+    }
+    __syncthreads();
+    // lane r, in every wave: row r's tokens and the first of them in `order`
+    const uint32_t of_row = count[lane];
+    uint32_t end = of_row;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const uint32_t o = (uint32_t)__shfl_up((int)end, d);
+        if (lane >= d) end += o;
+    }
+    if (w == 0) first[lane + 1] = end;
+    if (tid == 0) first[0] = 0;
+    for (uint64_t todo = __ballot(of_row > 0 && (lane & 3) == w); todo; todo &= todo - 1) {
+        const int r = __ffsll((unsigned long long)todo) - 1;
+        uint32_t at = (uint32_t)__shfl((int)(end - of_row), r);
+        for (uint32_t i = 0; i < n; i += 64) {
+            const uint32_t e = i + lane < n ? list[i + lane] : 0xffffffffu;
+            const uint64_t same = __ballot(e >> 16 == (uint32_t)r);
+            if (e >> 16 == (uint32_t)r) order[at + (uint32_t)__popcll(same & below)] = (uint16_t)e;
+            at += (uint32_t)__popcll(same);
+        }
+    }
+    __syncthreads();
+    const int g = tid / 16, t = tid % 16, c0 = (int)blockIdx.y * 16 * kEmbVec, c = c0 + t * kEmbVec;
+    const TY* dy = (const TY*)a.dy;
+    const int64_t limit = (a.T - 1) * a.ldy + a.D;
+    const auto sum = [&](uint32_t lo, uint32_t hi, float* acc) {
+        for (uint32_t at = lo; at < hi; at += U) {
+            RawCols<TY> raw[U];
+            int64_t from[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                from[u] = (int64_t)order[min(at + u, hi - 1)] * a.ldy;
+                raw[u] = load_raw_cols<TY>(dy, from[u], c, a.D, limit, true);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float row[kEmbVec];
+                unpack_cols<TY>(raw[u], dy, from[u], c, a.D, limit, at + u < hi, row);
+#pragma unroll
+                for (int i = 0; i < kEmbVec; ++i) acc[i] += row[i];
+            }
+        }
+    };
+    for (int r = g; r < mine; r += 16) {
+        const uint32_t lo = first[r], hi = first[r + 1];
+        if (hi - lo > kFewAlone || c >= a.D) continue;
+        float acc[kEmbVec] = {};
+        sum(lo, hi, acc);
+        if (hi > lo) put_row<TW>(a, v0 + r * apart, c, acc);
+        else if (!a.accumulate) store_cols<TW>((TW*)a.out + (int64_t)(v0 + r * apart) * a.ldw + c, a.D - c, acc);
+    }
+    for (uint64_t todo = __ballot(of_row > kFewAlone); todo; todo &= todo - 1) {   // the same in every wave
+        const int r = __ffsll((unsigned long long)todo) - 1;
+        const uint32_t lo = first[r], k = first[r + 1] - lo, per = (k + 15) / 16;
+        float acc[kEmbVec] = {};
+        sum(lo + min(g * per, k), lo + min((g + 1) * per, k), acc);
+        __syncthreads();   // the row before has been joined
+#pragma unroll
+        for (int i = 0; i < kEmbVec; ++i) red[g][t * kEmbVec + i] = acc[i];
+        __syncthreads();
+        if (tid < 16 * kEmbVec && c0 + tid < a.D) {
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s += red[i][tid];
+            TW* p = (TW*)a.out + (int64_t)(v0 + r * apart) * a.ldw + c0 + tid;
+            *p = dyt::from_f32<TW>(a.accumulate ? __builtin_fmaf(s, a.scale, to_f32(*p)) : s * a.scale);
+        }
+    }
+}
+
 // Runs that begin in a chunk and go on: the tail and the heads of the chunks
 // after it. A workgroup looks at kJoinChunks borders between chunks (a launch
 // of one each would take longer to hand out than to run: 65 us of 1,023

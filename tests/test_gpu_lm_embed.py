@@ -63,6 +63,38 @@ def test_runs(dyt, T, V, D, spread, token):
     run(dyt, w, t, dy, 1.0, torch.float32, torch.float32)
 
 
+# around the border of one launch (2,048 tokens): even, and with one token for most places
+@pytest.mark.parametrize("T,V,D,spread", [(2048, 700, 24, 700), (2049, 700, 24, 700), (2048, 1, 130, 1), (2049, 1, 130, 1),
+                                          (2047, 65536, 8, 65536), (2048, 65537, 8, 65537), (2048, 3, 257, 2), (1, 65536, 9, 9),
+                                          (2048, 3000, 129, 40), (1000, 4099, 300, 4099), (9, 100, 1, 1), (8, 1, 1, 1),
+                                          (2048, 8191, 2048, 8191), (2048, 8193, 2048, 8193)])
+@pytest.mark.parametrize("dt", DTYPES)
+def test_around_the_border_of_one_launch(dyt, T, V, D, spread, dt):
+    w, t, dy = make(T + V, T, V, D, DTYPES[dt], DTYPES[dt], spread, token=torch.int32)
+    g = torch.Generator().manual_seed(T)
+    t[(torch.rand(T, generator=g) < 0.4).cuda()] = V // 2   # as often as all others together
+    _, dw = run(dyt, w, t, dy, -0.5, DTYPES[dt], DTYPES[dt])
+    assert torch.equal(dw, dyt.dyt_embed_backward(dy, t, V, -0.5, dtype=DTYPES[dt]))
+
+
+@pytest.mark.parametrize("D", [1, 3, 8, 33, 128, 255, 1000])
+@pytest.mark.parametrize("wdt,ydt,gdt", [("f32", "f32", "f32"), ("bf16", "bf16", "bf16"), ("f32", "bf16", "f32"),
+                                         ("f16", "f32", "f16"), ("bf16", "f16", "f32"), ("f16", "f16", "bf16")])
+def test_widths_of_many_tokens(dyt, D, wdt, ydt, gdt):
+    w, t, dy = make(D, 2100, 600, D, DTYPES[wdt], DTYPES[ydt])
+    t[:500] = 17
+    run(dyt, w, t, dy, math.sqrt(D), DTYPES[ydt], DTYPES[gdt])
+    pitch = D + 3
+    buf = torch.full((600 * pitch + 1,), math.nan, dtype=DTYPES[gdt], device="cuda")
+    dys = torch.full((2100 * pitch + 1,), math.nan, dtype=DTYPES[ydt], device="cuda").as_strided((2100, D), (pitch, 1), 1)
+    dys.copy_(dy)
+    dys[t < 0] = math.nan
+    dws = buf.as_strided((600, D), (pitch, 1), 1)
+    dyt.dyt_embed_backward(dys, t, 600, 1.5, dweight=dws)
+    check_embed_backward(dy, t, 600, 1.5, dws)
+    assert int(torch.isnan(buf).sum()) == buf.numel() - 600 * D
+
+
 def test_tokens_outside(dyt):
     w, t, dy = make(1, 200, 50, 24, torch.float32, torch.float32, ignored=0.0)
     t[::7] = torch.tensor([-1, 50, 51, -(1 << 40), 1 << 40, (1 << 32) + 3, -100]).cuda().repeat(29)[:len(t[::7])]
