@@ -52,7 +52,7 @@ EmbedPlan embed_plan(int64_t T, int64_t V, int64_t D) {
     p.keys = (size_t)up(T * 4, 16);
     p.counts = T > kSortOne ? (size_t)(p.tiles + 1) * kRadix * 4 : 0;
     p.part = (size_t)p.chunks * 2 * D * 4;
-    p.bytes = 4 * p.keys + p.counts + p.part;
+    p.bytes = 4 * p.keys + std::max(p.counts, p.part);   // the sums begin where the sort has ended
     return p;
 }
 
@@ -61,8 +61,9 @@ EmbedPlan embed_plan(int64_t T, int64_t V, int64_t D) {
 // of 8,192 with 128 9.3 and 25.2, 2,000 of 2,048 with 2,048 17.0 and 31.0, 2,048 of
 // 8,192 with 2,048 (2^24 elements, where writing them is most of it) 27.9 and 33.1;
 // 2,048 equal tokens with 8 columns, which one workgroup adds up, 26.9 and 20.9.
+// (D: the grid's second axis takes 65,535.)
 bool embed_few(int64_t T, int64_t V, int64_t D) {
-    return T > 0 && T <= kFewTokens && V <= kFewRows * 1024 && V * D <= (1 << 24) && T * D >= kEmbVec;
+    return T > 0 && T <= kFewTokens && V <= kFewRows * 1024 && D <= (1 << 20) && V * D <= (1 << 24) && T * D >= kEmbVec;
 }
 
 template <typename F>
@@ -122,9 +123,8 @@ int embed_backward(const void* dy, int64_t lddy, const void* tokens, void* dw, i
     const int64_t sw = dtype_size(wdt), sy = dtype_size(ydt);
     if (!aligned({dw}, sw) || !aligned({dy}, sy) || !aligned({tokens}, bits / 8)) return DYT_ERR_MISALIGNED;
     const EmbedPlan p = embed_plan(T, V, D);
-    const int64_t zero_wgs = accumulate ? 0 : (V + kZeroRows - 1) / kZeroRows;
+    const int64_t zero_wgs = accumulate ? 0 : std::min<int64_t>((V + kZeroRows - 1) / kZeroRows, 1 << 20);
     const int64_t sum_wgs = (p.chunks + p.groups - 1) / p.groups * p.col_tiles;
-    if (sum_wgs + zero_wgs >= ((int64_t)1 << 24)) return DYT_ERR_INVALID_ARG;   // 2^32 threads of a launch
     if (T > 0 && (ws_bytes < p.bytes || !ws)) return DYT_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned({ws}, 16)) return DYT_ERR_MISALIGNED;
     const Range in[] = {{dy, T ? ((T - 1) * lddy + D) * sy : 0}, {tokens, T * (bits / 8)}};
@@ -136,7 +136,7 @@ int embed_backward(const void* dy, int64_t lddy, const void* tokens, void* dw, i
     for (int k = 0; k < 2; ++k, at += p.keys) a.keys[k] = (uint32_t*)at;
     for (int k = 0; k < 2; ++k, at += p.keys) a.places[k] = (uint32_t*)at;
     a.counts = (uint32_t*)at;
-    a.part = (float*)(at + p.counts);
+    a.part = (float*)at;
     a.tiles = (uint32_t)p.tiles;
     a.token_bits = bits; a.tpr = p.tpr; a.chunk = (int32_t)p.chunk; a.chunks = (int32_t)p.chunks;
     a.col_tiles = p.col_tiles; a.sum_wgs = (int32_t)sum_wgs; a.accumulate = accumulate; a.scale = scale;

@@ -28,7 +28,7 @@ constexpr int kRadixBits = 9, kRadix = 1 << kRadixBits;
 // CU's vector units 8 us a pass.)
 constexpr int kSortOneWaves = 16, kSortManyWaves = 4;
 constexpr int64_t kSortOne = 16384;
-constexpr int kSortTile = 2048;
+constexpr int kSortTile = 1024;
 constexpr int kScanTiles = 64;          // up to here every workgroup adds up the tiles before it itself
 constexpr int kEmbVec = 8;              // columns of a thread
 constexpr int kZeroRows = 64;           // rows that a workgroup looks up and clears
@@ -394,25 +394,29 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs a, int sorted)
     const uint32_t V = (uint32_t)a.V;
     if ((int)blockIdx.x >= a.sum_wgs) {
         __shared__ uint8_t absent[kZeroRows];
-        const int64_t v0 = (int64_t)((int)blockIdx.x - a.sum_wgs) * kZeroRows, v = v0 + threadIdx.x;
-        if (threadIdx.x < kZeroRows) {
-            int64_t lo = 0, hi = a.T;   // the first key of at least v
-            while (lo < hi) {
-                const int64_t mid = (lo + hi) / 2;
-                if ((int64_t)keys[mid] < v) lo = mid + 1;
-                else hi = mid;
-            }
-            absent[threadIdx.x] = v < a.V && (lo == a.T || (int64_t)keys[lo] != v);
-        }
-        __syncthreads();
         // 16 bytes to a lane: whole lines to a wave
         constexpr int W = VecOf<TW>::n;
         const int lanes = min((a.D + W - 1) / W, 256), groups = 256 / lanes;
         const int g = (int)threadIdx.x / lanes, t = (int)threadIdx.x - g * lanes;
         const float zero[W] = {};
-        for (int r = g < groups ? g : kZeroRows; r < kZeroRows; r += groups) {
-            if (!absent[r]) continue;
-            for (int c = t * W; c < a.D; c += lanes * W) store_vec<TW, 0>((TW*)a.out, (v0 + r) * a.ldw, c, a.D, zero);
+        const int64_t step = (int64_t)(gridDim.x - a.sum_wgs) * kZeroRows;
+        for (int64_t v0 = (int64_t)((int)blockIdx.x - a.sum_wgs) * kZeroRows; v0 < a.V; v0 += step) {
+            const int64_t v = v0 + threadIdx.x;
+            __syncthreads();   // the rows before have been looked up
+            if (threadIdx.x < kZeroRows) {
+                int64_t lo = 0, hi = a.T;   // the first key of at least v
+                while (lo < hi) {
+                    const int64_t mid = (lo + hi) / 2;
+                    if ((int64_t)keys[mid] < v) lo = mid + 1;
+                    else hi = mid;
+                }
+                absent[threadIdx.x] = v < a.V && (lo == a.T || (int64_t)keys[lo] != v);
+            }
+            __syncthreads();
+            for (int r = g < groups ? g : kZeroRows; r < kZeroRows; r += groups) {
+                if (!absent[r]) continue;
+                for (int c = t * W; c < a.D; c += lanes * W) store_vec<TW, 0>((TW*)a.out, (v0 + r) * a.ldw, c, a.D, zero);
+            }
         }
         return;
     }

@@ -97,7 +97,7 @@ size_t dyt_embed_backward_workspace_size(int64_t T, int64_t V, int64_t D);
 /* Writes every row of dweight, zeros for tokens that do not occur; with
  * `accumulate` it adds to the rows of those that do and leaves the others
  * alone. Sums are taken in the order of the places, in pieces that depend on
- * T and D only. */
+ * T, V, D and how often a token occurs. */
 int dyt_embed_backward(const void* dy, int64_t lddy, const void* tokens, void* dweight, int64_t lddw,
                        void* workspace, size_t workspace_bytes, int64_t T, int64_t V, int64_t D,
                        float scale, int dy_dtype, int dw_dtype, int token_bits, int accumulate,

@@ -77,6 +77,12 @@ def test_around_the_border_of_one_launch(dyt, T, V, D, spread, dt):
     assert torch.equal(dw, dyt.dyt_embed_backward(dy, t, V, -0.5, dtype=DTYPES[dt]))
 
 
+@pytest.mark.parametrize("D", [(1 << 20) - 1, (1 << 20) + 8, 1 << 23])
+def test_wide_rows(dyt, D):
+    w, t, dy = make(5, 5, 2, D, torch.bfloat16, torch.bfloat16)
+    run(dyt, w, t, dy, 1.0, torch.bfloat16, torch.bfloat16)
+
+
 @pytest.mark.parametrize("D", [1, 3, 8, 33, 128, 255, 1000])
 @pytest.mark.parametrize("wdt,ydt,gdt", [("f32", "f32", "f32"), ("bf16", "bf16", "bf16"), ("f32", "bf16", "f32"),
                                          ("f16", "f32", "f16"), ("bf16", "f16", "f32"), ("f16", "f16", "bf16")])
@@ -122,6 +128,17 @@ def test_row_strides(dyt, dt, D, pitch, at):
     check_embed_backward(dy, t, V, 1.5, dws)
     for b, n in zip(bufs[2:], (T, V)):
         assert int(torch.isnan(b).sum()) == b.numel() - n * D
+
+
+def test_more_rows_than_workgroups(dyt):
+    """Zero rows of a launch that walks them (2^20 workgroups of 64 rows)."""
+    V = (1 << 26) + 200
+    t = torch.tensor([3, V - 1, 1 << 26, 3, (1 << 26) - 1], device="cuda")
+    dy = torch.arange(1, 6, device="cuda", dtype=torch.float32).view(5, 1).expand(5, 2).contiguous()
+    dw = torch.full((V, 2), 9.0, device="cuda")
+    dyt.dyt_embed_backward(dy, t, V, dweight=dw)
+    assert [dw[i].tolist() for i in (3, V - 1, 1 << 26, (1 << 26) - 1)] == [[5, 5], [2, 2], [3, 3], [5, 5]]
+    assert int((dw != 0).sum()) == 8
 
 
 def test_nothing_there(dyt):
