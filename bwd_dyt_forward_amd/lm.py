@@ -223,7 +223,8 @@ class AdamW(torch.optim.Optimizer):
     keeps a float32 copy of 16-bit parameters that the steps are taken on.
     ``capturable``: the step counter is on the device, and ``lr`` may be a
     float32 tensor there, so that a step captured into a graph moves on with
-    each replay; every parameter of a group then needs a gradient."""
+    each replay; every parameter of a group then needs a gradient, and the
+    states have to be there (one step) before the capture."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01, *,
                  state_bits: int = 32, min_8bit: int = 4096, master: bool = False, seed: int = 0,
@@ -282,13 +283,10 @@ class AdamW(torch.optim.Optimizer):
             for s in states:   # one counter for the group
                 s["step"] = steps
             steps.add_(1)
-        else:
-            for s in states:
-                s["step"] = int(s["step"]) + 1
         # a call for each step count and width of the states
         calls: dict = {}
         for p, s in zip(with_grad, states):
-            at = None if group["capturable"] else s["step"]
+            at = None if group["capturable"] else int(s["step"]) + 1
             calls.setdefault((at, "avg_scale" in s), []).append((p, s))
         for (at, bits8), members in calls.items():
             ps = [p for p, _ in members]
@@ -303,6 +301,9 @@ class AdamW(torch.optim.Optimizer):
                                [s["exp_avg_sq"] for s in ss], lr=group["lr"], betas=group["betas"], eps=group["eps"],
                                weight_decay=group["weight_decay"], step=ss[0]["step"] if at is None else at,
                                grad_scale=grad_scale, **kw)
+            if at is not None:
+                for s in ss:   # last: a call that is refused is no step
+                    s["step"] = at
 
     def load_state_dict(self, state_dict) -> None:
         """As the base class's, but the states keep their own types (it casts

@@ -120,7 +120,9 @@ int dyt_embed_backward(const void* dy, int64_t lddy, const void* tokens, void* d
  * two: the lowest float32 and bfloat16 values), is a masked place: p = 0 and
  * gradient 0. A row of nothing else has lse = -inf, logp = -inf, entropy 0 and
  * gradient 0. A NaN or +inf
- * makes its row's results NaN.
+ * makes its row's results NaN. Exponentials below 2^-126 count as 0. The
+ * gradient takes p from the float32 lse: its relative error grows with
+ * |lse| 2^-23.
  *
  * top_logp, top_tokens: [T, top] (top 0: NULL), the log probabilities
  * (float32) and places (int64) of the `top` largest logits in falling order,

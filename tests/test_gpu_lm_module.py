@@ -235,3 +235,90 @@ def test_optimizer_refusals(dyt):
     w.grad = torch.ones_like(w)
     with pytest.raises(ValueError):
         dyt.AdamW([w]).step()
+
+
+def test_a_refused_step_does_not_count(dyt):
+    p, w = nn.Parameter(torch.randn(8, device="cuda")), nn.Parameter(torch.randn(4, 6, device="cuda"))
+    opt = dyt.AdamW([p, w])
+    for x in (p, w):
+        x.grad = torch.ones_like(x)
+    opt.step()
+    before, w.data = p.detach().clone(), w.data.t()
+    w.grad = torch.ones_like(w)
+    with pytest.raises(ValueError):
+        opt.step()
+    assert torch.equal(p, before) and opt.state[p]["step"] == opt.state[w]["step"] == 1
+
+
+def test_nothing_there(dyt):
+    """Modules over no tokens and no rows: empty results, zero gradients."""
+    emb, norm, res = dyt.Embedding(7, 16, device="cuda"), dyt.RMSNorm(16, device="cuda"), dyt.RMSNormResidual(16, device="cuda")
+    tokens = torch.zeros(2, 0, dtype=torch.int64, device="cuda")
+    h, y = res(emb(tokens), norm(emb(tokens)))
+    logits = y @ emb.weight.t()
+    logp, entropy, best, places = dyt.token_log_probs(logits, tokens, top=2)
+    assert logp.shape == entropy.shape == (2, 0) and best.shape == places.shape == (2, 0, 2)
+    (logp.sum() + entropy.sum() + h.sum()).backward()
+    assert (emb.weight.grad == 0).all() and (norm.weight.grad == 0).all() and (res.weight.grad == 0).all()
+    q, s = norm.quantized(torch.zeros(0, 16, device="cuda"), group=32)
+    assert q.shape == (0, 16) and s.shape == (0, 1)
+
+
+@pytest.mark.parametrize("expand", [False, True])
+def test_upstream_gradients_of_any_strides(dyt, expand):
+    """Gradients that arrive expanded or transposed, as from sums and means."""
+    emb, norm = dyt.Embedding(9, 24, device="cuda"), dyt.RMSNorm(24, device="cuda")
+    tokens = torch.randint(0, 9, (4, 5), device="cuda")
+    w = torch.randn(24, 5, 4, device="cuda")
+    for back in (lambda y: y.sum(), lambda y: y.mean(0).sum()) if expand else (lambda y: (y.permute(2, 1, 0) * w).sum(),):
+        got, want = [], []
+        for contiguous in (False, True):
+            y = norm(emb(tokens))
+            if contiguous:
+                y.register_hook(lambda g: g.contiguous())
+            back(y).backward()
+            (want if contiguous else got).extend(p.grad.clone() for p in (emb.weight, norm.weight))
+            emb.weight.grad = norm.weight.grad = None
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(a.abs().sum() > 0 for a in got)
+
+
+def test_two_graphs_and_eager_work_between(dyt):
+    """Two captured training steps of the operators replayed in turn, with eager
+    calls of other sizes between: no workspace is shared."""
+    def make(seed, V, D, T):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        r = lambda *s: torch.randn(*s, device="cuda", generator=g)
+        return dict(w=r(V, D), g=1 + 0.1 * r(D), t=torch.randint(-1, V, (T,), device="cuda", generator=g), up=r(T))
+
+    def step(s):
+        x = dyt.dyt_embed_forward(s["w"], s["t"])
+        y, rstd = dyt.dyt_rms_forward(x, s["g"])
+        logits = y @ s["w"].t()
+        logp, entropy, lse = dyt.dyt_logprob_forward(logits, s["t"])
+        dl = dyt.dyt_logprob_backward(logits, s["t"], entropy, lse, s["up"], s["up"])
+        dx, dg = dyt.dyt_rms_backward(x, dl @ s["w"], rstd, s["g"])
+        return logp, entropy, dx, dg, dyt.dyt_embed_backward(dx, s["t"], s["w"].shape[0])
+
+    sets = [make(1, 300, 64, 4000), make(2, 50, 96, 900)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for s in sets:
+            step(s)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in sets], []
+    for graph, s in zip(graphs, sets):
+        with torch.cuda.graph(graph):
+            outs.append(step(s))
+    for i in range(4):
+        for s in sets:
+            s["t"].copy_(torch.randint(-1, s["w"].shape[0], s["t"].shape, generator=torch.Generator().manual_seed(i)).cuda())
+        want = [step(s) for s in sets]
+        torch.cuda.synchronize()
+        for graph in graphs:
+            graph.replay()
+        step(make(i, 100, 32, 5000))
+        torch.cuda.synchronize()
+        for a, b in zip(want, outs):
+            assert all(torch.equal(x, y) for x, y in zip(a, b)), i
