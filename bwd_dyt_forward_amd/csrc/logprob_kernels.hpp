@@ -17,8 +17,9 @@
 //
 // The backward is bound by HBM. In the forward the vector unit is as busy as
 // HBM: one exponential (a quarter of the rate) and six other operations an
-// element. Hence y - m in one fused operation, maxima of three, 32-bit places,
-// and checks for a row's ends outside of the vectors that lie within it.
+// element. Hence y - m in one fused operation, maxima of three, 32-bit places, one
+// change of the maximum for 16 elements, and checks for a row's ends and for masked
+// places' -inf times 0 outside of the vectors that hold none.
 //
 // Alternatives: the best k by (value, lowest index), as one 64-bit key each.
 // Neighbouring eight lanes share a line of memory; its maximum (three lane
@@ -71,6 +72,7 @@ struct Lse {
 // scale) then has an exponential of 0.
 __device__ __forceinline__ Lse lse_none() { return {-3.402823466e+38f, 0.0f, 0.0f}; }
 
+// (fmaxf would first bring each operand into its canonical form.)
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
@@ -118,27 +120,40 @@ __device__ __forceinline__ Lse lse_group(Lse v, Lse* waves) {
     return lse_lanes(waves[threadIdx.x & 3], 4);
 }
 
-// One vector's elements (-inf where there are none); returns their maximum.
 template <int VEC>
-__device__ __forceinline__ float lse_add(Lse& a, const float* x, float k2) {
-    float mv;
-    if constexpr (VEC == 8) mv = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7]));
-    else mv = max3(x[0], x[1], fmaxf(x[2], x[3]));
-    const float m = mv * k2;
+__device__ __forceinline__ float vec_max(const float* x) {
+    if constexpr (VEC == 8) return max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), max3(x[6], x[7], x[7]));
+    else return max3(max3(x[0], x[1], x[2]), x[3], x[3]);
+}
+
+// N elements (-inf where there are none), `most` their maximum.
+template <int N>
+__device__ __forceinline__ void lse_add(Lse& a, const float* x, float most, float k2) {
+    const float m = most * k2;
     if (m > a.m) {
         const float d = a.m - m, f = __builtin_amdgcn_exp2f(d);
         a.t = f * (a.t + fmaxf(d, -1e30f) * a.s);
         a.s *= f;
         a.m = m;
     }
+    float t = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
+    for (int i = 0; i < N; ++i) {
         const float z = __builtin_fmaf(x[i], k2, -a.m);
         const float e = __builtin_amdgcn_exp2f(z);
         a.s += e;
-        a.t = __builtin_fmaf(fmaxf(z, -1e30f), e, a.t);   // -inf times an exact 0 would be NaN
+        t = __builtin_fmaf(z, e, t);
     }
-    return mv;
+    if (t != t) {   // -inf times an exact 0: once more, with the maximum that an element would cost each time
+        t = 0.0f;
+        asm volatile("" : "+v"(t));   // stays a branch
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float z = __builtin_fmaf(x[i], k2, -a.m);
+            t = __builtin_fmaf(fmaxf(z, -1e30f), __builtin_amdgcn_exp2f(z), t);
+        }
+    }
+    a.t += t;
 }
 
 // A part of a row on the 16-byte grid: its vectors are the aligned 16 bytes of
@@ -300,17 +315,19 @@ __device__ __forceinline__ void top_rank(const uint64_t* list, int k, const TopS
 }
 
 // --------------------------------------------------------------- forward
-// A row to tpr lanes, several rows to a workgroup (V up to a few vectors a
-// lane), or a row or a part of one to the workgroup (tpr == 256). U vectors of
-// a thread at a time, the next ones loaded before the current ones are used.
-template <typename T, bool TOP, bool NT, int U>
+// ROW: a row or a part of one to the workgroup; else a row to tpr lanes, several
+// rows to a workgroup (V up to a few vectors a lane). Two vectors of a thread at a
+// time, the next ones loaded before the current ones are used: where all of them
+// are whole, without a check, and added at once.
+template <typename T, bool TOP, bool ROW, bool NT>
 __global__ __launch_bounds__(kLpThreads) void lp_fwd_kernel(LpArgs a) {
-    constexpr int VEC = VecOf<T>::n;
+    static_assert(ROW || !TOP, "alternatives take a workgroup");
+    constexpr int VEC = VecOf<T>::n, U = 2;
     constexpr int LINE = 8 * VEC;   // elements of a line: eight lanes' vectors
     extern __shared__ uint64_t dyn[];
     const float k2 = a.scale * kLog2e;
-    const int tpr = TOP ? kLpThreads : a.tpr;
-    const int t = (int)threadIdx.x & (tpr - 1), g = (int)threadIdx.x / tpr;
+    const int tpr = ROW ? kLpThreads : a.tpr;
+    const int t = (int)threadIdx.x & (tpr - 1), g = ROW ? 0 : (int)threadIdx.x / tpr;
     const uint32_t item = blockIdx.x * (uint32_t)(kLpThreads / tpr) + (uint32_t)g;   // (row, part)
     const uint32_t m = item / (uint32_t)a.parts, part = item - m * (uint32_t)a.parts;
     const RowPart<T> r((const T*)a.logits, m, part, a);
@@ -319,15 +336,45 @@ __global__ __launch_bounds__(kLpThreads) void lp_fwd_kernel(LpArgs a) {
     const int step = tpr * VEC;
     int base = r.first;   // the row's first lane's place: the same for all its lanes
     u32x4 next[U];
+    const auto whole = [&](int b) { return ROW && b >= r.lo && b + U * step <= r.hi; };   // for all lanes
+    const auto load = [&](int b) {
+        if (whole(b)) {
+            const char* from = (const char*)r.p;
 #pragma unroll
-    for (int u = 0; u < U; ++u) next[u] = r.template load<NT>(base + t * VEC + u * step);
+            for (int u = 0; u < U; ++u) {
+                const u32x4* at = (const u32x4*)(from + (uint32_t)(b + u * step + t * VEC) * (uint32_t)sizeof(T));
+                if constexpr (NT) next[u] = __builtin_nontemporal_load(at);
+                else next[u] = *at;
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) next[u] = r.template load<NT>(b + u * step + t * VEC);
+        }
+    };
+    // the maximum of a line; `e`: the place of the lane's vector of it
+    const auto line = [&](float most, int e) {
+        if constexpr (TOP) {
+            most = lanes_max8(most);
+            if ((t & 7) == 0 && e < r.end) line_max[(uint32_t)(e - r.first) / LINE] = most;
+        }
+    };
+    load(base);
     const RowToken<T> token(a, m);
     for (; base < r.end; base += U * step) {
         u32x4 now[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            now[u] = next[u];
-            next[u] = r.template load<NT>(base + t * VEC + (U + u) * step);
+        for (int u = 0; u < U; ++u) now[u] = next[u];
+        if (base + U * step < r.end) load(base + U * step);
+        if (whole(base)) {
+            float x[U][VEC], most[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                unpack16<T>(now[u], x[u]);
+                most[u] = vec_max<VEC>(x[u]);
+                line(most[u], base + u * step + t * VEC);
+            }
+            lse_add<U * VEC>(v, x[0], max3(most[0], most[1], most[1]), k2);
+            continue;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -335,18 +382,14 @@ __global__ __launch_bounds__(kLpThreads) void lp_fwd_kernel(LpArgs a) {
             if (b >= r.end) continue;
             float x[VEC];
             unpack16<T>(now[u], x);
-            if (b < r.lo || b + step > r.hi) {   // a vector of some lane is not whole
-                if (!r.whole(e)) r.elements(e, x);
-            }
-            float mv = lse_add<VEC>(v, x, k2);
-            if constexpr (TOP) {
-                mv = lanes_max8(mv);
-                if ((t & 7) == 0 && e < r.end) line_max[(uint32_t)(e - r.first) / LINE] = mv;
-            }
+            if (!r.whole(e)) r.elements(e, x);
+            const float most = vec_max<VEC>(x);
+            line(most, e);
+            lse_add<VEC>(v, x, most, k2);
         }
     }
     __shared__ Lse red[kLpThreads / 64];
-    if (tpr == kLpThreads) v = lse_group(v, red);
+    if constexpr (ROW) v = lse_group(v, red);
     else v = lse_lanes(v, tpr);
     if (t == 0 && m < a.T) {
         if (a.parts == 1) {

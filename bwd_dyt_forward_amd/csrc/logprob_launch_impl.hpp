@@ -9,16 +9,17 @@ namespace dytb {
 // Two vectors of a thread at a time with two more on their way leave the
 // registers to eight waves per SIMD (four and four to half of them: 175 us for
 // 162 at 8,192 x 50,257 bfloat16).
-template <typename T, bool TOP>
+template <typename T, bool TOP, bool ROW>
 void lp_fwd_pick(const LpArgs& a, int64_t grid, size_t shared, hipStream_t s) {
-    if (a.stream) lp_fwd_kernel<T, TOP, true, 2><<<(unsigned)grid, kLpThreads, shared, s>>>(a);
-    else lp_fwd_kernel<T, TOP, false, 2><<<(unsigned)grid, kLpThreads, shared, s>>>(a);
+    if (a.stream) lp_fwd_kernel<T, TOP, ROW, true><<<(unsigned)grid, kLpThreads, shared, s>>>(a);
+    else lp_fwd_kernel<T, TOP, ROW, false><<<(unsigned)grid, kLpThreads, shared, s>>>(a);
 }
 
 template <typename T>
 void lp_launch_forward(const LpArgs& a, int64_t grid, size_t shared, size_t join_shared, hipStream_t s) {
-    if (a.top) lp_fwd_pick<T, true>(a, grid, shared, s);
-    else lp_fwd_pick<T, false>(a, grid, 0, s);
+    if (a.top) lp_fwd_pick<T, true, true>(a, grid, shared, s);
+    else if (a.tpr == kLpThreads) lp_fwd_pick<T, false, true>(a, grid, 0, s);
+    else lp_fwd_pick<T, false, false>(a, grid, 0, s);
     if (a.parts == 1) return;
     if (a.top) lp_join_kernel<T, true><<<(unsigned)a.T, kLpThreads, join_shared, s>>>(a);
     else lp_join_kernel<T, false><<<(unsigned)a.T, kLpThreads, 0, s>>>(a);
