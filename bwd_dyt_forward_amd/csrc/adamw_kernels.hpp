@@ -74,7 +74,7 @@ __device__ __forceinline__ const AdamArgs& adam_args() {
     return *(const AdamArgs*)__builtin_amdgcn_kernarg_segment_ptr();
 }
 
-// A 32-bit hash (the finalizer of MurmurHash3; A. Appleby, 2011).
+// A 32-bit hash (the finalizer of a published one: A. Appleby, 2011).
 __host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
     x = (x ^ (x >> 16)) * 0x85EBCA6Bu;
     x = (x ^ (x >> 13)) * 0xC2B2AE35u;

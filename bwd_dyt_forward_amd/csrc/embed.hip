@@ -123,7 +123,10 @@ int embed_backward(const void* dy, int64_t lddy, const void* tokens, void* dw, i
     const int64_t sw = dtype_size(wdt), sy = dtype_size(ydt);
     if (!aligned({dw}, sw) || !aligned({dy}, sy) || !aligned({tokens}, bits / 8)) return DYT_ERR_MISALIGNED;
     const EmbedPlan p = embed_plan(T, V, D);
-    const int64_t zero_wgs = accumulate ? 0 : std::min<int64_t>((V + kZeroRows - 1) / kZeroRows, 1 << 20);
+    // Zero rows of a workgroup: some 128 KB, so that others write while it looks its rows
+    // up (128,000 rows of 8 KB: 210 us with 16 and 220 with 64; 50,000 of 640 bytes 56 and 48).
+    const int64_t zero_rows = std::min<int64_t>(std::max<int64_t>((128 << 10) / (D * sw), 16), kZeroRows);
+    const int64_t zero_wgs = accumulate ? 0 : std::min<int64_t>((V + zero_rows - 1) / zero_rows, 1 << 20);
     const int64_t sum_wgs = (p.chunks + p.groups - 1) / p.groups * p.col_tiles;
     if (T > 0 && (ws_bytes < p.bytes || !ws)) return DYT_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned({ws}, 16)) return DYT_ERR_MISALIGNED;
@@ -139,7 +142,7 @@ int embed_backward(const void* dy, int64_t lddy, const void* tokens, void* dw, i
     a.part = (float*)at;
     a.tiles = (uint32_t)p.tiles;
     a.token_bits = bits; a.tpr = p.tpr; a.chunk = (int32_t)p.chunk; a.chunks = (int32_t)p.chunks;
-    a.col_tiles = p.col_tiles; a.sum_wgs = (int32_t)sum_wgs; a.accumulate = accumulate; a.scale = scale;
+    a.col_tiles = p.col_tiles; a.sum_wgs = (int32_t)sum_wgs; a.zero_rows = (int32_t)zero_rows; a.accumulate = accumulate; a.scale = scale;
     const hipStream_t s = (hipStream_t)stream;
     if (embed_few(T, V, D)) {
         // 1,024 workgroups where there are rows for them

@@ -31,7 +31,7 @@ constexpr int64_t kSortOne = 16384;
 constexpr int kSortTile = 1024;
 constexpr int kScanTiles = 64;          // up to here every workgroup adds up the tiles before it itself
 constexpr int kEmbVec = 8;              // columns of a thread
-constexpr int kZeroRows = 64;           // rows that a workgroup looks up and clears
+constexpr int kZeroRows = 64;           // most rows that a workgroup looks up and clears at once
 
 // The token at place t, or V where there is none.
 __device__ __forceinline__ uint32_t token_at(const void* tokens, int bits, int64_t t, int64_t V) {
@@ -106,6 +106,7 @@ struct EmbedArgs {
     int32_t chunks;
     int32_t col_tiles;    // of tpr * kEmbVec columns
     int32_t sum_wgs;      // workgroups that sum; the rest write zero rows
+    int32_t zero_rows;    // rows that a workgroup looks up and clears at once
     int32_t accumulate;
     float scale;
 };
@@ -386,7 +387,7 @@ __device__ __forceinline__ void put_row(const EmbedArgs& a, uint32_t key, int c,
 
 // Sums of the runs of chunks, tpr threads to a chunk and column tile, U rows
 // of dy on their way (U = 1: also for a dy of fewer elements than a vector);
-// and (workgroups from sum_wgs on, kZeroRows rows each) zeros for the rows of
+// and (workgroups from sum_wgs on, zero_rows rows each) zeros for the rows of
 // tokens that do not occur.
 template <typename TY, typename TW, int U>
 __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs a, int sorted) {
@@ -399,11 +400,11 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs a, int sorted)
         const int lanes = min((a.D + W - 1) / W, 256), groups = 256 / lanes;
         const int g = (int)threadIdx.x / lanes, t = (int)threadIdx.x - g * lanes;
         const float zero[W] = {};
-        const int64_t step = (int64_t)(gridDim.x - a.sum_wgs) * kZeroRows;
-        for (int64_t v0 = (int64_t)((int)blockIdx.x - a.sum_wgs) * kZeroRows; v0 < a.V; v0 += step) {
+        const int64_t step = (int64_t)(gridDim.x - a.sum_wgs) * a.zero_rows;
+        for (int64_t v0 = (int64_t)((int)blockIdx.x - a.sum_wgs) * a.zero_rows; v0 < a.V; v0 += step) {
             const int64_t v = v0 + threadIdx.x;
             __syncthreads();   // the rows before have been looked up
-            if (threadIdx.x < kZeroRows) {
+            if (threadIdx.x < a.zero_rows) {
                 int64_t lo = 0, hi = a.T;   // the first key of at least v
                 while (lo < hi) {
                     const int64_t mid = (lo + hi) / 2;
@@ -413,7 +414,7 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(EmbedArgs a, int sorted)
                 absent[threadIdx.x] = v < a.V && (lo == a.T || (int64_t)keys[lo] != v);
             }
             __syncthreads();
-            for (int r = g < groups ? g : kZeroRows; r < kZeroRows; r += groups) {
+            for (int r = g < groups ? g : a.zero_rows; r < a.zero_rows; r += groups) {
                 if (!absent[r]) continue;
                 for (int c = t * W; c < a.D; c += lanes * W) store_vec<TW, 0>((TW*)a.out, (v0 + r) * a.ldw, c, a.D, zero);
             }
