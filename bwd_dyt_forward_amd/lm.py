@@ -268,6 +268,10 @@ class AdamW(torch.optim.Optimizer):
         with_grad = [p for p in group["params"] if p.grad is not None]
         if not with_grad:
             return
+        if with_grad[0].is_cuda and torch.cuda.is_current_stream_capturing():
+            # a replay would take the same step again, or begin with new states
+            if not group["capturable"] or not all(isinstance(self.state[p].get("step"), torch.Tensor) for p in with_grad):
+                raise RuntimeError("a captured step needs capturable=True and a step before the capture")
         for p in with_grad:
             if p.grad.is_sparse:
                 raise ValueError("sparse gradients are not supported")

@@ -322,3 +322,68 @@ def test_two_graphs_and_eager_work_between(dyt):
         torch.cuda.synchronize()
         for a, b in zip(want, outs):
             assert all(torch.equal(x, y) for x, y in zip(a, b)), i
+
+
+def test_single_rows_and_single_tokens(dyt):
+    """A vector in place of a batch: one dimension, and tokens of none."""
+    emb, norm, res = dyt.Embedding(7, 40, device="cuda"), dyt.RMSNorm(40, device="cuda"), dyt.RMSNormResidual(40, device="cuda")
+    token = torch.tensor(3, device="cuda")
+    h, y = res(emb(token), norm(emb(token)))
+    assert h.shape == y.shape == (40,)
+    logits = emb.weight @ y
+    logp, entropy, best, places = dyt.token_log_probs(logits, token, top=2)
+    assert logp.shape == entropy.shape == () and best.shape == places.shape == (2,)
+    (logp + entropy).backward()
+    # logp is next to 0 here (the token's own row): its error is that of a sum of seven
+    # exponentials and its logarithm (10 roundings of numbers of order one) and of the
+    # difference of two logits (two roundings of them)
+    off = (d(logp) - torch.log_softmax(d(logits), 0)[3]).abs()
+    assert off <= (10 + 2 * d(logits).abs().max()) * 2.0 ** -24
+    assert emb.weight.grad.shape == (7, 40) and torch.isfinite(emb.weight.grad).all() and norm.weight.grad.abs().sum() > 0
+    q, s = norm.quantized(y.detach(), group=32)
+    assert q.shape == (40,) and s.shape == (2,)
+
+
+def test_two_streams_at_once(dyt):
+    """The same calls on two streams at the same time: no memory between them."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    sets = [dict(t=torch.randint(-1, 900, (T,), device="cuda", generator=g), dy=torch.randn(T, 200, device="cuda", generator=g),
+                 x=torch.randn(T, 900, device="cuda", generator=g), gamma=torch.ones(200, device="cuda")) for T in (6000, 7000)]
+
+    def work(s):
+        dw = dyt.dyt_embed_backward(s["dy"], s["t"], 900)
+        logp, entropy, lse, best, at = dyt.dyt_logprob_forward(s["x"][:300], s["t"][:300], top=5)
+        y, rstd = dyt.dyt_rms_forward(s["dy"], s["gamma"])
+        return (dw, logp, entropy, lse, best, at, y, *dyt.dyt_rms_backward(s["dy"], y, rstd, s["gamma"]))
+
+    want = [work(s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = []
+        for stream, s in zip(streams, sets):
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                got.append(work(s))
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_a_capture_without_states_or_counter_is_refused(dyt, capturable):
+    p = nn.Parameter(torch.randn(64, device="cuda"))
+    p.grad = torch.ones_like(p)
+    opt = dyt.AdamW([p], capturable=capturable)
+    if not capturable:
+        opt.step()
+    before = p.detach().clone()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        with pytest.raises(RuntimeError, match="capture"):
+            opt.step()
+        p.grad.add_(0)   # a graph of something
+    torch.cuda.synchronize()
+    assert torch.equal(p, before)
+    opt.step()
+    assert not torch.equal(p, before)
