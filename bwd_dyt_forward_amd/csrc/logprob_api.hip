@@ -13,6 +13,7 @@ namespace {
 
 static_assert(kLpMaxTop == DYT_LOGPROB_MAX_TOP, "the kernels' limit is the header's");
 constexpr int64_t kMaxV = (int64_t)1 << 26;
+constexpr int64_t kPastCache = (int64_t)256 << 20;   // the last-level cache
 // With alternatives: lines of a part and parts of a row, for what of both is in
 // LDS (51 KB of maxima and candidates of a part, 32 KB of candidates of a row),
 // and the longest row that they leave.
@@ -115,7 +116,7 @@ int lp_forward(const void* logits, int64_t ld, const void* tokens, float* logp, 
     // them: nontemporal loads (8,192 x 50,257 bfloat16: 187 -> 147 us; 8,192 x 4,096,
     // which fit, 22 -> 26). The backward, whose reads and writes both pass through
     // it, is slower with such loads or stores (289 -> 305).
-    a.stream = T * V * s >= ((int64_t)256 << 20);
+    a.stream = T * V * s >= kPastCache;
     with_type(dt, [&](auto* t) {
         lp_launch_forward<std::remove_pointer_t<decltype(t)>>(a, p.grid, p.shared, p.join_shared, (hipStream_t)stream);
     });
@@ -147,6 +148,7 @@ int lp_backward(const void* logits, int64_t ld, const void* tokens, const float*
     a.dlogp = dlogp; a.dentropy = dentropy; a.dlogits = dlogits; a.ld = ld; a.ldd = ldd; a.T = T; a.V = V;
     a.part_len = p.part_len; a.parts = p.parts; a.token_bits = bits; a.tpr = p.tpr;
     a.scale = scale;
+    a.stream = T * V * s >= kPastCache;
     with_type(dt, [&](auto* t) {
         lp_launch_backward<std::remove_pointer_t<decltype(t)>>(a, p.grid, (hipStream_t)stream);
     });

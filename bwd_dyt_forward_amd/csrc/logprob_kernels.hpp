@@ -60,7 +60,7 @@ struct LpArgs {
     int32_t top;
     int32_t token_bits;
     int32_t tpr;          // threads of a row, a power of two up to 64, or 256
-    int32_t stream;       // 1: nontemporal loads
+    int32_t stream;       // 1: past the last-level cache: nontemporal loads of the forward
     float scale;
 };
 
