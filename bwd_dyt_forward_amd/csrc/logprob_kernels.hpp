@@ -136,22 +136,19 @@ __device__ __forceinline__ void lse_add(Lse& a, const float* x, float most, floa
         a.s *= f;
         a.m = m;
     }
-    float t = 0.0f;
+    float t = 0.0f, z[N], e[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float z = __builtin_fmaf(x[i], k2, -a.m);
-        const float e = __builtin_amdgcn_exp2f(z);
-        a.s += e;
-        t = __builtin_fmaf(z, e, t);
+        z[i] = __builtin_fmaf(x[i], k2, -a.m);
+        e[i] = __builtin_amdgcn_exp2f(z[i]);
+        a.s += e[i];
+        t = __builtin_fmaf(z[i], e[i], t);
     }
     if (t != t) {   // -inf times an exact 0: once more, with the maximum that an element would cost each time
         t = 0.0f;
         asm volatile("" : "+v"(t));   // stays a branch
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float z = __builtin_fmaf(x[i], k2, -a.m);
-            t = __builtin_fmaf(fmaxf(z, -1e30f), __builtin_amdgcn_exp2f(z), t);
-        }
+        for (int i = 0; i < N; ++i) t = __builtin_fmaf(fmaxf(z[i], -1e30f), e[i], t);
     }
     a.t += t;
 }

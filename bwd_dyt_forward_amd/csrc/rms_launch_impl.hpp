@@ -27,8 +27,14 @@ void rms_fwd_one(const RmsArgs& a, hipStream_t s) {
         if (a.r) rms_fwd_kernel<T, TPR, V, U, true, Q8, NT><<<grid, S::threads, 0, s>>>(a);
         else rms_fwd_kernel<T, TPR, V, U, false, Q8, NT><<<grid, S::threads, 0, s>>>(a);
     };
-    // the codes are half a 16-bit row: left to the caches for what reads them next
-    if constexpr (Q8) return with(std::integral_constant<int, 0>{}, kRmsGridThreads);
+    if constexpr (Q8) {
+        // The codes are half a 16-bit row, left to the caches for what reads them next; the
+        // other tensors pass them by (16,384 x 4,096 bfloat16 with the residual 80 us for 95),
+        // and the second reduction wants all the workgroups (83).
+        if (a.traffic == 2) with(std::integral_constant<int, 2>{}, kRmsGridThreads);
+        else with(std::integral_constant<int, 0>{}, kRmsGridThreads);
+        return;
+    }
     if (a.traffic == 2) with(std::integral_constant<int, 2>{}, kRmsGridThreadsFew);
     else if (a.traffic) with(std::integral_constant<int, 1>{}, kRmsGridThreadsFew);
     else with(std::integral_constant<int, 0>{}, kRmsGridThreads);

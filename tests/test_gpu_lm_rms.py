@@ -111,6 +111,22 @@ def test_rows_of_large_tensors(dyt, M, N):
     assert ((dg.double() - want).abs() <= (M / 256 + 356) * 2.0 ** -24 * 1.01 * size + 2.0 ** -24 * want.abs()).all()
 
 
+@pytest.mark.parametrize("M,N,group", [(8300, 8192, 0), (33000, 2047, 32), (270000, 256, 128)])
+def test_8_bits_of_large_tensors(dyt, M, N, group):
+    """Nontemporal instances of the 8-bit output: first, middle and last rows."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x, r = (torch.randn(M, N, device="cuda", generator=g).bfloat16() for _ in range(2))
+    gm = torch.randn(N, device="cuda", generator=g)
+    at = [0, 1, M // 2, M - 2, M - 1]
+    h, q, scales = dyt.dyt_rms_forward_residual_q8(x, r, gm, EPS, group)
+    assert torch.equal(h, x + r)
+    check_rms_q8(h[at], gm, EPS, group, q[at], scales[at])
+    q, scales = dyt.dyt_rms_forward_q8(x, gm, EPS, group)
+    check_rms_q8(x[at], gm, EPS, group, q[at], scales[at])
+    few = dyt.dyt_rms_forward_q8(x[:100], gm, EPS, group)
+    assert torch.equal(q[:100].view(torch.uint8), few[0].view(torch.uint8)) and torch.equal(scales[:100], few[1])
+
+
 @pytest.mark.parametrize("dt", DTYPES)
 @pytest.mark.parametrize("N,pitch,at", [(64, 72, 0), (64, 67, 0), (100, 101, 3), (1000, 1032, 8), (2050, 2051, 1),
                                         (17000, 17003, 5), (70000, 70001, 3), (1, 9, 2)])
