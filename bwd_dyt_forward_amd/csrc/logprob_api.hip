@@ -113,8 +113,8 @@ int lp_forward(const void* logits, int64_t ld, const void* tokens, float* logp, 
     a.ld = ld; a.T = T; a.V = V; a.part_len = p.part_len; a.parts = p.parts; a.top = top; a.token_bits = bits;
     a.tpr = p.tpr; a.scale = scale;
     // Logits past the last-level cache (256 MB) leave it to what was written before
-    // them: nontemporal loads (8,192 x 50,257 bfloat16: 187 -> 147 us; 8,192 x 4,096,
-    // which fit, 22 -> 26). The backward, whose reads and writes both pass through
+    // them: nontemporal loads (8,192 x 50,257 bfloat16: 182 -> 140 us; 8,192 x 4,096,
+    // which fit, 17.8 -> 18.4). The backward, whose reads and writes both pass through
     // it, is slower with such loads or stores (289 -> 305).
     a.stream = T * V * s >= kPastCache;
     with_type(dt, [&](auto* t) {
