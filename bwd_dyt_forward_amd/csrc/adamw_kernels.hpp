@@ -250,11 +250,12 @@ __device__ __forceinline__ float sq_code(uint32_t w, int i) { return (float)((w 
 // Of the two codes c and c + 1 around y = 127^2 |m| / a, the upper one if u =
 // (random + 0.5) / 65536 is below y's place between them, y > c^2 + u (2 c + 1). That
 // is (c + u)^2 + u (1 - u): the square root of y - u (1 - u), and 1/2 - u added,
-// rounds to it. (y may pass 127^2 by a rounding.)
-__device__ __forceinline__ float avg_round(float m, float scale, float random) {
+// rounds to it. (y may pass 127^2 by a rounding.) `inv` is 1 / a, without 127^2: with
+// it the factor of a block below 127^2 / 2^128 would be infinite.
+__device__ __forceinline__ float avg_round(float m, float inv, float random) {
     const float h = __builtin_fmaf(random, -0x1p-16f, 0.5f);   // 1/2 - u
     const float w = __builtin_fmaf(h, h, -0.25f);              // -u (1 - u)
-    const float root = __builtin_amdgcn_sqrtf(fmaxf(__builtin_fmaf(__builtin_fabsf(m), scale, w), 0.0f));
+    const float root = __builtin_amdgcn_sqrtf(fmaxf(__builtin_fmaf(__builtin_fabsf(m) * inv, 16129.0f, w), 0.0f));
     return fminf(__builtin_rintf(root + h), 127.0f);
 }
 
@@ -270,7 +271,7 @@ __device__ __forceinline__ float sq_round(float z, float random) {
     return fmaxf(c, __builtin_amdgcn_fmed3f(z * 0x1p100f, 0.0f, 1.0f));
 }
 
-// Bound by arithmetic: about 61 operations and four of a quarter of the rate an
+// Bound by arithmetic: about 62 operations and four of a quarter of the rate an
 // element. Hence one root of v for the step and for its code, factors of a block
 // in front of the loop over its elements (a lane's eight), codes of both signs
 // as c + 128 until they are packed, and an instance of its own for rounding at
@@ -320,7 +321,7 @@ __global__ __launch_bounds__(kAdamThreads) void adamw8_kernel(AdamArgs) {
             top_v = max(top_v, __float_as_uint(v));
         }
         const float new_m = block_max(top_m), new_v = block_max(top_v);
-        const float inv_m = 16129.0f * __builtin_amdgcn_rcpf(new_m), inv_v = 65025.0f * __builtin_amdgcn_rsqf(new_v);
+        const float inv_m = __builtin_amdgcn_rcpf(new_m), inv_v = 65025.0f * __builtin_amdgcn_rsqf(new_v);
         const uint64_t vec = (uint64_t)i / V;
         uint32_t r = SEEDED ? mix32((uint32_t)vec ^ key ^ mix32((uint32_t)(vec >> 32))) | 1u : 0u;
         cm = cv = u32x2{0, 0};

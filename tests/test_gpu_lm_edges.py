@@ -35,3 +35,39 @@ def test_codes_are_the_rounded_quotients(dyt, M, N, group):
     s = scales.cpu().repeat_interleave(group or N, 1)[:, :N]
     want = (y.cpu() / s).to(torch.float8_e4m3fn)
     assert torch.equal(q.cpu().view(torch.uint8), want.view(torch.uint8))
+
+
+# ------------------------------------------------------------------- AdamW
+def nearest_avg_codes(m, scale):
+    """Codes of float32 moments m [blocks, 128], rounded to the nearest, and
+    where the rounding is sure."""
+    y = m.abs() / scale.view(-1, 1) * 127.0 ** 2
+    low = y.sqrt().floor().clamp(max=126)
+    middle = low.square() + low + 0.5
+    # the scale's reciprocal (2 U), two products, 1/4 and 1/2 of the rounding's square
+    # and sum; the root (2 U) counts twice in y
+    slack = 16 * U * y + 1e-4
+    sure = (y - middle).abs() > slack
+    return torch.where(y > middle, low + 1, low) * m.sign(), sure
+
+
+def test_first_moments_of_small_blocks(dyt):
+    """Blocks whose largest first moment is next to the least scale, 2^-126:
+    every moment gets its own code."""
+    most = torch.tensor([1.2e-38, 1e-37, 1e-36, 4e-35, 5e-35, 1e-30, 1e-3])
+    g = torch.Generator().manual_seed(3)
+    part = torch.rand(len(most), 128, generator=g) * torch.exp(-4 * torch.rand(len(most), 128, generator=g))
+    part[:, 0], part[:, 1], part[:, 2], part[:, 3:6] = 1.0, 0.25, 1e-3, 0.0
+    grad = (part * most.view(-1, 1)) * torch.where(torch.rand(part.shape, generator=g) < 0.5, -10.0, 10.0)
+    n = grad.numel()
+    p = torch.zeros(n, device="cuda")
+    m, v = torch.zeros(n, dtype=torch.int8, device="cuda"), torch.zeros(n, dtype=torch.uint8, device="cuda")
+    sm, sv = (torch.zeros(len(most), device="cuda") for _ in range(2))
+    dyt.dyt_adamw_step([p], [grad.view(-1).cuda()], [m], [v], lr=1e-3, step=1, avg_scales=[sm], sq_scales=[sv])
+    moment = torch.from_numpy(grad.numpy() * np.float32(1 - 0.9)).double()   # a float32 product
+    scale = moment.abs().amax(1).clamp(min=2.0 ** -126)
+    assert torch.equal(d(sm), scale)
+    want, sure = nearest_avg_codes(moment, scale)
+    got = d(m).view(-1, 128)
+    assert (got[sure] == want[sure]).all() and sure.double().mean() > 0.98
+    assert ((got - want).abs() <= 1).all()
