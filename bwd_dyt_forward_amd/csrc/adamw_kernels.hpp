@@ -307,16 +307,18 @@ __global__ __launch_bounds__(kAdamThreads) void adamw8_kernel(AdamArgs) {
                     cv[j / 4] |= (uint32_t)((const uint8_t*)x.sq)[i + j] << (8 * (j % 4));
                 }
         }
-        const float am = x.avg_scale[i / kAdamBlock] * (1.0f / 16129.0f);
+        // beta1 a: a / 127^2 would be subnormal, with few digits, in blocks below 2e-34
+        AdamStep of_block = step;
+        of_block.beta1 *= x.avg_scale[i / kAdamBlock];
         const float av = __builtin_amdgcn_sqrtf(x.sq_scale[i / kAdamBlock]) * (1.0f / 65025.0f);
         uint32_t top_m = 0, top_v = 0;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const float c = (float)avg_code(cm[j / 4], j % 4), c2 = sq_code(cv[j / 4], j % 4);
-            m[j] = c * __builtin_fabsf(c) * am;
+            m[j] = c * __builtin_fabsf(c) * (1.0f / 16129.0f);   // the moment / a
             const float r = c2 * c2 * av;
             float v = r * r;
-            root[j] = step(p[j], m[j], v, g[j] * gs);
+            root[j] = of_block(p[j], m[j], v, g[j] * gs);
             top_m = max(top_m, __float_as_uint(m[j]) & 0x7fffffffu);
             top_v = max(top_v, __float_as_uint(v));
         }

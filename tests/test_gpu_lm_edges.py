@@ -71,3 +71,29 @@ def test_first_moments_of_small_blocks(dyt):
     got = d(m).view(-1, 128)
     assert (got[sure] == want[sure]).all() and sure.double().mean() > 0.98
     assert ((got - want).abs() <= 1).all()
+
+
+def test_small_first_moments_keep_their_digits(dyt):
+    """A step without a gradient: beta1 times what the codes stand for, in blocks
+    with scales down to the least."""
+    scale = torch.tensor([2.0 ** -126, 1.3e-38, 1e-37, 1e-36, 3e-34, 1e-20])
+    g = torch.Generator().manual_seed(4)
+    codes = torch.randint(-126, 127, (len(scale), 128), generator=g).to(torch.int8)
+    codes[:, 0] = 127
+    n = codes.numel()
+    p, grad = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    m, v = codes.view(-1).cuda(), torch.zeros(n, dtype=torch.uint8, device="cuda")
+    sm, sv = scale.cuda(), torch.zeros(len(scale), device="cuda")
+    before = avg_values(m, sm).view(-1, 128)
+    dyt.dyt_adamw_step([p], [grad], [m], [v], lr=1e-3, step=5, avg_scales=[sm], sq_scales=[sv])
+    want = (0.9 * before[:, 0]).clamp(min=2.0 ** -126)
+    # 1 / 127^2, its product, beta1 and beta1's with the scale, the moment; a subnormal
+    # product is off by half its step, which 127^2 codes multiply no further
+    check("scales", sm, want, 6 * U * want + 2 * 2.0 ** -150)
+    codes_after, sure = nearest_avg_codes(0.9 * before, want)
+    # subnormal moments are rounded to multiples of 2^-149 (beta1 times the scale too)
+    y = (0.9 * before).abs() / want.view(-1, 1) * 127.0 ** 2
+    low = y.sqrt().floor()
+    coarse = 3 * 2.0 ** -150 / want.view(-1, 1) * 127.0 ** 2
+    sure &= ((y - (low.square() + low + 0.5)).abs() > coarse)
+    assert (d(m).view(-1, 128)[sure] == codes_after[sure]).all() and sure.double().mean() > 0.95
