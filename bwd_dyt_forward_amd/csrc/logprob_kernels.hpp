@@ -529,7 +529,8 @@ __global__ __launch_bounds__(kLpThreads) void lp_bwd_kernel(LpArgs a) {
         for (int i = 0; i < VEC; ++i) {
             const float z = __builtin_fmaf(x[i], a.scale, -lse);
             const float p = __builtin_amdgcn_exp2f(z * kLog2e);
-            x[i] = p * __builtin_fmaf(fmaxf(z, -1e30f), slope, base);
+            // (a masked place's z and large upstream gradients have products that are not finite)
+            x[i] = p == 0.0f ? 0.0f : p * __builtin_fmaf(z, slope, base);
         }
         if ((uint32_t)(at - e) < (uint32_t)VEC) {
 #pragma unroll

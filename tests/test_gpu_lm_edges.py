@@ -37,6 +37,32 @@ def test_codes_are_the_rounded_quotients(dyt, M, N, group):
     assert torch.equal(q.cpu().view(torch.uint8), want.view(torch.uint8))
 
 
+# ------------------------------------------------- token log probabilities
+def make(seed, T, V, dt=torch.float32, spread=2.5):
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn(T, V, generator=g) * spread).to(dt)
+    t = torch.randint(0, V, (T,), generator=g)
+    t[::9] = -1
+    return x, t.cuda(), torch.randn(T, generator=g).cuda(), torch.randn(T, generator=g).cuda() * 0.3
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("V", [40, 3000, 70000])
+def test_masked_places_under_large_gradients(dyt, dt, V):
+    """A masked place's gradient is 0, however large the upstream gradients are."""
+    x, t, up, ue = make(1, 4, V, DTYPES[dt])
+    t[:] = 1
+    x[:, 3::2] = -math.inf
+    x[1, 3::2] = torch.finfo(DTYPES[dt]).min
+    x = x.cuda()
+    hidden = d(x) < -1e4
+    _, entropy, lse = dyt.dyt_logprob_forward(x, t)
+    for big in (1e9, 1e30, 3e38):
+        for a, b in ((up, ue * big / 3), (up * big / 4, None), (up * big / 4, ue * big / 3)):
+            dx = d(dyt.dyt_logprob_backward(x, t, entropy, lse, a, b))
+            assert (dx[hidden] == 0).all(), (big, b is None)
+
+
 # ------------------------------------------------------------------- AdamW
 def nearest_avg_codes(m, scale):
     """Codes of float32 moments m [blocks, 128], rounded to the nearest, and
