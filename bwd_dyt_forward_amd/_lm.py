@@ -47,6 +47,8 @@ SIGNATURES = {
                                   _vp]),
     "dyt_logprob_forward_workspace_size": (_size, [_i64, _i64, _int, _int]),
     "dyt_logprob_forward": (_int, [_vp, _i64] + [_vp] * 7 + [_size, _i64, _i64, _f32, _int, _int, _int, _vp]),
+    "dyt_logprob_forward_norm": (_int, [_vp, _i64] + [_vp] * 8 + [_size, _i64, _i64, _f32, _int, _int, _int, _vp]),
+    "dyt_logprob_backward_norm": (_int, [_vp, _i64] + [_vp] * 6 + [_i64, _i64, _i64, _f32, _int, _int, _vp]),
     "dyt_logprob_backward": (_int, [_vp, _i64] + [_vp] * 6 + [_i64, _i64, _i64, _f32, _int, _int, _vp]),
     "dyt_adamw_step": (_int, [_vp, _i64, _vp, _vp]),
     "dyt_adamw_values": (_int, [_vp, _i64, _int, _vp]),
@@ -61,7 +63,10 @@ def _load(path: str = LM_LIB_PATH, any_sources: bool = False) -> ctypes.CDLL:
             "(python bwd_dyt_forward_amd/build.py, or __graft_entry__.build())")
     lib = ctypes.CDLL(path, mode=ctypes.RTLD_LOCAL)
     for name, (res, args) in SIGNATURES.items():
-        fn = getattr(lib, name)
+        fn = getattr(lib, name, None)
+        if fn is None:
+            raise ImportError(f"{path} has no {name}: it was built from other sources; rebuild it "
+                              "(python bwd_dyt_forward_amd/build.py)")
         fn.restype = res
         fn.argtypes = args
     found = lib.dyt_lm_abi_version()
@@ -351,6 +356,12 @@ def _check_scale(scale: float) -> None:
         raise ValueError("scale must be positive and finite")
 
 
+def _check_norm(norm, logits: torch.Tensor, T: int) -> None:
+    _on_device("norm", norm, logits)
+    if norm.dtype != torch.float32 or norm.shape != (T, 2) or not norm.is_contiguous():
+        raise ValueError(f"norm must be a contiguous float32 [{T}, 2] tensor")
+
+
 def dyt_logprob_forward_workspace_size(T: int, V: int, top: int, dtype) -> int:
     return int(lm_lib.dyt_logprob_forward_workspace_size(int(T), int(V), int(top), _lib._code(dtype)))
 
@@ -358,12 +369,14 @@ def dyt_logprob_forward_workspace_size(T: int, V: int, top: int, dtype) -> int:
 def dyt_logprob_forward(logits: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0, top: int = 0,
                         logp: torch.Tensor | None = None, entropy: torch.Tensor | None = None,
                         lse: torch.Tensor | None = None, top_logp: torch.Tensor | None = None,
-                        top_tokens: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+                        top_tokens: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                        norm: torch.Tensor | None = None, stream=None):
     """Log probabilities of tokens [T] (int32 or int64) under the rows of
     logits [T, V] (row-strided; times ``scale``, an inverse temperature):
     (logp, entropy, lse), each [T] float32; with ``top`` also (top_logp,
     top_tokens) [T, top], the largest logits' in falling order, equal ones from
-    the lowest place on. A token outside [0, V) has logp 0."""
+    the lowest place on. A token outside [0, V) has logp 0. ``norm`` (float32 [T, 2]),
+    where given, is filled for the backward."""
     ld = _check_rows("logits", logits)
     T, V = logits.shape
     code = _code("logits", logits)
@@ -396,9 +409,15 @@ def dyt_logprob_forward(logits: torch.Tensor, tokens: torch.Tensor, *, scale: fl
     else:
         top_logp = top_tokens = None
     workspace, need = _workspace(workspace, lm_lib.dyt_logprob_forward_workspace_size(T, V, top, code), logits)
-    _check("dyt_logprob_forward", lm_lib.dyt_logprob_forward(
-        logits.data_ptr(), ld, tokens.data_ptr(), logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(), _ptr(top_logp),
-        _ptr(top_tokens), _ptr(workspace), need, T, V, scale, top, code, bits, s))
+    if norm is None:
+        _check("dyt_logprob_forward", lm_lib.dyt_logprob_forward(
+            logits.data_ptr(), ld, tokens.data_ptr(), logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
+            _ptr(top_logp), _ptr(top_tokens), _ptr(workspace), need, T, V, scale, top, code, bits, s))
+    else:
+        _check_norm(norm, logits, T)
+        _check("dyt_logprob_forward_norm", lm_lib.dyt_logprob_forward_norm(
+            logits.data_ptr(), ld, tokens.data_ptr(), logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
+            norm.data_ptr(), _ptr(top_logp), _ptr(top_tokens), _ptr(workspace), need, T, V, scale, top, code, bits, s))
     if stream is not None:
         _keep_alive_on(stream, *(t for t, m in zip((logp, entropy, lse, top_logp, top_tokens, workspace), made)
                                  if m and t is not None))
@@ -407,10 +426,13 @@ def dyt_logprob_forward(logits: torch.Tensor, tokens: torch.Tensor, *, scale: fl
 
 def dyt_logprob_backward(logits: torch.Tensor, tokens: torch.Tensor, entropy: torch.Tensor, lse: torch.Tensor,
                          dlogp: torch.Tensor | None = None, dentropy: torch.Tensor | None = None, *,
-                         scale: float = 1.0, dlogits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                         scale: float = 1.0, dlogits: torch.Tensor | None = None, norm: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
     """Gradient of the logits for those of logp and entropy ([T] float32, each
-    may be None) with the forward's entropy and lse. ``dlogits`` may be the
-    logits themselves."""
+    may be None) with the forward's entropy and lse. With the forward's ``norm`` it
+    is taken from that, not from lse: lse is one float32 number, and the gradient's
+    relative error then grows with |lse| 2^-23. ``dlogits`` may be the logits
+    themselves."""
     ld = _check_rows("logits", logits)
     T, V = logits.shape
     code = _code("logits", logits)
@@ -427,9 +449,15 @@ def dyt_logprob_backward(logits: torch.Tensor, tokens: torch.Tensor, entropy: to
         ldd = V
     else:
         ldd = _check_rows("dlogits", dlogits, logits)
-    _check("dyt_logprob_backward", lm_lib.dyt_logprob_backward(
-        logits.data_ptr(), ld, tokens.data_ptr(), entropy.data_ptr(), lse.data_ptr(), _ptr(dlogp), _ptr(dentropy),
-        dlogits.data_ptr(), ldd, T, V, scale, code, bits, s))
+    if norm is None:
+        _check("dyt_logprob_backward", lm_lib.dyt_logprob_backward(
+            logits.data_ptr(), ld, tokens.data_ptr(), entropy.data_ptr(), lse.data_ptr(), _ptr(dlogp), _ptr(dentropy),
+            dlogits.data_ptr(), ldd, T, V, scale, code, bits, s))
+    else:
+        _check_norm(norm, logits, T)
+        _check("dyt_logprob_backward_norm", lm_lib.dyt_logprob_backward_norm(
+            logits.data_ptr(), ld, tokens.data_ptr(), entropy.data_ptr(), norm.data_ptr(), _ptr(dlogp), _ptr(dentropy),
+            dlogits.data_ptr(), ldd, T, V, scale, code, bits, s))
     if stream is not None and made:
         _keep_alive_on(stream, dlogits)
     return dlogits

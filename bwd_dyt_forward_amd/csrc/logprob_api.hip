@@ -85,7 +85,7 @@ void with_type(int dt, F&& f) {
 }
 
 int lp_forward(const void* logits, int64_t ld, const void* tokens, float* logp, float* entropy, float* lse,
-               float* top_logp, int64_t* top_tokens, void* ws, size_t ws_bytes, int64_t T, int64_t V, float scale,
+               float* norm, float* top_logp, int64_t* top_tokens, void* ws, size_t ws_bytes, int64_t T, int64_t V, float scale,
                int top, int dt, int bits, void* stream) {
     if (int e = lp_shape(T, V, top, dt)) return e;
     if (ld == 0) ld = V;
@@ -95,7 +95,7 @@ int lp_forward(const void* logits, int64_t ld, const void* tokens, float* logp, 
         (top > 0) != (top_tokens != nullptr))
         return DYT_ERR_INVALID_ARG;
     const int64_t s = dtype_size(dt);
-    if (!aligned({logits}, s) || !aligned({tokens}, bits / 8) || !aligned({logp, entropy, lse, top_logp}, 4) ||
+    if (!aligned({logits}, s) || !aligned({tokens}, bits / 8) || !aligned({logp, entropy, lse, norm, top_logp}, 4) ||
         !aligned({top_tokens}, 8))
         return DYT_ERR_MISALIGNED;
     const LpPlan p = lp_plan(T, V, top, dt);
@@ -103,11 +103,11 @@ int lp_forward(const void* logits, int64_t ld, const void* tokens, float* logp, 
     if (p.bytes && (ws_bytes < p.bytes || !ws)) return DYT_ERR_WORKSPACE_TOO_SMALL;
     if (p.bytes && !aligned({ws}, 16)) return DYT_ERR_MISALIGNED;
     const Range in[] = {{logits, ((T - 1) * ld + V) * s}, {tokens, T * (bits / 8)}};
-    const Range out[] = {{logp, T * 4}, {entropy, T * 4}, {lse, T * 4}, {top_logp, T * top * 4},
+    const Range out[] = {{logp, T * 4}, {entropy, T * 4}, {lse, T * 4}, {norm, T * 8}, {top_logp, T * top * 4},
                          {top_tokens, T * top * 8}, {ws, (int64_t)p.bytes}};
-    if (!disjoint(in, 2, out, 6)) return DYT_ERR_INVALID_ARG;
+    if (!disjoint(in, 2, out, 7)) return DYT_ERR_INVALID_ARG;
     LpArgs a{};
-    a.logits = logits; a.tokens = tokens; a.logp = logp; a.entropy = entropy; a.lse = lse;
+    a.logits = logits; a.tokens = tokens; a.logp = logp; a.entropy = entropy; a.lse = lse; a.norm = norm;
     a.top_logp = top_logp; a.top_tokens = top_tokens; a.part = (float*)ws;
     a.part_top = (uint64_t*)((uint8_t*)ws + p.part_bytes);
     a.ld = ld; a.T = T; a.V = V; a.part_len = p.part_len; a.parts = p.parts; a.top = top; a.token_bits = bits;
@@ -123,8 +123,9 @@ int lp_forward(const void* logits, int64_t ld, const void* tokens, float* logp, 
     return hip_status();
 }
 
+// The sums of the rows: lse, or norm in its place.
 int lp_backward(const void* logits, int64_t ld, const void* tokens, const float* entropy, const float* lse,
-                const float* dlogp, const float* dentropy, void* dlogits, int64_t ldd, int64_t T, int64_t V, float scale,
+                const float* norm, const float* dlogp, const float* dentropy, void* dlogits, int64_t ldd, int64_t T, int64_t V, float scale,
                 int dt, int bits, void* stream) {
     if (int e = lp_shape(T, V, 0, dt)) return e;
     if (ld == 0) ld = V;
@@ -132,19 +133,19 @@ int lp_backward(const void* logits, int64_t ld, const void* tokens, const float*
     if ((bits != 32 && bits != 64) || !(scale > 0.0f) || std::isinf(scale) || !pitch_ok(T, V, ld) || !pitch_ok(T, V, ldd))
         return DYT_ERR_INVALID_ARG;
     if (T == 0) return DYT_OK;
-    if (V == 0 || !logits || !tokens || !entropy || !lse || !dlogits) return DYT_ERR_INVALID_ARG;
+    if (V == 0 || !logits || !tokens || !entropy || (!lse && !norm) || !dlogits) return DYT_ERR_INVALID_ARG;
     const int64_t s = dtype_size(dt);
-    if (!aligned({logits, dlogits}, s) || !aligned({tokens}, bits / 8) || !aligned({entropy, lse, dlogp, dentropy}, 4))
+    if (!aligned({logits, dlogits}, s) || !aligned({tokens}, bits / 8) || !aligned({entropy, lse, norm, dlogp, dentropy}, 4))
         return DYT_ERR_MISALIGNED;
     const LpPlan p = lp_plan(T, V, 0, dt, true);
     if (p.grid >= ((int64_t)1 << 24)) return DYT_ERR_INVALID_ARG;
     const bool same = dlogits == logits && ldd == ld;   // in place
     const Range in[] = {{same ? nullptr : logits, ((T - 1) * ld + V) * s}, {tokens, T * (bits / 8)}, {entropy, T * 4},
-                        {lse, T * 4}, {dlogp, T * 4}, {dentropy, T * 4}};
+                        {lse, T * 4}, {norm, T * 8}, {dlogp, T * 4}, {dentropy, T * 4}};
     const Range out[] = {{dlogits, ((T - 1) * ldd + V) * s}};
-    if (!disjoint(in, 6, out, 1)) return DYT_ERR_INVALID_ARG;
+    if (!disjoint(in, 7, out, 1)) return DYT_ERR_INVALID_ARG;
     LpArgs a{};
-    a.logits = logits; a.tokens = tokens; a.entropy = const_cast<float*>(entropy); a.lse = const_cast<float*>(lse);
+    a.logits = logits; a.tokens = tokens; a.entropy = const_cast<float*>(entropy); a.lse = const_cast<float*>(lse); a.norm = const_cast<float*>(norm);
     a.dlogp = dlogp; a.dentropy = dentropy; a.dlogits = dlogits; a.ld = ld; a.ldd = ldd; a.T = T; a.V = V;
     a.part_len = p.part_len; a.parts = p.parts; a.token_bits = bits; a.tpr = p.tpr;
     a.scale = scale;
@@ -170,15 +171,31 @@ size_t dyt_logprob_forward_workspace_size(int64_t T, int64_t V, int top, int dty
 int dyt_logprob_forward(const void* logits, int64_t ld, const void* tokens, float* logp, float* entropy, float* lse,
                         float* top_logp, int64_t* top_tokens, void* workspace, size_t workspace_bytes, int64_t T,
                         int64_t V, float scale, int top, int dtype, int token_bits, void* stream) {
-    return lp_forward(logits, ld, tokens, logp, entropy, lse, top_logp, top_tokens, workspace, workspace_bytes, T, V,
-                      scale, top, dtype, token_bits, stream);
+    return lp_forward(logits, ld, tokens, logp, entropy, lse, nullptr, top_logp, top_tokens, workspace,
+                      workspace_bytes, T, V, scale, top, dtype, token_bits, stream);
+}
+
+int dyt_logprob_forward_norm(const void* logits, int64_t ld, const void* tokens, float* logp, float* entropy, float* lse,
+                             float* norm, float* top_logp, int64_t* top_tokens, void* workspace,
+                             size_t workspace_bytes, int64_t T, int64_t V, float scale, int top, int dtype,
+                             int token_bits, void* stream) {
+    if (T > 0 && !norm) return DYT_ERR_INVALID_ARG;
+    return lp_forward(logits, ld, tokens, logp, entropy, lse, norm, top_logp, top_tokens, workspace, workspace_bytes,
+                      T, V, scale, top, dtype, token_bits, stream);
 }
 
 int dyt_logprob_backward(const void* logits, int64_t ld, const void* tokens, const float* entropy, const float* lse,
                          const float* dlogp, const float* dentropy, void* dlogits, int64_t ldd, int64_t T, int64_t V,
                          float scale, int dtype, int token_bits, void* stream) {
-    return lp_backward(logits, ld, tokens, entropy, lse, dlogp, dentropy, dlogits, ldd, T, V, scale, dtype, token_bits,
-                       stream);
+    return lp_backward(logits, ld, tokens, entropy, lse, nullptr, dlogp, dentropy, dlogits, ldd, T, V, scale, dtype,
+                       token_bits, stream);
+}
+
+int dyt_logprob_backward_norm(const void* logits, int64_t ld, const void* tokens, const float* entropy,
+                              const float* norm, const float* dlogp, const float* dentropy, void* dlogits, int64_t ldd,
+                              int64_t T, int64_t V, float scale, int dtype, int token_bits, void* stream) {
+    return lp_backward(logits, ld, tokens, entropy, nullptr, norm, dlogp, dentropy, dlogits, ldd, T, V, scale, dtype,
+                       token_bits, stream);
 }
 
 }  // extern "C"

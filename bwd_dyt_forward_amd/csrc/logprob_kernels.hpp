@@ -46,6 +46,7 @@ struct LpArgs {
     float* logp;          // forward's results; the backward reads entropy, lse
     float* entropy;
     float* lse;
+    float* norm;          // [T, 2] or null: m and log2 s; the backward's in place of lse
     float* top_logp;      // [T, top]
     int64_t* top_tokens;
     const float* dlogp;   // backward, each or null
@@ -219,6 +220,10 @@ __device__ __forceinline__ void lp_write(const LpArgs& a, int64_t m, Lse v, floa
     const float log2_s = log2f(v.s);
     const bool none = v.s == 0.0f;   // every logit is -inf
     a.lse[m] = none ? -INFINITY : (v.m + log2_s) * kLn2;
+    if (a.norm) {
+        a.norm[2 * m] = v.m;
+        a.norm[2 * m + 1] = log2_s;   // -inf for none
+    }
     a.entropy[m] = none ? 0.0f : (log2_s - v.t / v.s) * kLn2;
     a.logp[m] = real ? lp_of(v, log2_s, x, k2) : 0.0f;
 }
@@ -493,7 +498,10 @@ __global__ __launch_bounds__(kLpThreads) void lp_join_kernel(LpArgs a) {
 // A tile of kLpBwdVecs vectors a thread of one row (or, of short rows, all of
 // several): neighbouring workgroups read and write neighbouring memory. A row
 // without an upstream gradient counts as zeros.
-template <typename T>
+// NORM: y = k x - m - log2 s from the forward's two numbers, whose difference to k x
+// is small wherever the row's logits lie; the one float32 lse is rounded by up to
+// |lse| 2^-24, and with it every p of the row.
+template <typename T, bool NORM>
 __global__ __launch_bounds__(kLpThreads) void lp_bwd_kernel(LpArgs a) {
     constexpr int VEC = VecOf<T>::n;
     constexpr int U = kLpBwdVecs;
@@ -511,12 +519,15 @@ __global__ __launch_bounds__(kLpThreads) void lp_bwd_kernel(LpArgs a) {
     const int64_t token = a.token_bits == 64 ? ((const int64_t*)a.tokens)[m] : (int64_t)((const int32_t*)a.tokens)[m];
     const bool real = token >= 0 && token < a.V;
     const int at = real ? (int)token + r.skew : -VEC;
-    const float lse = a.lse[m], h = a.entropy[m];
+    const float h = a.entropy[m];
+    const float lse = NORM ? a.norm[2 * (int64_t)m] : a.lse[m];   // or m
+    const float log2_s = NORM ? a.norm[2 * (int64_t)m + 1] : 0.0f;
     const float up = real && a.dlogp ? a.dlogp[m] : 0.0f;
     const float ue = a.dentropy ? a.dentropy[m] : 0.0f;
-    const bool dead = (up == 0.0f && ue == 0.0f) || lse == -INFINITY;
+    const bool dead = (up == 0.0f && ue == 0.0f) || (NORM ? log2_s : lse) == -INFINITY;
     // dx = -scale p (up + ue (z - lse + h)), and scale up more at the token
-    const float base = -a.scale * (up + ue * h), slope = -a.scale * ue;
+    const float base = -a.scale * (up + ue * h), slope = -a.scale * ue * (NORM ? kLn2 : 1.0f);
+    const float factor = NORM ? a.scale * kLog2e : a.scale;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int e = e0 + u * tpr * VEC;
@@ -527,8 +538,9 @@ __global__ __launch_bounds__(kLpThreads) void lp_bwd_kernel(LpArgs a) {
         if (!whole) r.elements(e, x);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            const float z = __builtin_fmaf(x[i], a.scale, -lse);
-            const float p = __builtin_amdgcn_exp2f(z * kLog2e);
+            float z = __builtin_fmaf(x[i], factor, -lse);
+            if constexpr (NORM) z -= log2_s;
+            const float p = __builtin_amdgcn_exp2f(NORM ? z : z * kLog2e);
             // (a masked place's z and large upstream gradients have products that are not finite)
             x[i] = p == 0.0f ? 0.0f : p * __builtin_fmaf(z, slope, base);
         }

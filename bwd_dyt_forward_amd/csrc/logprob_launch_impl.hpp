@@ -33,7 +33,9 @@ constexpr size_t kLpBwdApart = 40000;
 
 template <typename T>
 void lp_launch_backward(const LpArgs& a, int64_t grid, hipStream_t s) {
-    lp_bwd_kernel<T><<<(unsigned)grid, kLpThreads, a.stream ? kLpBwdApart : 0, s>>>(a);
+    const size_t apart = a.stream ? kLpBwdApart : 0;
+    if (a.norm) lp_bwd_kernel<T, true><<<(unsigned)grid, kLpThreads, apart, s>>>(a);
+    else lp_bwd_kernel<T, false><<<(unsigned)grid, kLpThreads, apart, s>>>(a);
 }
 
 }  // namespace dytb

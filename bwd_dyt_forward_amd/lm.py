@@ -176,14 +176,20 @@ class Embedding(nn.Module):
 
 # ------------------------------------------------- token log probabilities
 class LogProbFunction(torch.autograd.Function):
-    """Saves the logits and the rows' entropies and log sums; the probabilities
-    are computed again in the backward."""
+    """Saves the logits and the rows' entropies and log sums (in two numbers each, so
+    that the gradient's digits do not depend on where the logits lie); the
+    probabilities are computed again in the backward."""
 
     @staticmethod
     def forward(ctx, logits: torch.Tensor, tokens: torch.Tensor, scale: float, top: int):
         x2, at = _rows(logits), tokens.reshape(-1).contiguous()
-        logp, entropy, lse, *best = _lm.dyt_logprob_forward(x2, at, scale=scale, top=top)
-        ctx.save_for_backward(x2, at, entropy, lse)
+        # (none for tensors on the host, which the call refuses)
+        norm = None
+        if ctx.needs_input_grad[0] and x2.is_cuda:
+            norm = torch.empty((x2.shape[0], 2), dtype=torch.float32, device=x2.device)
+        more = {} if norm is None else {"norm": norm}
+        logp, entropy, lse, *best = _lm.dyt_logprob_forward(x2, at, scale=scale, top=top, **more)
+        ctx.save_for_backward(x2, at, entropy, lse, norm)
         ctx.set_materialize_grads(False)   # an unused output's gradient arrives as None
         ctx.scale, ctx.shape = scale, logits.shape
         best = tuple(t.view(*tokens.shape, top) for t in best)
@@ -195,11 +201,12 @@ class LogProbFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dlogp, dentropy, *_):
-        x2, at, entropy, lse = ctx.saved_tensors
+        x2, at, entropy, lse, norm = ctx.saved_tensors
         if dlogp is None and dentropy is None:
             return None, None, None, None
         up = [g if g is None else g.reshape(-1).contiguous() for g in (dlogp, dentropy)]
-        dx = _lm.dyt_logprob_backward(x2, at, entropy, lse, *up, scale=ctx.scale)
+        more = {} if norm is None else {"norm": norm}
+        dx = _lm.dyt_logprob_backward(x2, at, entropy, lse, *up, scale=ctx.scale, **more)
         return dx.view(ctx.shape), None, None, None
 
 

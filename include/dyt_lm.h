@@ -120,8 +120,12 @@ int dyt_embed_backward(const void* dy, int64_t lddy, const void* tokens, void* d
  * two: the lowest float32 and bfloat16 values), is a masked place: p = 0 and
  * gradient 0. A row of nothing else has lse = -inf, logp = -inf, entropy 0 and
  * gradient 0. A NaN or +inf
- * makes its row's results NaN. Exponentials below 2^-126 count as 0. The
- * gradient takes p from the float32 lse: its relative error grows with
+ * makes its row's results NaN. Exponentials below 2^-126 count as 0.
+ *
+ * norm: [T, 2] float32, m and log2 s with p[j] = 2^(k x[j] - m - log2 s), k the float32
+ * product of scale and log2(e): a row's lse in powers of two, in two numbers (log2 s
+ * -inf where every place is masked). The gradient from norm keeps its digits
+ * wherever the logits lie; from the one float32 lse its relative error grows with
  * |lse| 2^-23.
  *
  * top_logp, top_tokens: [T, top] (top 0: NULL), the log probabilities
@@ -138,6 +142,13 @@ int dyt_logprob_forward(const void* logits, int64_t ld, const void* tokens, floa
                         void* workspace, size_t workspace_bytes, int64_t T, int64_t V, float scale,
                         int top, int dtype, int token_bits, void* stream);
 
+/* As dyt_logprob_forward, and writes norm. */
+int dyt_logprob_forward_norm(const void* logits, int64_t ld, const void* tokens, float* logp,
+                             float* entropy, float* lse, float* norm, float* top_logp,
+                             int64_t* top_tokens, void* workspace, size_t workspace_bytes,
+                             int64_t T, int64_t V, float scale, int top, int dtype, int token_bits,
+                             void* stream);
+
 /* entropy and lse are the forward's; dlogp and dentropy may each be NULL (no
  * gradient of it). dlogits may be the logits themselves (same address and
  * pitch). A row whose upstream gradients are zero gets zeros, whatever it
@@ -146,6 +157,12 @@ int dyt_logprob_backward(const void* logits, int64_t ld, const void* tokens, con
                          const float* lse, const float* dlogp, const float* dentropy, void* dlogits,
                          int64_t ldd, int64_t T, int64_t V, float scale, int dtype, int token_bits,
                          void* stream);
+
+/* The same with the forward's norm in place of lse. */
+int dyt_logprob_backward_norm(const void* logits, int64_t ld, const void* tokens, const float* entropy,
+                              const float* norm, const float* dlogp, const float* dentropy,
+                              void* dlogits, int64_t ldd, int64_t T, int64_t V, float scale, int dtype,
+                              int token_bits, void* stream);
 
 /* -------------------------------------------------------------------- AdamW
  *

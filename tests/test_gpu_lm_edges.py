@@ -7,7 +7,7 @@ import pytest
 import torch
 from torch import nn
 
-from block_ref import HALF, U, check, d
+from block_ref import HALF, TINY, U, check, d
 from lm_ref import EXP2, LogProb, avg_values
 
 pytestmark = pytest.mark.gpu
@@ -61,6 +61,76 @@ def test_masked_places_under_large_gradients(dyt, dt, V):
         for a, b in ((up, ue * big / 3), (up * big / 4, None), (up * big / 4, ue * big / 3)):
             dx = d(dyt.dyt_logprob_backward(x, t, entropy, lse, a, b))
             assert (dx[hidden] == 0).all(), (big, b is None)
+
+
+def check_gradient(ref, up, ue, scale, dx):
+    """dlogits against the gradient of the logits themselves, in float64."""
+    up = d(up).masked_fill(~ref.real, 0).view(-1, 1)
+    ue = d(ue).view(-1, 1)
+    none = ref.none.view(-1, 1)
+    lp = (ref.x - ref.top) * ref.scale - ref.log_s.masked_fill(ref.none, 0).view(-1, 1)
+    p, h = lp.exp(), ref.entropy.view(-1, 1)
+    lp = lp.masked_fill(lp == -math.inf, 0)
+    hit = torch.zeros_like(p)
+    hit[ref.real, ref.t[ref.real]] = 1
+    want = (scale * (up * (hit - p) - ue * p * (lp + h))).masked_fill(none, 0)
+    away, ls, rel = (v.view(-1, 1) for v in (ref.away, ref.log_s.masked_fill(ref.none, 0).abs(), ref.rel))
+    # p: of its argument the distance to the maximum (two roundings and the factor's
+    # error, 4 U, which counts against the row's mean distance), log s (its sum and its
+    # own error) and their difference; then the exponential
+    rel_p = 8 * U * (lp.abs() + away + ls) + rel + 2 * EXP2
+    # the entropy (as in LogProb.check_forward), z - lse + h and three products
+    off_h = rel * (1 + 2 * away) + 6 * U * (ls + away)
+    size = up.abs() + (ue * h).abs() + (ue * lp).abs()
+    bound = scale * (p * (rel_p + 6 * U) * size + p * ue.abs() * (off_h + rel_p) + 2 * U * (up * hit).abs())
+    # an exponential below float32's normal range counts as 0
+    bound += scale * size * torch.where(p < 2.0 ** -125, 2.0 ** -126, 0.0) + U * want.abs() + 2.0 ** -149
+    check("dlogits", dx, want, 1.02 * bound + HALF[dx.dtype] * want.abs() + TINY[dx.dtype])
+
+
+@pytest.mark.parametrize("T,V", [(300, 32), (50, 1000), (20, 9001), (3, 70001)])
+@pytest.mark.parametrize("offset", [0.0, 30.0, 1000.0, -1000.0, 30000.0])
+@pytest.mark.parametrize("scale", [1.0, 0.7])
+def test_an_offset_of_the_logits_costs_the_gradient_nothing(dyt, T, V, offset, scale):
+    x, t, up, ue = make(V, T, V)
+    x = (x + offset).cuda().requires_grad_()
+    logp, entropy = dyt.token_log_probs(x, t, scale)
+    torch.autograd.backward([logp, entropy], [up, ue])
+    check_gradient(LogProb(x, t, scale), up, ue, scale, x.grad)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("T,V", [(700, 50), (600, 2049), (30, 9001), (2, 130001)])
+def test_the_sums_in_two_numbers(dyt, dt, T, V):
+    """The kernels' own calls: the same results beside norm, its two numbers, strides,
+    in place, masked rows and places, parts of a row, alternatives."""
+    x, t, up, ue = make(V, T, V, DTYPES[dt])
+    x[0, 1::3] = -math.inf
+    if T > 2:
+        x[2] = -math.inf
+    t[0] = 0
+    x = x.cuda()
+    buf = torch.full((T, V + 3), math.nan, dtype=x.dtype, device="cuda")
+    xs = buf[:, 2:2 + V]
+    xs.copy_(x)
+    norm = torch.full((T, 2), math.nan, device="cuda")
+    top = min(V, 5)
+    plain = dyt.dyt_logprob_forward(xs, t, scale=0.7, top=top)
+    got = dyt.dyt_logprob_forward(xs, t, scale=0.7, top=top, norm=norm)
+    assert all(torch.equal(a, b) for a, b in zip(plain, got))
+    ref = LogProb(x, t, 0.7)
+    real = ~ref.none
+    assert (norm.cpu()[ref.none, 1] == -math.inf).all()
+    # (m + log2 s) ln 2 is the lse: the factor k is off by 2 U of the maximum, the rest as in the forward
+    lse = d(norm).sum(1)[real] * math.log(2)
+    check("norm", lse, ref.lse[real], ref.rel[real] + 4 * U * (ref.log_s[real].abs() + ref.m[real].abs()))
+    for a, b in ((up, ue), (up, None), (None, ue)):
+        dx = dyt.dyt_logprob_backward(xs, t, got[1], got[2], a, b, scale=0.7, norm=norm)
+        check_gradient(ref, up if a is not None else 0 * up, ue if b is not None else 0 * ue, 0.7, dx)
+    again = dyt.dyt_logprob_backward(xs, t, got[1], got[2], None, ue, scale=0.7, norm=norm, dlogits=xs)
+    assert again is xs and torch.equal(xs, dx) and torch.isnan(buf[:, :2]).all() and torch.isnan(buf[:, 2 + V:]).all()
+    with pytest.raises(ValueError, match="norm"):
+        dyt.dyt_logprob_forward(x, t, norm=norm[:, 0])
 
 
 # ------------------------------------------------------------------- AdamW
