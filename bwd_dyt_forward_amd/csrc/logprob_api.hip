@@ -35,7 +35,7 @@ int lp_shape(int64_t T, int64_t V, int top, int dt) {
 // vectors a thread at least.
 struct LpPlan {
     int tpr, parts;
-    int64_t part_len, grid;
+    int64_t part_len;
     size_t shared, join_shared, part_bytes, bytes;
 };
 
@@ -56,15 +56,12 @@ LpPlan lp_plan(int64_t T, int64_t V, int top, int dt, bool backward = false) {
         // tiles that follow each other in memory: 290 us for 320 of a workgroup for each row
         p.part_len = kLpBwdVecs * step;
         p.parts = (int)((V + vec - 1 + p.part_len - 1) / p.part_len);
-        p.grid = T * p.parts;
         return p;
     }
     // a row may begin up to vec - 1 places after the 16-byte grid
     const int64_t places = V + vec - 1;
     p.part_len = p.tpr == 256 ? ((places + parts - 1) / parts + step - 1) / step * step : places;
     p.parts = (int)((places + p.part_len - 1) / p.part_len);
-    const int64_t per = 256 / p.tpr;
-    p.grid = (T * p.parts + per - 1) / per;
     if (top) {
         const int64_t lines = p.part_len / (8 * vec);
         p.shared = (size_t)((lines + 1) / 2 + top * 4 * std::max((lines + 255) / 256, 2 * vec)) * 8;
@@ -75,6 +72,32 @@ LpPlan lp_plan(int64_t T, int64_t V, int top, int dt, bool backward = false) {
         p.bytes = p.part_bytes + (size_t)T * p.parts * top * 8;
     }
     return p;
+}
+
+// A launch has fewer than 2^32 threads, 2^24 workgroups: more rows than that take
+// several, launch(arguments, workgroups) for each run of rows.
+template <typename Launch>
+void in_launches(LpArgs a, const LpPlan& p, int64_t elem_bytes, Launch&& launch) {
+    const int64_t per = 256 / p.tpr, most = (((int64_t)1 << 24) - 1) * per / p.parts, T = a.T;
+    for (int64_t done = 0; done < T; done += a.T) {
+        a.T = std::min(most, T - done);
+        launch(a, (a.T * p.parts + per - 1) / per);
+        const int64_t n = a.T;
+        const auto on = [n](auto*& q, int64_t of_row) {
+            using Q = std::remove_reference_t<decltype(q)>;
+            if (q) q = (Q)((uintptr_t)q + (uintptr_t)(n * of_row));
+        };
+        on(a.logits, a.ld * elem_bytes);
+        on(a.dlogits, a.ldd * elem_bytes);
+        on(a.tokens, a.token_bits / 8);
+        for (float** q : {&a.logp, &a.entropy, &a.lse}) on(*q, 4);
+        for (const float** q : {&a.dlogp, &a.dentropy}) on(*q, 4);
+        on(a.norm, 8);
+        on(a.top_logp, 4 * (int64_t)a.top);
+        on(a.top_tokens, 8 * (int64_t)a.top);
+        on(a.part, 16 * (int64_t)p.parts);
+        on(a.part_top, 8 * (int64_t)p.parts * a.top);
+    }
 }
 
 template <typename F>
@@ -99,7 +122,6 @@ int lp_forward(const void* logits, int64_t ld, const void* tokens, float* logp, 
         !aligned({top_tokens}, 8))
         return DYT_ERR_MISALIGNED;
     const LpPlan p = lp_plan(T, V, top, dt);
-    if (p.grid >= ((int64_t)1 << 24) || T >= ((int64_t)1 << 31)) return DYT_ERR_INVALID_ARG;   // 2^32 threads of a launch
     if (p.bytes && (ws_bytes < p.bytes || !ws)) return DYT_ERR_WORKSPACE_TOO_SMALL;
     if (p.bytes && !aligned({ws}, 16)) return DYT_ERR_MISALIGNED;
     const Range in[] = {{logits, ((T - 1) * ld + V) * s}, {tokens, T * (bits / 8)}};
@@ -109,7 +131,7 @@ int lp_forward(const void* logits, int64_t ld, const void* tokens, float* logp, 
     LpArgs a{};
     a.logits = logits; a.tokens = tokens; a.logp = logp; a.entropy = entropy; a.lse = lse; a.norm = norm;
     a.top_logp = top_logp; a.top_tokens = top_tokens; a.part = (float*)ws;
-    a.part_top = (uint64_t*)((uint8_t*)ws + p.part_bytes);
+    a.part_top = p.bytes ? (uint64_t*)((uint8_t*)ws + p.part_bytes) : nullptr;
     a.ld = ld; a.T = T; a.V = V; a.part_len = p.part_len; a.parts = p.parts; a.top = top; a.token_bits = bits;
     a.tpr = p.tpr; a.scale = scale;
     // Logits past the last-level cache (256 MB) leave it to what was written before
@@ -118,7 +140,9 @@ int lp_forward(const void* logits, int64_t ld, const void* tokens, float* logp, 
     // it, is slower with such loads or stores (289 -> 305).
     a.stream = T * V * s >= kPastCache;
     with_type(dt, [&](auto* t) {
-        lp_launch_forward<std::remove_pointer_t<decltype(t)>>(a, p.grid, p.shared, p.join_shared, (hipStream_t)stream);
+        in_launches(a, p, s, [&](const LpArgs& b, int64_t grid) {
+            lp_launch_forward<std::remove_pointer_t<decltype(t)>>(b, grid, p.shared, p.join_shared, (hipStream_t)stream);
+        });
     });
     return hip_status();
 }
@@ -138,7 +162,6 @@ int lp_backward(const void* logits, int64_t ld, const void* tokens, const float*
     if (!aligned({logits, dlogits}, s) || !aligned({tokens}, bits / 8) || !aligned({entropy, lse, norm, dlogp, dentropy}, 4))
         return DYT_ERR_MISALIGNED;
     const LpPlan p = lp_plan(T, V, 0, dt, true);
-    if (p.grid >= ((int64_t)1 << 24)) return DYT_ERR_INVALID_ARG;
     const bool same = dlogits == logits && ldd == ld;   // in place
     const Range in[] = {{same ? nullptr : logits, ((T - 1) * ld + V) * s}, {tokens, T * (bits / 8)}, {entropy, T * 4},
                         {lse, T * 4}, {norm, T * 8}, {dlogp, T * 4}, {dentropy, T * 4}};
@@ -151,7 +174,9 @@ int lp_backward(const void* logits, int64_t ld, const void* tokens, const float*
     a.scale = scale;
     a.stream = T * V * s >= kPastCache;
     with_type(dt, [&](auto* t) {
-        lp_launch_backward<std::remove_pointer_t<decltype(t)>>(a, p.grid, (hipStream_t)stream);
+        in_launches(a, p, s, [&](const LpArgs& b, int64_t grid) {
+            lp_launch_backward<std::remove_pointer_t<decltype(t)>>(b, grid, (hipStream_t)stream);
+        });
     });
     return hip_status();
 }

@@ -133,6 +133,26 @@ def test_the_sums_in_two_numbers(dyt, dt, T, V):
         dyt.dyt_logprob_forward(x, t, norm=norm[:, 0])
 
 
+@pytest.mark.parametrize("back", [False, True])
+def test_more_rows_than_a_launch_has_workgroups(dyt, back):
+    """2^24 rows of a workgroup each and a few more: the last rows as in a call of
+    their own, the first too. With alternatives a row takes a workgroup however
+    short it is, else one of more than 128 vectors does."""
+    T, V, top = (1 << 24) + 37, 1030 if back else 16, 0 if back else 2
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, V, generator=g, device="cuda", dtype=torch.bfloat16)
+    t = torch.randint(-1, V, (T,), generator=g, device="cuda")
+    out = dyt.dyt_logprob_forward(x, t, top=top)
+    parts = [slice(0, 600), slice((1 << 24) - 700, T)]
+    for part in parts:
+        assert all(torch.equal(a[part], b) for a, b in zip(out, dyt.dyt_logprob_forward(x[part], t[part], top=top)))
+    if back:
+        up = torch.randn(T, generator=g, device="cuda")
+        want = [dyt.dyt_logprob_backward(x[s], t[s], out[1][s], out[2][s], up[s]) for s in parts]
+        dyt.dyt_logprob_backward(x, t, out[1], out[2], up, dlogits=x)
+        assert all(torch.equal(x[s], w) for s, w in zip(parts, want))
+
+
 # ------------------------------------------------------------------- AdamW
 def nearest_avg_codes(m, scale):
     """Codes of float32 moments m [blocks, 128], rounded to the nearest, and
