@@ -544,7 +544,7 @@ __global__ __launch_bounds__(kLpThreads) void lp_bwd_kernel(LpArgs a) {
             // (a masked place's z and large upstream gradients have products that are not finite)
             x[i] = p == 0.0f ? 0.0f : p * __builtin_fmaf(z, slope, base);
         }
-        if ((uint32_t)(at - e) < (uint32_t)VEC) {
+        if ((uint32_t)(at - e) < (uint32_t)VEC) {   // (at a masked place too: [j = c] stays 1)
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
                 if (at == e + i) x[i] = __builtin_fmaf(a.scale, up, x[i]);

@@ -118,9 +118,10 @@ int dyt_embed_backward(const void* dy, int64_t lddy, const void* tokens, void* d
  *
  * A logit of -inf, or with scale x below -2.35e38 (float32's range as a power of
  * two: the lowest float32 and bfloat16 values), is a masked place: p = 0 and
- * gradient 0. A row of nothing else has lse = -inf, logp = -inf, entropy 0 and
- * gradient 0. A NaN or +inf
- * makes its row's results NaN. Exponentials below 2^-126 count as 0.
+ * gradient 0, but for the row's own token, whose dx is scale dlogp there too (as
+ * everywhere, [j = c] - p[j] is 1) and whose logp is -inf. A row of nothing else has
+ * lse = -inf, logp = -inf, entropy 0 and gradient 0, the token's included. A NaN, +inf
+ * or scale x above 2.35e38 makes its row's results NaN. Exponentials below 2^-126 count as 0.
  *
  * norm: [T, 2] float32, m and log2 s with p[j] = 2^(k x[j] - m - log2 s), k the float32
  * product of scale and log2(e): a row's lse in powers of two, in two numbers (log2 s

@@ -63,6 +63,27 @@ def test_masked_places_under_large_gradients(dyt, dt, V):
             assert (dx[hidden] == 0).all(), (big, b is None)
 
 
+@pytest.mark.parametrize("V,T", [(32, 200), (3000, 20), (70000, 3)])
+@pytest.mark.parametrize("dt", DTYPES)
+def test_a_masked_token_keeps_its_gradient(dyt, dt, V, T):
+    """The row's own token at a masked place: log probability -inf, gradient scale dlogp
+    there; 0 at the other masked places, and 0 everywhere in a row of nothing else."""
+    X = DTYPES[dt]
+    x, t, up, _ = make(2, T, V, X)
+    t[:] = 5
+    x[:, 4:9] = -math.inf
+    x[1, 4:9] = -math.inf if dt == "f16" else torch.finfo(X).min   # (float16's lowest is far from float32's)
+    x[2] = -math.inf
+    x = x.cuda()
+    logp, entropy, lse = dyt.dyt_logprob_forward(x, t, scale=1.5)
+    assert (logp == -math.inf).all()
+    dx = d(dyt.dyt_logprob_backward(x, t, entropy, lse, up, scale=1.5))
+    want = 1.5 * d(up)
+    want[2] = 0
+    check("at the token", dx[:, 5], want, (U + HALF[X]) * want.abs() + 2.0 ** -24)
+    assert (dx[:, [4, 6, 7, 8]] == 0).all() and (dx[2] == 0).all()
+
+
 def check_gradient(ref, up, ue, scale, dx):
     """dlogits against the gradient of the logits themselves, in float64."""
     up = d(up).masked_fill(~ref.real, 0).view(-1, 1)
