@@ -51,6 +51,7 @@ SIGNATURES = {
     "dyt_logprob_backward_norm": (_int, [_vp, _i64] + [_vp] * 6 + [_i64, _i64, _i64, _f32, _int, _int, _vp]),
     "dyt_logprob_backward": (_int, [_vp, _i64] + [_vp] * 6 + [_i64, _i64, _i64, _f32, _int, _int, _vp]),
     "dyt_adamw_step": (_int, [_vp, _i64, _vp, _vp]),
+    "dyt_adamw_check": (_int, [_vp, _i64, _vp]),
     "dyt_adamw_values": (_int, [_vp, _i64, _int, _vp]),
 }
 
@@ -498,6 +499,26 @@ def dyt_adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, lr, betas=(0.9, 0.99
 
     ``step`` counts from 1. ``lr``, ``step`` (int64) and ``grad_scale`` may be
     device tensors of one element, which a captured step then follows."""
+    table = _adamw_table(params, grads, exp_avgs, exp_avg_sqs, lr=lr, betas=betas, eps=eps, weight_decay=weight_decay,
+                         step=step, masters=masters, avg_scales=avg_scales, sq_scales=sq_scales, grad_scale=grad_scale,
+                         seed=seed, stream=stream)
+    if table is not None:
+        _adamw_run(params, table)
+
+
+def _adamw_check(table) -> None:
+    """Raises what _adamw_run would be refused with."""
+    _check("dyt_adamw_step", lm_lib.dyt_adamw_check(*table[:3]))
+
+
+def _adamw_run(params, table) -> None:
+    _check("dyt_adamw_step", lm_lib.dyt_adamw_step(*table))
+    increment_version(params)
+
+
+def _adamw_table(params, grads, exp_avgs, exp_avg_sqs, *, lr, betas, eps, weight_decay, step, masters=None, avg_scales=None,
+                 sq_scales=None, grad_scale=None, seed=None, stream=None):
+    """dyt_adamw_step's checks; the arguments of the library's call (None of no tensors)."""
     n = len(params)
     if not (len(grads) == len(exp_avgs) == len(exp_avg_sqs) == n):
         raise ValueError("params, grads, exp_avgs and exp_avg_sqs must have equal lengths")
@@ -508,7 +529,7 @@ def dyt_adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, lr, betas=(0.9, 0.99
         if x is not None and len(x) != n:
             raise ValueError(f"{name} must have one entry for each parameter")
     if n == 0:
-        return
+        return None
     dev = params[0].get_device()
     if dev < 0:
         raise ValueError("params must be device tensors")
@@ -558,8 +579,7 @@ def dyt_adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, lr, betas=(0.9, 0.99
             raise ValueError(f"{name} is out of range: {x}")
     options = _ADAMW_OPTIONS.pack(lr, betas[0], betas[1], eps, weight_decay, int(step), lr_dev, step_dev, gs,
                                   (seed or 0) & 0xFFFFFFFF, 0 if seed is None else 1, 8 if bits8 else 32, 0)
-    _check("dyt_adamw_step", lm_lib.dyt_adamw_step(b"".join(rows), n, options, s))
-    increment_version(params)
+    return b"".join(rows), n, options, s
 
 
 _CODE = _lib._TORCH_TO_CODE

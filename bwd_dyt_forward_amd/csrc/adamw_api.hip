@@ -65,7 +65,8 @@ bool in_batches(AdamArgs& a, int64_t count, int64_t chunk, Pick&& pick, Launch&&
     return any;
 }
 
-int adamw_step(const dyt_adamw_tensor* list, int64_t count, const dyt_adamw_options* o, void* stream) {
+// What a step refuses; `bytes`: of all its tensors.
+int adamw_check(const dyt_adamw_tensor* list, int64_t count, const dyt_adamw_options* o, int64_t& bytes) {
     if (count < 0 || count > 0x7fffffff || !o || (count > 0 && !list)) return DYT_ERR_INVALID_ARG;
     for (double v : {o->lr, o->beta1, o->beta2, o->eps, o->weight_decay})
         if (!(v >= 0.0) || std::isinf(v)) return DYT_ERR_INVALID_ARG;
@@ -100,9 +101,15 @@ int adamw_step(const dyt_adamw_tensor* list, int64_t count, const dyt_adamw_opti
         add(spans, t.sq_scale, blocks * 4, true);
         add(spans, t.master, t.n * 4, true);
     }
-    int64_t bytes = 0;
+    bytes = 0;
     for (const Span& t : spans) bytes += (int64_t)(t.hi - t.lo);
-    if (!apart(spans)) return DYT_ERR_INVALID_ARG;
+    return apart(spans) ? DYT_OK : DYT_ERR_INVALID_ARG;
+}
+
+int adamw_step(const dyt_adamw_tensor* list, int64_t count, const dyt_adamw_options* o, void* stream) {
+    int64_t bytes = 0;
+    if (int e = adamw_check(list, count, o, bytes)) return e;
+    const bool bits8 = o->state_bits == 8;
     AdamArgs a{};
     const bool stream_past = bytes >= ((int64_t)256 << 20);   // the last-level cache
     a.seeded = o->seeded; a.seed = o->seed;
@@ -181,6 +188,15 @@ using namespace dytb;
 extern "C" {
 
 // The lists of spans are the only memory these calls ask the host for.
+int dyt_adamw_check(const dyt_adamw_tensor* tensors, int64_t count, const dyt_adamw_options* options) {
+    try {
+        int64_t bytes = 0;
+        return adamw_check(tensors, count, options, bytes);
+    } catch (const std::bad_alloc&) {
+        return DYT_ERR_INVALID_ARG;
+    }
+}
+
 int dyt_adamw_step(const dyt_adamw_tensor* tensors, int64_t count, const dyt_adamw_options* options, void* stream) {
     try {
         return adamw_step(tensors, count, options, stream);

@@ -267,17 +267,45 @@ class AdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        # all calls of the step, checked before the first one: a step that is refused
+        # moves and counts nothing
+        calls, counters = [], []
         for index, group in enumerate(self.param_groups):
-            self._step_group(index, group, grad_scale)
+            self._group_calls(index, group, grad_scale, calls, counters)
+        tables = None   # (one call is checked by itself; of tensors on the host the first is refused)
+        if len(calls) > 1 and any(args[0][0].is_cuda for args, _, _ in calls):
+            tables = [_lm._adamw_table(*args, **kw) for args, kw, _ in calls]
+            for table in tables:
+                _lm._adamw_check(table)
+        for counter in counters:
+            counter.add_(1)
+        begun = False
+        try:
+            for i, (args, kw, states) in enumerate(calls):
+                if tables:
+                    _lm._adamw_run(args[0], tables[i])
+                else:
+                    _lm.dyt_adamw_step(*args, **kw)
+                begun = True
+                if not isinstance(kw["step"], torch.Tensor):
+                    for s in states:
+                        s["step"] = kw["step"]
+        except Exception:
+            for counter in () if begun else counters:
+                counter.sub_(1)
+            raise
         return loss
 
-    def _step_group(self, index: int, group: dict, grad_scale) -> None:
+    def _group_calls(self, index: int, group: dict, grad_scale, calls: list, counters: list) -> None:
+        """Appends a group's calls, (arguments, keywords, states) each, and its
+        counter on the device."""
         with_grad = [p for p in group["params"] if p.grad is not None]
         if not with_grad:
             return
         if with_grad[0].is_cuda and torch.cuda.is_current_stream_capturing():
             # a replay would take the same step again, or begin with new states
-            if not group["capturable"] or not all(isinstance(self.state[p].get("step"), torch.Tensor) for p in with_grad):
+            counts = [self.state[p].get("step") for p in with_grad]
+            if not group["capturable"] or not all(isinstance(c, torch.Tensor) and c is counts[0] for c in counts):
                 raise RuntimeError("a captured step needs capturable=True and a step before the capture")
         for p in with_grad:
             if p.grad.is_sparse:
@@ -288,33 +316,43 @@ class AdamW(torch.optim.Optimizer):
         if group["capturable"]:
             if len(with_grad) != len(group["params"]):
                 raise ValueError("capturable: every parameter of a group needs a gradient")
-            steps = states[0]["step"]
-            if not isinstance(steps, torch.Tensor):
-                steps = torch.tensor(steps, dtype=torch.int64, device=with_grad[0].device)
-            for s in states:   # one counter for the group
-                s["step"] = steps
-            steps.add_(1)
+            if not self._join_counters(states, with_grad[0].device):
+                raise ValueError("capturable: a group's parameters have taken different numbers of steps")
+            counters.append(states[0]["step"])
         # a call for each step count and width of the states
-        calls: dict = {}
+        members: dict = {}
         for p, s in zip(with_grad, states):
             at = None if group["capturable"] else int(s["step"]) + 1
-            calls.setdefault((at, "avg_scale" in s), []).append((p, s))
-        for (at, bits8), members in calls.items():
-            ps = [p for p, _ in members]
-            ss = [s for _, s in members]
+            members.setdefault((at, "avg_scale" in s), []).append((p, s))
+        for (at, bits8), pairs in members.items():
+            ps = [p for p, _ in pairs]
+            ss = [s for _, s in pairs]
             kw = {}
             if bits8:
                 kw.update(avg_scales=[s["avg_scale"] for s in ss], sq_scales=[s["sq_scale"] for s in ss],
                           seed=group["seed"] + 0x632BE5AB * index)
             if group["master"]:
                 kw.update(masters=[s.get("master") for s in ss])
-            _lm.dyt_adamw_step(ps, [p.grad.contiguous() for p in ps], [s["exp_avg"] for s in ss],
-                               [s["exp_avg_sq"] for s in ss], lr=group["lr"], betas=group["betas"], eps=group["eps"],
-                               weight_decay=group["weight_decay"], step=ss[0]["step"] if at is None else at,
-                               grad_scale=grad_scale, **kw)
-            if at is not None:
-                for s in ss:   # last: a call that is refused is no step
-                    s["step"] = at
+            args = (ps, [p.grad.contiguous() for p in ps], [s["exp_avg"] for s in ss], [s["exp_avg_sq"] for s in ss])
+            kw.update(lr=group["lr"], betas=group["betas"], eps=group["eps"], weight_decay=group["weight_decay"],
+                      step=ss[0]["step"] if at is None else at, grad_scale=grad_scale)
+            calls.append((args, kw, ss))
+
+    @staticmethod
+    def _join_counters(states: list, device) -> bool:
+        """One counter on the device for all the states, whose counts have to be equal
+        (else False, and they stay as they are)."""
+        counter = states[0]["step"]
+        if isinstance(counter, torch.Tensor) and all(s["step"] is counter for s in states):
+            return True
+        counts = {int(s["step"]) for s in states}
+        if len(counts) > 1:
+            return False
+        if not (isinstance(counter, torch.Tensor) and counter.dtype == torch.int64 and counter.device == device):
+            counter = torch.tensor(counts.pop(), dtype=torch.int64, device=device)
+        for s in states:
+            s["step"] = counter
+        return True
 
     def load_state_dict(self, state_dict) -> None:
         """As the base class's, but the states keep their own types (it casts
@@ -327,3 +365,7 @@ class AdamW(torch.optim.Optimizer):
                 if isinstance(value, torch.Tensor):
                     value = value.detach().to(p.device, copy=True)
                 self.state[p][name] = value
+        for group in self.param_groups:   # (counts that differ are refused by the next step)
+            states = [self.state[p] for p in group["params"] if "step" in self.state.get(p, ())]
+            if group["capturable"] and states:
+                self._join_counters(states, group["params"][0].device)

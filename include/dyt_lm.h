@@ -217,6 +217,10 @@ typedef struct dyt_adamw_options {
 int dyt_adamw_step(const dyt_adamw_tensor* tensors, int64_t count, const dyt_adamw_options* options,
                    void* stream);
 
+/* The status that dyt_adamw_step would refuse this call with, or DYT_OK; enqueues
+ * nothing. (For a step of several calls, all or none of which are to be taken.) */
+int dyt_adamw_check(const dyt_adamw_tensor* tensors, int64_t count, const dyt_adamw_options* options);
+
 /* The values [n] of values_dtype that 8-bit codes stand for; second: 0 the
  * first moment's codes, 1 the second's. */
 typedef struct dyt_adamw_codes {

@@ -234,3 +234,36 @@ def test_small_first_moments_keep_their_digits(dyt):
     coarse = 3 * 2.0 ** -150 / want.view(-1, 1) * 127.0 ** 2
     sure &= ((y - (low.square() + low + 0.5)).abs() > coarse)
     assert (d(m).view(-1, 128)[sure] == codes_after[sure]).all() and sure.double().mean() > 0.95
+
+
+def test_a_refused_step_moves_and_counts_nothing(dyt):
+    """Two widths of states and two groups: the last call of the step is refused."""
+    for capturable in (False, True):
+        for second in (False, True):
+            a, b, w = (nn.Parameter(torch.randn(64, 100, device="cuda")) for _ in range(3))
+            small = nn.Parameter(torch.randn(40, device="cuda"))
+            groups = [{"params": [small, a]}, {"params": [b, w]}] if second else [{"params": [small, a, b, w]}]
+            opt = dyt.AdamW(groups, state_bits=8, capturable=capturable)
+            params = [small, a, b, w]
+            for x in params:
+                x.grad = torch.ones_like(x)
+            opt.step()
+            before = [x.detach().clone() for x in params]
+            states = [{k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in opt.state[x].items()} for x in params]
+            w.data = w.data.t()
+            w.grad = torch.ones_like(w)
+            with pytest.raises(ValueError):
+                opt.step()
+            w.data = w.data.t()
+            w.grad = torch.ones_like(w)
+            # memory that is written twice: found by the library
+            keep = opt.state[w]["exp_avg_sq"]
+            opt.state[w]["exp_avg_sq"] = opt.state[b]["exp_avg_sq"]
+            with pytest.raises(RuntimeError):
+                opt.step()
+            opt.state[w]["exp_avg_sq"] = keep
+            assert all(torch.equal(x, y) for x, y in zip(params, before))
+            for x, s in zip(params, states):
+                assert all(torch.equal(v, s[k]) if isinstance(v, torch.Tensor) else v == s[k] for k, v in opt.state[x].items())
+            opt.step()
+            assert all(int(opt.state[x]["step"]) == 2 and not torch.equal(x, y) for x, y in zip(params, before))
