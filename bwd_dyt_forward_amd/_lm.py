@@ -48,7 +48,7 @@ SIGNATURES = {
     "dyt_logprob_forward_workspace_size": (_size, [_i64, _i64, _int, _int]),
     "dyt_logprob_forward": (_int, [_vp, _i64] + [_vp] * 7 + [_size, _i64, _i64, _f32, _int, _int, _int, _vp]),
     "dyt_logprob_forward_norm": (_int, [_vp, _i64] + [_vp] * 8 + [_size, _i64, _i64, _f32, _int, _int, _int, _vp]),
-    "dyt_logprob_backward_norm": (_int, [_vp, _i64] + [_vp] * 6 + [_i64, _i64, _i64, _f32, _int, _int, _vp]),
+    "dyt_logprob_backward_norm": (_int, [_vp, _i64] + [_vp] * 5 + [_i64, _i64, _i64, _f32, _int, _int, _vp]),
     "dyt_logprob_backward": (_int, [_vp, _i64] + [_vp] * 6 + [_i64, _i64, _i64, _f32, _int, _int, _vp]),
     "dyt_adamw_step": (_int, [_vp, _i64, _vp, _vp]),
     "dyt_adamw_check": (_int, [_vp, _i64, _vp]),
@@ -359,8 +359,8 @@ def _check_scale(scale: float) -> None:
 
 def _check_norm(norm, logits: torch.Tensor, T: int) -> None:
     _on_device("norm", norm, logits)
-    if norm.dtype != torch.float32 or norm.shape != (T, 2) or not norm.is_contiguous():
-        raise ValueError(f"norm must be a contiguous float32 [{T}, 2] tensor")
+    if norm.dtype != torch.float32 or norm.shape != (T, 3) or not norm.is_contiguous():
+        raise ValueError(f"norm must be a contiguous float32 [{T}, 3] tensor")
 
 
 def dyt_logprob_forward_workspace_size(T: int, V: int, top: int, dtype) -> int:
@@ -376,7 +376,7 @@ def dyt_logprob_forward(logits: torch.Tensor, tokens: torch.Tensor, *, scale: fl
     logits [T, V] (row-strided; times ``scale``, an inverse temperature):
     (logp, entropy, lse), each [T] float32; with ``top`` also (top_logp,
     top_tokens) [T, top], the largest logits' in falling order, equal ones from
-    the lowest place on. A token outside [0, V) has logp 0. ``norm`` (float32 [T, 2]),
+    the lowest place on. A token outside [0, V) has logp 0. ``norm`` (float32 [T, 3]),
     where given, is filled for the backward."""
     ld = _check_rows("logits", logits)
     T, V = logits.shape
@@ -425,15 +425,15 @@ def dyt_logprob_forward(logits: torch.Tensor, tokens: torch.Tensor, *, scale: fl
     return (logp, entropy, lse, top_logp, top_tokens) if top else (logp, entropy, lse)
 
 
-def dyt_logprob_backward(logits: torch.Tensor, tokens: torch.Tensor, entropy: torch.Tensor, lse: torch.Tensor,
+def dyt_logprob_backward(logits: torch.Tensor, tokens: torch.Tensor, entropy: torch.Tensor | None = None,
+                         lse: torch.Tensor | None = None,
                          dlogp: torch.Tensor | None = None, dentropy: torch.Tensor | None = None, *,
                          scale: float = 1.0, dlogits: torch.Tensor | None = None, norm: torch.Tensor | None = None,
                          stream=None) -> torch.Tensor:
     """Gradient of the logits for those of logp and entropy ([T] float32, each
-    may be None) with the forward's entropy and lse. With the forward's ``norm`` it
-    is taken from that, not from lse: lse is one float32 number, and the gradient's
-    relative error then grows with |lse| 2^-23. ``dlogits`` may be the logits
-    themselves."""
+    may be None) with the forward's entropy and lse, or with its ``norm`` in their
+    place: lse is one float32 number, and the relative error of a gradient from it
+    grows with |lse| 2^-23. ``dlogits`` may be the logits themselves."""
     ld = _check_rows("logits", logits)
     T, V = logits.shape
     code = _code("logits", logits)
@@ -441,8 +441,12 @@ def dyt_logprob_backward(logits: torch.Tensor, tokens: torch.Tensor, entropy: to
     if tokens.shape != (T,):
         raise ValueError(f"tokens must have shape ({T},)")
     _check_scale(scale)
-    _check_stats(logits, T, entropy=entropy, lse=lse,
-                 **{n: t for n, t in (("dlogp", dlogp), ("dentropy", dentropy)) if t is not None})
+    stats = {"entropy": entropy, "lse": lse} if norm is None else {}
+    if dlogp is not None:
+        stats["dlogp"] = dlogp
+    if dentropy is not None:
+        stats["dentropy"] = dentropy
+    _check_stats(logits, T, **stats)
     s = _stream_for(logits, stream)
     made = dlogits is None
     if made:
@@ -457,8 +461,8 @@ def dyt_logprob_backward(logits: torch.Tensor, tokens: torch.Tensor, entropy: to
     else:
         _check_norm(norm, logits, T)
         _check("dyt_logprob_backward_norm", lm_lib.dyt_logprob_backward_norm(
-            logits.data_ptr(), ld, tokens.data_ptr(), entropy.data_ptr(), norm.data_ptr(), _ptr(dlogp), _ptr(dentropy),
-            dlogits.data_ptr(), ldd, T, V, scale, code, bits, s))
+            logits.data_ptr(), ld, tokens.data_ptr(), norm.data_ptr(), _ptr(dlogp), _ptr(dentropy), dlogits.data_ptr(),
+            ldd, T, V, scale, code, bits, s))
     if stream is not None and made:
         _keep_alive_on(stream, dlogits)
     return dlogits

@@ -92,7 +92,7 @@ void in_launches(LpArgs a, const LpPlan& p, int64_t elem_bytes, Launch&& launch)
         on(a.tokens, a.token_bits / 8);
         for (float** q : {&a.logp, &a.entropy, &a.lse}) on(*q, 4);
         for (const float** q : {&a.dlogp, &a.dentropy}) on(*q, 4);
-        on(a.norm, 8);
+        on(a.norm, 12);
         on(a.top_logp, 4 * (int64_t)a.top);
         on(a.top_tokens, 8 * (int64_t)a.top);
         on(a.part, 16 * (int64_t)p.parts);
@@ -125,7 +125,7 @@ int lp_forward(const void* logits, int64_t ld, const void* tokens, float* logp, 
     if (p.bytes && (ws_bytes < p.bytes || !ws)) return DYT_ERR_WORKSPACE_TOO_SMALL;
     if (p.bytes && !aligned({ws}, 16)) return DYT_ERR_MISALIGNED;
     const Range in[] = {{logits, ((T - 1) * ld + V) * s}, {tokens, T * (bits / 8)}};
-    const Range out[] = {{logp, T * 4}, {entropy, T * 4}, {lse, T * 4}, {norm, T * 8}, {top_logp, T * top * 4},
+    const Range out[] = {{logp, T * 4}, {entropy, T * 4}, {lse, T * 4}, {norm, T * 12}, {top_logp, T * top * 4},
                          {top_tokens, T * top * 8}, {ws, (int64_t)p.bytes}};
     if (!disjoint(in, 2, out, 7)) return DYT_ERR_INVALID_ARG;
     LpArgs a{};
@@ -147,7 +147,7 @@ int lp_forward(const void* logits, int64_t ld, const void* tokens, float* logp, 
     return hip_status();
 }
 
-// The sums of the rows: lse, or norm in its place.
+// The sums of the rows: entropy and lse, or norm in their place.
 int lp_backward(const void* logits, int64_t ld, const void* tokens, const float* entropy, const float* lse,
                 const float* norm, const float* dlogp, const float* dentropy, void* dlogits, int64_t ldd, int64_t T, int64_t V, float scale,
                 int dt, int bits, void* stream) {
@@ -157,14 +157,14 @@ int lp_backward(const void* logits, int64_t ld, const void* tokens, const float*
     if ((bits != 32 && bits != 64) || !(scale > 0.0f) || std::isinf(scale) || !pitch_ok(T, V, ld) || !pitch_ok(T, V, ldd))
         return DYT_ERR_INVALID_ARG;
     if (T == 0) return DYT_OK;
-    if (V == 0 || !logits || !tokens || !entropy || (!lse && !norm) || !dlogits) return DYT_ERR_INVALID_ARG;
+    if (V == 0 || !logits || !tokens || (!norm && (!entropy || !lse)) || !dlogits) return DYT_ERR_INVALID_ARG;
     const int64_t s = dtype_size(dt);
     if (!aligned({logits, dlogits}, s) || !aligned({tokens}, bits / 8) || !aligned({entropy, lse, norm, dlogp, dentropy}, 4))
         return DYT_ERR_MISALIGNED;
     const LpPlan p = lp_plan(T, V, 0, dt, true);
     const bool same = dlogits == logits && ldd == ld;   // in place
     const Range in[] = {{same ? nullptr : logits, ((T - 1) * ld + V) * s}, {tokens, T * (bits / 8)}, {entropy, T * 4},
-                        {lse, T * 4}, {norm, T * 8}, {dlogp, T * 4}, {dentropy, T * 4}};
+                        {lse, T * 4}, {norm, T * 12}, {dlogp, T * 4}, {dentropy, T * 4}};
     const Range out[] = {{dlogits, ((T - 1) * ldd + V) * s}};
     if (!disjoint(in, 7, out, 1)) return DYT_ERR_INVALID_ARG;
     LpArgs a{};
@@ -216,10 +216,11 @@ int dyt_logprob_backward(const void* logits, int64_t ld, const void* tokens, con
                        token_bits, stream);
 }
 
-int dyt_logprob_backward_norm(const void* logits, int64_t ld, const void* tokens, const float* entropy,
-                              const float* norm, const float* dlogp, const float* dentropy, void* dlogits, int64_t ldd,
-                              int64_t T, int64_t V, float scale, int dtype, int token_bits, void* stream) {
-    return lp_backward(logits, ld, tokens, entropy, nullptr, norm, dlogp, dentropy, dlogits, ldd, T, V, scale, dtype,
+int dyt_logprob_backward_norm(const void* logits, int64_t ld, const void* tokens, const float* norm,
+                              const float* dlogp, const float* dentropy, void* dlogits, int64_t ldd, int64_t T, int64_t V,
+                              float scale, int dtype, int token_bits, void* stream) {
+    if (T > 0 && !norm) return DYT_ERR_INVALID_ARG;
+    return lp_backward(logits, ld, tokens, nullptr, nullptr, norm, dlogp, dentropy, dlogits, ldd, T, V, scale, dtype,
                        token_bits, stream);
 }
 

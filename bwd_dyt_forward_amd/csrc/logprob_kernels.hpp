@@ -46,7 +46,7 @@ struct LpArgs {
     float* logp;          // forward's results; the backward reads entropy, lse
     float* entropy;
     float* lse;
-    float* norm;          // [T, 2] or null: m and log2 s; the backward's in place of lse
+    float* norm;          // [T, 3] or null: m, log2 s and the entropy, for the backward
     float* top_logp;      // [T, top]
     int64_t* top_tokens;
     const float* dlogp;   // backward, each or null
@@ -220,11 +220,13 @@ __device__ __forceinline__ void lp_write(const LpArgs& a, int64_t m, Lse v, floa
     const float log2_s = log2f(v.s);
     const bool none = v.s == 0.0f;   // every logit is -inf
     a.lse[m] = none ? -INFINITY : (v.m + log2_s) * kLn2;
+    const float entropy = none ? 0.0f : (log2_s - v.t / v.s) * kLn2;
+    a.entropy[m] = entropy;
     if (a.norm) {
-        a.norm[2 * m] = v.m;
-        a.norm[2 * m + 1] = log2_s;   // -inf for none
+        a.norm[3 * m] = v.m;
+        a.norm[3 * m + 1] = log2_s;   // -inf for none
+        a.norm[3 * m + 2] = entropy;
     }
-    a.entropy[m] = none ? 0.0f : (log2_s - v.t / v.s) * kLn2;
     a.logp[m] = real ? lp_of(v, log2_s, x, k2) : 0.0f;
 }
 
@@ -519,9 +521,10 @@ __global__ __launch_bounds__(kLpThreads) void lp_bwd_kernel(LpArgs a) {
     const int64_t token = a.token_bits == 64 ? ((const int64_t*)a.tokens)[m] : (int64_t)((const int32_t*)a.tokens)[m];
     const bool real = token >= 0 && token < a.V;
     const int at = real ? (int)token + r.skew : -VEC;
-    const float h = a.entropy[m];
-    const float lse = NORM ? a.norm[2 * (int64_t)m] : a.lse[m];   // or m
-    const float log2_s = NORM ? a.norm[2 * (int64_t)m + 1] : 0.0f;
+    const float* norm = NORM ? a.norm + 3 * (int64_t)m : nullptr;
+    const float lse = NORM ? norm[0] : a.lse[m];   // or m
+    const float log2_s = NORM ? norm[1] : 0.0f;
+    const float h = NORM ? norm[2] : a.entropy[m];
     const float up = real && a.dlogp ? a.dlogp[m] : 0.0f;
     const float ue = a.dentropy ? a.dentropy[m] : 0.0f;
     const bool dead = (up == 0.0f && ue == 0.0f) || (NORM ? log2_s : lse) == -INFINITY;

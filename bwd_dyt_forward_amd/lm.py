@@ -176,37 +176,40 @@ class Embedding(nn.Module):
 
 # ------------------------------------------------- token log probabilities
 class LogProbFunction(torch.autograd.Function):
-    """Saves the logits and the rows' entropies and log sums (in two numbers each, so
-    that the gradient's digits do not depend on where the logits lie); the
-    probabilities are computed again in the backward."""
+    """Saves the logits and, of each row, its log sum in two numbers (so that the
+    gradient's digits do not depend on where the logits lie) and its entropy, which
+    the caller may change in its own copy; the probabilities are computed again in the
+    backward."""
 
     @staticmethod
     def forward(ctx, logits: torch.Tensor, tokens: torch.Tensor, scale: float, top: int):
         x2, at = _rows(logits), tokens.reshape(-1).contiguous()
-        # (none for tensors on the host, which the call refuses)
-        norm = None
-        if ctx.needs_input_grad[0] and x2.is_cuda:
-            norm = torch.empty((x2.shape[0], 2), dtype=torch.float32, device=x2.device)
-        more = {} if norm is None else {"norm": norm}
-        logp, entropy, lse, *best = _lm.dyt_logprob_forward(x2, at, scale=scale, top=top, **more)
-        ctx.save_for_backward(x2, at, entropy, lse, norm)
         ctx.set_materialize_grads(False)   # an unused output's gradient arrives as None
         ctx.scale, ctx.shape = scale, logits.shape
+        if x2.is_cuda and ctx.needs_input_grad[0]:
+            norm = torch.empty((x2.shape[0], 3), dtype=torch.float32, device=x2.device)
+            logp, entropy, _, *best = _lm.dyt_logprob_forward(x2, at, scale=scale, top=top, norm=norm)
+            ctx.save_for_backward(x2, at, norm)
+        else:   # (the call refuses tensors on the host)
+            logp, entropy, lse, *best = _lm.dyt_logprob_forward(x2, at, scale=scale, top=top)
+            ctx.save_for_backward(x2, at, entropy, lse)
+            if ctx.needs_input_grad[0]:
+                entropy = entropy.clone()   # the caller may change its results, the backward needs the entropy
         best = tuple(t.view(*tokens.shape, top) for t in best)
         ctx.mark_non_differentiable(*best)
-        if ctx.needs_input_grad[0]:
-            entropy = entropy.clone()   # the caller may change its results, the backward needs the entropy
         return (logp.view(tokens.shape), entropy.view(tokens.shape), *best)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dlogp, dentropy, *_):
-        x2, at, entropy, lse, norm = ctx.saved_tensors
+        x2, at, *sums = ctx.saved_tensors
         if dlogp is None and dentropy is None:
             return None, None, None, None
         up = [g if g is None else g.reshape(-1).contiguous() for g in (dlogp, dentropy)]
-        more = {} if norm is None else {"norm": norm}
-        dx = _lm.dyt_logprob_backward(x2, at, entropy, lse, *up, scale=ctx.scale, **more)
+        if len(sums) == 1:
+            dx = _lm.dyt_logprob_backward(x2, at, None, None, *up, scale=ctx.scale, norm=sums[0])
+        else:
+            dx = _lm.dyt_logprob_backward(x2, at, *sums, *up, scale=ctx.scale)
         return dx.view(ctx.shape), None, None, None
 
 

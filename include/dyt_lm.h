@@ -123,9 +123,9 @@ int dyt_embed_backward(const void* dy, int64_t lddy, const void* tokens, void* d
  * lse = -inf, logp = -inf, entropy 0 and gradient 0, the token's included. A NaN, +inf
  * or scale x above 2.35e38 makes its row's results NaN. Exponentials below 2^-126 count as 0.
  *
- * norm: [T, 2] float32, m and log2 s with p[j] = 2^(k x[j] - m - log2 s), k the float32
- * product of scale and log2(e): a row's lse in powers of two, in two numbers (log2 s
- * -inf where every place is masked). The gradient from norm keeps its digits
+ * norm: [T, 3] float32, m and log2 s with p[j] = 2^(k x[j] - m - log2 s), k the float32
+ * product of scale and log2(e), and the entropy: a row's lse in powers of two, in two
+ * numbers (log2 s -inf where every place is masked). The gradient from norm keeps its digits
  * wherever the logits lie; from the one float32 lse its relative error grows with
  * |lse| 2^-23.
  *
@@ -159,11 +159,11 @@ int dyt_logprob_backward(const void* logits, int64_t ld, const void* tokens, con
                          int64_t ldd, int64_t T, int64_t V, float scale, int dtype, int token_bits,
                          void* stream);
 
-/* The same with the forward's norm in place of lse. */
-int dyt_logprob_backward_norm(const void* logits, int64_t ld, const void* tokens, const float* entropy,
-                              const float* norm, const float* dlogp, const float* dentropy,
-                              void* dlogits, int64_t ldd, int64_t T, int64_t V, float scale, int dtype,
-                              int token_bits, void* stream);
+/* The same with the forward's norm in place of entropy and lse. */
+int dyt_logprob_backward_norm(const void* logits, int64_t ld, const void* tokens, const float* norm,
+                              const float* dlogp, const float* dentropy, void* dlogits, int64_t ldd,
+                              int64_t T, int64_t V, float scale, int dtype, int token_bits,
+                              void* stream);
 
 /* -------------------------------------------------------------------- AdamW
  *

@@ -134,7 +134,7 @@ def test_the_sums_in_two_numbers(dyt, dt, T, V):
     buf = torch.full((T, V + 3), math.nan, dtype=x.dtype, device="cuda")
     xs = buf[:, 2:2 + V]
     xs.copy_(x)
-    norm = torch.full((T, 2), math.nan, device="cuda")
+    norm = torch.full((T, 3), math.nan, device="cuda")
     top = min(V, 5)
     plain = dyt.dyt_logprob_forward(xs, t, scale=0.7, top=top)
     got = dyt.dyt_logprob_forward(xs, t, scale=0.7, top=top, norm=norm)
@@ -143,12 +143,13 @@ def test_the_sums_in_two_numbers(dyt, dt, T, V):
     real = ~ref.none
     assert (norm.cpu()[ref.none, 1] == -math.inf).all()
     # (m + log2 s) ln 2 is the lse: the factor k is off by 2 U of the maximum, the rest as in the forward
-    lse = d(norm).sum(1)[real] * math.log(2)
+    assert torch.equal(norm[:, 2], got[1])
+    lse = d(norm)[:, :2].sum(1)[real] * math.log(2)
     check("norm", lse, ref.lse[real], ref.rel[real] + 4 * U * (ref.log_s[real].abs() + ref.m[real].abs()))
     for a, b in ((up, ue), (up, None), (None, ue)):
-        dx = dyt.dyt_logprob_backward(xs, t, got[1], got[2], a, b, scale=0.7, norm=norm)
+        dx = dyt.dyt_logprob_backward(xs, t, None, None, a, b, scale=0.7, norm=norm)
         check_gradient(ref, up if a is not None else 0 * up, ue if b is not None else 0 * ue, 0.7, dx)
-    again = dyt.dyt_logprob_backward(xs, t, got[1], got[2], None, ue, scale=0.7, norm=norm, dlogits=xs)
+    again = dyt.dyt_logprob_backward(xs, t, dentropy=ue, scale=0.7, norm=norm, dlogits=xs)
     assert again is xs and torch.equal(xs, dx) and torch.isnan(buf[:, :2]).all() and torch.isnan(buf[:, 2 + V:]).all()
     with pytest.raises(ValueError, match="norm"):
         dyt.dyt_logprob_forward(x, t, norm=norm[:, 0])
