@@ -147,11 +147,15 @@ __device__ __forceinline__ void store_vec(T* p, int64_t row, int c, int N, const
 }
 
 __device__ __forceinline__ float inv_sqrt(float v) {
-    // one Newton step on the hardware estimate
+    // One Newton step on the hardware estimate, which takes a subnormal for 0: small
+    // values are scaled, by powers of two.
+    const bool small = v < 0x1p-100f;
+    if (small) v *= 0x1p60f;
     const float y = __builtin_amdgcn_rsqf(v);
     const float e = __builtin_fmaf(-v * y, y, 1.0f);
     const float z = __builtin_fmaf(0.5f * y, e, y);
-    return (v > 0.0f && v < INFINITY) ? z : y;   // 0 and inf keep the estimate's inf and 0
+    const float r = (v > 0.0f && v < INFINITY) ? z : y;   // 0 and inf keep the estimate's inf and 0
+    return small ? r * 0x1p30f : r;
 }
 
 // TPR threads per row, TH per workgroup. NT: 1 nontemporal stores, 2 loads as

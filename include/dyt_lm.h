@@ -40,7 +40,8 @@ const char* dyt_lm_build_id(void);
  * x, y, dy, dx, h, r, dres: [M, N] of x_dtype; ld*: row pitch in elements
  * (>= N; 0 means N). gamma, dgamma: [N] of param_dtype. rstd: [M] float32.
  * The squares are float32: a row whose sum of squares passes 3.4e38 has
- * rstd = 0. M == 0 or N == 0: nothing is read; the backward still writes
+ * rstd = 0, and elements below 1e-19 lose digits in their squares (which matters with
+ * an eps of 0 only). M == 0 or N == 0: nothing is read; the backward still writes
  * zeros to dgamma.
  */
 int dyt_rms_forward(const void* x, int64_t ldx, const void* gamma, void* y, int64_t ldy,

@@ -37,6 +37,27 @@ def test_codes_are_the_rounded_quotients(dyt, M, N, group):
     assert torch.equal(q.cpu().view(torch.uint8), want.view(torch.uint8))
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [8, 300, 5000, 70001])
+def test_squares_below_the_normal_range(dyt, dt, N):
+    """Elements of 3e-20 without an eps: their squares are subnormal."""
+    x = torch.full((3, N), 3e-20).to(DTYPES[dt]).cuda()
+    x[1] = 3e-19
+    x[2, ::2] = -x[2, ::2]
+    gamma, beta = torch.ones(N, device="cuda"), torch.zeros(N, device="cuda")
+    y, rstd = dyt.dyt_rms_forward(x, gamma, 0.0)
+    # a square of 9e-40 is rounded by up to 2^-150, as is each sum, and the mean once more
+    # by its factor: 3 in 9e-40 / 2^-150, half of it in the root
+    bound = 2 * 2.0 ** -150 / 8.9e-40 + 8 * U + N / 256 * U
+    want = 1 / d(x).square().mean(1).sqrt()
+    check("rstd", rstd, want, (bound + (80 + N / 256) * U) * want)
+    n = d(x) * want.view(-1, 1)
+    check("y", y, n, (bound + HALF[y.dtype] + (80 + N / 256) * U) * n.abs())
+    if N % 2 == 0:   # a mean of zero
+        _, mean, r = dyt.dyt_ln_forward(x[2:], gamma, beta, 0.0)
+        check("layer norm's rstd", r, want[2:], (bound + (80 + N / 256) * U) * want[2:])
+
+
 # ------------------------------------------------- token log probabilities
 def make(seed, T, V, dt=torch.float32, spread=2.5):
     g = torch.Generator().manual_seed(seed)
