@@ -156,11 +156,16 @@ __device__ __forceinline__ void store_some(T* p, int64_t n, const float* v) {
 struct AdamStep {
     float beta1, one_beta1, beta2, one_beta2, eps, keep, rate, root_corr2;
 
-    // Returns the second moment's root.
-    __device__ __forceinline__ float operator()(float& p, float& m, float& v, float g) const {
+    // Returns the second moment's root. SMALL: of subnormal moments too, which the
+    // hardware's root takes for 0 (with an eps of 0 the step would be infinite); free beside
+    // float32 states, while 8-bit states, where the arithmetic is the bound, hold no such moments.
+    template <bool SMALL>
+    __device__ __forceinline__ float step(float& p, float& m, float& v, float g) const {
         m = __builtin_fmaf(m, beta1, g * one_beta1);
         v = __builtin_fmaf(v, beta2, g * g * one_beta2);
-        const float root = __builtin_amdgcn_sqrtf(v);
+        const bool small = SMALL && v < 0x1p-100f;
+        float root = __builtin_amdgcn_sqrtf(small ? v * 0x1p60f : v);
+        if (small) root *= 0x1p-30f;
         const float inv = __builtin_amdgcn_rcpf(__builtin_fmaf(root, root_corr2, eps));
         p = __builtin_fmaf(-rate * m, inv, p * keep);
         return root;
@@ -218,7 +223,7 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(AdamArgs) {
         for (int u = 0; u < U; ++u) {
             const int64_t i = base + u * kAdamThreads * V, n = decltype(whole)::value ? V : x.n - i;
 #pragma unroll
-            for (int j = 0; j < V; ++j) step(p[u][j], m[u][j], v[u][j], g[u][j] * gs);
+            for (int j = 0; j < V; ++j) step.step<true>(p[u][j], m[u][j], v[u][j], g[u][j] * gs);
             if constexpr (MASTER) store_some<float, V, NT>(x.master + i, n, p[u]);
             store_some<TP, V, NT>((TP*)x.param + i, n, p[u]);
             store_some<float, V, NT>((float*)x.avg + i, n, m[u]);
@@ -318,7 +323,7 @@ __global__ __launch_bounds__(kAdamThreads) void adamw8_kernel(AdamArgs) {
             m[j] = c * __builtin_fabsf(c) * (1.0f / 16129.0f);   // the moment / a
             const float r = c2 * c2 * av;
             float v = r * r;
-            root[j] = of_block(p[j], m[j], v, g[j] * gs);
+            root[j] = of_block.step<false>(p[j], m[j], v, g[j] * gs);
             top_m = max(top_m, __float_as_uint(m[j]) & 0x7fffffffu);
             top_v = max(top_v, __float_as_uint(v));
         }

@@ -182,7 +182,8 @@ int dyt_logprob_backward_norm(const void* logits, int64_t ld, const void* tokens
  * between two codes takes the upper one if a random number in (0, 1) is below
  * its place between them: with `seeded` one that depends on seed, step, the
  * tensor's place in the list and the element's index, else 1/2. The second
- * moment's code is at least 1 where the moment is not zero. The step itself
+ * moment's code is at least 1 where the moment is not zero; one below 2^-126 counts as
+ * zero, in the step too. The step itself
  * uses the values before they are coded. A NaN or infinite moment spoils its
  * block's codes. All zero bytes and scales are states of zero.
  *

@@ -258,6 +258,34 @@ def test_small_first_moments_keep_their_digits(dyt):
     assert (d(m).view(-1, 128)[sure] == codes_after[sure]).all() and sure.double().mean() > 0.95
 
 
+@pytest.mark.parametrize("master", [False, True])
+def test_second_moments_below_the_normal_range(dyt, master):
+    """Gradients of 1e-18 to 3e-20 without an eps: the second moments are subnormal, and
+    the first step is lr wide all the same."""
+    g = torch.tensor([1e-18, 1e-19, 3e-20, 3e-20], device="cuda").repeat_interleave(300)
+    g[-300:] *= -1
+    n = g.numel()
+    p = torch.zeros(n, device="cuda", dtype=torch.bfloat16 if master else torch.float32)
+    m, v, copy = (torch.zeros(n, device="cuda") for _ in range(3))
+    dyt.dyt_adamw_step([p], [g], [m], [v], lr=0.5, betas=(0.9, 0.99), eps=0.0, weight_decay=0.0, step=1,
+                       masters=[copy] if master else None)
+    # v: the gradient's square and its product with 1 - beta2 are rounded to multiples of 2^-149,
+    # half of which counts in the root; else some ten roundings
+    bound = 0.5 * ((2.0 ** -150 / (0.01 * d(g).square()) + 2.0 ** -150 / d(g).square()) / 2 + 10 * U + 2 * EXP2)
+    check("step", copy if master else p, -0.5 * d(g).sign(), 1.01 * bound)
+
+
+def test_second_moments_in_8_bits_below_the_normal_range(dyt):
+    """They count as zero: code 0, the least scale, and the step that eps leaves."""
+    g = torch.tensor([1e-18, 3e-20], device="cuda").repeat_interleave(128)
+    p, m, v = torch.zeros(256, device="cuda"), torch.zeros(256, dtype=torch.int8, device="cuda"), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    sm, sv = (torch.zeros(2, device="cuda") for _ in range(2))
+    dyt.dyt_adamw_step([p], [g], [m], [v], lr=0.5, weight_decay=0.0, step=1, avg_scales=[sm], sq_scales=[sv])
+    assert (m == 127).all() and (v == 0).all() and (sv == 2.0 ** -126).all()
+    want = -0.5 * d(g) / 1e-8
+    check("step", p, want, (10 * U + EXP2) * want.abs() + 1e-9 * want.abs())
+
+
 def test_a_refused_step_moves_and_counts_nothing(dyt):
     """Two widths of states and two groups: the last call of the step is refused."""
     for capturable in (False, True):
