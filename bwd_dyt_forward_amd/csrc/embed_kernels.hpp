@@ -23,11 +23,14 @@ namespace dytb {
 
 constexpr int kRadixBits = 9, kRadix = 1 << kRadixBits;
 // One workgroup of 16 waves sorts up to kSortOne tokens alone, in one launch;
-// beyond, workgroups of 4 waves take a tile each and a pass is a launch. (A
-// round of 64 tokens is some 70 instructions of a wave: 16,384 tokens keep one
-// CU's vector units 8 us a pass.)
+// beyond, workgroups of 4 waves take a tile each and a pass is two launches. The
+// whole gradient (64 bfloat16 columns, V of 500, 50,000 and 300,000: one, two and three
+// passes) with one workgroup and with many, in us: 2,049 tokens 21.3, 21.6, 37.2 and
+// 24.4, 30.5, 51.4; 4,096 tokens 23.9, 26.8, 45.5 and 25.2, 32.1, 52.8; 6,000 tokens 26.6,
+// 32.9, 59.2 and 24.6, 33.0, 55.7; 8,192 tokens 29.5, 37.4, 67.8 and 24.9, 33.0, 55.1;
+// 16,384 tokens 39.4, 59.6, 111.4 and 24.0, 35.3, 58.9.
 constexpr int kSortOneWaves = 16, kSortManyWaves = 4;
-constexpr int64_t kSortOne = 16384;
+constexpr int64_t kSortOne = 5120;
 constexpr int kSortTile = 1024;
 constexpr int kScanTiles = 64;          // up to here every workgroup adds up the tiles before it itself
 constexpr int kEmbVec = 8;              // columns of a thread

@@ -8,7 +8,7 @@ import torch
 from torch import nn
 
 from block_ref import HALF, TINY, U, check, d
-from lm_ref import EXP2, LogProb, avg_values
+from lm_ref import EXP2, LogProb, avg_values, check_embed_backward
 
 pytestmark = pytest.mark.gpu
 DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
@@ -56,6 +56,18 @@ def test_squares_below_the_normal_range(dyt, dt, N):
     if N % 2 == 0:   # a mean of zero
         _, mean, r = dyt.dyt_ln_forward(x[2:], gamma, beta, 0.0)
         check("layer norm's rstd", r, want[2:], (bound + (80 + N / 256) * U) * want[2:])
+
+
+# --------------------------------------------------------------- embedding
+@pytest.mark.parametrize("T", [5119, 5120, 5121, 6000])
+@pytest.mark.parametrize("V", [300, 70000, 300000])
+def test_both_sorts_of_the_embedding(dyt, T, V):
+    """Around the number of tokens from which many workgroups sort."""
+    g = torch.Generator().manual_seed(T)
+    t = (torch.rand(T, generator=g) ** 4 * (V + 9)).long() - 4
+    dy = torch.randn(T, 33, generator=g).bfloat16().cuda()
+    dw = dyt.dyt_embed_backward(dy, t.cuda(), V, 3.0, dtype=torch.float32)
+    check_embed_backward(dy, t, V, 3.0, dw)
 
 
 # ------------------------------------------------- token log probabilities
