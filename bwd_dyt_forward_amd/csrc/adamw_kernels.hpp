@@ -280,10 +280,12 @@ __device__ __forceinline__ float sq_round(float z, float random) {
 // element. Hence one root of v for the step and for its code, factors of a block
 // in front of the loop over its elements (a lane's eight), codes of both signs
 // as c + 128 until they are packed, and an instance of its own for rounding at
-// random.
+// random. Loads and stores are ordinary ones: nontemporal loads give 16 million
+// bfloat16 parameters 42 us for 39 (with masters 58 for 42), 40 million 89 for 84 (119 for
+// 127), 60 million 126 for 131, 120 million 262 for 258, 300 million with masters 945 for 926.
 template <typename TP, typename TG, bool MASTER, bool SEEDED>
 __global__ __launch_bounds__(kAdamThreads) void adamw8_kernel(AdamArgs) {
-    constexpr int V = 8, NT = 2;   // nontemporal loads, see adamw_kernel
+    constexpr int V = 8;
     const AdamArgs& a = adam_args();
     const AdamTensor& x = a.t[adam_tensor(a, blockIdx.x)];
     const AdamStep step = adam_step(a);
@@ -298,12 +300,12 @@ __global__ __launch_bounds__(kAdamThreads) void adamw8_kernel(AdamArgs) {
         const int64_t n = end - i;
         float p[V], g[V], m[V], root[V];
         u32x2 cm = {0, 0}, cv = {0, 0};
-        if constexpr (MASTER) load_some<float, V, NT>(x.master + i, n, p);
-        else load_some<TP, V, NT>((const TP*)x.param + i, n, p);
-        load_some<TG, V, NT>((const TG*)x.grad + i, n, g);
+        if constexpr (MASTER) load_some<float, V>(x.master + i, n, p);
+        else load_some<TP, V>((const TP*)x.param + i, n, p);
+        load_some<TG, V>((const TG*)x.grad + i, n, g);
         if (n >= V) {
-            cm = load8<(NT & 2) != 0>((const uint8_t*)x.avg + i);
-            cv = load8<(NT & 2) != 0>((const uint8_t*)x.sq + i);
+            cm = load8<false>((const uint8_t*)x.avg + i);
+            cv = load8<false>((const uint8_t*)x.sq + i);
         } else {
 #pragma unroll
             for (int j = 0; j < V; ++j)
@@ -343,8 +345,8 @@ __global__ __launch_bounds__(kAdamThreads) void adamw8_kernel(AdamArgs) {
         }
         cm ^= 0x80808080u;   // c + 128 to two's complement
         if (n >= V) {
-            store8<(NT & 1) != 0>((uint8_t*)x.avg + i, cm);
-            store8<(NT & 1) != 0>((uint8_t*)x.sq + i, cv);
+            store8<false>((uint8_t*)x.avg + i, cm);
+            store8<false>((uint8_t*)x.sq + i, cv);
         } else {
 #pragma unroll
             for (int j = 0; j < V; ++j)
@@ -357,14 +359,15 @@ __global__ __launch_bounds__(kAdamThreads) void adamw8_kernel(AdamArgs) {
             x.avg_scale[i / kAdamBlock] = new_m;
             x.sq_scale[i / kAdamBlock] = new_v;
         }
-        if constexpr (MASTER) store_some<float, V, NT>(x.master + i, n, p);
-        store_some<TP, V, NT>((TP*)x.param + i, n, p);
+        if constexpr (MASTER) store_some<float, V>(x.master + i, n, p);
+        store_some<TP, V>((TP*)x.param + i, n, p);
     }
 }
 
 // The values that codes stand for. `avg` holds the codes, `param` the values;
-// `number`: 0 the first moment, 1 the second. Nontemporal loads: both moments of
-// 90.7 million parameters to bfloat16 105 us for 119.
+// `number`: 0 the first moment, 1 the second. Ordinary loads: both moments of 20
+// million parameters to bfloat16 19 us, with nontemporal loads 24; of 60 million 68 and 60;
+// of 90 million 100 and 100; of 300 million 314 and 318.
 template <typename TO>
 __global__ __launch_bounds__(kAdamThreads) void adamw_values_kernel(AdamArgs) {
     const AdamArgs& a = adam_args();
@@ -377,7 +380,7 @@ __global__ __launch_bounds__(kAdamThreads) void adamw_values_kernel(AdamArgs) {
         const int64_t n = end - i;
         uint32_t c[2] = {0, 0};
         if (n >= V) {
-            const u32x2 w = load8<true>((const uint8_t*)x.avg + i);
+            const u32x2 w = load8<false>((const uint8_t*)x.avg + i);
             c[0] = w[0];
             c[1] = w[1];
         } else {
