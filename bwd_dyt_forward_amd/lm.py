@@ -368,7 +368,10 @@ class AdamW(torch.optim.Optimizer):
                 if isinstance(value, torch.Tensor):
                     value = value.detach().to(p.device, copy=True)
                 self.state[p][name] = value
-        for group in self.param_groups:   # (counts that differ are refused by the next step)
+        for group in self.param_groups:
+            if isinstance(group["lr"], torch.Tensor):   # saved on whatever device
+                group["lr"] = group["lr"].to(group["params"][0].device)
+            # (counts that differ are refused by the next step)
             states = [self.state[p] for p in group["params"] if "step" in self.state.get(p, ())]
             if group["capturable"] and states:
                 self._join_counters(states, group["params"][0].device)

@@ -329,3 +329,38 @@ def test_a_refused_step_moves_and_counts_nothing(dyt):
                 assert all(torch.equal(v, s[k]) if isinstance(v, torch.Tensor) else v == s[k] for k, v in opt.state[x].items())
             opt.step()
             assert all(int(opt.state[x]["step"]) == 2 and not torch.equal(x, y) for x, y in zip(params, before))
+
+
+def test_states_loaded_from_the_host_can_be_stepped_and_captured(dyt):
+    """A checkpoint read to the host, of counters and rate on the device: the loaded
+    optimizer goes on as the saved one does, in a graph too."""
+    def make():
+        p = [nn.Parameter(torch.full((n,), 0.5, device="cuda")) for n in (700, 5000)]
+        for x in p:
+            x.grad = torch.linspace(-1, 1, x.numel(), device="cuda")
+        return p, dyt.AdamW(p, lr=torch.tensor(1e-2, device="cuda"), capturable=True, state_bits=8)
+
+    p, a = make()
+    a.step()
+    saved = a.state_dict()
+    saved["state"] = {k: {n: v.cpu() for n, v in s.items()} for k, s in saved["state"].items()}
+    saved["param_groups"] = [{**g, "lr": g["lr"].cpu()} for g in saved["param_groups"]]
+    q, b = make()
+    b.load_state_dict(saved)
+    assert b.param_groups[0]["lr"].is_cuda and b.state[q[0]]["step"] is b.state[q[1]]["step"]
+    with torch.no_grad():
+        for x, y in zip(p, q):
+            y.copy_(x)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        b.step()
+    for i in range(4):
+        b.param_groups[0]["lr"].fill_(1e-2 / (i + 1))
+        a.param_groups[0]["lr"].fill_(1e-2 / (i + 1))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        a.step()
+        assert all(torch.equal(x, y) for x, y in zip(p, q)), i
+    assert int(b.state[q[0]]["step"]) == 5
