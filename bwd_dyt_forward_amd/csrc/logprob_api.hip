@@ -134,6 +134,8 @@ int lp_forward(const void* logits, int64_t ld, const void* tokens, float* logp, 
     a.part_top = p.bytes ? (uint64_t*)((uint8_t*)ws + p.part_bytes) : nullptr;
     a.ld = ld; a.T = T; a.V = V; a.part_len = p.part_len; a.parts = p.parts; a.top = top; a.token_bits = bits;
     a.tpr = p.tpr; a.scale = scale;
+    const float k = scale * kLog2e;   // as the kernels round it
+    a.to_ln = (double)scale / (double)k;
     // Logits past the last-level cache (256 MB) leave it to what was written before
     // them: nontemporal loads (8,192 x 50,257 bfloat16: 182 -> 140 us; 8,192 x 4,096,
     // which fit, 17.8 -> 18.4). The backward, whose reads and writes both pass through

@@ -63,6 +63,7 @@ struct LpArgs {
     int32_t tpr;          // threads of a row, a power of two up to 64, or 256
     int32_t stream;       // 1: past the last-level cache: nontemporal loads of the forward
     float scale;
+    double to_ln;         // scale / k, see lp_fwd_kernel: ln 2 but for the rounding of k
 };
 
 struct Lse {
@@ -211,23 +212,40 @@ __device__ __forceinline__ float lanes_max8(float v) {
 
 constexpr float kLn2 = 0x1.62e43p-1f;
 
-// log p of a logit.
-__device__ __forceinline__ float lp_of(Lse v, float log2_s, float x, float k2) {
-    return v.s == 0.0f ? -INFINITY : (__builtin_fmaf(x, k2, -v.m) - log2_s) * kLn2;
-}
+// A row's log sum, m + log2 s. In two float32 numbers it has their digits; added up,
+// and brought to natural logarithms, it has them in 64 bits only: one lse of 15 rounds
+// to 2^-21, and with it log p. (A few operations a row.) `none`: every logit is -inf.
+struct RowSum {
+    double log2_sum;
+    float log2_s, k2;
+    bool none;
+
+    __device__ __forceinline__ RowSum(Lse v, float k2) : k2(k2), none(v.s == 0.0f) {
+        // s = f 2^e with f in [1/2, 1): the error of log2 f does not grow with s
+        const float e = (float)__builtin_amdgcn_frexp_expf(v.s), f = log2f(__builtin_amdgcn_frexp_mantf(v.s));
+        log2_s = none ? -INFINITY : e + f;
+        log2_sum = (double)v.m + ((double)e + (double)f);
+    }
+
+    // log p of a logit; to_ln: scale / k2.
+    __device__ __forceinline__ float log_p(float x, double to_ln) const {
+        // (what is masked in float32 would be a number in 64 bits)
+        if (none || x * k2 == -INFINITY) return -INFINITY;
+        return (float)(((double)x * (double)k2 - log2_sum) * to_ln);
+    }
+};
 
 __device__ __forceinline__ void lp_write(const LpArgs& a, int64_t m, Lse v, float x, bool real, float k2) {
-    const float log2_s = log2f(v.s);
-    const bool none = v.s == 0.0f;   // every logit is -inf
-    a.lse[m] = none ? -INFINITY : (v.m + log2_s) * kLn2;
-    const float entropy = none ? 0.0f : (log2_s - v.t / v.s) * kLn2;
+    const RowSum r(v, k2);
+    a.lse[m] = r.none ? -INFINITY : (float)(r.log2_sum * a.to_ln);
+    const float entropy = r.none ? 0.0f : (r.log2_s - v.t / v.s) * kLn2;
     a.entropy[m] = entropy;
     if (a.norm) {
         a.norm[3 * m] = v.m;
-        a.norm[3 * m + 1] = log2_s;   // -inf for none
+        a.norm[3 * m + 1] = r.log2_s;   // -inf for none
         a.norm[3 * m + 2] = entropy;
     }
-    a.logp[m] = real ? lp_of(v, log2_s, x, k2) : 0.0f;
+    a.logp[m] = real ? r.log_p(x, a.to_ln) : 0.0f;
 }
 
 // The row's token, whether there is one, and its logit.
@@ -451,12 +469,13 @@ __global__ __launch_bounds__(kLpThreads) void lp_fwd_kernel(LpArgs a) {
         each([&](uint64_t key) { best = max(best, key); });
         bound = top_bound(best, k, sh);
         each([&](uint64_t key) { top_keep(key, bound, list, sh); });
+        const RowSum row(v, k2);
         top_rank(list, k, sh, [&](int place, uint64_t best_key) {
             if (a.parts > 1) {
                 a.part_top[(int64_t)item * k + place] = best_key;
             } else {
                 a.top_tokens[(int64_t)m * k + place] = key_at(best_key);
-                a.top_logp[(int64_t)m * k + place] = lp_of(v, log2f(v.s), key_value(best_key), k2);
+                a.top_logp[(int64_t)m * k + place] = row.log_p(key_value(best_key), a.to_ln);
             }
         });
         // a part of fewer than k elements
@@ -488,10 +507,10 @@ __global__ __launch_bounds__(kLpThreads) void lp_join_kernel(LpArgs a) {
         for (int i = t; i < n; i += kLpThreads) best = max(best, keys[i]);
         const uint64_t bound = top_bound(best, k, sh);
         for (int i = t; i < n; i += kLpThreads) top_keep(keys[i], bound, list, sh);
-        const float log2_s = log2f(v.s);
+        const RowSum row(v, k2);
         top_rank(list, k, sh, [&](int place, uint64_t key) {
             a.top_tokens[m * k + place] = key_at(key);
-            a.top_logp[m * k + place] = lp_of(v, log2_s, key_value(key), k2);
+            a.top_logp[m * k + place] = row.log_p(key_value(key), a.to_ln);
         });
     }
 }

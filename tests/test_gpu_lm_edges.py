@@ -188,6 +188,31 @@ def test_the_sums_in_two_numbers(dyt, dt, T, V):
         dyt.dyt_logprob_forward(x, t, norm=norm[:, 0])
 
 
+@pytest.mark.parametrize("V", [16, 700, 5000, 70000])
+@pytest.mark.parametrize("scale", [1.0, 0.7, 1.3])
+def test_the_log_sum_is_rounded_once(dyt, V, scale):
+    """Rows of one finite logit and of two equal ones: lse is scale x (and ln 2), logp 0
+    (and -ln 2), top_logp too."""
+    g = torch.Generator().manual_seed(V)
+    x = torch.full((40, V), -math.inf)
+    at = torch.randint(0, V - 1, (40,), generator=g)
+    value = torch.randn(40, generator=g) * torch.exp(torch.randn(40, generator=g) * 3)
+    x[torch.arange(40), at] = value
+    x[20:][torch.arange(20), at[20:] + 1] = value[20:]
+    two = (torch.arange(40) >= 20).double()
+    scale = float(np.float32(scale))
+    logp, entropy, lse, top_logp, _ = dyt.dyt_logprob_forward(x.cuda(), at.cuda(), scale=scale, top=2)
+    want = scale * value.double() + two * math.log(2)
+    # one rounding, and what s is off by: it is 2^d or twice that, where d is what m, the
+    # rounded k x, leaves of k x. The hardware's exponential of that is off by EXP2 of
+    # it, and its logarithm, where 2^d is not exactly 1, by a rounding.
+    s_off = EXP2 + 2 * U
+    check("lse", lse, want, 1.001 * U * want.abs() + s_off)
+    check("logp", logp, -two * math.log(2), 1.001 * U * two + s_off)
+    check("top_logp", top_logp[:, 0], -two * math.log(2), 1.001 * U * two + s_off)
+    assert (top_logp[:20, 1] == -math.inf).all() and torch.equal(top_logp[20:, 0], top_logp[20:, 1])
+
+
 @pytest.mark.parametrize("back", [False, True])
 def test_more_rows_than_a_launch_has_workgroups(dyt, back):
     """2^24 rows of a workgroup each and a few more: the last rows as in a call of
