@@ -79,7 +79,7 @@ struct ByScale {
 
     __device__ __forceinline__ float operator()(float y) const {
         const float q = y * inv;
-        return __builtin_fmaf(__builtin_fmaf(-q, scale, y), inv, q);
+        return __builtin_fmaf(-__builtin_fmaf(q, scale, -y), inv, q);   // (so written a -0 keeps its sign)
     }
 };
 
